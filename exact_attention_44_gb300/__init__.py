@@ -14,7 +14,10 @@ from ._binding import (FA_DTYPE_BF16, FA_DTYPE_F16, FA_ERR_ALIGNMENT, FA_ERR_CUD
                        fa_fwd_raw, fa_fwd_splitkv, fa_fwd_splitkv_noalloc, fa_fwd_splitkv_raw, fa_fwd_splitkv_workspace_size,
                        fa_fwd_splitkv_workspace_size_for, fa_lse_merge,
                        fa_status_string, fa_strides, library_path, load, use_library, workspace_for)
+from ._binding import FA_ERR_PAGE
 from .build import build
+from .paged import (fa_cache_append, fa_cache_commit, fa_cache_fork, fa_cache_fork_workspace_size, fa_fwd_paged,
+                    fa_fwd_paged_workspace_size)
 
 
 def attention(q, k, v, **kwargs):
@@ -33,5 +36,6 @@ __all__ = ["attention", "attention_varlen", "fa_fwd", "fa_bwd", "fa_bwd_ex", "fa
            "fa_debug_inject_stall", "fa_debug_force_split", "fa_debug_force_chains", "fa_debug_force_pair", "fa_debug_exp2", "FA_ERR_WORKSPACE", "FA_MERGE_MAX_PARTS",
            "fa_debug_set_wait_limit_ms", "fa_strides", "FaError", "build", "load", "library_path", "FA_OK",
            "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_ALIGNMENT", "FA_ERR_CUDA", "FA_ERR_DEVICE_TIMEOUT",
-           "FA_ERR_DEVICE_CHECK", "use_library",
+           "FA_ERR_DEVICE_CHECK", "FA_ERR_PAGE", "use_library", "fa_fwd_paged", "fa_fwd_paged_workspace_size",
+           "fa_cache_append", "fa_cache_commit", "fa_cache_fork", "fa_cache_fork_workspace_size",
            "FA_DTYPE_F16", "FA_DTYPE_BF16"]

@@ -18,6 +18,7 @@
 #include "fa_bwd_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
 #include "fa_launch.h"
+#include "fa_paged.h"
 
 namespace {
 
@@ -218,6 +219,19 @@ CUresult make_map(CUtensorMap* map, const void* ptr, fa_dtype dt, int D, int N, 
 }  // namespace
 
 namespace fa {
+cudaError_t device_facts(DeviceFacts* out) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    LaunchInfo li;
+    if (err == cudaSuccess) err = device_info(dev, &li);
+    if (err != cudaSuccess) return err;
+    *out = DeviceFacts{li.sms, li.status, wait_limit_ns(), g_inject_stall.load()};
+    return cudaSuccess;
+}
+bool split_scale(float scale, float* c, int* negate) { return fwd_scale(scale, c, negate); }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
+fa_status report_cuda(const char* what, cudaError_t e) { return cuda_fail(what, e); }
+
 uint64_t current_context_id() {
     const CtxFns& f = ctx_fns();
     if (f.get_current == nullptr || f.get_id == nullptr) return 0;
@@ -709,6 +723,7 @@ const char* fa_status_string(fa_status s) {
         case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT";
         case FA_ERR_WORKSPACE: return "FA_ERR_WORKSPACE";
         case FA_ERR_DEVICE_CHECK: return "FA_ERR_DEVICE_CHECK";
+        case FA_ERR_PAGE: return "FA_ERR_PAGE";
     }
     return "FA_ERR_UNKNOWN";
 }

@@ -1,0 +1,84 @@
+// Parameters and launchers of the paged-cache operators: attention over a
+// paged cache (fa_fwd_paged) and the cache's own operations (append, commit,
+// fork).  Host and device.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime_api.h>
+
+#include <cstdint>
+
+namespace fa {
+
+constexpr uint32_t STATUS_PAGE = 8;  // FA_ERR_PAGE: a block table entry outside the cache was needed
+
+// Where a bad page was met; recorded in bits 8-15 of the device status word.
+enum PageSite : uint32_t {
+    SITE_PAGE_ATTENTION = 60,
+    SITE_PAGE_APPEND = 61,
+    SITE_PAGE_COMMIT = 62,
+    SITE_PAGE_FORK = 63,
+};
+
+// Attention over a paged cache.  Strides are in elements; the cache's are
+// (page, head, slot) with the head dim contiguous.
+struct PagedParams {
+    const void* q;
+    const void* kc;
+    const void* vc;
+    void* o;
+    float* lse;                // (Z, Hq, T) fp32 contiguous, or nullptr
+    int64_t sq_z, sq_h, sq_n;
+    int64_t so_z, so_h, so_n;
+    int64_t sk_p, sk_h, sk_n;
+    int64_t sv_p, sv_h, sv_n;
+    const int32_t* table;      // page of positions page * i .. page * i + page - 1 of sequence z at [z * st_z + i]
+    int64_t st_z;
+    const int32_t* lens;       // (Z) positions before the new tokens
+    const int32_t* news;       // (Z) new tokens, or nullptr: T each
+    const uint32_t* mask;      // bit j of words [z * sm_z + t * words ..]: new token t sees new token j; nullptr: j <= t
+    int64_t sm_z;
+    int words;                 // ceil(T / 32)
+    int Z, Hq, Hkv, G, T;      // G = Hq / Hkv
+    int page, M, P;            // slots a page, table columns, pages of the cache
+    int cap;                   // M * page: positions a sequence can have
+    int tile_rows;             // query rows of a tile (a row is a (token, head of the group) pair, heads innermost)
+    int tiles;                 // tiles of one (z, kv head): ceil(T * G / tile_rows)
+    float scale_log2;          // scale * log2(e) (rows kernel: signed; tile kernel: its magnitude)
+    int negate_s;              // tile kernel: the scale is negative
+    float* scratch;            // two partial-result slots a CTA, slot_floats floats each
+    int64_t slot_floats;
+    uint32_t* status;
+    uint64_t wait_limit_ns;
+    int inject_stall;
+};
+
+struct PagedLaunch {
+    PagedParams params;
+    int grid;                  // CTAs of the attention kernel
+    int rows;                  // rows kernel: 16 or 32 query rows a tile; 0: the tile kernel
+    const CUtensorMap* tmK;    // tile kernel only
+    const CUtensorMap* tmV;
+    cudaStream_t stream;
+};
+
+cudaError_t launch_paged_d16(const PagedLaunch& a, bool bf16);
+cudaError_t launch_paged_d32(const PagedLaunch& a, bool bf16);
+cudaError_t launch_paged_d64(const PagedLaunch& a, bool bf16);
+cudaError_t launch_paged_d128(const PagedLaunch& a, bool bf16);
+cudaError_t launch_paged_d256(const PagedLaunch& a, bool bf16);
+
+// What a launch needs from the library's per-device state (fa_api.cu).
+struct DeviceFacts {
+    int sms;
+    uint32_t* status;
+    uint64_t wait_limit_ns;
+    int inject_stall;
+};
+cudaError_t device_facts(DeviceFacts* out);
+// |scale| log2(e) and the scale's sign; false for a scale that cannot be taken
+bool split_scale(float scale, float* c, int* negate);
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+}  // namespace fa

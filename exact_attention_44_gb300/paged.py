@@ -1,0 +1,255 @@
+"""Attention over a paged key/value cache, and the cache's operations (libfa's
+fa_fwd_paged, fa_cache_append, fa_cache_commit and fa_cache_fork).
+
+A cache is two tensors k_cache and v_cache, (pages, Hkv, page_size, D) of one
+layer or (layers, pages, Hkv, page_size, D) of all (any strides with D
+contiguous, so (pages, page_size, Hkv, D) storage works as a transposed view);
+a block table (Z, max_pages) int32 names the page of every page_size positions
+of each sequence, -1 where it has none; seq_lens (Z) int32 holds the positions
+that each sequence has.  One step of speculative decoding:
+
+    fa_cache_fork(k, v, table, lens, refs, room=T, missing=missing)   # pages for T more positions
+    for layer in ...:
+        fa_cache_append(k_new, v_new, k[layer], v[layer], table, lens)
+        o, lse = fa_fwd_paged(q, k[layer], v[layer], table, lens, tree_mask=mask)
+    fa_cache_commit(k, v, table, lens, accepted, accepted_lens)       # all layers
+    lens += accepted_lens
+
+Everything is argument marshalling: the work, the lengths and the page
+bookkeeping stay on the device, and no call synchronises.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+
+from . import _binding
+from ._binding import FA_DTYPE_BF16, FA_DTYPE_F16, FA_OK, FaError, fa_strides
+
+
+def _ints(name, t, shape):
+    import torch
+
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return t
+
+
+def _table(block_table, Z):
+    import torch
+
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    if block_table.dim() != 2 or block_table.shape[0] != Z:
+        raise ValueError(f"block_table must be (Z, max_pages) = ({Z}, ...), got {tuple(block_table.shape)}")
+    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table rows must be contiguous")
+    return block_table.shape[1], block_table.stride(0)
+
+
+def _caches(k_cache, v_cache, layers):
+    """(L, layer strides, P, Hkv, page_size, D) of a pair of caches; layers: whether 5-D ones are allowed."""
+    dims = (4, 5) if layers else (4,)
+    if k_cache.dim() not in dims or k_cache.shape != v_cache.shape:
+        want = "(pages, Hkv, page_size, D)" + (" or (layers, pages, Hkv, page_size, D)" if layers else "")
+        raise ValueError(f"k_cache and v_cache must both be {want}, got {tuple(k_cache.shape)}, {tuple(v_cache.shape)}")
+    if k_cache.dtype != v_cache.dtype or k_cache.element_size() != 2:
+        raise TypeError("k_cache and v_cache must share one 16-bit dtype")
+    if k_cache.dim() == 5:
+        return (k_cache.shape[0], (k_cache.stride(0), v_cache.stride(0)), *k_cache.shape[1:])
+    return (1, (0, 0), *k_cache.shape)
+
+
+def _strides(t):
+    return ctypes.byref(fa_strides(*t.stride()[-4:]))
+
+
+def _call(name, device, stream, tensors, *args):
+    """Call libfa's `name` on `device`, its last argument the stream's handle."""
+    import torch
+
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: every tensor must be on {device}, got one on {t.device}")
+    if device.type != "cuda":
+        raise ValueError(f"{name} takes CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    fn = getattr(_binding._lib or _binding.load(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream.cuda_stream)
+    if rc != FA_OK:
+        raise FaError(rc, name)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def fa_fwd_paged_workspace_size(D: int, device=None) -> int:
+    """Workspace bytes fa_fwd_paged needs for head dim D on `device` (default: current)."""
+    import torch
+
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        rc = _binding.load().fa_fwd_paged_workspace_size(int(D), ctypes.byref(n))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_fwd_paged_workspace_size")
+    return n.value
+
+
+def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *, new_lens=None, tree_mask=None,
+                 scale: float | None = None, workspace=None, stream=None, want_lse: bool = True):
+    """Attention of the T newest tokens of every sequence over its paged cache (libfa's fa_fwd_paged).
+
+    q: (Z, Hq, T, D) fp16 or bf16; k_cache, v_cache: (pages, Hkv, page_size, D)
+    of the same dtype; block_table: (Z, max_pages) int32; seq_lens: (Z) int32,
+    the positions before the new tokens, which are already in the cache behind
+    them.  new_lens: (Z) int32, how many of the T new tokens a sequence has
+    (default T).  tree_mask: int32 bit words, (T, ceil(T/32)) for all sequences
+    or (Z, T, ceil(T/32)): bit j of token t's words says that t sees new token
+    j; None is a chain (t sees 0 .. t).  Every new token sees all earlier
+    positions.  Tokens that see nothing or do not exist get o = 0, lse = -inf.
+    workspace: a CUDA uint8 tensor of fa_fwd_paged_workspace_size(D) bytes;
+    one is allocated when omitted.  Returns (o, lse), lse (Z, Hq, T) fp32 or
+    None, without synchronising.
+    """
+    import torch
+
+    if q.dim() != 4:
+        raise ValueError("q must be 4-D (Z, Hq, T, D)")
+    Z, Hq, T, D = q.shape
+    _, _, P, Hkv, page, Dk = _caches(k_cache, v_cache, False)
+    if Dk != D:
+        raise ValueError(f"head dims differ: q has {D}, the cache {Dk}")
+    dt = FA_DTYPE_BF16 if q.dtype == torch.bfloat16 else FA_DTYPE_F16
+    if q.dtype not in (torch.float16, torch.bfloat16) or k_cache.dtype != q.dtype:
+        raise TypeError("q and the caches must share one dtype, float16 or bfloat16")
+    M, table_stride = _table(block_table, Z)
+    _ints("seq_lens", seq_lens, (Z,))
+    if new_lens is not None:
+        _ints("new_lens", new_lens, (Z,))
+    mask_stride = 0
+    if tree_mask is not None:
+        words = (T + 31) // 32
+        _ints("tree_mask", tree_mask, (T, words) if tree_mask.dim() == 2 else (Z, T, words))
+        if T > 1 and tree_mask.stride(-2) != words:
+            raise ValueError("tree_mask's words must be contiguous within a sequence")
+        mask_stride = tree_mask.stride(0) if tree_mask.dim() == 3 else 0
+    if o is None:
+        o = torch.empty((Z, Hq, T, D), dtype=q.dtype, device=q.device)
+    elif o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must match q's shape and dtype")
+    if lse is None:
+        if want_lse:
+            lse = torch.empty((Z, Hq, T), dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Z, Hq, T) or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 (Z, Hq, T) tensor")
+    if workspace is None and q.device.type == "cuda":
+        workspace = torch.empty(fa_fwd_paged_workspace_size(D, q.device), dtype=torch.uint8, device=q.device)
+    _call("fa_fwd_paged", q.device, stream,
+          (k_cache, v_cache, block_table, seq_lens, new_lens, tree_mask, o, lse, workspace),
+          q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _ptr(lse), block_table.data_ptr(),
+          seq_lens.data_ptr(), _ptr(new_lens), _ptr(tree_mask), Z, Hq, Hkv, T, D, P, page, M, table_stride, mask_stride,
+          _strides(q), _strides(k_cache), _strides(v_cache), _strides(o),
+          1.0 / math.sqrt(D) if scale is None else float(scale), dt, _ptr(workspace),
+          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    return o, lse
+
+
+def fa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, *, new_lens=None, stream=None) -> None:
+    """Write new rows into one layer's cache (libfa's fa_cache_append).
+
+    k, v: (Z, Hkv, T, D) of the cache's dtype, any strides with D contiguous;
+    row (z, :, t) goes to position seq_lens[z] + t for t < new_lens[z] (default
+    T).  seq_lens is not changed.
+    """
+    _, _, P, Hkv, page, D = _caches(k_cache, v_cache, False)
+    if k.dim() != 4 or k.shape != v.shape or k.shape[1] != Hkv or k.shape[3] != D:
+        raise ValueError(f"k and v must both be (Z, {Hkv}, T, {D}), got {tuple(k.shape)}, {tuple(v.shape)}")
+    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+        raise TypeError("k and v must have the cache's dtype")
+    Z, _, T, _ = k.shape
+    M, table_stride = _table(block_table, Z)
+    _ints("seq_lens", seq_lens, (Z,))
+    if new_lens is not None:
+        _ints("new_lens", new_lens, (Z,))
+    _call("fa_cache_append", k.device, stream, (v, k_cache, v_cache, block_table, seq_lens, new_lens),
+          k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+          seq_lens.data_ptr(), _ptr(new_lens), Z, Hkv, T, D, P, page, M, table_stride, _strides(k), _strides(v),
+          _strides(k_cache), _strides(v_cache))
+
+
+def fa_cache_commit(k_cache, v_cache, block_table, seq_lens, accepted, accepted_lens, *, stream=None) -> None:
+    """Keep the accepted ones of the drafted tokens (libfa's fa_cache_commit).
+
+    Position seq_lens[z] + accepted[z, i] moves to seq_lens[z] + i, for i <
+    accepted_lens[z], in every layer of the caches ((layers, pages, Hkv,
+    page_size, D), or one layer without the first dimension).  accepted: (Z, A)
+    int32, strictly increasing within accepted_lens[z]; accepted_lens: (Z)
+    int32.  seq_lens is not changed: add accepted_lens to it.
+    """
+    L, (kl, vl), P, Hkv, page, D = _caches(k_cache, v_cache, True)
+    if accepted.dim() != 2:
+        raise ValueError("accepted must be (Z, A)")
+    Z, A = accepted.shape
+    _ints("accepted", accepted, (Z, A))
+    _ints("accepted_lens", accepted_lens, (Z,))
+    _ints("seq_lens", seq_lens, (Z,))
+    M, table_stride = _table(block_table, Z)
+    _call("fa_cache_commit", k_cache.device, stream, (v_cache, block_table, seq_lens, accepted, accepted_lens),
+          k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), accepted.data_ptr(),
+          accepted_lens.data_ptr(), Z, L, Hkv, A, D, P, page, M, table_stride, accepted.stride(0), kl, vl,
+          _strides(k_cache), _strides(v_cache))
+
+
+def fa_cache_fork_workspace_size(Z: int, max_pages: int) -> int:
+    """Workspace bytes fa_cache_fork needs (host only)."""
+    n = ctypes.c_size_t(0)
+    rc = _binding.load().fa_cache_fork_workspace_size(int(Z), int(max_pages), ctypes.byref(n))
+    if rc != FA_OK:
+        raise FaError(rc, "fa_cache_fork_workspace_size")
+    return n.value
+
+
+def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=None, *, room: int = 0, missing=None,
+                  workspace=None, stream=None) -> None:
+    """Fork, free and give room to the sequences of a cache, in place (libfa's fa_cache_fork).
+
+    source: (Z) int32, which sequence (as it was before the call) each one
+    becomes a copy of -- itself: it stays; -1: it is emptied and its pages
+    released; None: all stay.  Copies share full pages (ref_counts, (pages)
+    int32, counts the table entries of a page; 0 is free) and get their own copy
+    of the partly filled one, in every layer of the caches.  Then every sequence
+    that is not emptied gets pages for `room` more positions.  missing: (1)
+    int32, receives how many pages lacked (0: none).  workspace: a CUDA uint8
+    tensor of fa_cache_fork_workspace_size(Z, max_pages) bytes; one is allocated
+    when omitted.
+    """
+    import torch
+
+    L, (kl, vl), P, Hkv, page, D = _caches(k_cache, v_cache, True)
+    if seq_lens.dim() != 1:
+        raise ValueError("seq_lens must be (Z)")
+    Z = seq_lens.shape[0]
+    _ints("seq_lens", seq_lens, (Z,))
+    _ints("ref_counts", ref_counts, (P,))
+    if source is not None:
+        _ints("source", source, (Z,))
+    if missing is not None:
+        _ints("missing", missing, (1,))
+    M, table_stride = _table(block_table, Z)
+    if workspace is None and k_cache.device.type == "cuda":
+        workspace = torch.empty(fa_cache_fork_workspace_size(Z, M), dtype=torch.uint8, device=k_cache.device)
+    _call("fa_cache_fork", k_cache.device, stream,
+          (v_cache, block_table, seq_lens, ref_counts, source, missing, workspace),
+          k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+          _ptr(source), _ptr(missing), Z, L, Hkv, D, P, page, M, int(room), table_stride, kl, vl, _strides(k_cache),
+          _strides(v_cache), _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0)

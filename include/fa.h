@@ -42,8 +42,10 @@ typedef enum {
     FA_ERR_CUDA = 4,            /* a CUDA runtime/driver call failed (launch, tensor map, device query) */
     FA_ERR_DEVICE_TIMEOUT = 5,  /* a bounded device-side wait ran out (see fa_device_status) */
     FA_ERR_WORKSPACE = 6,       /* workspace missing, not 256-byte aligned, or smaller than required */
-    FA_ERR_DEVICE_CHECK = 7     /* debug-check builds only: a kernel role decoded a unit outside the
+    FA_ERR_DEVICE_CHECK = 7,    /* debug-check builds only: a kernel role decoded a unit outside the
                                    launch's sizes (see fa_device_status) and stopped */
+    FA_ERR_PAGE = 8             /* a block table entry that was needed lies outside the cache, or a fork's source
+                                   outside the batch (see fa_device_status) */
 } fa_status;
 
 typedef enum { FA_DTYPE_F16 = 0, FA_DTYPE_BF16 = 1 } fa_dtype;
@@ -440,6 +442,121 @@ typedef struct {
 
 fa_status fa_fwd_schedule(int Z, int Hq, int Hkv, int Nq, int Nkv, int D, int causal, int splitkv, int num_sms,
                           int64_t l2_bytes, fa_fwd_schedule_info* out);
+
+/* ------------------------------------------------------------ paged cache ---
+ * The keys and values of many sequences, in pages of `page_size` positions:
+ *
+ *   k_cache, v_cache  (P, Hkv, page_size, D) dtype, any strides {b: page,
+ *                     h: head, n: slot, d: 1} that are multiples of 8
+ *                     elements; base 16-byte aligned
+ *   block_table       (Z, max_pages) int32, rows `table_stride` apart: position
+ *                     p of sequence z is slot p % page_size of page
+ *                     block_table[z][p / page_size]; -1 where it has none
+ *   seq_lens          (Z) int32: positions sequence z holds
+ *
+ * page_size is a multiple of 16; max_pages * page_size <= 2^30; Z <= 65535.
+ * The arrays live on the device and are read there: no call synchronises or
+ * reads anything back, so every call can be captured in a CUDA graph (after one
+ * call in the context) and follows the lengths and tables that it finds when
+ * it runs.  Calls that write a cache or share a workspace must be ordered.  A
+ * needed table entry outside 0 .. P - 1 is never followed: its positions read
+ * as zeros (attention) or are skipped (the others), and FA_ERR_PAGE is
+ * recorded (fa_device_status).  Lengths are clamped to what the table can
+ * hold.
+ */
+
+/*
+ * fa_fwd_paged -- attention of the T newest tokens of every sequence over its
+ * cache: a decode step (T = 1), a chunk of a prompt, or a tree of drafted
+ * tokens to be verified.
+ *
+ *   q         (Z, Hq, T, D) dtype, strides *sq
+ *   o         (Z, Hq, T, D) dtype, strides *so    (written)
+ *   lse       (Z, Hq, T) fp32 contiguous          (written; may be NULL)
+ *   seq_lens  positions BEFORE the new tokens; new token t of sequence z is
+ *             position seq_lens[z] + t and is in the cache already
+ *             (fa_cache_append)
+ *   new_lens  NULL, or (Z) int32: sequence z has only new_lens[z] <= T new
+ *             tokens
+ *   tree_mask NULL (a chain: new token t sees new tokens 0 .. t), or
+ *             ceil(T / 32) int32 words for each (z, t), contiguous within a
+ *             sequence, sequences mask_stride words apart (0: one tree for
+ *             all): bit j % 32 of word j / 32 says that new token t sees new
+ *             token j.  A token sees itself only if its bit says so.
+ *   scale     any finite value as for fa_fwd
+ *   workspace fa_fwd_paged_workspace_size(D) bytes, 256-byte aligned
+ *
+ * Every new token sees all positions before seq_lens[z].  With query head hq
+ * on kv head hq / (Hq / Hkv), O and lse are softmax attention over the seen
+ * positions (fp32 sums, lse natural).  A token that sees nothing, and a token
+ * t >= new_lens[z], gets O = 0 and lse = -inf.  What a page holds behind the
+ * last position is never used.  A new token's K that a query does not see has
+ * no effect on it whatever it holds; its V must be finite (the products weigh
+ * it with 0).
+ *
+ * D in {16, 32, 64, 128, 256}; Hq % Hkv == 0.  Results are bitwise
+ * reproducible for the same arguments and lengths.
+ */
+fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
+                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens,
+                       const int32_t* tree_mask, int Z, int Hq, int Hkv, int T, int D, int P, int page_size,
+                       int max_pages, int64_t table_stride, int64_t mask_stride, const fa_strides* sq,
+                       const fa_strides* sk, const fa_strides* sv, const fa_strides* so, float scale, fa_dtype dtype,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+/* Workspace bytes of fa_fwd_paged for head dim D on the current device. */
+fa_status fa_fwd_paged_workspace_size(int D, size_t* bytes);
+
+/*
+ * fa_cache_append -- write new rows: k, v (Z, Hkv, T, D) with strides *sk, *sv
+ * go to positions seq_lens[z] + t, t < new_lens[z] (NULL: T).  seq_lens is not
+ * changed (one call a layer).  Bits are moved unchanged; any 16-bit type.
+ */
+fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* block_table,
+                          const int32_t* seq_lens, const int32_t* new_lens, int Z, int Hkv, int T, int D, int P,
+                          int page_size, int max_pages, int64_t table_stride, const fa_strides* sk,
+                          const fa_strides* sv, const fa_strides* skc, const fa_strides* svc, cudaStream_t stream);
+
+/*
+ * fa_cache_commit -- keep the accepted ones of the drafted tokens: position
+ * seq_lens[z] + accepted[z][i] moves to seq_lens[z] + i for i <
+ * accepted_lens[z] <= A, in L layers of both caches (layer strides in
+ * elements), in place.  accepted (Z, A) int32, rows accepted_stride apart,
+ * strictly increasing within accepted_lens[z] (other orders leave the moved
+ * rows undefined, nothing else).  seq_lens is not changed: the caller adds
+ * accepted_lens to it.
+ */
+fa_status fa_cache_commit(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
+                          const int32_t* accepted, const int32_t* accepted_lens, int Z, int L, int Hkv, int A, int D,
+                          int P, int page_size, int max_pages, int64_t table_stride, int64_t accepted_stride,
+                          int64_t k_layer_stride, int64_t v_layer_stride, const fa_strides* skc, const fa_strides* svc,
+                          cudaStream_t stream);
+
+/*
+ * fa_cache_fork -- fork, free and give room, for the whole batch at once, in
+ * place.  ref_counts (P) int32 counts the table entries that hold a page; a
+ * page whose count is 0 is free.  Sequence z becomes a copy of sequence
+ * source[z] as it was before the call: z itself (it stays), another one, or -1
+ * (it is emptied); source NULL: all stay.  A copy shares the source's full
+ * pages and gets its own copy (all L layers) of the partly filled one; what it
+ * held before is released.  Then every sequence that is not emptied gets pages
+ * for `room` more positions.  Pages are taken lowest first from those that
+ * were free before the call, for sequences in order, columns in order; pages
+ * released by a call can be handed out by the next one.  If they do not
+ * suffice the last ones stay -1 (and a partly filled page uncopied), and
+ * *missing (int32, may be NULL) is the number of pages that lacked, columns
+ * past max_pages included; 0 otherwise.
+ *
+ * Valid state: a row's entries are its ceil(len / page_size) pages, then
+ * pages of room, then -1; a page with room to write belongs to one sequence.
+ * fa_cache_fork keeps it so.  Z <= 8192.  workspace:
+ * fa_cache_fork_workspace_size(Z, max_pages) bytes, 256-byte aligned.
+ */
+fa_status fa_cache_fork(void* k_cache, void* v_cache, int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts,
+                        const int32_t* source, int32_t* missing, int Z, int L, int Hkv, int D, int P, int page_size,
+                        int max_pages, int room, int64_t table_stride, int64_t k_layer_stride, int64_t v_layer_stride,
+                        const fa_strides* skc, const fa_strides* svc, void* workspace, size_t workspace_bytes,
+                        cudaStream_t stream);
+fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes);
 
 /*
  * Test hooks for the failure-detection path; not for production use.
