@@ -44,6 +44,7 @@ struct PagedParams {
     int page, M, P;            // slots a page, table columns, pages of the cache
     int cap;                   // M * page: positions a sequence can have
     int tile_rows;             // query rows of a tile (a row is a (token, head of the group) pair, heads innermost)
+    int box_rows;              // tile kernel: positions a TMA box holds, gcd(page, positions a block)
     int tiles;                 // tiles of one (z, kv head): ceil(T * G / tile_rows)
     float scale_log2;          // scale * log2(e) (rows kernel: signed; tile kernel: its magnitude)
     int negate_s;              // tile kernel: the scale is negative
@@ -58,7 +59,9 @@ struct PagedLaunch {
     PagedParams params;
     int grid;                  // CTAs of the attention kernel
     int rows;                  // rows kernel: 16 or 32 query rows a tile; 0: the tile kernel
-    const CUtensorMap* tmK;    // tile kernel only
+    int merge_slices;          // CTAs of the merge a tile
+    const CUtensorMap* tmQ;    // tile kernel only
+    const CUtensorMap* tmK;
     const CUtensorMap* tmV;
     cudaStream_t stream;
 };

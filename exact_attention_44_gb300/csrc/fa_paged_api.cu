@@ -61,6 +61,39 @@ fa_status check_ints(const void* p, bool needed) {
 int64_t slot_floats(int rows, int D) { return ((int64_t)rows * (D + 1) + 63) / 64 * 64; }
 size_t paged_workspace_bytes(int D, int sms) { return (size_t)2 * sms * slot_floats(128, D) * sizeof(float); }
 
+// 4-D tensor map with the head dim innermost (dims: D, then `dims` outermost
+// last) and boxes of one swizzle chunk x the given extents.
+struct MapDim {
+    int64_t extent, stride;  // stride in elements
+    int box;
+};
+CUresult make_paged_map(CUtensorMap* map, const void* ptr, bool bf16, int D, const MapDim (&dims)[3]) {
+    const int swe = D < 64 ? D : 64;
+    const CUtensorMapSwizzle sw = swe == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : swe == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_32B;
+    cuuint64_t ext[4] = {(cuuint64_t)D, 0, 0, 0}, str[3];
+    cuuint32_t box[4] = {(cuuint32_t)swe, 0, 0, 0}, ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        ext[i + 1] = (cuuint64_t)dims[i].extent;
+        // a dimension of extent 1 is never stepped along; give it a harmless stride
+        str[i] = dims[i].extent > 1 ? (cuuint64_t)dims[i].stride * 2 : (cuuint64_t)D * 2;
+        box[i + 1] = (cuuint32_t)dims[i].box;
+    }
+    const auto fn = fa::tensor_map_encoder();
+    if (fn == nullptr) return CUDA_ERROR_NOT_SUPPORTED;
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr),
+              ext, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// Largest box of whole page rows that tiles a block of `bn` positions.
+int box_rows_for(int page, int bn) {
+    int r = 16;
+    while (r < bn && page % (2 * r) == 0) r *= 2;
+    return r;
+}
+
 cudaError_t launch_paged(int D, const fa::PagedLaunch& a, bool bf16) {
     switch (D) {
         case 16: return fa::launch_paged_d16(a, bf16);
@@ -112,7 +145,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     const int G = Hq / Hkv;
     const int64_t rows = (int64_t)Z * Hq * T;
     // (row and tile indices fit in 32 bits)
-    if ((int64_t)T * G > (int64_t(1) << 30) || (int64_t)Z * Hkv * cdiv((int64_t)T * G, 16) > INT32_MAX)
+    if ((int64_t)T * G > (int64_t(1) << 30) || (int64_t)Z * Hkv * cdiv((int64_t)T * G, 16) > INT32_MAX / 8)
         return FA_ERR_UNSUPPORTED;
     if (rows == 0) return FA_OK;
     if ((st = check_strided(q, sq, Z, Hq, T, false)) != FA_OK) return st;
@@ -157,14 +190,42 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     p.inject_stall = f.inject_stall;
     a.stream = stream;
 
-    a.rows = T * G <= 16 || D == 256 ? 16 : 32;
-    p.tile_rows = a.rows;
-    p.scale_log2 = negate ? -c : c;
+    const bool bf16 = dtype == FA_DTYPE_BF16;
+    // Few rows of a (sequence, kv head) run on the rows kernel.  The tile
+    // kernel needs a whole group in a tile and a cache to map.
+    const bool tiles = T * (int64_t)G > 32 && G <= 128 && P > 0;
+    CUtensorMap mq, mk, mv;
+    if (tiles) {
+        const int bn = D == 256 ? 64 : 128, tokens = 128 / G;
+        a.rows = 0;
+        p.tile_rows = tokens * G;
+        p.box_rows = box_rows_for(page_size, bn);
+        p.scale_log2 = c;
+        p.negate_s = negate;
+        p.slot_floats = slot_floats(128, D);
+        a.merge_slices = 8;
+        const MapDim dq[3] = {{Hq, sq->h, G}, {T, sq->n, tokens}, {Z, sq->b, 1}};
+        const MapDim dk[3] = {{page_size, sk->n, p.box_rows}, {Hkv, sk->h, 1}, {P, sk->b, 1}};
+        const MapDim dv[3] = {{page_size, sv->n, p.box_rows}, {Hkv, sv->h, 1}, {P, sv->b, 1}};
+        if (make_paged_map(&mq, q, bf16, D, dq) != CUDA_SUCCESS || make_paged_map(&mk, k_cache, bf16, D, dk) != CUDA_SUCCESS ||
+            make_paged_map(&mv, v_cache, bf16, D, dv) != CUDA_SUCCESS)
+            return FA_ERR_CUDA;
+        a.tmQ = &mq;
+        a.tmK = &mk;
+        a.tmV = &mv;
+    } else {
+        a.rows = T * (int64_t)G <= 16 || D == 256 ? 16 : 32;
+        p.tile_rows = a.rows;
+        p.scale_log2 = negate ? -c : c;
+        p.slot_floats = slot_floats(a.rows, D);
+        a.merge_slices = 1;
+    }
     p.tiles = (int)cdiv((int64_t)T * G, p.tile_rows);
-    p.slot_floats = slot_floats(p.tile_rows, D);
-    const int64_t blocks = (int64_t)Z * Hkv * p.tiles * cdiv(p.cap, 64);  // at most
-    a.grid = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)f.sms * (D <= 128 ? 2 : 1)));
-    err = launch_paged(D, a, dtype == FA_DTYPE_BF16);
+    const int bk = tiles ? (D == 256 ? 64 : 128) : 64;
+    const int64_t blocks = (int64_t)Z * Hkv * p.tiles * cdiv(p.cap, bk);  // at most
+    const int64_t ctas = (int64_t)f.sms * (tiles || D > 128 ? 1 : 2);
+    a.grid = (int)std::max<int64_t>(1, std::min(blocks, ctas));
+    err = launch_paged(D, a, bf16);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("paged attention launch", err);
 }
 

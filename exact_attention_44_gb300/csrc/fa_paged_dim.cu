@@ -6,18 +6,20 @@
 #include "fa_launch.h"
 #include "fa_paged.h"
 #include "fa_paged_rows_kernel.cuh"
+#include "fa_paged_tile_kernel.cuh"
 
 namespace fa {
 
 template <int BK, bool BF16, bool COLS>
 static cudaError_t launch_merge(const PagedLaunch& a, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((int64_t)a.params.Z * a.params.Hkv * a.params.tiles));
+    cfg.gridDim = dim3((unsigned)((int64_t)a.params.Z * a.params.Hkv * a.params.tiles * a.merge_slices));
     cfg.blockDim = dim3(PAGED_MERGE_THREADS);
     cfg.stream = a.stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<FA_HEAD_DIM, BK, BF16, COLS>, a.params, a.grid);
+    return cudaLaunchKernelEx(&cfg, fa_paged_merge_kernel<FA_HEAD_DIM, BK, BF16, COLS>, a.params, a.grid,
+                              a.merge_slices);
 }
 
 template <int RT, bool BF16>
@@ -41,9 +43,31 @@ static cudaError_t launch_rows(const PagedLaunch& a) {
     return err == cudaSuccess ? launch_merge<ROWS_BK, BF16, false>(a, attr) : err;
 }
 
+template <bool BF16>
+static cudaError_t launch_tile(const PagedLaunch& a) {
+    using T = TileTraits<FA_HEAD_DIM>;
+    auto kernel = fa_paged_tile_kernel<FA_HEAD_DIM, BF16>;
+    static std::atomic<uint64_t> configured{0};
+    cudaError_t err = set_smem_for_context(kernel, T::SMEM_BYTES, configured);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.grid);
+    cfg.blockDim = dim3(T::THREADS);
+    cfg.dynamicSmemBytes = T::SMEM_BYTES;
+    cfg.stream = a.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kernel, *a.tmQ, *a.tmK, *a.tmV, a.params);
+    return err == cudaSuccess ? launch_merge<T::BN, BF16, true>(a, attr) : err;
+}
+
 #define FA_CAT2(a, b) a##b
 #define FA_CAT(a, b) FA_CAT2(a, b)
 cudaError_t FA_CAT(launch_paged_d, FA_HEAD_DIM)(const PagedLaunch& a, bool bf16) {
+    if (a.rows == 0) return bf16 ? launch_tile<true>(a) : launch_tile<false>(a);
 #if FA_HEAD_DIM <= 128
     if (a.rows == 32) return bf16 ? launch_rows<32, true>(a) : launch_rows<32, false>(a);
 #endif

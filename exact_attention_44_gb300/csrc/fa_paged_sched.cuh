@@ -200,7 +200,7 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ merge ---------
-// One block per (sequence, kv head, tile).  A tile that the cuts crossed has
+// `slices` blocks per (sequence, kv head, tile), each a share of its rows.  A tile that the cuts crossed has
 // its parts in slots 2 c0 + 1 (the CTA c0 of its first block) and 2 c (CTAs
 // c0 + 1 .. c1); with lambda_s the base-2 log-sum-exp of part s and O_s its O / l,
 //     lambda = log2 sum_s 2^lambda_s,   O = sum_s 2^(lambda_s - lambda) O_s,
@@ -213,18 +213,22 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 constexpr int PAGED_MERGE_THREADS = 512;
 
 template <int D, int BK, bool BF16, bool COLS>
-__global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int grid) {
+__global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int grid, int slices) {
     __shared__ int64_t red[32];
     __shared__ float sh[PAGED_MERGE_THREADS * 6];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int tid = threadIdx.x;
     const int per_z = p.Hkv * p.tiles;
-    const int z = blockIdx.x / per_z, r = blockIdx.x - z * per_z;
+    const int tile = blockIdx.x / slices, slice = blockIdx.x - tile * slices;
+    const int z = tile / per_z, r = tile - z * per_z;
     const int hk = r / p.tiles, mt = r - hk * p.tiles;
     const SeqLen s = seq_len(p, z);
     const int row0 = mt * p.tile_rows;
-    const int rows = min(p.tile_rows, s.nl * p.G - row0);  // live rows, may be <= 0
+    // this block's rows of the tile, the live ones first
+    const int share = (p.tile_rows + slices - 1) / slices, lo = slice * share, hi = min(lo + share, p.tile_rows);
+    const int live = min(hi, s.nl * p.G - row0);
+    const int rows = live - lo;  // may be <= 0
     constexpr int W = D / 4;
     auto row_at = [&](int row, int64_t& lse_at, int64_t& o_at) {  // row of the (sequence, kv head)
         const int t = row / p.G, h = hk * p.G + row - t * p.G;
@@ -233,7 +237,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     };
     // rows without a token
     {
-        const int first = max(rows, 0), last = min(p.tile_rows, p.T * p.G - row0);
+        const int first = max(live, lo), last = min(hi, p.T * p.G - row0);
         for (int i = first * W + tid; i < last * W; i += PAGED_MERGE_THREADS) {
             const int row = i / W, c = i - row * W;
             int64_t la, oa;
@@ -266,7 +270,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     for (int i0 = 0; i0 < items; i0 += per_round) {
         const int i = i0 + tid - g * per_round;
         const bool ok = g < spl && i < items;
-        const int row = !ok ? 0 : COLS ? i % rows : i / W, c = !ok ? 0 : COLS ? i / rows : i % W;
+        const int row = !ok ? 0 : lo + (COLS ? i % rows : i / W), c = !ok ? 0 : COLS ? i / rows : i % W;
         float mx = -INFINITY, den = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (ok) {

@@ -1,0 +1,539 @@
+// Attention over a paged cache for many query rows (a wide tree, a chunk of a
+// prompt): the forward of fa_fwd_kernel.cuh -- S = Q Kᵀ and O += P V on
+// tcgen05 with S, P and O in tensor memory, K and V through TMA rings, an
+// online softmax over four column groups -- with
+//   * a tile of up to 128 (new token, query head) rows of one (sequence, kv
+//     head), so that K and V of a position are loaded and multiplied once for
+//     the whole group;
+//   * K and V blocks gathered from their pages: a block of BN positions is
+//     BN / RB boxes of RB = gcd(page, BN) rows, one lane of the producer warp
+//     per box, each through its own block table entry (out of range: the
+//     tensor map fills zeros);
+//   * the device-side division of the work of fa_paged_sched.cuh;
+//   * the tree's bits as one 32-bit word per thread and block (a thread holds
+//     32 positions of a row);
+//   * V rows behind the sequence's end zeroed in shared memory before the
+//     product reads them: whatever the page holds there (NaN included) must
+//     not meet the zero weights.
+// Warps whose 32 rows hold no token skip the softmax and only keep the
+// barriers' counts.  Every wait is bounded as in fa_fwd_kernel.cuh.
+#pragma once
+
+#include "fa_fwd_kernel.cuh"
+#include "fa_paged_sched.cuh"
+
+namespace fa {
+
+template <int D_>
+struct TileTraits : Traits<D_> {
+    using Base = Traits<D_>;
+    static constexpr int B_VFIX = Base::NUM_BARS;             // [2] V slot's rows behind the end zeroed
+    static constexpr int NUM_BARS = B_VFIX + 2;
+    static constexpr int OFF_MISC = Base::OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM_USED = OFF_MISC + 16;
+    static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static_assert((int)sizeof(PagedFind) <= 2 * Base::HAND_ROWS * BM * 4, "the range search fits the hand-over area");
+};
+
+// A block's boxes: lane b of the producer warp has the box of positions
+// kj * BN + b * rb .. (b * rb < BN), if the sequence has any of them.
+struct PageBox {
+    int page, slot;
+    bool there;
+};
+__device__ __forceinline__ PageBox page_box(const PagedParams& p, const int32_t* row, int k0, int rb, int bn, int end,
+                                            int lane) {
+    PageBox b{p.P, 0, false};
+    const int k = k0 + lane * rb;
+    if (lane * rb < bn && k < end) {
+        const int col = k / p.page;
+        b.slot = k - col * p.page;
+        b.page = ldi(row + col);
+        b.there = true;
+    }
+    return b;
+}
+// Called by the warp: one block into shared memory at dst, completing on bar.
+template <int D>
+__device__ __forceinline__ void load_boxes(const PagedParams& p, PageBox b, const CUtensorMap* tm, uint32_t dst,
+                                           uint32_t bar, int hk, int rb, int lane, uint64_t policy) {
+    using T = Traits<D>;
+    if (b.there && (unsigned)b.page >= (unsigned)p.P) {
+        record_bad_page(p.status, SITE_PAGE_ATTENTION);
+        b.page = p.P;  // outside the map: zeros
+    }
+    const uint32_t n = __popc(__ballot_sync(0xffffffffu, b.there));
+    if (lane == 0) ptx::mbar_arrive_expect_tx(bar, n * rb * T::SW * T::NCHUNK);
+    __syncwarp();
+    if (b.there)
+        for (int c = 0; c < T::NCHUNK; ++c)
+            ptx::tma_load_4d(dst + c * (T::BN * T::SW) + lane * rb * T::SW, tm, bar, c * T::SWE, b.slot, hk, b.page,
+                             policy);
+}
+
+template <int D>
+__device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK, const PagedParams& p, PagedWalk w,
+                                 uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
+    using T = TileTraits<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int lane = threadIdx.x % 32;
+    const uint64_t pol_q = ptx::policy_evict_first(), pol_kv = ptx::policy_evict_last();
+    uint32_t qi = 0, ki = 0;
+    bool ok = true, withheld = false;
+    auto load_q = [&](const PagedSeg& sg) -> bool {
+        const uint32_t s = qi % T::Q_STAGES, ph = (qi / T::Q_STAGES) & 1u;
+        if (!warp_wait_phase(bar(T::B_QEMPTY + s), ph ^ 1u, ctl, SITE_Q_EMPTY)) return false;
+        if (lane == 0) {
+            ptx::mbar_arrive_expect_tx(bar(T::B_QFULL + s), (uint32_t)p.tile_rows * T::SW * T::NCHUNK);
+            const uint32_t dst = sbase + T::OFF_Q + s * T::Q_BYTES;
+            for (int c = 0; c < T::NCHUNK; ++c)
+                ptx::tma_load_4d(dst + c * (BM * T::SW), tmQ, bar(T::B_QFULL + s), c * T::SWE, sg.hk * p.G,
+                                 sg.row0 / p.G, sg.z, pol_q);
+        }
+        __syncwarp();
+        ++qi;
+        return true;
+    };
+    PagedSeg sg{};
+    if (w.left > 0) {
+        sg = paged_seg<T::BN>(p, w);
+        ok = load_q(sg);
+    }
+    while (ok && w.left > 0) {
+        paged_next(p, sg, w);
+        PagedSeg nx{};
+        if (w.left > 0) nx = paged_seg<T::BN>(p, w);
+        const int32_t* row = p.table + (int64_t)sg.z * p.st_z;
+        const int end = sg.len + sg.nl;
+        PageBox b = page_box(p, row, sg.jb * T::BN, p.box_rows, T::BN, end, lane);
+        for (int j = sg.jb; j < sg.je; ++j) {
+            PageBox after = b;
+            if (j + 1 < sg.je) after = page_box(p, row, (j + 1) * T::BN, p.box_rows, T::BN, end, lane);
+            const uint32_t s = ki & 1u;
+            if (ki >= 2 && !warp_wait_phase(bar(T::B_SFULL + rslot<T::SR>(ki - 2)), rphase<T::SR>(ki - 2), ctl,
+                                            SITE_K_EMPTY)) { ok = false; break; }
+            if (p.inject_stall && blockIdx.x == 0 && !withheld) {
+                withheld = true;  // never issued: the S issuer's wait for this block must time out
+            } else {
+                load_boxes<D>(p, b, tmK, sbase + T::OFF_K + s * T::KV_BYTES, bar(T::B_KFULL + s), sg.hk, p.box_rows,
+                              lane, pol_kv);
+            }
+            ++ki;
+            b = after;
+            const int q_at = T::Q_STAGES >= 2 ? sg.jb : sg.je - 1;
+            if (j == q_at && w.left > 0 && !load_q(nx)) {
+                ok = false;
+                break;
+            }
+        }
+        sg = nx;
+    }
+    if (!ok) {
+        const uint64_t lim = ctl.limit_ns;
+        for (uint32_t i = qi > (uint32_t)T::Q_STAGES ? qi - T::Q_STAGES : 0; i < qi; ++i)
+            drain_phase(bar(T::B_QFULL + i % T::Q_STAGES), (i / T::Q_STAGES) & 1u, lim);
+        for (uint32_t i = ki > 2u ? ki - 2u : 0u; i < ki; ++i)
+            drain_phase(bar(T::B_KFULL + (i & 1u)), (i >> 1) & 1u, withheld ? lim / 64 : lim);
+    }
+}
+
+template <int D>
+__device__ void tile_producer_v(const CUtensorMap* tmV, const PagedParams& p, PagedWalk w, uint32_t sbase,
+                                uint32_t bar0, const Ctl& ctl) {
+    using T = TileTraits<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int lane = threadIdx.x % 32;
+    const uint64_t pol_kv = ptx::policy_evict_last();
+    uint32_t vi = 0;
+    bool ok = true;
+    while (ok && w.left > 0) {
+        const PagedSeg sg = paged_seg<T::BN>(p, w);
+        paged_next(p, sg, w);
+        const int32_t* row = p.table + (int64_t)sg.z * p.st_z;
+        const int end = sg.len + sg.nl;
+        PageBox b = page_box(p, row, sg.jb * T::BN, p.box_rows, T::BN, end, lane);
+        for (int j = sg.jb; j < sg.je; ++j) {
+            PageBox after = b;
+            if (j + 1 < sg.je) after = page_box(p, row, (j + 1) * T::BN, p.box_rows, T::BN, end, lane);
+            const uint32_t s = vi & 1u;
+            if (vi >= 2 && !warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(vi - 2)), rphase<T::SR>(vi - 2), ctl,
+                                            SITE_V_EMPTY)) { ok = false; break; }
+            const uint32_t dst = sbase + T::OFF_V + s * T::KV_BYTES;
+            load_boxes<D>(p, b, tmV, dst, bar(T::B_VFULL + s), sg.hk, p.box_rows, lane, pol_kv);
+            ++vi;
+            b = after;
+            if ((j + 1) * T::BN > end) {
+                // zero the rows behind the end, once the copies have landed
+                if (!warp_wait_phase(bar(T::B_VFULL + s), ((vi - 1) >> 1) & 1u, ctl, SITE_V_FULL)) { ok = false; break; }
+                const int first = end - j * T::BN;  // 1 .. BN - 1
+                constexpr int PR = T::SW / 16;      // 16-byte pieces of a row's chunk
+                for (int c = 0; c < T::NCHUNK; ++c)
+                    for (int i = first * PR + lane; i < T::BN * PR; i += 32)
+                        ptx::st_shared_v4(dst + c * (T::BN * T::SW) + i * 16, 0u, 0u, 0u, 0u);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(bar(T::B_VFIX + s));
+            }
+        }
+    }
+    if (!ok)
+        for (uint32_t i = vi > 2u ? vi - 2u : 0u; i < vi; ++i)
+            drain_phase(bar(T::B_VFULL + (i & 1u)), (i >> 1) & 1u, ctl.limit_ns);
+}
+
+template <int D, bool BF16>
+__device__ void tile_mma_qk(const PagedParams& p, PagedWalk w, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+                            const Ctl& ctl) {
+    using T = TileTraits<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const uint32_t IDESC = ptx::idesc_f16(BM, T::BN, BF16, false, false) | (p.negate_s ? ptx::IDESC_NEGATE_A : 0u);
+    constexpr uint32_t HI = ptx::smem_desc_hi(8 * T::SW, T::SWIZZLE_CODE);
+    const uint32_t q_lo0 = ptx::smem_desc_lo(sbase + T::OFF_Q, 16);
+    const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16);
+    uint32_t qi = 0, g = 0;
+    bool ok = true;
+    while (ok && w.left > 0) {
+        const PagedSeg sg = paged_seg<T::BN>(p, w);
+        paged_next(p, sg, w);
+        const uint32_t qs = qi % T::Q_STAGES;
+        if (!wait_phase(bar(T::B_QFULL + qs), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
+        const uint32_t q_lo = q_lo0 + qs * (T::Q_BYTES >> 4);
+        for (int j = sg.jb; j < sg.je; ++j, ++g) {
+            const uint32_t kb = g & 1u, r = rslot<T::SR>(g);
+            if (!wait_phase(bar(T::B_KFULL + kb), (g >> 1) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
+            if (g >= (uint32_t)T::SR && !wait_phase(bar(T::B_PVDONE + r), rphase<T::SR>(g - T::SR), ctl, SITE_S_FREE)) {
+                ok = false;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t k_lo = k_lo0 + kb * (T::KV_BYTES >> 4);
+            const uint32_t d_tmem = tmem + T::TM_S + r * T::BN;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t a_off = (((kk * 16) / T::SWE) * (BM * T::SW) + ((kk * 16) % T::SWE) * 2) >> 4;
+                const uint32_t b_off = (((kk * 16) / T::SWE) * (T::BN * T::SW) + ((kk * 16) % T::SWE) * 2) >> 4;
+                ptx::mma_ss(d_tmem, ptx::desc64(q_lo + a_off, HI), ptx::desc64(k_lo + b_off, HI), IDESC,
+                            kk > 0 ? 1u : 0u);
+            }
+            ptx::tc_commit(bar(T::B_SFULL + r));
+            if (j == sg.je - 1) {
+                ptx::tc_commit(bar(T::B_QEMPTY + qs));
+                ++qi;
+            }
+        }
+    }
+    if (!ok) {
+        ptx::tc_commit(bar(T::B_DRAIN));
+        drain_phase(bar(T::B_DRAIN), 0u, ctl.limit_ns);
+    }
+}
+
+template <int D, bool BF16>
+__device__ void tile_mma_pv(const PagedParams& p, PagedWalk w, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+                            const Ctl& ctl) {
+    using T = TileTraits<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    constexpr uint32_t IDESC = ptx::idesc_f16(BM, D, BF16, false, true);
+    constexpr uint32_t HI = ptx::smem_desc_hi(8 * T::SW, T::SWIZZLE_CODE);
+    const uint32_t v_lo0 = ptx::smem_desc_lo(sbase + T::OFF_V, T::BN * T::SW);
+    uint32_t g = 0, ntile = 0, fixes[2] = {0, 0};
+    bool ok = true;
+    for (; ok && w.left > 0; ++ntile) {
+        const PagedSeg sg = paged_seg<T::BN>(p, w);
+        paged_next(p, sg, w);
+        for (int j = sg.jb; j < sg.je; ++j, ++g) {
+            const uint32_t vb = g & 1u, r = rslot<T::SR>(g);
+            if (j == sg.jb && ntile > 0 &&
+                !wait_phase(bar(T::B_OFREE), (ntile - 1) & 1u, ctl, SITE_O_FREE)) { ok = false; break; }
+            if (!wait_phase(bar(T::B_PFULL + r), rphase<T::SR>(g), ctl, SITE_P_FULL)) { ok = false; break; }
+            if (!wait_phase(bar(T::B_VFULL + vb), (g >> 1) & 1u, ctl, SITE_V_FULL)) { ok = false; break; }
+            if ((j + 1) * T::BN > sg.len + sg.nl) {
+                const uint32_t n = vb == 0 ? fixes[0]++ : fixes[1]++;
+                if (!wait_phase(bar(T::B_VFIX + vb), n & 1u, ctl, SITE_V_FULL)) { ok = false; break; }
+            }
+            ptx::tc_fence_after();
+            const uint32_t v_lo = v_lo0 + vb * (T::KV_BYTES >> 4);
+            const uint32_t a_tmem = tmem + T::TM_S + r * T::BN;
+            const uint32_t acc0 = j > sg.jb ? 1u : 0u;
+#pragma unroll
+            for (int kk = 0; kk < T::BN / 16; ++kk)
+                ptx::mma_ts(tmem + T::TM_O, a_tmem + kk * 8, ptx::desc64(v_lo + ((kk * 16 * T::SW) >> 4), HI), IDESC,
+                            kk > 0 ? 1u : acc0);
+            ptx::tc_commit(bar(T::B_PVDONE + r));
+        }
+    }
+    if (!ok) {
+        ptx::tc_commit(bar(T::B_DRAIN + 1));
+        drain_phase(bar(T::B_DRAIN + 1), 0u, ctl.limit_ns);
+    }
+}
+
+// Which of positions k0 .. k0 + 31 new token t sees, as bits.
+__device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, const PagedSeg& sg, int t, int k0) {
+    const int j0 = k0 - sg.len;  // new token of the first position (negative: before the new tokens)
+    const int lim = (p.mask == nullptr ? min(t + 1, sg.nl) : sg.nl) - j0;
+    if (lim <= 0) return 0u;
+    uint32_t bits = lim >= 32 ? 0xffffffffu : (1u << lim) - 1u;
+    if (p.mask != nullptr && j0 > -32) {
+        const uint32_t* row = p.mask + sg.z * p.sm_z + (int64_t)t * p.words;
+        if (j0 >= 0) {
+            const int i = j0 >> 5;
+            const uint32_t lo = i < p.words ? __ldcg(row + i) : 0u, hi = i + 1 < p.words ? __ldcg(row + i + 1) : 0u;
+            bits &= __funnelshift_r(lo, hi, j0 & 31);
+        } else {
+            bits &= (__ldcg(row) << -j0) | ((1u << -j0) - 1u);
+        }
+    }
+    return bits;
+}
+
+template <int D, bool BF16>
+__device__ void tile_softmax(const PagedParams& p, PagedWalk w, uint32_t bar0, uint32_t tmem, float* hand, float* red,
+                             int h, const Ctl& ctl) {
+    using T = TileTraits<D>;
+    constexpr int BN = T::BN, NG = T::NG, HC = BN / NG;
+    static_assert(HC == 32, "a thread holds 32 positions");
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int quad = (threadIdx.x / 32) % 4;
+    const int row = quad * 32 + threadIdx.x % 32;
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    const float c = p.scale_log2;
+    const uint64_t c2 = ptx::pack_f32x2(c, c);
+    uint32_t step = 0, ntile = 0;
+    for (; w.left > 0; ++ntile) {
+        const PagedSeg sg = paged_seg<BN>(p, w);
+        paged_next(p, sg, w);
+        const int tok = min((sg.row0 + row) / p.G, p.T - 1);
+        const bool idle = quad * 32 >= sg.rows;  // none of the warp's rows holds a token
+        float m = -INFINITY, l = 0.f;
+        for (int j = sg.jb; j < sg.je; ++j) {
+            const uint32_t r = rslot<T::SR>(step);
+            const uint32_t b = step & 1u, ph = (step >> 1) & 1u;
+            if (!warp_wait_phase(bar(T::B_SFULL + r), rphase<T::SR>(step), ctl, SITE_S_FULL)) return;
+            if (idle) {
+                // (P of these rows stays what S left there: rows do not mix)
+                ptx::mbar_arrive(bar(T::B_RED + b));
+                ptx::mbar_arrive(bar(T::B_PFULL + r));
+                ++step;
+                continue;
+            }
+            ptx::tc_fence_after();
+            const uint32_t s_addr = tmem + lane_addr + T::TM_S + r * BN;
+            float s[HC];
+            {
+                uint32_t rr[HC];
+                ptx::tmem_ld32(s_addr + h * HC, rr);
+#pragma unroll
+                for (int x = 0; x < HC; ++x) s[x] = __uint_as_float(rr[x]);
+            }
+            if (j * BN + BN > sg.len) {
+                const uint32_t bits = seen_bits(p, sg, tok, j * BN + h * HC);
+#pragma unroll
+                for (int x = 0; x < HC; ++x)
+                    if (!((bits >> x) & 1u)) s[x] = -INFINITY;
+            }
+            float mx0 = fmaxf(s[0], s[1]), mx1 = fmaxf(s[2], s[3]);
+#pragma unroll
+            for (int x = 4; x < HC; x += 4) {
+                mx0 = ptx::fmax3(mx0, s[x], s[x + 1]);
+                mx1 = ptx::fmax3(mx1, s[x + 2], s[x + 3]);
+            }
+            const float pmax = fmaxf(mx0, mx1);
+            red[(b * NG + h) * BM + row] = pmax;
+            ptx::mbar_arrive(bar(T::B_RED + b));
+            auto block_max = [&]() {
+                float mm = pmax;
+#pragma unroll
+                for (int g2 = 0; g2 < NG; ++g2) mm = fmaxf(mm, red[(b * NG + g2) * BM + row]);
+                return mm * c;
+            };
+            if (j == sg.jb) {
+                if (!warp_wait_phase(bar(T::B_RED + b), ph, ctl, SITE_MAX_XCHG)) return;
+                m = block_max();
+            }
+            constexpr int NP = HC / 2;
+            uint32_t pk[NP];
+            auto exps = [&](float ref) -> uint64_t {
+                ref = ref == -INFINITY ? 0.f : ref;  // nothing seen so far: p = 0, not 2^(-inf + inf)
+                const uint64_t negm2 = ptx::pack_f32x2(-ref, -ref);
+                uint64_t sum2 = ptx::pack_f32x2(0.f, 0.f);
+#pragma unroll
+                for (int x = 0; x < NP; ++x) {
+                    float a0, a1;
+                    ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(s[2 * x], s[2 * x + 1]), c2, negm2), a0, a1);
+                    const float p0 = ptx::ex2(a0), p1 = ptx::ex2(a1);
+                    sum2 = ptx::fadd2(sum2, ptx::pack_f32x2(p0, p1));
+                    pk[x] = pack2<BF16>(p0, p1);
+                }
+                return sum2;
+            };
+            uint64_t sum2 = exps(m);
+            float alpha = 1.f;
+            if (j > sg.jb) {
+                if (!warp_wait_phase(bar(T::B_RED + b), ph, ctl, SITE_MAX_XCHG)) return;
+                const float m_tile = block_max();
+                if (__any_sync(0xffffffffu, m_tile > m + RESCALE_LOG2)) {
+                    const float m_new = fmaxf(m, m_tile);
+                    alpha = m == -INFINITY ? 0.f : ptx::ex2(m - m_new);
+                    m = m_new;
+                    sum2 = exps(m);
+                    const uint32_t g = step - 1;
+                    if (!warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(g)), rphase<T::SR>(g), ctl, SITE_PV_DONE))
+                        return;
+                    ptx::tc_fence_after();
+                    rescale_o<D / NG>(tmem + lane_addr + T::TM_O + h * (D / NG), alpha);
+                }
+            }
+            ptx::tmem_st16(s_addr + h * NP, pk);
+            ptx::tmem_wait_st();
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(T::B_PFULL + r));
+            float sl, sh;
+            ptx::unpack_f32x2(sum2, sl, sh);
+            l = l * alpha + (sl + sh);
+            ++step;
+        }
+        const uint32_t slot = ntile & 1u;
+        if (!warp_wait_phase(bar(T::B_EPIEMPTY + slot), ((ntile >> 1) & 1u) ^ 1u, ctl, SITE_EPI_EMPTY)) return;
+        if (h == 0) hand[slot * T::HAND_ROWS * BM + row] = m;
+        hand[slot * T::HAND_ROWS * BM + (1 + h) * BM + row] = l;
+        ptx::mbar_arrive(bar(T::B_EPIFULL + slot));
+    }
+}
+
+template <int D, bool BF16>
+__device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, uint32_t tmem, const float* hand,
+                              const Ctl& ctl) {
+    using T = TileTraits<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int quad = (threadIdx.x / 32) % 4;
+    const int row = quad * 32 + threadIdx.x % 32;
+    const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O;
+    uint32_t step = 0, ntile = 0;
+    constexpr int CH = D >= 32 ? 32 : 16;
+    for (; w.left > 0; ++ntile) {
+        const PagedSeg sg = paged_seg<T::BN>(p, w);
+        paged_next(p, sg, w);
+        step += sg.je - sg.jb;
+        const uint32_t slot = ntile & 1u;
+        if (!warp_wait_phase(bar(T::B_EPIFULL + slot), (ntile >> 1) & 1u, ctl, SITE_EPI_FULL)) return;
+        const float m = hand[slot * T::HAND_ROWS * BM + row];
+        float l = 0.f;
+#pragma unroll
+        for (int g2 = 0; g2 < T::NG; ++g2) l += hand[slot * T::HAND_ROWS * BM + (1 + g2) * BM + row];
+        ptx::mbar_arrive(bar(T::B_EPIEMPTY + slot));
+        const uint32_t g = step - 1;
+        if (!warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(g)), rphase<T::SR>(g), ctl, SITE_PV_DONE)) return;
+        ptx::tc_fence_after();
+        const bool keep = row < sg.rows;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        if (sg.slot >= 0) {
+            // a part: float4 column group c4 of row r at [c4][r], then the base-2 log-sum-exps
+            float* part = p.scratch + (int64_t)sg.slot * p.slot_floats;
+            float4* col = reinterpret_cast<float4*>(part) + row;
+#pragma unroll 1
+            for (int i = 0; i < D / CH; ++i) {
+                uint32_t r[CH];
+                if constexpr (CH == 32) ptx::tmem_ld32(o_addr + i * CH, r);
+                else ptx::tmem_ld16(o_addr + i * CH, r);
+                if (keep) {
+#pragma unroll
+                    for (int x = 0; x < CH / 4; ++x)
+                        col[(i * (CH / 4) + x) * BM] =
+                            make_float4(__uint_as_float(r[4 * x]) * inv, __uint_as_float(r[4 * x + 1]) * inv,
+                                        __uint_as_float(r[4 * x + 2]) * inv, __uint_as_float(r[4 * x + 3]) * inv);
+                }
+            }
+            ptx::tc_fence_before();
+            ptx::mbar_arrive(bar(T::B_OFREE));
+            if (keep) part[(int64_t)BM * D + row] = lse2;
+            continue;
+        }
+        const int grow = sg.row0 + row, t = grow / p.G, hq = sg.hk * p.G + grow - t * p.G;
+        uint16_t* orow = static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h + t * p.so_n;
+#pragma unroll 1
+        for (int i = 0; i < D / CH; ++i) {
+            uint32_t r[CH];
+            if constexpr (CH == 32) ptx::tmem_ld32(o_addr + i * CH, r);
+            else ptx::tmem_ld16(o_addr + i * CH, r);
+            if (keep) {
+#pragma unroll
+                for (int x = 0; x < CH / 8; ++x) {
+                    uint4 v;
+                    v.x = pack2<BF16>(__uint_as_float(r[8 * x]) * inv, __uint_as_float(r[8 * x + 1]) * inv);
+                    v.y = pack2<BF16>(__uint_as_float(r[8 * x + 2]) * inv, __uint_as_float(r[8 * x + 3]) * inv);
+                    v.z = pack2<BF16>(__uint_as_float(r[8 * x + 4]) * inv, __uint_as_float(r[8 * x + 5]) * inv);
+                    v.w = pack2<BF16>(__uint_as_float(r[8 * x + 6]) * inv, __uint_as_float(r[8 * x + 7]) * inv);
+                    *reinterpret_cast<uint4*>(orow + i * CH + 8 * x) = v;
+                }
+            }
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(bar(T::B_OFREE));
+        if (keep && p.lse != nullptr) p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
+    }
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
+    fa_paged_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ CUtensorMap tmV, const PagedParams p) {
+    using T = TileTraits<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_addr(smem);
+    const uint32_t bar0 = sbase + T::OFF_BAR;
+    float* hand = reinterpret_cast<float*>(smem + T::OFF_HAND);
+    float* red = reinterpret_cast<float*>(smem + T::OFF_RED);
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + T::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::OFF_MISC + 4);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T::NUM_BARS; ++i) ptx::mbar_init(bar0 + 8u * i, T::bar_count(i));
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmQ);
+        ptx::prefetch_tmap(&tmK);
+        ptx::prefetch_tmap(&tmV);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), T::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Ctl ctl{abort_flag, p.status, p.wait_limit_ns};
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const PagedWalk walk = paged_range<T::BN>(p, blockIdx.x, gridDim.x, reinterpret_cast<PagedFind*>(hand));
+    __syncthreads();
+
+    constexpr int SOFTMAX_END = 4 + 4 * T::NG;
+    if (warp == 0) {
+        tile_producer_qk<D>(&tmQ, &tmK, p, walk, sbase, bar0, ctl);
+    } else if (warp == 3) {
+        tile_producer_v<D>(&tmV, p, walk, sbase, bar0, ctl);
+    } else if (warp == 1) {
+        if (lane == 0) tile_mma_qk<D, BF16>(p, walk, sbase, bar0, tmem, ctl);
+    } else if (warp == 2) {
+        if (lane == 0) tile_mma_pv<D, BF16>(p, walk, sbase, bar0, tmem, ctl);
+    } else if (warp < SOFTMAX_END) {
+        tile_softmax<D, BF16>(p, walk, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
+    } else {
+        tile_epilogue<D, BF16>(p, walk, bar0, tmem, hand, ctl);
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, T::TMEM_COLS);
+    }
+}
+
+}  // namespace fa

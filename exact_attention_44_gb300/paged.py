@@ -24,67 +24,86 @@ import ctypes
 import math
 
 from . import _binding
-from ._binding import FA_DTYPE_BF16, FA_DTYPE_F16, FA_OK, FaError, fa_strides
+from ._binding import FA_DTYPE_BF16, FA_DTYPE_F16, FA_OK, FaError
+
+# A decode step makes one or two of these calls a layer, each a few microseconds of GPU time, so the
+# marshalling itself is kept short: torch is looked up once, the strides of a call go through one
+# ctypes array, and the stream's handle comes from the call that torch's own launches use.
+torch = None
+_raw_stream = None
+
+
+def _setup():
+    global torch, _raw_stream
+    import torch as t
+
+    _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
+        lambda index: t.cuda.current_stream(index).cuda_stream)
+    torch = t
 
 
 def _ints(name, t, shape):
-    import torch
-
     if t.dtype != torch.int32:
         raise TypeError(f"{name} must be int32")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+    if shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t
 
 
 def _table(block_table, Z):
-    import torch
-
     if block_table.dtype != torch.int32:
         raise TypeError("block_table must be int32")
     if block_table.dim() != 2 or block_table.shape[0] != Z:
         raise ValueError(f"block_table must be (Z, max_pages) = ({Z}, ...), got {tuple(block_table.shape)}")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
+    row, col = block_table.stride()
+    M = block_table.shape[1]
+    if M > 1 and col != 1:
         raise ValueError("block_table rows must be contiguous")
-    return block_table.shape[1], block_table.stride(0)
+    return M, row
 
 
 def _caches(k_cache, v_cache, layers):
-    """(L, layer strides, P, Hkv, page_size, D) of a pair of caches; layers: whether 5-D ones are allowed."""
-    dims = (4, 5) if layers else (4,)
-    if k_cache.dim() not in dims or k_cache.shape != v_cache.shape:
+    """The caches' shape; layers: whether 5-D ones are allowed."""
+    shape = k_cache.shape
+    if shape != v_cache.shape or not (len(shape) == 4 or layers and len(shape) == 5):
         want = "(pages, Hkv, page_size, D)" + (" or (layers, pages, Hkv, page_size, D)" if layers else "")
-        raise ValueError(f"k_cache and v_cache must both be {want}, got {tuple(k_cache.shape)}, {tuple(v_cache.shape)}")
+        raise ValueError(f"k_cache and v_cache must both be {want}, got {tuple(shape)}, {tuple(v_cache.shape)}")
     if k_cache.dtype != v_cache.dtype or k_cache.element_size() != 2:
         raise TypeError("k_cache and v_cache must share one 16-bit dtype")
-    if k_cache.dim() == 5:
-        return (k_cache.shape[0], (k_cache.stride(0), v_cache.stride(0)), *k_cache.shape[1:])
-    return (1, (0, 0), *k_cache.shape)
+    return shape
 
 
-def _strides(t):
-    return ctypes.byref(fa_strides(*t.stride()[-4:]))
+def _layered(k_cache, v_cache):
+    """(L, layer strides of K and V, P, Hkv, page_size, D, strides of K and V within a layer)."""
+    shape, ks, vs = _caches(k_cache, v_cache, True), k_cache.stride(), v_cache.stride()
+    if len(shape) == 5:
+        return (shape[0], ks[0], vs[0], *shape[1:], ks[1:] + vs[1:])
+    return (1, 0, 0, *shape, ks + vs)
 
 
-def _call(name, device, stream, tensors, *args):
-    """Call libfa's `name` on `device`, its last argument the stream's handle."""
-    import torch
+def _strides(values):
+    """fa_strides structures laid end to end: (the array, which the caller keeps until the call, its address)."""
+    a = (ctypes.c_int64 * len(values))(*values)
+    return a, ctypes.addressof(a)
 
+
+def _call(name, lead, stream, tensors, args):
+    """Call libfa's `name` on the device of the tensor `lead`; its last argument is the stream's handle."""
+    index = lead.get_device()
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"{name}: every tensor must be on {device}, got one on {t.device}")
-    if device.type != "cuda":
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name}: every tensor must be on {lead.device}, got one on {t.device}")
+    if index < 0:
         raise ValueError(f"{name} takes CUDA tensors")
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    fn = getattr(_binding._lib or _binding.load(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, stream.cuda_stream)
+    lib = _binding._lib or _binding.load()
+    handle = _raw_stream(index) if stream is None else stream.cuda_stream
+    fn = getattr(lib, name)
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, handle)
     else:
-        with torch.cuda.device(device):
-            rc = fn(*args, stream.cuda_stream)
+        with torch.cuda.device(index):
+            rc = fn(*args, handle)
     if rc != FA_OK:
         raise FaError(rc, name)
 
@@ -95,8 +114,8 @@ def _ptr(t):
 
 def fa_fwd_paged_workspace_size(D: int, device=None) -> int:
     """Workspace bytes fa_fwd_paged needs for head dim D on `device` (default: current)."""
-    import torch
-
+    if torch is None:
+        _setup()
     n = ctypes.c_size_t(0)
     with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
         rc = _binding.load().fa_fwd_paged_workspace_size(int(D), ctypes.byref(n))
@@ -121,17 +140,24 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *
     one is allocated when omitted.  Returns (o, lse), lse (Z, Hq, T) fp32 or
     None, without synchronising.
     """
-    import torch
-
-    if q.dim() != 4:
+    if torch is None:
+        _setup()
+    shape = q.shape
+    if len(shape) != 4:
         raise ValueError("q must be 4-D (Z, Hq, T, D)")
-    Z, Hq, T, D = q.shape
-    _, _, P, Hkv, page, Dk = _caches(k_cache, v_cache, False)
+    Z, Hq, T, D = shape
+    P, Hkv, page, Dk = _caches(k_cache, v_cache, False)
     if Dk != D:
         raise ValueError(f"head dims differ: q has {D}, the cache {Dk}")
-    dt = FA_DTYPE_BF16 if q.dtype == torch.bfloat16 else FA_DTYPE_F16
-    if q.dtype not in (torch.float16, torch.bfloat16) or k_cache.dtype != q.dtype:
-        raise TypeError("q and the caches must share one dtype, float16 or bfloat16")
+    dtype, device = q.dtype, q.device
+    if dtype == torch.bfloat16:
+        code = FA_DTYPE_BF16
+    elif dtype == torch.float16:
+        code = FA_DTYPE_F16
+    else:
+        raise TypeError(f"fa_fwd_paged takes float16 or bfloat16 tensors, got {dtype}")
+    if k_cache.dtype != dtype:
+        raise TypeError("q and the caches must share one dtype")
     M, table_stride = _table(block_table, Z)
     _ints("seq_lens", seq_lens, (Z,))
     if new_lens is not None:
@@ -139,28 +165,31 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *
     mask_stride = 0
     if tree_mask is not None:
         words = (T + 31) // 32
-        _ints("tree_mask", tree_mask, (T, words) if tree_mask.dim() == 2 else (Z, T, words))
+        if tree_mask.dim() == 3:
+            _ints("tree_mask", tree_mask, (Z, T, words))
+            mask_stride = tree_mask.stride(0)
+        else:
+            _ints("tree_mask", tree_mask, (T, words))
         if T > 1 and tree_mask.stride(-2) != words:
             raise ValueError("tree_mask's words must be contiguous within a sequence")
-        mask_stride = tree_mask.stride(0) if tree_mask.dim() == 3 else 0
     if o is None:
-        o = torch.empty((Z, Hq, T, D), dtype=q.dtype, device=q.device)
-    elif o.shape != q.shape or o.dtype != q.dtype:
+        o = torch.empty(shape, dtype=dtype, device=device)
+    elif o.shape != shape or o.dtype != dtype:
         raise ValueError("o must match q's shape and dtype")
     if lse is None:
         if want_lse:
-            lse = torch.empty((Z, Hq, T), dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or tuple(lse.shape) != (Z, Hq, T) or not lse.is_contiguous():
+            lse = torch.empty((Z, Hq, T), dtype=torch.float32, device=device)
+    elif lse.dtype != torch.float32 or lse.shape != (Z, Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 (Z, Hq, T) tensor")
-    if workspace is None and q.device.type == "cuda":
-        workspace = torch.empty(fa_fwd_paged_workspace_size(D, q.device), dtype=torch.uint8, device=q.device)
-    _call("fa_fwd_paged", q.device, stream,
+    if workspace is None and device.type == "cuda":
+        workspace = torch.empty(fa_fwd_paged_workspace_size(D, device), dtype=torch.uint8, device=device)
+    keep, st = _strides(q.stride() + k_cache.stride() + v_cache.stride() + o.stride())
+    _call("fa_fwd_paged", q, stream,
           (k_cache, v_cache, block_table, seq_lens, new_lens, tree_mask, o, lse, workspace),
-          q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _ptr(lse), block_table.data_ptr(),
-          seq_lens.data_ptr(), _ptr(new_lens), _ptr(tree_mask), Z, Hq, Hkv, T, D, P, page, M, table_stride, mask_stride,
-          _strides(q), _strides(k_cache), _strides(v_cache), _strides(o),
-          1.0 / math.sqrt(D) if scale is None else float(scale), dt, _ptr(workspace),
-          workspace.numel() * workspace.element_size() if workspace is not None else 0)
+          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _ptr(lse), block_table.data_ptr(),
+           seq_lens.data_ptr(), _ptr(new_lens), _ptr(tree_mask), Z, Hq, Hkv, T, D, P, page, M, table_stride,
+           mask_stride, st, st + 32, st + 64, st + 96, 1.0 / math.sqrt(D) if scale is None else float(scale), code,
+           _ptr(workspace), 0 if workspace is None else workspace.nbytes))
     return o, lse
 
 
@@ -171,7 +200,9 @@ def fa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, *, new_lens=N
     row (z, :, t) goes to position seq_lens[z] + t for t < new_lens[z] (default
     T).  seq_lens is not changed.
     """
-    _, _, P, Hkv, page, D = _caches(k_cache, v_cache, False)
+    if torch is None:
+        _setup()
+    P, Hkv, page, D = _caches(k_cache, v_cache, False)
     if k.dim() != 4 or k.shape != v.shape or k.shape[1] != Hkv or k.shape[3] != D:
         raise ValueError(f"k and v must both be (Z, {Hkv}, T, {D}), got {tuple(k.shape)}, {tuple(v.shape)}")
     if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
@@ -181,10 +212,10 @@ def fa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, *, new_lens=N
     _ints("seq_lens", seq_lens, (Z,))
     if new_lens is not None:
         _ints("new_lens", new_lens, (Z,))
-    _call("fa_cache_append", k.device, stream, (v, k_cache, v_cache, block_table, seq_lens, new_lens),
-          k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-          seq_lens.data_ptr(), _ptr(new_lens), Z, Hkv, T, D, P, page, M, table_stride, _strides(k), _strides(v),
-          _strides(k_cache), _strides(v_cache))
+    keep, st = _strides(k.stride() + v.stride() + k_cache.stride() + v_cache.stride())
+    _call("fa_cache_append", k, stream, (v, k_cache, v_cache, block_table, seq_lens, new_lens),
+          (k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
+           seq_lens.data_ptr(), _ptr(new_lens), Z, Hkv, T, D, P, page, M, table_stride, st, st + 32, st + 64, st + 96))
 
 
 def fa_cache_commit(k_cache, v_cache, block_table, seq_lens, accepted, accepted_lens, *, stream=None) -> None:
@@ -196,7 +227,9 @@ def fa_cache_commit(k_cache, v_cache, block_table, seq_lens, accepted, accepted_
     int32, strictly increasing within accepted_lens[z]; accepted_lens: (Z)
     int32.  seq_lens is not changed: add accepted_lens to it.
     """
-    L, (kl, vl), P, Hkv, page, D = _caches(k_cache, v_cache, True)
+    if torch is None:
+        _setup()
+    L, kl, vl, P, Hkv, page, D, strides = _layered(k_cache, v_cache)
     if accepted.dim() != 2:
         raise ValueError("accepted must be (Z, A)")
     Z, A = accepted.shape
@@ -204,10 +237,10 @@ def fa_cache_commit(k_cache, v_cache, block_table, seq_lens, accepted, accepted_
     _ints("accepted_lens", accepted_lens, (Z,))
     _ints("seq_lens", seq_lens, (Z,))
     M, table_stride = _table(block_table, Z)
-    _call("fa_cache_commit", k_cache.device, stream, (v_cache, block_table, seq_lens, accepted, accepted_lens),
-          k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), accepted.data_ptr(),
-          accepted_lens.data_ptr(), Z, L, Hkv, A, D, P, page, M, table_stride, accepted.stride(0), kl, vl,
-          _strides(k_cache), _strides(v_cache))
+    keep, st = _strides(strides)
+    _call("fa_cache_commit", k_cache, stream, (v_cache, block_table, seq_lens, accepted, accepted_lens),
+          (k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), accepted.data_ptr(),
+           accepted_lens.data_ptr(), Z, L, Hkv, A, D, P, page, M, table_stride, accepted.stride(0), kl, vl, st, st + 32))
 
 
 def fa_cache_fork_workspace_size(Z: int, max_pages: int) -> int:
@@ -233,9 +266,9 @@ def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=No
     tensor of fa_cache_fork_workspace_size(Z, max_pages) bytes; one is allocated
     when omitted.
     """
-    import torch
-
-    L, (kl, vl), P, Hkv, page, D = _caches(k_cache, v_cache, True)
+    if torch is None:
+        _setup()
+    L, kl, vl, P, Hkv, page, D, strides = _layered(k_cache, v_cache)
     if seq_lens.dim() != 1:
         raise ValueError("seq_lens must be (Z)")
     Z = seq_lens.shape[0]
@@ -248,8 +281,8 @@ def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=No
     M, table_stride = _table(block_table, Z)
     if workspace is None and k_cache.device.type == "cuda":
         workspace = torch.empty(fa_cache_fork_workspace_size(Z, M), dtype=torch.uint8, device=k_cache.device)
-    _call("fa_cache_fork", k_cache.device, stream,
-          (v_cache, block_table, seq_lens, ref_counts, source, missing, workspace),
-          k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-          _ptr(source), _ptr(missing), Z, L, Hkv, D, P, page, M, int(room), table_stride, kl, vl, _strides(k_cache),
-          _strides(v_cache), _ptr(workspace), workspace.numel() * workspace.element_size() if workspace is not None else 0)
+    keep, st = _strides(strides)
+    _call("fa_cache_fork", k_cache, stream, (v_cache, block_table, seq_lens, ref_counts, source, missing, workspace),
+          (k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+           _ptr(source), _ptr(missing), Z, L, Hkv, D, P, page, M, int(room), table_stride, kl, vl, st, st + 32,
+           _ptr(workspace), 0 if workspace is None else workspace.nbytes))

@@ -317,3 +317,21 @@ def test_agrees_with_the_contiguous_forward():
     o2, lse2 = fa.fa_fwd_paged(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), zero)
     to, tl = pu.tolerances(q.double().numpy(), k, v, "bf16", 1 / math.sqrt(128))
     assert (o.double() - o2.double()).abs().max() <= 2 * to and (lse - lse2).abs().max() <= 2 * tl
+
+
+def test_stall_times_out_and_recovers():
+    import exact_attention_44_gb300 as fa
+    args = (40, [300, 1000], 8, 2, 40, 64, 16, "fp16")
+    kc, vc, table, k, v = pu.make_cache(40, [340, 1040], 2, 64, 16, "fp16")
+    q = torch.randn(2, 8, 40, 64).half().cuda()
+    lens = torch.tensor([300, 1000], dtype=torch.int32, device="cuda")
+    fa.fa_debug_set_wait_limit_ms(100)
+    fa.fa_debug_inject_stall(True)
+    try:
+        fa.fa_fwd_paged(q, kc.cuda(), vc.cuda(), table.cuda(), lens)
+        code, word = fa.fa_device_status()
+    finally:
+        fa.fa_debug_inject_stall(False)
+        fa.fa_debug_set_wait_limit_ms(0)
+    assert code == fa.FA_ERR_DEVICE_TIMEOUT and (word >> 16) == 0
+    check(*args)
