@@ -44,12 +44,14 @@ struct PagedParams {
     int page, M, P;            // slots a page, table columns, pages of the cache
     int cap;                   // M * page: positions a sequence can have
     int tile_rows;             // query rows of a tile (a row is a (token, head of the group) pair, heads innermost)
-    int box_rows;              // tile kernel: positions a TMA box holds, gcd(page, positions a block)
+    int box_rows;              // positions a TMA box holds: gcd(page, positions a block)
     int tiles;                 // tiles of one (z, kv head): ceil(T * G / tile_rows)
     float scale_log2;          // scale * log2(e) (rows kernel: signed; tile kernel: its magnitude)
     int negate_s;              // tile kernel: the scale is negative
-    float* scratch;            // two partial-result slots a CTA, slot_floats floats each
+    float* scratch;            // two partial-result slots a worker, slot_floats floats each
     int64_t slot_floats;
+    void* cuts;                // PagedCut of each team
+    int team, teams;           // workers of a team; teams (team * teams workers)
     uint32_t* status;
     uint64_t wait_limit_ns;
     int inject_stall;
@@ -57,12 +59,10 @@ struct PagedParams {
 
 struct PagedLaunch {
     PagedParams params;
-    int grid;                  // CTAs of the attention kernel
-    int rows;                  // rows kernel: 16 or 32 query rows a tile; 0: the tile kernel
-    int merge_slices;          // CTAs of the merge a tile
-    const CUtensorMap* tmQ;    // tile kernel only
+    bool tiles;                // the tile kernel, else the rows kernel
     const CUtensorMap* tmK;
     const CUtensorMap* tmV;
+    const CUtensorMap* tmQ;    // tile kernel only
     cudaStream_t stream;
 };
 
@@ -71,6 +71,11 @@ cudaError_t launch_paged_d32(const PagedLaunch& a, bool bf16);
 cudaError_t launch_paged_d64(const PagedLaunch& a, bool bf16);
 cudaError_t launch_paged_d128(const PagedLaunch& a, bool bf16);
 cudaError_t launch_paged_d256(const PagedLaunch& a, bool bf16);
+void paged_facts_d16(int* workers, int* block);
+void paged_facts_d32(int* workers, int* block);
+void paged_facts_d64(int* workers, int* block);
+void paged_facts_d128(int* workers, int* block);
+void paged_facts_d256(int* workers, int* block);
 
 // What a launch needs from the library's per-device state (fa_api.cu).
 struct DeviceFacts {

@@ -54,12 +54,33 @@ fa_status check_ints(const void* p, bool needed) {
     return misaligned(p, 4) ? FA_ERR_ALIGNMENT : FA_OK;
 }
 
-// A partial-result slot holds at most 128 rows of O / l and their base-2
-// log-sum-exps, padded to 256 bytes; two slots a CTA of the tile kernel (one
-// CTA an SM).  The rows kernel's two CTAs an SM with at most 32 rows a slot
-// need half of that.
+// Workers of the rows kernel an SM (warps), and the positions of its key block.
+struct RowsFacts {
+    int workers, block;
+};
+RowsFacts rows_facts(int D) {
+    RowsFacts f{};
+    switch (D) {
+        case 16: fa::paged_facts_d16(&f.workers, &f.block); break;
+        case 32: fa::paged_facts_d32(&f.workers, &f.block); break;
+        case 64: fa::paged_facts_d64(&f.workers, &f.block); break;
+        case 128: fa::paged_facts_d128(&f.workers, &f.block); break;
+        default: fa::paged_facts_d256(&f.workers, &f.block); break;
+    }
+    return f;
+}
+constexpr int kMaxTeams = 1280;  // parts that the merge can hold (PAGED_MAX_TEAMS)
+
+// A partial-result slot holds the rows of O / l of a tile (16 in the rows
+// kernel, 128 in the tile kernel) and their base-2 log-sum-exps, padded to 256
+// bytes; two slots a worker.  Behind the slots: where each team's range
+// starts, 48 bytes.
 int64_t slot_floats(int rows, int D) { return ((int64_t)rows * (D + 1) + 63) / 64 * 64; }
-size_t paged_workspace_bytes(int D, int sms) { return (size_t)2 * sms * slot_floats(128, D) * sizeof(float); }
+size_t paged_slot_bytes(int D, int sms) {
+    const int64_t rows = std::min(rows_facts(D).workers * sms, kMaxTeams) * slot_floats(16, D);
+    return (size_t)(2 * std::max(rows, sms * slot_floats(128, D))) * sizeof(float);
+}
+size_t paged_workspace_bytes(int D, int sms) { return paged_slot_bytes(D, sms) + 48 * kMaxTeams; }
 
 // 4-D tensor map with the head dim innermost (dims: D, then `dims` outermost
 // last) and boxes of one swizzle chunk x the given extents.
@@ -145,7 +166,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     const int G = Hq / Hkv;
     const int64_t rows = (int64_t)Z * Hq * T;
     // (row and tile indices fit in 32 bits)
-    if ((int64_t)T * G > (int64_t(1) << 30) || (int64_t)Z * Hkv * cdiv((int64_t)T * G, 16) > INT32_MAX / 8)
+    if ((int64_t)T * G > (int64_t(1) << 30) || (int64_t)Z * Hkv * cdiv((int64_t)T * G, 16) > INT32_MAX)
         return FA_ERR_UNSUPPORTED;
     if (rows == 0) return FA_OK;
     if ((st = check_strided(q, sq, Z, Hq, T, false)) != FA_OK) return st;
@@ -183,7 +204,7 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     p.words = (T + 31) / 32;
     p.Z = Z, p.Hq = Hq, p.Hkv = Hkv, p.G = G, p.T = T;
     p.page = page_size, p.M = max_pages, p.P = P;
-    p.cap = max_pages * page_size;
+    p.cap = P > 0 ? max_pages * page_size : 0;  // a cache without pages holds nothing
     p.scratch = static_cast<float*>(workspace);
     p.status = f.status;
     p.wait_limit_ns = f.wait_limit_ns;
@@ -192,39 +213,44 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
 
     const bool bf16 = dtype == FA_DTYPE_BF16;
     // Few rows of a (sequence, kv head) run on the rows kernel.  The tile
-    // kernel needs a whole group in a tile and a cache to map.
-    const bool tiles = T * (int64_t)G > 32 && G <= 128 && P > 0;
-    CUtensorMap mq, mk, mv;
-    if (tiles) {
-        const int bn = D == 256 ? 64 : 128, tokens = 128 / G;
-        a.rows = 0;
+    // kernel needs a whole group in a tile.
+    a.tiles = T * (int64_t)G > 16 && G <= 128;
+    CUtensorMap mq{}, mk{}, mv{};
+    int bk, workers;
+    if (a.tiles) {
+        const int tokens = 128 / G;
+        bk = D == 256 ? 64 : 128;
+        workers = f.sms;
         p.tile_rows = tokens * G;
-        p.box_rows = box_rows_for(page_size, bn);
         p.scale_log2 = c;
         p.negate_s = negate;
         p.slot_floats = slot_floats(128, D);
-        a.merge_slices = 8;
         const MapDim dq[3] = {{Hq, sq->h, G}, {T, sq->n, tokens}, {Z, sq->b, 1}};
+        if (make_paged_map(&mq, q, bf16, D, dq) != CUDA_SUCCESS) return FA_ERR_CUDA;
+        a.tmQ = &mq;
+    } else {
+        const RowsFacts rf = rows_facts(D);
+        bk = rf.block;
+        workers = std::min(rf.workers * f.sms, kMaxTeams);
+        p.tile_rows = 16;
+        p.scale_log2 = negate ? -c : c;
+        p.slot_floats = slot_floats(16, D);
+    }
+    p.box_rows = box_rows_for(page_size, bk);
+    if (P > 0) {
         const MapDim dk[3] = {{page_size, sk->n, p.box_rows}, {Hkv, sk->h, 1}, {P, sk->b, 1}};
         const MapDim dv[3] = {{page_size, sv->n, p.box_rows}, {Hkv, sv->h, 1}, {P, sv->b, 1}};
-        if (make_paged_map(&mq, q, bf16, D, dq) != CUDA_SUCCESS || make_paged_map(&mk, k_cache, bf16, D, dk) != CUDA_SUCCESS ||
-            make_paged_map(&mv, v_cache, bf16, D, dv) != CUDA_SUCCESS)
+        if (make_paged_map(&mk, k_cache, bf16, D, dk) != CUDA_SUCCESS || make_paged_map(&mv, v_cache, bf16, D, dv) != CUDA_SUCCESS)
             return FA_ERR_CUDA;
-        a.tmQ = &mq;
-        a.tmK = &mk;
-        a.tmV = &mv;
-    } else {
-        a.rows = T * (int64_t)G <= 16 || D == 256 ? 16 : 32;
-        p.tile_rows = a.rows;
-        p.scale_log2 = negate ? -c : c;
-        p.slot_floats = slot_floats(a.rows, D);
-        a.merge_slices = 1;
     }
+    a.tmK = &mk;
+    a.tmV = &mv;
     p.tiles = (int)cdiv((int64_t)T * G, p.tile_rows);
-    const int bk = tiles ? (D == 256 ? 64 : 128) : 64;
-    const int64_t blocks = (int64_t)Z * Hkv * p.tiles * cdiv(p.cap, bk);  // at most
-    const int64_t ctas = (int64_t)f.sms * (tiles || D > 128 ? 1 : 2);
-    a.grid = (int)std::max<int64_t>(1, std::min(blocks, ctas));
+    p.team = a.tiles ? std::min(p.tiles, 8) : 1;
+    // more teams than there can be blocks would find no work
+    const int64_t blocks = (int64_t)Z * Hkv * cdiv(p.tiles, p.team) * cdiv(p.cap, bk);
+    p.teams = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, workers / p.team));
+    p.cuts = static_cast<char*>(workspace) + paged_slot_bytes(D, f.sms);
     err = launch_paged(D, a, bf16);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("paged attention launch", err);
 }

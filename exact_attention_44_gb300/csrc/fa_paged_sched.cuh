@@ -4,13 +4,16 @@
 // A tile is up to p.tile_rows query rows of one (sequence, kv head); a row is
 // a (new token, query head of the group) pair with the heads innermost, so
 // that the rows of a sequence with fewer new tokens than T are a prefix and
-// the K/V rows are read once for the whole group.  The (tile, key block)
-// pairs, in the order sequence, kv head, tile, block, are laid end to end and
-// cut into one equal range per CTA, whatever the lengths are; a tile that a cut
-// crosses leaves partial results (O / l in fp32 and the base-2 log-sum-exp) in
-// slots of the workspace, two per CTA, and fa_paged_merge_kernel joins them in
-// the order of the keys.  Nothing depends on timing: the same inputs give the
-// same bits.
+// the K/V rows are read once for the whole group.  A worker is a warp of the
+// rows kernel or a CTA of the tile kernel.  p.team workers form a team that
+// takes p.team neighbouring tiles of a kv head at the same time, one each,
+// over the same key blocks, so that the blocks come from DRAM once and from L2
+// for the others.  The (tile group, key block) pairs, in the order sequence,
+// kv head, group, block, are laid end to end and cut into one equal range per
+// team, whatever the lengths are; a tile that a cut crosses leaves partial
+// results (O / l in fp32 and the base-2 log-sum-exp) in slots of the workspace,
+// two per worker, and fa_paged_merge_kernel joins them in the order of the
+// keys.  Nothing depends on timing: the same inputs give the same bits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -55,19 +58,24 @@ __device__ __forceinline__ int tile_blocks(const PagedParams& p, const SeqLen& s
 __device__ __forceinline__ int live_tiles(const PagedParams& p, const SeqLen& s) {
     return (s.nl * p.G + p.tile_rows - 1) / p.tile_rows;
 }
-// blocks of one (sequence, kv head), of tiles 0 .. mt - 1
-template <int BK>
-__device__ __forceinline__ int64_t head_blocks_before(const PagedParams& p, const SeqLen& s, int mt) {
-    if (s.nl == 0) return 0;
-    if (p.mask != nullptr) return (int64_t)mt * tile_blocks<BK>(p, s, 0);
-    int64_t n = 0;
-    for (int m = 0; m < mt; ++m) n += tile_blocks<BK>(p, s, m);
-    return n;
+__device__ __forceinline__ int live_groups(const PagedParams& p, const SeqLen& s) {
+    return (live_tiles(p, s) + p.team - 1) / p.team;
 }
+// blocks of tile group gi: those of its last tile (a tile of a chain sees at
+// least what the one before it sees)
 template <int BK>
-__device__ __forceinline__ int64_t seq_blocks(const PagedParams& p, int z) {
-    const SeqLen s = seq_len(p, z);
-    return p.Hkv * head_blocks_before<BK>(p, s, live_tiles(p, s));
+__device__ __forceinline__ int group_blocks(const PagedParams& p, const SeqLen& s, int gi) {
+    return tile_blocks<BK>(p, s, min((gi + 1) * p.team, live_tiles(p, s)) - 1);
+}
+// blocks of all groups of one (sequence, kv head)
+template <int BK>
+__device__ __forceinline__ int64_t head_blocks(const PagedParams& p, const SeqLen& s) {
+    if (s.nl == 0) return 0;
+    const int n = live_groups(p, s);
+    if (p.mask != nullptr) return (int64_t)n * group_blocks<BK>(p, s, 0);
+    int64_t sum = 0;
+    for (int i = 0; i < n; ++i) sum += group_blocks<BK>(p, s, i);
+    return sum;
 }
 
 // Sum over the block's threads; `red` holds one value per warp.
@@ -81,107 +89,226 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
     return s;
 }
 
-// A CTA's place in the order: the segments of its range, one after another.
+// A team's place in the order, and the lengths of its sequence.
 struct PagedWalk {
-    int z, hk, mt;   // tile
+    int z, hk, gi;   // tile group
     int jb;          // its first block in this range
     int64_t left;    // blocks left in the range
+    SeqLen s;
 };
+// A worker's part of it: one tile's key blocks.
 struct PagedSeg {
-    int z, hk, mt;
+    int z, hk;
     int jb, je;      // key blocks
     int slot;        // -1: the whole tile; else where its part goes
     int len, nl;
     int row0, rows;  // first query row of the tile and its live rows
 };
+// Unsigned division that takes the 32-bit route where both fit: the 64-bit one
+// costs a few hundred cycles, which a short call would feel.
+__device__ __forceinline__ int64_t fast_div(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 
-struct PagedFind {
-    int64_t red[32];
-    int64_t z_before;  // blocks before sequence z
-    int z;
+// The cut of `total` blocks into `teams` ranges: q blocks each, one more for
+// the first rem.  There are no empty ranges (the merge reads the slots of every
+// range between a tile's first and last).
+struct PagedCuts {
+    int64_t q;
+    int rem, teams;
+    __device__ __forceinline__ int64_t start(int c) const { return q * c + min(c, rem); }
+    __device__ __forceinline__ int team_of(int64_t x) const {
+        const int64_t big = (q + 1) * rem;
+        return x < big ? (int)fast_div(x, q + 1) : rem + (int)fast_div(x - big, q);
+    }
+};
+__device__ __forceinline__ PagedCuts paged_cuts(int64_t total, int teams) {
+    PagedCuts c{0, 0, (int)min((int64_t)teams, total)};
+    if (total > 0) {
+        c.q = fast_div(total, c.teams);
+        c.rem = (int)(total - c.q * c.teams);
+    }
+    return c;
+}
+
+// Where a team's range starts, for the merge (z = -1: it has none).
+struct alignas(16) PagedCut {
+    int z, hk, gi, jb;
+    int len, nl, rem, teams;
+    int64_t q;
 };
 
-// Every thread of the CTA: total blocks, and the start of CTA c's range.
-template <int BK>
-__device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, int c, int grid, PagedFind* f) {
-    const int tid = threadIdx.x, nt = blockDim.x;
-    int64_t own = 0;
-    for (int z = tid; z < p.Z; z += nt) own += seq_blocks<BK>(p, z);
-    const int64_t total = block_sum(own, f->red);
-    PagedWalk w{p.Z, 0, 0, 0, 0};
-    if (total < grid) grid = (int)total;  // no empty ranges between the others: the merge reads each one's slot
-    if (c >= grid) return w;              // the same answer in every thread
-    const int64_t lo = total * c / grid, hi = total * (c + 1) / grid;
-    int64_t base = 0;
-    for (int z0 = 0; z0 < p.Z; z0 += nt) {
-        const int z = z0 + tid;
-        const int64_t v = z < p.Z ? seq_blocks<BK>(p, z) : 0;
+template <int RANGES>
+struct PagedFind {
+    int64_t red[32];
+    int64_t z_before[RANGES];  // blocks before sequence z
+    int64_t lo[RANGES];
+    int z[RANGES], len[RANGES], nl[RANGES];
+};
+
+// Every thread of the CTA: where the range of team first + mine starts (RANGES
+// teams a CTA, mine the same in all threads of a warp), recorded for the merge
+// by the thread that `records`.  pads: some sequence has fewer than T new
+// tokens.
+template <int BK, int RANGES>
+__device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind<RANGES>* f, int first, int mine,
+                                                 bool records, bool& pads) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid % 32;
+    const int c = first + mine;
+    PagedWalk w{-1, 0, 0, 0, 0, {0, 0}};
+    PagedCuts cuts;
+    int64_t before = 0;  // blocks before sequence w.z
+    if (p.Z <= 32) {
+        // each warp by itself, one sequence a lane
+        SeqLen s{0, 0};
+        int64_t v = 0;
+        if (lane < p.Z) {
+            s = seq_len(p, lane);
+            v = p.Hkv * head_blocks<BK>(p, s);
+        }
+        pads = __any_sync(0xffffffffu, lane < p.Z && s.nl < p.T);
         int64_t x = v;
         for (int d = 1; d < 32; d *= 2) {
             const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (tid % 32 >= d) x += y;
+            if (lane >= d) x += y;
+        }
+        cuts = paged_cuts(__shfl_sync(0xffffffffu, x, 31), p.teams);
+        if (c < cuts.teams) {
+            const int64_t lo = cuts.start(c);
+            w.z = __ffs(__ballot_sync(0xffffffffu, lo < x)) - 1;
+            before = __shfl_sync(0xffffffffu, x - v, w.z);
+            w.s = SeqLen{__shfl_sync(0xffffffffu, s.len, w.z), __shfl_sync(0xffffffffu, s.nl, w.z)};
+        }
+    } else {
+        SeqLen s{0, 0};
+        int64_t own = 0, v = 0;
+        bool pad = false;
+        for (int z = tid; z < p.Z; z += nt) {
+            s = seq_len(p, z);
+            v = p.Hkv * head_blocks<BK>(p, s);
+            own += v;
+            pad |= s.nl < p.T;
+        }
+        cuts = paged_cuts(block_sum(own, f->red), p.teams);
+        if (tid < RANGES) f->lo[tid] = first + tid < cuts.teams ? cuts.start(first + tid) : -1;
+        pads = __syncthreads_or(pad);
+        int64_t base = 0;
+        for (int z0 = 0; z0 < p.Z; z0 += nt) {
+            const int z = z0 + tid;
+            if (p.Z > nt) {  // (with at most one sequence a thread its lengths are read once)
+                s = z < p.Z ? seq_len(p, z) : SeqLen{0, 0};
+                v = p.Hkv * head_blocks<BK>(p, s);
+            }
+            int64_t x = v;
+            for (int d = 1; d < 32; d *= 2) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            __syncthreads();
+            if (lane == 31) f->red[tid / 32] = x;
+            __syncthreads();
+            int64_t sum = 0;
+            x += base;
+            for (int i = 0; i < nt / 32; ++i) {
+                if (i < tid / 32) x += f->red[i];
+                sum += f->red[i];
+            }
+#pragma unroll
+            for (int r = 0; r < RANGES; ++r)
+                if (x - v <= f->lo[r] && f->lo[r] < x) {
+                    f->z[r] = z;
+                    f->len[r] = s.len;
+                    f->nl[r] = s.nl;
+                    f->z_before[r] = x - v;
+                }
+            base += sum;
         }
         __syncthreads();
-        if (tid % 32 == 31) f->red[tid / 32] = x;
-        if (tid == 0) f->z = -1;
-        __syncthreads();
-        int64_t before = base, sum = 0;
-        for (int i = 0; i < nt / 32; ++i) {
-            if (i < tid / 32) before += f->red[i];
-            sum += f->red[i];
+        if (c < cuts.teams) {
+            w.z = f->z[mine];
+            w.s = SeqLen{f->len[mine], f->nl[mine]};
+            before = f->z_before[mine];
         }
-        x += before;
-        if (x - v <= lo && lo < x) {
-            f->z = z;
-            f->z_before = x - v;
-        }
-        __syncthreads();
-        if (f->z >= 0) break;
-        base += sum;
     }
-    w.z = f->z;
-    int64_t rem = lo - f->z_before;
-    const SeqLen s = seq_len(p, w.z);
-    const int64_t per = head_blocks_before<BK>(p, s, live_tiles(p, s));
-    w.hk = (int)(rem / per);
-    rem -= w.hk * per;
-    w.mt = 0;
-    for (int64_t n; rem >= (n = tile_blocks<BK>(p, s, w.mt)); ++w.mt) rem -= n;
-    w.jb = (int)rem;
-    w.left = hi - lo;
+    if (c < cuts.teams) {
+        int64_t rem = cuts.start(c) - before;
+        const int64_t per = head_blocks<BK>(p, w.s);
+        w.hk = (int)fast_div(rem, per);
+        rem -= w.hk * per;
+        for (int64_t n; rem >= (n = group_blocks<BK>(p, w.s, w.gi)); ++w.gi) rem -= n;
+        w.jb = (int)rem;
+        w.left = cuts.start(c + 1) - cuts.start(c);
+    }
+    if (records && c < p.teams)
+        static_cast<PagedCut*>(p.cuts)[c] = PagedCut{w.z, w.hk, w.gi, w.jb, w.s.len, w.s.nl, cuts.rem, cuts.teams, cuts.q};
     return w;
 }
 
+// On to the next tile group (sequences without new tokens have none).
 template <int BK>
-__device__ __forceinline__ PagedSeg paged_seg(const PagedParams& p, const PagedWalk& w) {
-    PagedSeg g;
-    const SeqLen s = seq_len(p, w.z);
-    const int n = tile_blocks<BK>(p, s, w.mt);
-    g.z = w.z;
-    g.hk = w.hk;
-    g.mt = w.mt;
-    g.jb = w.jb;
-    g.je = n - w.jb <= w.left ? n : w.jb + (int)w.left;
-    g.slot = g.jb == 0 && g.je == n ? -1 : 2 * (int)blockIdx.x + (g.jb > 0 ? 0 : 1);
-    g.len = s.len;
-    g.nl = s.nl;
-    g.row0 = w.mt * p.tile_rows;
-    g.rows = min(p.tile_rows, s.nl * p.G - g.row0);
-    return g;
-}
-
-// On to the next segment (sequences without new tokens have no tiles).
-__device__ __forceinline__ void paged_next(const PagedParams& p, const PagedSeg& g, PagedWalk& w) {
-    w.left -= g.je - g.jb;
+__device__ __forceinline__ void paged_next(const PagedParams& p, PagedWalk& w) {
+    w.left -= group_blocks<BK>(p, w.s, w.gi) - w.jb;
     w.jb = 0;
     if (w.left <= 0) return;
-    if (++w.mt * p.tile_rows < g.nl * p.G) return;
-    w.mt = 0;
+    if (++w.gi < live_groups(p, w.s)) return;
+    w.gi = 0;
     if (++w.hk < p.Hkv) return;
     w.hk = 0;
-    for (++w.z; w.z < p.Z && seq_len(p, w.z).nl == 0; ++w.z) {
+    do {
+        if (++w.z >= p.Z) {
+            w.left = 0;
+            return;
+        }
+        w.s = seq_len(p, w.z);
+    } while (w.s.nl == 0);
+}
+
+// The next segment of a team's member at or after w's place (worker: its
+// number in the launch); false when the range is done.
+template <int BK>
+__device__ __forceinline__ bool paged_seg(const PagedParams& p, PagedWalk& w, PagedSeg& g, int worker) {
+    for (; w.left > 0; paged_next<BK>(p, w)) {
+        const int mt = w.gi * p.team + worker % p.team;
+        g.row0 = mt * p.tile_rows;
+        g.rows = min(p.tile_rows, w.s.nl * p.G - g.row0);
+        if (g.rows <= 0) continue;
+        const int own = tile_blocks<BK>(p, w.s, mt);
+        g.z = w.z;
+        g.hk = w.hk;
+        g.jb = w.jb;
+        g.je = own - w.jb <= w.left ? own : w.jb + (int)w.left;
+        if (g.je <= g.jb) continue;
+        g.slot = g.jb == 0 && g.je == own ? -1 : 2 * worker + (g.jb > 0 ? 0 : 1);
+        g.len = w.s.len;
+        g.nl = w.s.nl;
+        return true;
     }
-    if (w.z >= p.Z) w.left = 0;
+    return false;
+}
+
+// O = 0 and lse = -inf for the rows of tokens t >= nl: one (sequence, query
+// head) pair a warp, the pairs dealt to all warps of the launch (this one is
+// number `warp` of `warps`).
+template <int D>
+__device__ __forceinline__ void paged_fill(const PagedParams& p, int warp, int warps) {
+    const int lane = threadIdx.x % 32;
+    const int64_t pairs = (int64_t)p.Z * p.Hq;
+    for (int64_t i0 = warp; i0 < pairs; i0 += (int64_t)warps * 32) {
+        const int64_t i = i0 + (int64_t)warps * lane;
+        const int z = i < pairs ? (int)(i / p.Hq) : 0, h = (int)(i - (int64_t)z * p.Hq);
+        const int nl = i < pairs ? seq_len(p, z).nl : p.T;
+        for (uint32_t todo = __ballot_sync(0xffffffffu, nl < p.T); todo != 0; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            const int64_t zz = __shfl_sync(0xffffffffu, z, src), hh = __shfl_sync(0xffffffffu, h, src);
+            const int first = __shfl_sync(0xffffffffu, nl, src);
+            for (int64_t k = lane; k < (int64_t)(p.T - first) * (D / 8); k += 32) {
+                const int t = first + (int)(k / (D / 8)), c = (int)(k % (D / 8));
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + zz * p.so_z + hh * p.so_h + t * p.so_n + 8 * c) =
+                    make_uint4(0u, 0u, 0u, 0u);
+                if (c == 0 && p.lse != nullptr) p.lse[(zz * p.Hq + hh) * p.T + t] = -INFINITY;
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ void record_bad_page(uint32_t* status, uint32_t site) {
@@ -200,128 +327,122 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 }
 
 // ------------------------------------------------------------ merge ---------
-// `slices` blocks per (sequence, kv head, tile), each a share of its rows.  A tile that the cuts crossed has
-// its parts in slots 2 c0 + 1 (the CTA c0 of its first block) and 2 c (CTAs
-// c0 + 1 .. c1); with lambda_s the base-2 log-sum-exp of part s and O_s its O / l,
-//     lambda = log2 sum_s 2^lambda_s,   O = sum_s 2^(lambda_s - lambda) O_s,
-// taken in one pass with a running maximum.  Rows of new tokens that the
-// sequence does not have get O = 0 and lse = -inf.  A thread takes four
-// columns of a row; with few rows several threads share them and split the
-// parts, and join through shared memory.  COLS: a slot holds float4 column
-// groups [D / 4][128] (the tile kernel's threads each own a row), else rows
-// [tile_rows][D].
-constexpr int PAGED_MERGE_THREADS = 512;
+// Blocks ((b - 1) * team + member) * sub + 0 .. sub - 1 look at the cut between
+// the ranges of teams b - 1 and b.  If it falls inside a tile group, the
+// member's tile of it has its parts with the teams c0 (slot 2c + 1) and c0 + 1
+// .. c1 (slots 2c); the cuts inside the tile are c0 + 1 .. c1, and each of
+// their blocks merges one share of the tile's (row, four columns) items.  With
+// lambda_s the base-2 log-sum-exp of part s and O_s its O / l,
+//     lambda = log2 sum_s 2^lambda_s,   O = sum_s 2^(lambda_s - lambda) O_s.
+// A warp per row turns the parts' lambdas into weights first, so that the loads
+// of the parts' O depend on nothing; with few items several threads share one
+// and split the parts.
+constexpr int PAGED_MERGE_THREADS = 256;
+constexpr int PAGED_MAX_TEAMS = 1280;
 
-template <int D, int BK, bool BF16, bool COLS>
-__global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int grid, int slices) {
-    __shared__ int64_t red[32];
-    __shared__ float sh[PAGED_MERGE_THREADS * 6];
+template <int D, int BK, bool BF16>
+__global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int sub) {
+    constexpr int W = D / 4, NT = PAGED_MERGE_THREADS;
+    // weights of (rows of the share) x (parts): a share of live * W / (cuts * sub) items touches
+    // at most live / (cuts * sub) + 2 rows, times cuts + 1 parts: below 2 * 128 + 2 * teams
+    __shared__ float wt[2 * 128 + 2 * PAGED_MAX_TEAMS];
+    __shared__ float4 sh[NT];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int tid = threadIdx.x;
-    const int per_z = p.Hkv * p.tiles;
-    const int tile = blockIdx.x / slices, slice = blockIdx.x - tile * slices;
-    const int z = tile / per_z, r = tile - z * per_z;
-    const int hk = r / p.tiles, mt = r - hk * p.tiles;
-    const SeqLen s = seq_len(p, z);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int per_cut = p.team * sub;
+    const int b = 1 + (int)blockIdx.x / per_cut, in = (int)blockIdx.x % per_cut, member = in / sub;
+    const int4* rec = reinterpret_cast<const int4*>(static_cast<const PagedCut*>(p.cuts) + b);
+    const int4 cut = __ldcg(rec), more = __ldcg(rec + 1);
+    const PagedCuts cuts{__ldcg(reinterpret_cast<const long long*>(rec + 2)), more.z, more.w};
+    if (cut.x < 0 || cut.w == 0) return;  // no such range, or it starts with a tile
+    const int z = cut.x, hk = cut.y, mt = cut.z * p.team + member;
+    const SeqLen s{more.x, more.y};
     const int row0 = mt * p.tile_rows;
-    // this block's rows of the tile, the live ones first
-    const int share = (p.tile_rows + slices - 1) / slices, lo = slice * share, hi = min(lo + share, p.tile_rows);
-    const int live = min(hi, s.nl * p.G - row0);
-    const int rows = live - lo;  // may be <= 0
-    constexpr int W = D / 4;
-    auto row_at = [&](int row, int64_t& lse_at, int64_t& o_at) {  // row of the (sequence, kv head)
-        const int t = row / p.G, h = hk * p.G + row - t * p.G;
-        lse_at = ((int64_t)z * p.Hq + h) * p.T + t;
-        o_at = (int64_t)z * p.so_z + h * p.so_h + t * p.so_n;
+    const int live = min(p.tile_rows, s.nl * p.G - row0);
+    if (live <= 0) return;
+    const int64_t t0 = cuts.start(b) - cut.w, t1 = t0 + tile_blocks<BK>(p, s, mt) - 1;
+    const int c0 = cuts.team_of(t0), c1 = cuts.team_of(t1);
+    if (b > c1) return;  // the cut is behind this tile's last block
+    const int parts = c1 - c0 + 1, shares = (c1 - c0) * sub, share = (live * W + shares - 1) / shares;
+    const int first = ((b - 1 - c0) * sub + in % sub) * share, last = min(first + share, live * W);
+    if (first >= last) return;
+    const int lo = first / W, rows = (last - 1) / W - lo + 1;  // rows of the share
+    auto slot = [&](int i) -> const float* {
+        const int worker = (c0 + i) * p.team + member;
+        return p.scratch + (int64_t)(i == 0 ? 2 * worker + 1 : 2 * worker) * p.slot_floats;
     };
-    // rows without a token
-    {
-        const int first = max(live, lo), last = min(hi, p.T * p.G - row0);
-        for (int i = first * W + tid; i < last * W; i += PAGED_MERGE_THREADS) {
-            const int row = i / W, c = i - row * W;
-            int64_t la, oa;
-            row_at(row0 + row, la, oa);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + oa + 4 * c) = make_uint2(0u, 0u);
-            if (c == 0 && p.lse != nullptr) p.lse[la] = -INFINITY;
+    for (int r = warp; r < rows; r += NT / 32) {
+        float mx = -INFINITY;
+        for (int i = lane; i < parts; i += 32) {
+            const float l = __ldcg(slot(i) + p.tile_rows * D + lo + r);
+            wt[r * parts + i] = l;
+            mx = fmaxf(mx, l);
+        }
+        for (int m = 16; m > 0; m /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+        float den = 0.f;
+        for (int i = lane; i < parts; i += 32) {
+            const float l = wt[r * parts + i];
+            const float w = l == -INFINITY ? 0.f : exp2f(l - mx);
+            wt[r * parts + i] = w;
+            den += w;
+        }
+        for (int m = 16; m > 0; m /= 2) den += __shfl_xor_sync(0xffffffffu, den, m);
+        const float inv = den == 0.f ? 0.f : 1.f / den;  // (a NaN score reaches O)
+        for (int i = lane; i < parts; i += 32) wt[r * parts + i] *= inv;
+        if (lane == 0 && p.lse != nullptr && (lo + r) * W >= first) {  // the share that starts the row writes its lse
+            const int row = row0 + lo + r, t = row / p.G, h = hk * p.G + row - t * p.G;
+            p.lse[((int64_t)z * p.Hq + h) * p.T + t] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
         }
     }
-    if (rows <= 0) return;
-    int64_t before = 0, all = 0;
-    for (int i = tid; i < p.Z; i += PAGED_MERGE_THREADS) {
-        const int64_t n = seq_blocks<BK>(p, i);
-        all += n;
-        if (i < z) before += n;
-    }
-    const int64_t total = block_sum(all, red);
-    if (total < grid) grid = (int)total;
-    const int64_t per = head_blocks_before<BK>(p, s, live_tiles(p, s));
-    const int64_t t0 = block_sum(before, red) + hk * per + head_blocks_before<BK>(p, s, mt);
-    const int64_t t1 = t0 + tile_blocks<BK>(p, s, mt) - 1;
-    // the CTA whose range [total c / grid, total (c + 1) / grid) holds position x
-    const int c0 = (int)(((t0 + 1) * grid + total - 1) / total - 1);
-    const int c1 = (int)(((t1 + 1) * grid + total - 1) / total - 1);
-    if (c0 == c1) return;  // the whole tile went straight to O
-    const int items = rows * W;
+    __syncthreads();
+    const int items = last - first;
     int spl = 1;
-    while (spl < 32 && items * spl * 2 <= PAGED_MERGE_THREADS) spl *= 2;
-    const int per_round = PAGED_MERGE_THREADS / spl;
-    const int g = tid / per_round;  // this thread's share of the parts
-    for (int i0 = 0; i0 < items; i0 += per_round) {
+    while (spl * 2 <= parts && items * spl * 2 <= NT) spl *= 2;
+    const int per_round = NT / spl, g = tid / per_round;
+    for (int i0 = first; i0 < last; i0 += per_round) {
         const int i = i0 + tid - g * per_round;
-        const bool ok = g < spl && i < items;
-        const int row = !ok ? 0 : lo + (COLS ? i % rows : i / W), c = !ok ? 0 : COLS ? i / rows : i % W;
-        float mx = -INFINITY, den = 0.f;
+        const bool ok = i < last;
+        const int r = ok ? i / W - lo : 0, c = i % W;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         if (ok) {
-#pragma unroll 4
-            for (int x = c0 + g; x <= c1; x += spl) {
-                const float* slot = p.scratch + (int64_t)(x == c0 ? 2 * x + 1 : 2 * x) * p.slot_floats;
-                const float l = __ldcg(slot + (COLS ? 128 : p.tile_rows) * D + row);
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot) + (COLS ? c * 128 + row : row * W + c));
-                const float top = fmaxf(mx, l);
-                const float a = mx == -INFINITY ? 0.f : exp2f(mx - top), b = l == -INFINITY ? 0.f : exp2f(l - top);
-                mx = top;
-                den = den * a + b;
-                acc.x = acc.x * a + b * v.x;
-                acc.y = acc.y * a + b * v.y;
-                acc.z = acc.z * a + b * v.z;
-                acc.w = acc.w * a + b * v.w;
+            for (int x0 = g; x0 < parts; x0 += 8 * spl) {
+                float4 v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (x0 + u * spl < parts) v[u] = __ldcg(reinterpret_cast<const float4*>(slot(x0 + u * spl)) + i);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if (x0 + u * spl < parts) {
+                        const float w = wt[r * parts + x0 + u * spl];
+                        acc.x += w * v[u].x;
+                        acc.y += w * v[u].y;
+                        acc.z += w * v[u].z;
+                        acc.w += w * v[u].w;
+                    }
             }
         }
         if (spl > 1) {
-            __syncthreads();
-            float* m = sh + tid;
-            m[0] = mx;
-            m[PAGED_MERGE_THREADS] = den;
-            m[2 * PAGED_MERGE_THREADS] = acc.x;
-            m[3 * PAGED_MERGE_THREADS] = acc.y;
-            m[4 * PAGED_MERGE_THREADS] = acc.z;
-            m[5 * PAGED_MERGE_THREADS] = acc.w;
-            __syncthreads();
-            if (g == 0 && ok) {
-                for (int k = 1; k < spl; ++k) {
-                    const float* n = sh + tid + k * per_round;
-                    const float top = fmaxf(mx, n[0]);
-                    const float a = mx == -INFINITY ? 0.f : exp2f(mx - top), b = n[0] == -INFINITY ? 0.f : exp2f(n[0] - top);
-                    mx = top;
-                    den = den * a + b * n[PAGED_MERGE_THREADS];
-                    acc.x = acc.x * a + b * n[2 * PAGED_MERGE_THREADS];
-                    acc.y = acc.y * a + b * n[3 * PAGED_MERGE_THREADS];
-                    acc.z = acc.z * a + b * n[4 * PAGED_MERGE_THREADS];
-                    acc.w = acc.w * a + b * n[5 * PAGED_MERGE_THREADS];
+            for (int k = spl / 2; k > 0; k /= 2) {
+                __syncthreads();
+                sh[tid] = acc;
+                __syncthreads();
+                if (g < k) {
+                    const float4 v = sh[tid + k * per_round];
+                    acc.x += v.x;
+                    acc.y += v.y;
+                    acc.z += v.z;
+                    acc.w += v.w;
                 }
             }
+            __syncthreads();
         }
         if (!ok || g != 0) continue;
-        int64_t la, oa;
-        row_at(row0 + row, la, oa);
-        const float inv = den == 0.f ? 0.f : 1.f / den;  // a NaN score reaches O
+        const int row = row0 + lo + r, t = row / p.G, h = hk * p.G + row - t * p.G;
         uint2 out;
-        out.x = pack_pair<BF16>(acc.x * inv, acc.y * inv);
-        out.y = pack_pair<BF16>(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + oa + 4 * c) = out;
-        if (c == 0 && p.lse != nullptr) p.lse[la] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
+        out.x = pack_pair<BF16>(acc.x, acc.y);
+        out.y = pack_pair<BF16>(acc.z, acc.w);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (int64_t)z * p.so_z + h * p.so_h + t * p.so_n + 4 * c) = out;
     }
 }
 

@@ -33,7 +33,7 @@ struct TileTraits : Traits<D_> {
     static constexpr int SMEM_USED = OFF_MISC + 16;
     static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
-    static_assert((int)sizeof(PagedFind) <= 2 * Base::HAND_ROWS * BM * 4, "the range search fits the hand-over area");
+    static_assert((int)sizeof(PagedFind<1>) <= 2 * Base::HAND_ROWS * BM * 4, "the range search fits the hand-over area");
 };
 
 // A block's boxes: lane b of the producer warp has the box of positions
@@ -95,15 +95,12 @@ __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK,
         ++qi;
         return true;
     };
-    PagedSeg sg{};
-    if (w.left > 0) {
-        sg = paged_seg<T::BN>(p, w);
-        ok = load_q(sg);
-    }
-    while (ok && w.left > 0) {
-        paged_next(p, sg, w);
-        PagedSeg nx{};
-        if (w.left > 0) nx = paged_seg<T::BN>(p, w);
+    PagedSeg sg{}, nx{};
+    bool have = paged_seg<T::BN>(p, w, sg, (int)blockIdx.x);
+    if (have) ok = load_q(sg);
+    while (ok && have) {
+        paged_next<T::BN>(p, w);
+        have = paged_seg<T::BN>(p, w, nx, (int)blockIdx.x);
         const int32_t* row = p.table + (int64_t)sg.z * p.st_z;
         const int end = sg.len + sg.nl;
         PageBox b = page_box(p, row, sg.jb * T::BN, p.box_rows, T::BN, end, lane);
@@ -122,7 +119,7 @@ __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK,
             ++ki;
             b = after;
             const int q_at = T::Q_STAGES >= 2 ? sg.jb : sg.je - 1;
-            if (j == q_at && w.left > 0 && !load_q(nx)) {
+            if (j == q_at && have && !load_q(nx)) {
                 ok = false;
                 break;
             }
@@ -147,9 +144,8 @@ __device__ void tile_producer_v(const CUtensorMap* tmV, const PagedParams& p, Pa
     const uint64_t pol_kv = ptx::policy_evict_last();
     uint32_t vi = 0;
     bool ok = true;
-    while (ok && w.left > 0) {
-        const PagedSeg sg = paged_seg<T::BN>(p, w);
-        paged_next(p, sg, w);
+    PagedSeg sg;
+    for (; ok && paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w)) {
         const int32_t* row = p.table + (int64_t)sg.z * p.st_z;
         const int end = sg.len + sg.nl;
         PageBox b = page_box(p, row, sg.jb * T::BN, p.box_rows, T::BN, end, lane);
@@ -193,9 +189,8 @@ __device__ void tile_mma_qk(const PagedParams& p, PagedWalk w, uint32_t sbase, u
     const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16);
     uint32_t qi = 0, g = 0;
     bool ok = true;
-    while (ok && w.left > 0) {
-        const PagedSeg sg = paged_seg<T::BN>(p, w);
-        paged_next(p, sg, w);
+    PagedSeg sg;
+    for (; ok && paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w)) {
         const uint32_t qs = qi % T::Q_STAGES;
         if (!wait_phase(bar(T::B_QFULL + qs), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
         const uint32_t q_lo = q_lo0 + qs * (T::Q_BYTES >> 4);
@@ -239,9 +234,8 @@ __device__ void tile_mma_pv(const PagedParams& p, PagedWalk w, uint32_t sbase, u
     const uint32_t v_lo0 = ptx::smem_desc_lo(sbase + T::OFF_V, T::BN * T::SW);
     uint32_t g = 0, ntile = 0, fixes[2] = {0, 0};
     bool ok = true;
-    for (; ok && w.left > 0; ++ntile) {
-        const PagedSeg sg = paged_seg<T::BN>(p, w);
-        paged_next(p, sg, w);
+    PagedSeg sg;
+    for (; ok && paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w), ++ntile) {
         for (int j = sg.jb; j < sg.je; ++j, ++g) {
             const uint32_t vb = g & 1u, r = rslot<T::SR>(g);
             if (j == sg.jb && ntile > 0 &&
@@ -301,9 +295,8 @@ __device__ void tile_softmax(const PagedParams& p, PagedWalk w, uint32_t bar0, u
     const float c = p.scale_log2;
     const uint64_t c2 = ptx::pack_f32x2(c, c);
     uint32_t step = 0, ntile = 0;
-    for (; w.left > 0; ++ntile) {
-        const PagedSeg sg = paged_seg<BN>(p, w);
-        paged_next(p, sg, w);
+    PagedSeg sg;
+    for (; paged_seg<BN>(p, w, sg, (int)blockIdx.x); paged_next<BN>(p, w), ++ntile) {
         const int tok = min((sg.row0 + row) / p.G, p.T - 1);
         const bool idle = quad * 32 >= sg.rows;  // none of the warp's rows holds a token
         float m = -INFINITY, l = 0.f;
@@ -404,7 +397,7 @@ __device__ void tile_softmax(const PagedParams& p, PagedWalk w, uint32_t bar0, u
 
 template <int D, bool BF16>
 __device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, uint32_t tmem, const float* hand,
-                              const Ctl& ctl) {
+                              bool pads, const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int quad = (threadIdx.x / 32) % 4;
@@ -412,9 +405,8 @@ __device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, 
     const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O;
     uint32_t step = 0, ntile = 0;
     constexpr int CH = D >= 32 ? 32 : 16;
-    for (; w.left > 0; ++ntile) {
-        const PagedSeg sg = paged_seg<T::BN>(p, w);
-        paged_next(p, sg, w);
+    PagedSeg sg;
+    for (; paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w), ++ntile) {
         step += sg.je - sg.jb;
         const uint32_t slot = ntile & 1u;
         if (!warp_wait_phase(bar(T::B_EPIFULL + slot), (ntile >> 1) & 1u, ctl, SITE_EPI_FULL)) return;
@@ -430,9 +422,9 @@ __device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, 
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
         const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
         if (sg.slot >= 0) {
-            // a part: float4 column group c4 of row r at [c4][r], then the base-2 log-sum-exps
+            // a part: rows of O / l, then the base-2 log-sum-exps
             float* part = p.scratch + (int64_t)sg.slot * p.slot_floats;
-            float4* col = reinterpret_cast<float4*>(part) + row;
+            float4* mine = reinterpret_cast<float4*>(part + row * D);
 #pragma unroll 1
             for (int i = 0; i < D / CH; ++i) {
                 uint32_t r[CH];
@@ -441,14 +433,14 @@ __device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, 
                 if (keep) {
 #pragma unroll
                     for (int x = 0; x < CH / 4; ++x)
-                        col[(i * (CH / 4) + x) * BM] =
+                        mine[i * (CH / 4) + x] =
                             make_float4(__uint_as_float(r[4 * x]) * inv, __uint_as_float(r[4 * x + 1]) * inv,
                                         __uint_as_float(r[4 * x + 2]) * inv, __uint_as_float(r[4 * x + 3]) * inv);
                 }
             }
             ptx::tc_fence_before();
             ptx::mbar_arrive(bar(T::B_OFREE));
-            if (keep) part[(int64_t)BM * D + row] = lse2;
+            if (keep) part[p.tile_rows * D + row] = lse2;
             continue;
         }
         const int grow = sg.row0 + row, t = grow / p.G, hq = sg.hk * p.G + grow - t * p.G;
@@ -474,6 +466,7 @@ __device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, 
         ptx::mbar_arrive(bar(T::B_OFREE));
         if (keep && p.lse != nullptr) p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
     }
+    if (pads) paged_fill<D>(p, (int)blockIdx.x * 4 + quad, (int)gridDim.x * 4);
 }
 
 template <int D, bool BF16>
@@ -495,9 +488,11 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
         for (int i = 0; i < T::NUM_BARS; ++i) ptx::mbar_init(bar0 + 8u * i, T::bar_count(i));
         *abort_flag = 0;
         ptx::fence_mbar_init();
-        ptx::prefetch_tmap(&tmQ);
-        ptx::prefetch_tmap(&tmK);
-        ptx::prefetch_tmap(&tmV);
+        if (p.P > 0) {
+            ptx::prefetch_tmap(&tmQ);
+            ptx::prefetch_tmap(&tmK);
+            ptx::prefetch_tmap(&tmV);
+        }
     }
     if (warp == 1) {
         ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), T::TMEM_COLS);
@@ -510,8 +505,11 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     const Ctl ctl{abort_flag, p.status, p.wait_limit_ns};
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const PagedWalk walk = paged_range<T::BN>(p, blockIdx.x, gridDim.x, reinterpret_cast<PagedFind*>(hand));
-    __syncthreads();
+    PagedFind<1>* find = reinterpret_cast<PagedFind<1>*>(hand);
+    bool pads;
+    const PagedWalk walk = paged_range<T::BN, 1>(p, find, (int)blockIdx.x / p.team, 0,
+                                                 threadIdx.x == 0 && blockIdx.x % p.team == 0, pads);
+    __syncthreads();  // (the search's area is the hand-over area of the roles)
 
     constexpr int SOFTMAX_END = 4 + 4 * T::NG;
     if (warp == 0) {
@@ -525,7 +523,7 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     } else if (warp < SOFTMAX_END) {
         tile_softmax<D, BF16>(p, walk, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
     } else {
-        tile_epilogue<D, BF16>(p, walk, bar0, tmem, hand, ctl);
+        tile_epilogue<D, BF16>(p, walk, bar0, tmem, hand, pads, ctl);
     }
 
     ptx::tc_fence_before();

@@ -335,3 +335,41 @@ def test_stall_times_out_and_recovers():
         fa.fa_debug_set_wait_limit_ms(0)
     assert code == fa.FA_ERR_DEVICE_TIMEOUT and (word >> 16) == 0
     check(*args)
+
+
+def test_stall_of_a_decode_step_times_out_and_recovers():
+    import exact_attention_44_gb300 as fa
+    kc, vc, table, k, v = pu.make_cache(41, [3001], 2, 64, 16, "fp16")
+    q = torch.randn(1, 8, 1, 64).half().cuda()
+    lens = torch.tensor([3000], dtype=torch.int32, device="cuda")
+    fa.fa_debug_set_wait_limit_ms(100)
+    fa.fa_debug_inject_stall(True)
+    try:
+        fa.fa_fwd_paged(q, kc.cuda(), vc.cuda(), table.cuda(), lens)
+        code, word = fa.fa_device_status()
+    finally:
+        fa.fa_debug_inject_stall(False)
+        fa.fa_debug_set_wait_limit_ms(0)
+    assert code == fa.FA_ERR_DEVICE_TIMEOUT and (word >> 16) == 0
+    check(41, [3000], 8, 2, 1, 64, 16, "fp16")
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_cache_without_pages_holds_nothing(T):
+    import exact_attention_44_gb300 as fa
+    empty = torch.empty(0, 2, 16, 64, dtype=torch.float16, device="cuda")
+    q = torch.randn(2, 4, T, 64).half().cuda()
+    o, lse = fa.fa_fwd_paged(q, empty, empty, torch.zeros(2, 3, dtype=torch.int32, device="cuda"),
+                             torch.tensor([5, 0], dtype=torch.int32, device="cuda"))
+    assert fa.fa_device_status()[0] == 0 and (o == 0).all() and torch.isneginf(lse).all()
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_expanded_queries(T):
+    import exact_attention_44_gb300 as fa
+    kc, vc, table, k, v = pu.make_cache(42, [60 + T] * 3, 2, 64, 16, "fp16")
+    args = (kc.cuda(), vc.cuda(), table.cuda(), torch.tensor([60] * 3, dtype=torch.int32, device="cuda"))
+    q = torch.randn(1, 4, 1, 64).half().cuda()
+    a, la = fa.fa_fwd_paged(q.expand(3, 4, T, 64), *args)
+    b, lb = fa.fa_fwd_paged(q.expand(3, 4, T, 64).contiguous(), *args)
+    assert torch.equal(a, b) and torch.equal(la, lb)
