@@ -69,7 +69,7 @@ RowsFacts rows_facts(int D) {
     }
     return f;
 }
-constexpr int kMaxTeams = 1280;  // parts that the merge can hold (PAGED_MAX_TEAMS)
+constexpr int kMaxTeams = 1280;  // eight workers an SM on up to 160 SMs; fewer an SM beyond
 
 // A partial-result slot holds the rows of O / l of a tile (16 in the rows
 // kernel, 128 in the tile kernel) and their base-2 log-sum-exps, padded to 256

@@ -334,22 +334,17 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 // their blocks merges one share of the tile's (row, four columns) items.  With
 // lambda_s the base-2 log-sum-exp of part s and O_s its O / l,
 //     lambda = log2 sum_s 2^lambda_s,   O = sum_s 2^(lambda_s - lambda) O_s.
-// A warp per row turns the parts' lambdas into weights first, so that the loads
-// of the parts' O depend on nothing; with few items several threads share one
-// and split the parts.
-constexpr int PAGED_MERGE_THREADS = 256;
-constexpr int PAGED_MAX_TEAMS = 1280;
+// in one pass with a running maximum, so that a part's lambda and its O are one
+// round of loads; with few items up to 32 neighbouring lanes share one, split
+// the parts and join by shuffles.
+constexpr int PAGED_MERGE_THREADS = 128;
 
 template <int D, int BK, bool BF16>
 __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int sub) {
     constexpr int W = D / 4, NT = PAGED_MERGE_THREADS;
-    // weights of (rows of the share) x (parts): a share of live * W / (cuts * sub) items touches
-    // at most live / (cuts * sub) + 2 rows, times cuts + 1 parts: below 2 * 128 + 2 * teams
-    __shared__ float wt[2 * 128 + 2 * PAGED_MAX_TEAMS];
-    __shared__ float4 sh[NT];
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int tid = threadIdx.x;
     const int per_cut = p.team * sub;
     const int b = 1 + (int)blockIdx.x / per_cut, in = (int)blockIdx.x % per_cut, member = in / sub;
     const int4* rec = reinterpret_cast<const int4*>(static_cast<const PagedCut*>(p.cuts) + b);
@@ -367,82 +362,71 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     const int parts = c1 - c0 + 1, shares = (c1 - c0) * sub, share = (live * W + shares - 1) / shares;
     const int first = ((b - 1 - c0) * sub + in % sub) * share, last = min(first + share, live * W);
     if (first >= last) return;
-    const int lo = first / W, rows = (last - 1) / W - lo + 1;  // rows of the share
     auto slot = [&](int i) -> const float* {
         const int worker = (c0 + i) * p.team + member;
         return p.scratch + (int64_t)(i == 0 ? 2 * worker + 1 : 2 * worker) * p.slot_floats;
     };
-    for (int r = warp; r < rows; r += NT / 32) {
-        float mx = -INFINITY;
-        for (int i = lane; i < parts; i += 32) {
-            const float l = __ldcg(slot(i) + p.tile_rows * D + lo + r);
-            wt[r * parts + i] = l;
-            mx = fmaxf(mx, l);
-        }
-        for (int m = 16; m > 0; m /= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-        float den = 0.f;
-        for (int i = lane; i < parts; i += 32) {
-            const float l = wt[r * parts + i];
-            const float w = l == -INFINITY ? 0.f : exp2f(l - mx);
-            wt[r * parts + i] = w;
-            den += w;
-        }
-        for (int m = 16; m > 0; m /= 2) den += __shfl_xor_sync(0xffffffffu, den, m);
-        const float inv = den == 0.f ? 0.f : 1.f / den;  // (a NaN score reaches O)
-        for (int i = lane; i < parts; i += 32) wt[r * parts + i] *= inv;
-        if (lane == 0 && p.lse != nullptr && (lo + r) * W >= first) {  // the share that starts the row writes its lse
-            const int row = row0 + lo + r, t = row / p.G, h = hk * p.G + row - t * p.G;
-            p.lse[((int64_t)z * p.Hq + h) * p.T + t] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
-        }
-    }
-    __syncthreads();
-    const int items = last - first;
     int spl = 1;
-    while (spl * 2 <= parts && items * spl * 2 <= NT) spl *= 2;
-    const int per_round = NT / spl, g = tid / per_round;
-    for (int i0 = first; i0 < last; i0 += per_round) {
-        const int i = i0 + tid - g * per_round;
+    while (spl < 32 && spl < parts && (last - first) * spl * 2 <= NT) spl *= 2;
+    const int sl = tid % spl;
+    for (int i0 = first; i0 < last; i0 += NT / spl) {
+        const int i = i0 + tid / spl;
         const bool ok = i < last;
-        const int r = ok ? i / W - lo : 0, c = i % W;
+        const int r = ok ? i / W : 0, c = i % W;
+        float mx = -INFINITY, den = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (ok) {
-            for (int x0 = g; x0 < parts; x0 += 8 * spl) {
-                float4 v[8];
+        constexpr int U = 4;
+        for (int x0 = sl; ok && x0 < parts; x0 += U * spl) {
+            float l[U];
+            float4 v[U];
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (x0 + u * spl < parts) v[u] = __ldcg(reinterpret_cast<const float4*>(slot(x0 + u * spl)) + i);
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if (x0 + u * spl < parts) {
-                        const float w = wt[r * parts + x0 + u * spl];
-                        acc.x += w * v[u].x;
-                        acc.y += w * v[u].y;
-                        acc.z += w * v[u].z;
-                        acc.w += w * v[u].w;
-                    }
-            }
-        }
-        if (spl > 1) {
-            for (int k = spl / 2; k > 0; k /= 2) {
-                __syncthreads();
-                sh[tid] = acc;
-                __syncthreads();
-                if (g < k) {
-                    const float4 v = sh[tid + k * per_round];
-                    acc.x += v.x;
-                    acc.y += v.y;
-                    acc.z += v.z;
-                    acc.w += v.w;
+            for (int u = 0; u < U; ++u) {
+                l[u] = -INFINITY;
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (x0 + u * spl < parts) {
+                    const float* from = slot(x0 + u * spl);
+                    l[u] = __ldcg(from + p.tile_rows * D + r);
+                    v[u] = __ldcg(reinterpret_cast<const float4*>(from) + i);
                 }
             }
-            __syncthreads();
+            float top = mx;
+#pragma unroll
+            for (int u = 0; u < U; ++u) top = fmaxf(top, l[u]);
+            const float a = mx == -INFINITY ? 0.f : exp2f(mx - top);
+            mx = top;
+            den *= a;
+            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = l[u] == -INFINITY ? 0.f : exp2f(l[u] - top);
+                den += w;
+                acc.x += w * v[u].x;
+                acc.y += w * v[u].y;
+                acc.z += w * v[u].z;
+                acc.w += w * v[u].w;
+            }
         }
-        if (!ok || g != 0) continue;
-        const int row = row0 + lo + r, t = row / p.G, h = hk * p.G + row - t * p.G;
+        for (int k = spl / 2; k > 0; k /= 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, mx, k), top = fmaxf(mx, other);
+            const float a = mx == -INFINITY ? 0.f : exp2f(mx - top);
+            mx = top;
+            den *= a;
+            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+            den += __shfl_xor_sync(0xffffffffu, den, k);
+            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, k);
+            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, k);
+            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, k);
+            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, k);
+        }
+        if (!ok || sl != 0) continue;
+        const int row = row0 + r, t = row / p.G, h = hk * p.G + row - t * p.G;
+        const float inv = den == 0.f ? 0.f : 1.f / den;  // (a NaN score reaches O)
         uint2 out;
-        out.x = pack_pair<BF16>(acc.x, acc.y);
-        out.y = pack_pair<BF16>(acc.z, acc.w);
+        out.x = pack_pair<BF16>(acc.x * inv, acc.y * inv);
+        out.y = pack_pair<BF16>(acc.z * inv, acc.w * inv);
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (int64_t)z * p.so_z + h * p.so_h + t * p.so_n + 4 * c) = out;
+        if (c == 0 && p.lse != nullptr)
+            p.lse[((int64_t)z * p.Hq + h) * p.T + t] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
     }
 }
 
