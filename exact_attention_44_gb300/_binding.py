@@ -50,16 +50,11 @@ _SIGNATURES = {
                                [ctypes.c_void_p] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
     "fa_lse_merge": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_void_p), ctypes.POINTER(ctypes.c_void_p)] +
                      [ctypes.c_int] * 4 + [ctypes.c_void_p] * 4 + [ctypes.c_int, ctypes.c_void_p]),
-    "fa_fwd_paged": (ctypes.c_int, [ctypes.c_void_p] * 9 + [ctypes.c_int] * 8 + [ctypes.c_int64] * 2 +
-                     [ctypes.c_void_p] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
-                                              ctypes.c_void_p]),
+    "fa_fwd_paged": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_append": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_commit": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_fork": (ctypes.c_int, [ctypes.c_void_p] * 2),
     "fa_fwd_paged_workspace_size": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
-    "fa_cache_append": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 7 + [ctypes.c_int64] +
-                        [ctypes.c_void_p] * 5),
-    "fa_cache_commit": (ctypes.c_int, [ctypes.c_void_p] * 6 + [ctypes.c_int] * 8 + [ctypes.c_int64] * 4 +
-                        [ctypes.c_void_p] * 3),
-    "fa_cache_fork": (ctypes.c_int, [ctypes.c_void_p] * 7 + [ctypes.c_int] * 8 + [ctypes.c_int64] * 3 +
-                      [ctypes.c_void_p] * 3 + [ctypes.c_size_t, ctypes.c_void_p]),
     "fa_cache_fork_workspace_size": (ctypes.c_int, [ctypes.c_int] * 2 + [ctypes.POINTER(ctypes.c_size_t)]),
     "fa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fa_device_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]),

@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "fa.h"
 #include "fa_cache.h"
@@ -37,17 +38,29 @@ fa_status check_strided(const void* ptr, const fa_strides* s, int64_t nb, int64_
 }
 
 // The cache's geometry and its block table.
-fa_status check_cache(int Z, int P, int page_size, int max_pages, const int32_t* table, int64_t table_stride,
-                      bool written) {
-    if (Z < 0 || P < 0 || max_pages < 0 || table_stride < 0) return FA_ERR_INVALID_ARG;
-    if (page_size < 16 || page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
-    if ((int64_t)max_pages * page_size > (int64_t(1) << 30) || Z > 65535) return FA_ERR_UNSUPPORTED;
-    if ((int64_t)Z * max_pages > 0) {
-        if (table == nullptr) return FA_ERR_INVALID_ARG;
-        if (misaligned(table, 4)) return FA_ERR_ALIGNMENT;
-        if (written && Z > 1 && table_stride < max_pages) return FA_ERR_INVALID_ARG;
+fa_status check_cache(const fa_paged_cache& c, bool table_written) {
+    if (c.Z < 0 || c.L < 0 || c.P < 0 || c.Hkv < 0 || c.max_pages < 0 || c.table_stride < 0) return FA_ERR_INVALID_ARG;
+    if (!head_dim_ok(c.D) || c.page_size < 16 || c.page_size % 16 != 0) return FA_ERR_UNSUPPORTED;
+    if ((int64_t)c.max_pages * c.page_size > (int64_t(1) << 30) || c.Z > 65535) return FA_ERR_UNSUPPORTED;
+    if ((int64_t)c.Z * c.max_pages > 0) {
+        if (c.block_table == nullptr) return FA_ERR_INVALID_ARG;
+        if (misaligned(c.block_table, 4)) return FA_ERR_ALIGNMENT;
+        if (table_written && c.Z > 1 && c.table_stride < c.max_pages) return FA_ERR_INVALID_ARG;
     }
+    if (c.L > 1)
+        for (const int64_t s : {c.k_layer, c.v_layer})
+            if (s <= 0 || s % 8 != 0 || s >= (int64_t(1) << 42)) return FA_ERR_ALIGNMENT;
     return FA_OK;
+}
+// Its tensors (where a call has work for them) and lengths.
+fa_status check_cache_data(const fa_paged_cache& c, bool written) {
+    if (c.L > 0)
+        for (const auto& t : {std::make_pair(c.k, &c.sk), std::make_pair(c.v, &c.sv)}) {
+            const fa_status st = check_strided(t.first, t.second, c.P, c.Hkv, c.page_size, written);
+            if (st != FA_OK) return st;
+        }
+    if (c.seq_lens == nullptr) return FA_ERR_INVALID_ARG;
+    return misaligned(c.seq_lens, 4) ? FA_ERR_ALIGNMENT : FA_OK;
 }
 fa_status check_ints(const void* p, bool needed) {
     if (p == nullptr) return needed ? FA_ERR_INVALID_ARG : FA_OK;
@@ -125,15 +138,8 @@ cudaError_t launch_paged(int D, const fa::PagedLaunch& a, bool bf16) {
     }
 }
 
-fa::CacheView view(void* base, const fa_strides* s, int64_t layer) {
-    return fa::CacheView{static_cast<uint16_t*>(base), layer, s->b, s->h, s->n};
-}
-
-fa_status check_layers(int L, int64_t layer_stride) {
-    if (L < 0) return FA_ERR_INVALID_ARG;
-    if (L > 1 && (layer_stride <= 0 || layer_stride % 8 != 0 || layer_stride >= (int64_t(1) << 42)))
-        return FA_ERR_ALIGNMENT;
-    return FA_OK;
+fa::CacheView view(void* base, const fa_strides& s, int64_t layer) {
+    return fa::CacheView{static_cast<uint16_t*>(base), layer, s.b, s.h, s.n};
 }
 
 }  // namespace
@@ -150,68 +156,60 @@ fa_status fa_fwd_paged_workspace_size(int D, size_t* bytes) {
     return FA_OK;
 }
 
-fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
-                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens,
-                       const int32_t* tree_mask, int Z, int Hq, int Hkv, int T, int D, int P, int page_size,
-                       int max_pages, int64_t table_stride, int64_t mask_stride, const fa_strides* sq,
-                       const fa_strides* sk, const fa_strides* sv, const fa_strides* so, float scale, fa_dtype dtype,
-                       void* workspace, size_t workspace_bytes, cudaStream_t stream) {
-    if (Hq < 0 || Hkv < 1 || T < 0 || Hq % Hkv != 0 || mask_stride < 0) return FA_ERR_INVALID_ARG;
-    if (!head_dim_ok(D) || (dtype != FA_DTYPE_F16 && dtype != FA_DTYPE_BF16)) return FA_ERR_UNSUPPORTED;
+fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
+    if (args == nullptr) return FA_ERR_INVALID_ARG;
+    const fa_fwd_paged_args& x = *args;
+    const fa_paged_cache& cache = x.cache;
+    const int Z = cache.Z, Hq = x.Hq, Hkv = cache.Hkv, T = x.T, D = cache.D, P = cache.P;
+    if (Hq < 0 || Hkv < 1 || T < 0 || Hq % Hkv != 0 || x.mask_stride < 0 || cache.L != 1) return FA_ERR_INVALID_ARG;
+    if (x.dtype != FA_DTYPE_F16 && x.dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
     float c = 0.f;
     int negate = 0;
-    if (!fa::split_scale(scale, &c, &negate)) return FA_ERR_INVALID_ARG;
-    fa_status st = check_cache(Z, P, page_size, max_pages, block_table, table_stride, false);
+    if (!fa::split_scale(x.scale, &c, &negate)) return FA_ERR_INVALID_ARG;
+    fa_status st = check_cache(cache, false);
     if (st != FA_OK) return st;
     const int G = Hq / Hkv;
-    const int64_t rows = (int64_t)Z * Hq * T;
     // (row and tile indices fit in 32 bits)
     if ((int64_t)T * G > (int64_t(1) << 30) || (int64_t)Z * Hkv * cdiv((int64_t)T * G, 16) > INT32_MAX)
         return FA_ERR_UNSUPPORTED;
-    if (rows == 0) return FA_OK;
-    if ((st = check_strided(q, sq, Z, Hq, T, false)) != FA_OK) return st;
-    if ((st = check_strided(o, so, Z, Hq, T, true)) != FA_OK) return st;
-    if ((st = check_strided(k_cache, sk, P, Hkv, page_size, false)) != FA_OK) return st;
-    if ((st = check_strided(v_cache, sv, P, Hkv, page_size, false)) != FA_OK) return st;
-    if ((st = check_ints(seq_lens, true)) != FA_OK) return st;
-    if ((st = check_ints(new_lens, false)) != FA_OK) return st;
-    if ((st = check_ints(tree_mask, false)) != FA_OK) return st;
-    if ((st = check_ints(lse, false)) != FA_OK) return st;
-    if (workspace == nullptr || misaligned(workspace, 256)) return FA_ERR_WORKSPACE;
+    if ((int64_t)Z * Hq * T == 0) return FA_OK;
+    if ((st = check_strided(x.q, &x.sq, Z, Hq, T, false)) != FA_OK) return st;
+    if ((st = check_strided(x.o, &x.so, Z, Hq, T, true)) != FA_OK) return st;
+    if ((st = check_cache_data(cache, false)) != FA_OK) return st;
+    if ((st = check_ints(x.new_lens, false)) != FA_OK) return st;
+    if ((st = check_ints(x.tree_mask, false)) != FA_OK) return st;
+    if ((st = check_ints(x.lse, false)) != FA_OK) return st;
+    if (x.workspace == nullptr || misaligned(x.workspace, 256)) return FA_ERR_WORKSPACE;
 
     fa::DeviceFacts f;
     cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
-    if (workspace_bytes < paged_workspace_bytes(D, f.sms)) return FA_ERR_WORKSPACE;
+    if (x.workspace_bytes < paged_workspace_bytes(D, f.sms)) return FA_ERR_WORKSPACE;
 
     fa::PagedLaunch a{};
     fa::PagedParams& p = a.params;
-    p.q = q;
-    p.kc = k_cache;
-    p.vc = v_cache;
-    p.o = o;
-    p.lse = lse;
-    p.sq_z = sq->b, p.sq_h = sq->h, p.sq_n = sq->n;
-    p.so_z = so->b, p.so_h = so->h, p.so_n = so->n;
-    p.sk_p = sk->b, p.sk_h = sk->h, p.sk_n = sk->n;
-    p.sv_p = sv->b, p.sv_h = sv->h, p.sv_n = sv->n;
-    p.table = block_table;
-    p.st_z = table_stride;
-    p.lens = seq_lens;
-    p.news = new_lens;
-    p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
-    p.sm_z = mask_stride;
+    p.q = x.q;
+    p.o = x.o;
+    p.lse = x.lse;
+    p.sq_z = x.sq.b, p.sq_h = x.sq.h, p.sq_n = x.sq.n;
+    p.so_z = x.so.b, p.so_h = x.so.h, p.so_n = x.so.n;
+    p.table = cache.block_table;
+    p.st_z = cache.table_stride;
+    p.lens = cache.seq_lens;
+    p.news = x.new_lens;
+    p.mask = reinterpret_cast<const uint32_t*>(x.tree_mask);
+    p.sm_z = x.mask_stride;
     p.words = (T + 31) / 32;
     p.Z = Z, p.Hq = Hq, p.Hkv = Hkv, p.G = G, p.T = T;
-    p.page = page_size, p.M = max_pages, p.P = P;
-    p.cap = P > 0 ? max_pages * page_size : 0;  // a cache without pages holds nothing
-    p.scratch = static_cast<float*>(workspace);
+    p.page = cache.page_size, p.M = cache.max_pages, p.P = P;
+    p.cap = P > 0 ? p.M * p.page : 0;
+    p.scratch = static_cast<float*>(x.workspace);
     p.status = f.status;
     p.wait_limit_ns = f.wait_limit_ns;
     p.inject_stall = f.inject_stall;
     a.stream = stream;
 
-    const bool bf16 = dtype == FA_DTYPE_BF16;
+    const bool bf16 = x.dtype == FA_DTYPE_BF16;
     // Few rows of a (sequence, kv head) run on the rows kernel.  The tile
     // kernel needs a whole group in a tile.
     a.tiles = T * (int64_t)G > 16 && G <= 128;
@@ -225,8 +223,8 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
         p.scale_log2 = c;
         p.negate_s = negate;
         p.slot_floats = slot_floats(128, D);
-        const MapDim dq[3] = {{Hq, sq->h, G}, {T, sq->n, tokens}, {Z, sq->b, 1}};
-        if (make_paged_map(&mq, q, bf16, D, dq) != CUDA_SUCCESS) return FA_ERR_CUDA;
+        const MapDim dq[3] = {{Hq, x.sq.h, G}, {T, x.sq.n, tokens}, {Z, x.sq.b, 1}};
+        if (make_paged_map(&mq, x.q, bf16, D, dq) != CUDA_SUCCESS) return FA_ERR_CUDA;
         a.tmQ = &mq;
     } else {
         const RowsFacts rf = rows_facts(D);
@@ -236,11 +234,13 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
         p.scale_log2 = negate ? -c : c;
         p.slot_floats = slot_floats(16, D);
     }
-    p.box_rows = box_rows_for(page_size, bk);
+    p.box_rows = box_rows_for(p.page, bk);
     if (P > 0) {
-        const MapDim dk[3] = {{page_size, sk->n, p.box_rows}, {Hkv, sk->h, 1}, {P, sk->b, 1}};
-        const MapDim dv[3] = {{page_size, sv->n, p.box_rows}, {Hkv, sv->h, 1}, {P, sv->b, 1}};
-        if (make_paged_map(&mk, k_cache, bf16, D, dk) != CUDA_SUCCESS || make_paged_map(&mv, v_cache, bf16, D, dv) != CUDA_SUCCESS)
+        const fa_strides &sk = cache.sk, &sv = cache.sv;
+        const MapDim dk[3] = {{p.page, sk.n, p.box_rows}, {Hkv, sk.h, 1}, {P, sk.b, 1}};
+        const MapDim dv[3] = {{p.page, sv.n, p.box_rows}, {Hkv, sv.h, 1}, {P, sv.b, 1}};
+        if (make_paged_map(&mk, cache.k, bf16, D, dk) != CUDA_SUCCESS ||
+            make_paged_map(&mv, cache.v, bf16, D, dv) != CUDA_SUCCESS)
             return FA_ERR_CUDA;
     }
     a.tmK = &mk;
@@ -250,77 +250,69 @@ fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, 
     // more teams than there can be blocks would find no work
     const int64_t blocks = (int64_t)Z * Hkv * cdiv(p.tiles, p.team) * cdiv(p.cap, bk);
     p.teams = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, workers / p.team));
-    p.cuts = static_cast<char*>(workspace) + paged_slot_bytes(D, f.sms);
+    p.cuts = static_cast<char*>(x.workspace) + paged_slot_bytes(D, f.sms);
     err = launch_paged(D, a, bf16);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("paged attention launch", err);
 }
 
-fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* block_table,
-                          const int32_t* seq_lens, const int32_t* new_lens, int Z, int Hkv, int T, int D, int P,
-                          int page_size, int max_pages, int64_t table_stride, const fa_strides* sk,
-                          const fa_strides* sv, const fa_strides* skc, const fa_strides* svc, cudaStream_t stream) {
-    if (Hkv < 0 || T < 0) return FA_ERR_INVALID_ARG;
-    if (!head_dim_ok(D)) return FA_ERR_UNSUPPORTED;
-    fa_status st = check_cache(Z, P, page_size, max_pages, block_table, table_stride, false);
+fa_status fa_cache_append(const fa_cache_append_args* args, cudaStream_t stream) {
+    if (args == nullptr) return FA_ERR_INVALID_ARG;
+    const fa_cache_append_args& x = *args;
+    const fa_paged_cache& c = x.cache;
+    if (x.T < 0 || c.L != 1) return FA_ERR_INVALID_ARG;
+    fa_status st = check_cache(c, false);
     if (st != FA_OK) return st;
-    if ((int64_t)Hkv * T * (D / 8) >= INT32_MAX) return FA_ERR_UNSUPPORTED;
-    if ((int64_t)Z * Hkv * T == 0) return FA_OK;
-    if ((st = check_strided(k, sk, Z, Hkv, T, false)) != FA_OK) return st;
-    if ((st = check_strided(v, sv, Z, Hkv, T, false)) != FA_OK) return st;
-    if ((st = check_strided(k_cache, skc, P, Hkv, page_size, true)) != FA_OK) return st;
-    if ((st = check_strided(v_cache, svc, P, Hkv, page_size, true)) != FA_OK) return st;
-    if ((st = check_ints(seq_lens, true)) != FA_OK) return st;
-    if ((st = check_ints(new_lens, false)) != FA_OK) return st;
+    if ((int64_t)c.Hkv * x.T * (c.D / 8) >= INT32_MAX) return FA_ERR_UNSUPPORTED;
+    if ((int64_t)c.Z * c.Hkv * x.T == 0) return FA_OK;
+    if ((st = check_strided(x.k, &x.sk, c.Z, c.Hkv, x.T, false)) != FA_OK) return st;
+    if ((st = check_strided(x.v, &x.sv, c.Z, c.Hkv, x.T, false)) != FA_OK) return st;
+    if ((st = check_cache_data(c, true)) != FA_OK) return st;
+    if ((st = check_ints(x.new_lens, false)) != FA_OK) return st;
     fa::DeviceFacts f;
     cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
     fa::AppendParams p{};
-    p.k = view(k_cache, skc, 0);
-    p.v = view(v_cache, svc, 0);
-    p.ks = static_cast<const uint16_t*>(k);
-    p.vs = static_cast<const uint16_t*>(v);
-    p.ks_z = sk->b, p.ks_h = sk->h, p.ks_n = sk->n;
-    p.vs_z = sv->b, p.vs_h = sv->h, p.vs_n = sv->n;
-    p.table = block_table;
-    p.st_z = table_stride;
-    p.lens = seq_lens;
-    p.news = new_lens;
-    p.Z = Z, p.H = Hkv, p.T = T, p.D = D, p.page = page_size, p.M = max_pages, p.P = P;
+    p.k = view(c.k, c.sk, 0);
+    p.v = view(c.v, c.sv, 0);
+    p.ks = static_cast<const uint16_t*>(x.k);
+    p.vs = static_cast<const uint16_t*>(x.v);
+    p.ks_z = x.sk.b, p.ks_h = x.sk.h, p.ks_n = x.sk.n;
+    p.vs_z = x.sv.b, p.vs_h = x.sv.h, p.vs_n = x.sv.n;
+    p.table = c.block_table;
+    p.st_z = c.table_stride;
+    p.lens = c.seq_lens;
+    p.news = x.new_lens;
+    p.Z = c.Z, p.H = c.Hkv, p.T = x.T, p.D = c.D, p.page = c.page_size, p.M = c.max_pages, p.P = c.P;
     p.status = f.status;
     err = fa::launch_cache_append(p, stream);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("cache append launch", err);
 }
 
-fa_status fa_cache_commit(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
-                          const int32_t* accepted, const int32_t* accepted_lens, int Z, int L, int Hkv, int A, int D,
-                          int P, int page_size, int max_pages, int64_t table_stride, int64_t accepted_stride,
-                          int64_t k_layer_stride, int64_t v_layer_stride, const fa_strides* skc, const fa_strides* svc,
-                          cudaStream_t stream) {
-    if (Hkv < 0 || A < 0 || accepted_stride < 0) return FA_ERR_INVALID_ARG;
-    if (!head_dim_ok(D)) return FA_ERR_UNSUPPORTED;
-    fa_status st = check_cache(Z, P, page_size, max_pages, block_table, table_stride, false);
+fa_status fa_cache_commit(const fa_cache_commit_args* args, cudaStream_t stream) {
+    if (args == nullptr) return FA_ERR_INVALID_ARG;
+    const fa_cache_commit_args& x = *args;
+    const fa_paged_cache& c = x.cache;
+    if (x.A < 0 || x.accepted_stride < 0) return FA_ERR_INVALID_ARG;
+    fa_status st = check_cache(c, false);
     if (st != FA_OK) return st;
-    if ((st = check_layers(L, k_layer_stride)) != FA_OK || (st = check_layers(L, v_layer_stride)) != FA_OK) return st;
-    if ((int64_t)L * 2 * Hkv * (D / 8) >= INT32_MAX) return FA_ERR_UNSUPPORTED;
-    if ((int64_t)Z * L * Hkv * A == 0) return FA_OK;
-    if ((st = check_strided(k_cache, skc, P, Hkv, page_size, true)) != FA_OK) return st;
-    if ((st = check_strided(v_cache, svc, P, Hkv, page_size, true)) != FA_OK) return st;
-    if ((st = check_ints(seq_lens, true)) != FA_OK) return st;
-    if ((st = check_ints(accepted, true)) != FA_OK) return st;
-    if ((st = check_ints(accepted_lens, true)) != FA_OK) return st;
+    if ((int64_t)c.L * 2 * c.Hkv * (c.D / 8) >= INT32_MAX) return FA_ERR_UNSUPPORTED;
+    if ((int64_t)c.Z * c.L * c.Hkv * x.A == 0) return FA_OK;
+    if ((st = check_cache_data(c, true)) != FA_OK) return st;
+    if ((st = check_ints(x.accepted, true)) != FA_OK) return st;
+    if ((st = check_ints(x.accepted_lens, true)) != FA_OK) return st;
     fa::DeviceFacts f;
     cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
     fa::CommitParams p{};
-    p.k = view(k_cache, skc, k_layer_stride);
-    p.v = view(v_cache, svc, v_layer_stride);
-    p.table = block_table;
-    p.st_z = table_stride;
-    p.lens = seq_lens;
-    p.path = accepted;
-    p.kept = accepted_lens;
-    p.sp_z = accepted_stride;
-    p.Z = Z, p.L = L, p.H = Hkv, p.A = A, p.D = D, p.page = page_size, p.M = max_pages, p.P = P;
+    p.k = view(c.k, c.sk, c.k_layer);
+    p.v = view(c.v, c.sv, c.v_layer);
+    p.table = c.block_table;
+    p.st_z = c.table_stride;
+    p.lens = c.seq_lens;
+    p.path = x.accepted;
+    p.kept = x.accepted_lens;
+    p.sp_z = x.accepted_stride;
+    p.Z = c.Z, p.L = c.L, p.H = c.Hkv, p.A = x.A, p.D = c.D, p.page = c.page_size, p.M = c.max_pages, p.P = c.P;
     p.status = f.status;
     err = fa::launch_cache_commit(p, stream);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("cache commit launch", err);
@@ -332,45 +324,38 @@ fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes) {
     return FA_OK;
 }
 
-fa_status fa_cache_fork(void* k_cache, void* v_cache, int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts,
-                        const int32_t* source, int32_t* missing, int Z, int L, int Hkv, int D, int P, int page_size,
-                        int max_pages, int room, int64_t table_stride, int64_t k_layer_stride, int64_t v_layer_stride,
-                        const fa_strides* skc, const fa_strides* svc, void* workspace, size_t workspace_bytes,
-                        cudaStream_t stream) {
-    if (Hkv < 0 || room < 0) return FA_ERR_INVALID_ARG;
-    if (!head_dim_ok(D)) return FA_ERR_UNSUPPORTED;
-    fa_status st = check_cache(Z, P, page_size, max_pages, block_table, table_stride, true);
+fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
+    if (args == nullptr) return FA_ERR_INVALID_ARG;
+    const fa_cache_fork_args& x = *args;
+    const fa_paged_cache& c = x.cache;
+    if (x.room < 0) return FA_ERR_INVALID_ARG;
+    fa_status st = check_cache(c, true);
     if (st != FA_OK) return st;
-    if ((st = check_layers(L, k_layer_stride)) != FA_OK || (st = check_layers(L, v_layer_stride)) != FA_OK) return st;
-    if (Z > 8192 || room > (1 << 30) || (int64_t)Z * max_pages > INT32_MAX || (int64_t)Hkv * page_size * (D / 8) > INT32_MAX)
+    if (c.Z > 8192 || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||
+        (int64_t)c.Hkv * c.page_size * (c.D / 8) > INT32_MAX)
         return FA_ERR_UNSUPPORTED;
-    if (Z == 0) return FA_OK;
-    if ((int64_t)L * Hkv > 0) {
-        if ((st = check_strided(k_cache, skc, P, Hkv, page_size, true)) != FA_OK) return st;
-        if ((st = check_strided(v_cache, svc, P, Hkv, page_size, true)) != FA_OK) return st;
-    }
-    if ((st = check_ints(seq_lens, true)) != FA_OK) return st;
-    if ((st = check_ints(ref_counts, P > 0)) != FA_OK) return st;
-    if ((st = check_ints(source, false)) != FA_OK) return st;
-    if ((st = check_ints(missing, false)) != FA_OK) return st;
-    if (workspace == nullptr || misaligned(workspace, 256) ||
-        workspace_bytes < (size_t)fa::fork_workspace_ints(Z, max_pages) * sizeof(int32_t))
+    if (c.Z == 0) return FA_OK;
+    if ((st = check_cache_data(c, true)) != FA_OK) return st;
+    if ((st = check_ints(x.ref_counts, c.P > 0)) != FA_OK) return st;
+    if ((st = check_ints(x.source, false)) != FA_OK) return st;
+    if ((st = check_ints(x.missing, false)) != FA_OK) return st;
+    if (x.workspace == nullptr || misaligned(x.workspace, 256) ||
+        x.workspace_bytes < (size_t)fa::fork_workspace_ints(c.Z, c.max_pages) * sizeof(int32_t))
         return FA_ERR_WORKSPACE;
     fa::DeviceFacts f;
     cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
     fa::ForkParams p{};
-    static const fa_strides none{0, 0, 0, 1};
-    p.k = view(k_cache, skc != nullptr ? skc : &none, k_layer_stride);
-    p.v = view(v_cache, svc != nullptr ? svc : &none, v_layer_stride);
-    p.table = block_table;
-    p.st_z = table_stride;
-    p.lens = seq_lens;
-    p.refs = ref_counts;
-    p.source = source;
-    p.missing = missing;
-    p.Z = Z, p.L = L, p.H = Hkv, p.D = D, p.page = page_size, p.M = max_pages, p.P = P, p.room = room;
-    p.ws = static_cast<int32_t*>(workspace);
+    p.k = view(c.k, c.sk, c.k_layer);
+    p.v = view(c.v, c.sv, c.v_layer);
+    p.table = c.block_table;
+    p.st_z = c.table_stride;
+    p.lens = c.seq_lens;
+    p.refs = x.ref_counts;
+    p.source = x.source;
+    p.missing = x.missing;
+    p.Z = c.Z, p.L = c.L, p.H = c.Hkv, p.D = c.D, p.page = c.page_size, p.M = c.max_pages, p.P = c.P, p.room = x.room;
+    p.ws = static_cast<int32_t*>(x.workspace);
     p.status = f.status;
     err = fa::launch_cache_fork(p, f.sms, stream);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("cache fork launch", err);

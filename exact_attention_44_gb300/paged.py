@@ -22,28 +22,38 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 from . import _binding
 from ._binding import FA_DTYPE_BF16, FA_DTYPE_F16, FA_OK, FaError
 
 # A decode step makes one or two of these calls a layer, each a few microseconds of GPU time, so the
-# marshalling itself is kept short: torch is looked up once, the strides of a call go through one
-# ctypes array, and the stream's handle comes from the call that torch's own launches use.
+# marshalling itself is kept short: torch is looked up once, a call's argument block (the structures
+# of include/fa.h) is packed in one step, and the stream's handle comes from the call that torch's own
+# launches use.
+_CACHE = "@2P8q2qPqP7i4x"  # fa_paged_cache
+_ATTEND = struct.Struct(_CACHE + "3P8q2PqPN2ifi").pack
+_APPEND = struct.Struct(_CACHE + "2P8qPi4x").pack
+_COMMIT = struct.Struct(_CACHE + "PqPi4x").pack
+_FORK = struct.Struct(_CACHE + "4PNi4x").pack
+
 torch = None
-_raw_stream = None
+_int32 = _raw_stream = _get_device = None
 
 
 def _setup():
-    global torch, _raw_stream
+    global torch, _int32, _raw_stream, _get_device
     import torch as t
 
+    _int32 = t.int32
     _raw_stream = getattr(t._C, "_cuda_getCurrentRawStream", None) or (
         lambda index: t.cuda.current_stream(index).cuda_stream)
+    _get_device = t.cuda.current_device
     torch = t
 
 
 def _ints(name, t, shape):
-    if t.dtype != torch.int32:
+    if t.dtype is not _int32:
         raise TypeError(f"{name} must be int32")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
@@ -51,65 +61,53 @@ def _ints(name, t, shape):
         raise ValueError(f"{name}'s last dimension must be contiguous")
 
 
-def _table(block_table, Z):
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be int32")
-    if block_table.dim() != 2 or block_table.shape[0] != Z:
-        raise ValueError(f"block_table must be (Z, max_pages) = ({Z}, ...), got {tuple(block_table.shape)}")
-    row, col = block_table.stride()
-    M = block_table.shape[1]
-    if M > 1 and col != 1:
-        raise ValueError("block_table rows must be contiguous")
-    return M, row
-
-
-def _caches(k_cache, v_cache, layers):
-    """The caches' shape; layers: whether 5-D ones are allowed."""
+def _cache(k_cache, v_cache, block_table, seq_lens, Z, layers):
+    """The fields of a fa_paged_cache, checked; layers: whether 5-D caches are allowed."""
     shape = k_cache.shape
-    if shape != v_cache.shape or not (len(shape) == 4 or layers and len(shape) == 5):
+    n = len(shape)
+    if shape != v_cache.shape or not (n == 4 or layers and n == 5):
         want = "(pages, Hkv, page_size, D)" + (" or (layers, pages, Hkv, page_size, D)" if layers else "")
         raise ValueError(f"k_cache and v_cache must both be {want}, got {tuple(shape)}, {tuple(v_cache.shape)}")
-    if k_cache.dtype != v_cache.dtype or k_cache.element_size() != 2:
+    if k_cache.dtype is not v_cache.dtype or k_cache.element_size() != 2:
         raise TypeError("k_cache and v_cache must share one 16-bit dtype")
-    return shape
+    if block_table.dtype is not _int32:
+        raise TypeError("block_table must be int32")
+    rows = block_table.shape
+    if len(rows) != 2 or rows[0] != Z:
+        raise ValueError(f"block_table must be (Z, max_pages) = ({Z}, ...), got {tuple(rows)}")
+    M = rows[1]
+    row, col = block_table.stride()
+    if M > 1 and col != 1:
+        raise ValueError("block_table rows must be contiguous")
+    _ints("seq_lens", seq_lens, (Z,))
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if n == 5:
+        L, P, H, page, D = shape
+        kl, vl, ks, vs = ks[0], vs[0], ks[1:], vs[1:]
+    else:
+        P, H, page, D = shape
+        L, kl, vl = 1, 0, 0
+    return (k_cache.data_ptr(), v_cache.data_ptr(), *ks, *vs, kl, vl, block_table.data_ptr(), row, seq_lens.data_ptr(),
+            Z, L, P, H, page, D, M)
 
 
-def _layered(k_cache, v_cache):
-    """(L, layer strides of K and V, P, Hkv, page_size, D, strides of K and V within a layer)."""
-    shape, ks, vs = _caches(k_cache, v_cache, True), k_cache.stride(), v_cache.stride()
-    if len(shape) == 5:
-        return (shape[0], ks[0], vs[0], *shape[1:], ks[1:] + vs[1:])
-    return (1, 0, 0, *shape, ks + vs)
-
-
-def _strides(values):
-    """fa_strides structures laid end to end: (the array, which the caller keeps until the call, its address)."""
-    a = (ctypes.c_int64 * len(values))(*values)
-    return a, ctypes.addressof(a)
-
-
-def _call(name, lead, stream, tensors, args):
-    """Call libfa's `name` on the device of the tensor `lead`; its last argument is the stream's handle."""
+def _call(name, lead, stream, tensors, block):
+    """Call libfa's `name` with its packed arguments on the device of the tensor `lead`."""
     index = lead.get_device()
     for t in tensors:
         if t is not None and t.get_device() != index:
             raise ValueError(f"{name}: every tensor must be on {lead.device}, got one on {t.device}")
     if index < 0:
         raise ValueError(f"{name} takes CUDA tensors")
-    lib = _binding._lib or _binding.load()
+    fn = getattr(_binding._lib or _binding.load(), name)
     handle = _raw_stream(index) if stream is None else stream.cuda_stream
-    fn = getattr(lib, name)
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, handle)
+    if _get_device() == index:
+        rc = fn(block, handle)
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, handle)
+            rc = fn(block, handle)
     if rc != FA_OK:
         raise FaError(rc, name)
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def fa_fwd_paged_workspace_size(D: int, device=None) -> int:
@@ -146,23 +144,22 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *
     if len(shape) != 4:
         raise ValueError("q must be 4-D (Z, Hq, T, D)")
     Z, Hq, T, D = shape
-    P, Hkv, page, Dk = _caches(k_cache, v_cache, False)
-    if Dk != D:
-        raise ValueError(f"head dims differ: q has {D}, the cache {Dk}")
-    dtype, device = q.dtype, q.device
-    if dtype == torch.bfloat16:
+    cache = _cache(k_cache, v_cache, block_table, seq_lens, Z, False)
+    if cache[20] != D:
+        raise ValueError(f"head dims differ: q has {D}, the cache {cache[20]}")
+    dtype = q.dtype
+    if dtype is torch.bfloat16:
         code = FA_DTYPE_BF16
-    elif dtype == torch.float16:
+    elif dtype is torch.float16:
         code = FA_DTYPE_F16
     else:
         raise TypeError(f"fa_fwd_paged takes float16 or bfloat16 tensors, got {dtype}")
-    if k_cache.dtype != dtype:
+    if k_cache.dtype is not dtype:
         raise TypeError("q and the caches must share one dtype")
-    M, table_stride = _table(block_table, Z)
-    _ints("seq_lens", seq_lens, (Z,))
+    new_ptr = mask_ptr = lse_ptr = mask_stride = 0
     if new_lens is not None:
         _ints("new_lens", new_lens, (Z,))
-    mask_stride = 0
+        new_ptr = new_lens.data_ptr()
     if tree_mask is not None:
         words = (T + 31) // 32
         if tree_mask.dim() == 3:
@@ -172,24 +169,25 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *
             _ints("tree_mask", tree_mask, (T, words))
         if T > 1 and tree_mask.stride(-2) != words:
             raise ValueError("tree_mask's words must be contiguous within a sequence")
+        mask_ptr = tree_mask.data_ptr()
     if o is None:
-        o = torch.empty(shape, dtype=dtype, device=device)
-    elif o.shape != shape or o.dtype != dtype:
+        o = torch.empty(shape, dtype=dtype, device=q.device)
+    elif o.shape != shape or o.dtype is not dtype:
         raise ValueError("o must match q's shape and dtype")
     if lse is None:
         if want_lse:
-            lse = torch.empty((Z, Hq, T), dtype=torch.float32, device=device)
-    elif lse.dtype != torch.float32 or lse.shape != (Z, Hq, T) or not lse.is_contiguous():
+            lse = torch.empty((Z, Hq, T), dtype=torch.float32, device=q.device)
+            lse_ptr = lse.data_ptr()
+    elif lse.dtype is not torch.float32 or lse.shape != (Z, Hq, T) or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 (Z, Hq, T) tensor")
-    if workspace is None and device.type == "cuda":
-        workspace = torch.empty(fa_fwd_paged_workspace_size(D, device), dtype=torch.uint8, device=device)
-    keep, st = _strides(q.stride() + k_cache.stride() + v_cache.stride() + o.stride())
-    _call("fa_fwd_paged", q, stream,
-          (k_cache, v_cache, block_table, seq_lens, new_lens, tree_mask, o, lse, workspace),
-          (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(), _ptr(lse), block_table.data_ptr(),
-           seq_lens.data_ptr(), _ptr(new_lens), _ptr(tree_mask), Z, Hq, Hkv, T, D, P, page, M, table_stride,
-           mask_stride, st, st + 32, st + 64, st + 96, 1.0 / math.sqrt(D) if scale is None else float(scale), code,
-           _ptr(workspace), 0 if workspace is None else workspace.nbytes))
+    else:
+        lse_ptr = lse.data_ptr()
+    if workspace is None and q.is_cuda:
+        workspace = torch.empty(fa_fwd_paged_workspace_size(D, q.device), dtype=torch.uint8, device=q.device)
+    _call("fa_fwd_paged", q, stream, (k_cache, v_cache, block_table, seq_lens, new_lens, tree_mask, o, lse, workspace),
+          _ATTEND(*cache, q.data_ptr(), o.data_ptr(), lse_ptr, *q.stride(), *o.stride(), new_ptr, mask_ptr, mask_stride,
+                  0 if workspace is None else workspace.data_ptr(), 0 if workspace is None else workspace.nbytes, Hq, T,
+                  1.0 / math.sqrt(D) if scale is None else scale, code))
     return o, lse
 
 
@@ -202,20 +200,21 @@ def fa_cache_append(k, v, k_cache, v_cache, block_table, seq_lens, *, new_lens=N
     """
     if torch is None:
         _setup()
-    P, Hkv, page, D = _caches(k_cache, v_cache, False)
-    if k.dim() != 4 or k.shape != v.shape or k.shape[1] != Hkv or k.shape[3] != D:
-        raise ValueError(f"k and v must both be (Z, {Hkv}, T, {D}), got {tuple(k.shape)}, {tuple(v.shape)}")
-    if k.dtype != k_cache.dtype or v.dtype != k_cache.dtype:
+    shape = k.shape
+    if len(shape) != 4 or shape != v.shape:
+        raise ValueError(f"k and v must both be (Z, Hkv, T, D), got {tuple(shape)}, {tuple(v.shape)}")
+    Z, H, T, D = shape
+    cache = _cache(k_cache, v_cache, block_table, seq_lens, Z, False)
+    if cache[18] != H or cache[20] != D:
+        raise ValueError(f"k and v must both be (Z, {cache[18]}, T, {cache[20]}), got {tuple(shape)}")
+    if k.dtype is not k_cache.dtype or v.dtype is not k_cache.dtype:
         raise TypeError("k and v must have the cache's dtype")
-    Z, _, T, _ = k.shape
-    M, table_stride = _table(block_table, Z)
-    _ints("seq_lens", seq_lens, (Z,))
+    new_ptr = 0
     if new_lens is not None:
         _ints("new_lens", new_lens, (Z,))
-    keep, st = _strides(k.stride() + v.stride() + k_cache.stride() + v_cache.stride())
+        new_ptr = new_lens.data_ptr()
     _call("fa_cache_append", k, stream, (v, k_cache, v_cache, block_table, seq_lens, new_lens),
-          (k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(),
-           seq_lens.data_ptr(), _ptr(new_lens), Z, Hkv, T, D, P, page, M, table_stride, st, st + 32, st + 64, st + 96))
+          _APPEND(*cache, k.data_ptr(), v.data_ptr(), *k.stride(), *v.stride(), new_ptr, T))
 
 
 def fa_cache_commit(k_cache, v_cache, block_table, seq_lens, accepted, accepted_lens, *, stream=None) -> None:
@@ -229,18 +228,14 @@ def fa_cache_commit(k_cache, v_cache, block_table, seq_lens, accepted, accepted_
     """
     if torch is None:
         _setup()
-    L, kl, vl, P, Hkv, page, D, strides = _layered(k_cache, v_cache)
     if accepted.dim() != 2:
         raise ValueError("accepted must be (Z, A)")
     Z, A = accepted.shape
     _ints("accepted", accepted, (Z, A))
     _ints("accepted_lens", accepted_lens, (Z,))
-    _ints("seq_lens", seq_lens, (Z,))
-    M, table_stride = _table(block_table, Z)
-    keep, st = _strides(strides)
+    cache = _cache(k_cache, v_cache, block_table, seq_lens, Z, True)
     _call("fa_cache_commit", k_cache, stream, (v_cache, block_table, seq_lens, accepted, accepted_lens),
-          (k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), accepted.data_ptr(),
-           accepted_lens.data_ptr(), Z, L, Hkv, A, D, P, page, M, table_stride, accepted.stride(0), kl, vl, st, st + 32))
+          _COMMIT(*cache, accepted.data_ptr(), accepted.stride(0), accepted_lens.data_ptr(), A))
 
 
 def fa_cache_fork_workspace_size(Z: int, max_pages: int) -> int:
@@ -268,21 +263,20 @@ def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=No
     """
     if torch is None:
         _setup()
-    L, kl, vl, P, Hkv, page, D, strides = _layered(k_cache, v_cache)
     if seq_lens.dim() != 1:
         raise ValueError("seq_lens must be (Z)")
     Z = seq_lens.shape[0]
-    _ints("seq_lens", seq_lens, (Z,))
-    _ints("ref_counts", ref_counts, (P,))
+    cache = _cache(k_cache, v_cache, block_table, seq_lens, Z, True)
+    _ints("ref_counts", ref_counts, (cache[17],))
+    source_ptr = missing_ptr = 0
     if source is not None:
         _ints("source", source, (Z,))
+        source_ptr = source.data_ptr()
     if missing is not None:
         _ints("missing", missing, (1,))
-    M, table_stride = _table(block_table, Z)
-    if workspace is None and k_cache.device.type == "cuda":
-        workspace = torch.empty(fa_cache_fork_workspace_size(Z, M), dtype=torch.uint8, device=k_cache.device)
-    keep, st = _strides(strides)
+        missing_ptr = missing.data_ptr()
+    if workspace is None and k_cache.is_cuda:
+        workspace = torch.empty(fa_cache_fork_workspace_size(Z, cache[21]), dtype=torch.uint8, device=k_cache.device)
     _call("fa_cache_fork", k_cache, stream, (v_cache, block_table, seq_lens, ref_counts, source, missing, workspace),
-          (k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-           _ptr(source), _ptr(missing), Z, L, Hkv, D, P, page, M, int(room), table_stride, kl, vl, st, st + 32,
-           _ptr(workspace), 0 if workspace is None else workspace.nbytes))
+          _FORK(*cache, ref_counts.data_ptr(), source_ptr, missing_ptr, 0 if workspace is None else workspace.data_ptr(),
+                0 if workspace is None else workspace.nbytes, int(room)))

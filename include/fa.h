@@ -444,47 +444,38 @@ fa_status fa_fwd_schedule(int Z, int Hq, int Hkv, int Nq, int Nkv, int D, int ca
                           int64_t l2_bytes, fa_fwd_schedule_info* out);
 
 /* ------------------------------------------------------------ paged cache ---
- * The keys and values of many sequences, in pages of `page_size` positions:
+ * The keys and values of many sequences, in pages of `page_size` positions.
+ * Position p of sequence z is slot p % page_size of page
+ * block_table[z][p / page_size].
  *
- *   k_cache, v_cache  (P, Hkv, page_size, D) dtype, any strides {b: page,
- *                     h: head, n: slot, d: 1} that are multiples of 8
- *                     elements; base 16-byte aligned
- *   block_table       (Z, max_pages) int32, rows `table_stride` apart: position
- *                     p of sequence z is slot p % page_size of page
- *                     block_table[z][p / page_size]; -1 where it has none
- *   seq_lens          (Z) int32: positions sequence z holds
- *
- * page_size is a multiple of 16; max_pages * page_size <= 2^30; Z <= 65535.
- * The arrays live on the device and are read there: no call synchronises or
- * reads anything back, so every call can be captured in a CUDA graph (after one
- * call in the context) and follows the lengths and tables that it finds when
- * it runs.  Calls that write a cache or share a workspace must be ordered.  A
- * needed table entry outside 0 .. P - 1 is never followed: its positions read
- * as zeros (attention) or are skipped (the others), and FA_ERR_PAGE is
- * recorded (fa_device_status).  Lengths are clamped to what the table can
- * hold.
+ * page_size is a multiple of 16; max_pages * page_size <= 2^30; Z <= 65535; D
+ * in {16, 32, 64, 128, 256}; bases 16-byte aligned, strides multiples of 8
+ * elements.  The arrays live on the device and are read there: no call
+ * synchronises or reads anything back, so every call can be captured in a CUDA
+ * graph (after one call in the context) and follows the lengths and tables
+ * that it finds when it runs.  Calls that write a cache or share a workspace
+ * must be ordered.  A needed table entry outside 0 .. P - 1 is never followed:
+ * its positions read as zeros (attention) or are skipped (the others), and
+ * FA_ERR_PAGE is recorded (fa_device_status).  Lengths are clamped to what the
+ * table can hold; a cache without pages (P = 0) holds nothing.
  */
+typedef struct {
+    void* k;                      /* (L, P, Hkv, page_size, D), 16-bit elements */
+    void* v;
+    fa_strides sk, sv;            /* within a layer: {b: page, h: head, n: slot, d: 1} */
+    int64_t k_layer, v_layer;     /* elements from a layer to the next (used when L > 1) */
+    int32_t* block_table;         /* (Z, max_pages), -1 where a sequence has no page */
+    int64_t table_stride;         /* entries from a sequence's row to the next */
+    int32_t* seq_lens;            /* (Z) positions that sequence z holds */
+    int Z, L, P, Hkv, page_size, D, max_pages;
+} fa_paged_cache;
 
 /*
  * fa_fwd_paged -- attention of the T newest tokens of every sequence over its
- * cache: a decode step (T = 1), a chunk of a prompt, or a tree of drafted
- * tokens to be verified.
- *
- *   q         (Z, Hq, T, D) dtype, strides *sq
- *   o         (Z, Hq, T, D) dtype, strides *so    (written)
- *   lse       (Z, Hq, T) fp32 contiguous          (written; may be NULL)
- *   seq_lens  positions BEFORE the new tokens; new token t of sequence z is
- *             position seq_lens[z] + t and is in the cache already
- *             (fa_cache_append)
- *   new_lens  NULL, or (Z) int32: sequence z has only new_lens[z] <= T new
- *             tokens
- *   tree_mask NULL (a chain: new token t sees new tokens 0 .. t), or
- *             ceil(T / 32) int32 words for each (z, t), contiguous within a
- *             sequence, sequences mask_stride words apart (0: one tree for
- *             all): bit j % 32 of word j / 32 says that new token t sees new
- *             token j.  A token sees itself only if its bit says so.
- *   scale     any finite value as for fa_fwd
- *   workspace fa_fwd_paged_workspace_size(D) bytes, 256-byte aligned
+ * cache (one layer, L = 1): a decode step (T = 1), a chunk of a prompt, or a
+ * tree of drafted tokens to be verified.  seq_lens counts the positions BEFORE
+ * the new tokens; new token t of sequence z is position seq_lens[z] + t and is
+ * in the cache already (fa_cache_append).
  *
  * Every new token sees all positions before seq_lens[z].  With query head hq
  * on kv head hq / (Hq / Hkv), O and lse are softmax attention over the seen
@@ -492,70 +483,91 @@ fa_status fa_fwd_schedule(int Z, int Hq, int Hkv, int Nq, int Nkv, int D, int ca
  * t >= new_lens[z], gets O = 0 and lse = -inf.  What a page holds behind the
  * last position is never used.  A new token's K that a query does not see has
  * no effect on it whatever it holds; its V must be finite (the products weigh
- * it with 0).
- *
- * D in {16, 32, 64, 128, 256}; Hq % Hkv == 0.  Results are bitwise
- * reproducible for the same arguments and lengths.
+ * it with 0).  Hq % Hkv == 0.  Results are bitwise reproducible for the same
+ * arguments and lengths.
  */
-fa_status fa_fwd_paged(const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
-                       const int32_t* block_table, const int32_t* seq_lens, const int32_t* new_lens,
-                       const int32_t* tree_mask, int Z, int Hq, int Hkv, int T, int D, int P, int page_size,
-                       int max_pages, int64_t table_stride, int64_t mask_stride, const fa_strides* sq,
-                       const fa_strides* sk, const fa_strides* sv, const fa_strides* so, float scale, fa_dtype dtype,
-                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+typedef struct {
+    fa_paged_cache cache;
+    const void* q;                /* (Z, Hq, T, D) */
+    void* o;                      /* (Z, Hq, T, D), written */
+    float* lse;                   /* (Z, Hq, T) fp32 contiguous, written; or NULL */
+    fa_strides sq, so;
+    const int32_t* new_lens;      /* NULL, or (Z): sequence z has only new_lens[z] <= T new tokens */
+    /* NULL (a chain: new token t sees new tokens 0 .. t), or ceil(T / 32) words for each (z, t), contiguous within
+     * a sequence, sequences mask_stride words apart (0: one tree for all): bit j % 32 of word j / 32 says that new
+     * token t sees new token j.  A token sees itself only if its bit says so. */
+    const int32_t* tree_mask;
+    int64_t mask_stride;
+    void* workspace;              /* fa_fwd_paged_workspace_size(D) bytes, 256-byte aligned */
+    size_t workspace_bytes;
+    int Hq, T;
+    float scale;                  /* any finite value as for fa_fwd */
+    int dtype;                    /* fa_dtype of q, o and the cache */
+} fa_fwd_paged_args;
+fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream);
 /* Workspace bytes of fa_fwd_paged for head dim D on the current device. */
 fa_status fa_fwd_paged_workspace_size(int D, size_t* bytes);
 
 /*
- * fa_cache_append -- write new rows: k, v (Z, Hkv, T, D) with strides *sk, *sv
- * go to positions seq_lens[z] + t, t < new_lens[z] (NULL: T).  seq_lens is not
- * changed (one call a layer).  Bits are moved unchanged; any 16-bit type.
+ * fa_cache_append -- write new rows to one layer (L = 1): row (z, :, t) of k
+ * and v goes to position seq_lens[z] + t, t < new_lens[z] (NULL: T).  seq_lens
+ * is not changed (one call a layer).  Bits are moved unchanged.
  */
-fa_status fa_cache_append(const void* k, const void* v, void* k_cache, void* v_cache, const int32_t* block_table,
-                          const int32_t* seq_lens, const int32_t* new_lens, int Z, int Hkv, int T, int D, int P,
-                          int page_size, int max_pages, int64_t table_stride, const fa_strides* sk,
-                          const fa_strides* sv, const fa_strides* skc, const fa_strides* svc, cudaStream_t stream);
+typedef struct {
+    fa_paged_cache cache;
+    const void* k;                /* (Z, Hkv, T, D) */
+    const void* v;
+    fa_strides sk, sv;
+    const int32_t* new_lens;
+    int T;
+} fa_cache_append_args;
+fa_status fa_cache_append(const fa_cache_append_args* args, cudaStream_t stream);
 
 /*
  * fa_cache_commit -- keep the accepted ones of the drafted tokens: position
  * seq_lens[z] + accepted[z][i] moves to seq_lens[z] + i for i <
- * accepted_lens[z] <= A, in L layers of both caches (layer strides in
- * elements), in place.  accepted (Z, A) int32, rows accepted_stride apart,
+ * accepted_lens[z] <= A, in all L layers of both caches, in place.  accepted is
  * strictly increasing within accepted_lens[z] (other orders leave the moved
  * rows undefined, nothing else).  seq_lens is not changed: the caller adds
  * accepted_lens to it.
  */
-fa_status fa_cache_commit(void* k_cache, void* v_cache, const int32_t* block_table, const int32_t* seq_lens,
-                          const int32_t* accepted, const int32_t* accepted_lens, int Z, int L, int Hkv, int A, int D,
-                          int P, int page_size, int max_pages, int64_t table_stride, int64_t accepted_stride,
-                          int64_t k_layer_stride, int64_t v_layer_stride, const fa_strides* skc, const fa_strides* svc,
-                          cudaStream_t stream);
+typedef struct {
+    fa_paged_cache cache;
+    const int32_t* accepted;      /* (Z, A), rows accepted_stride apart */
+    int64_t accepted_stride;
+    const int32_t* accepted_lens; /* (Z) */
+    int A;
+} fa_cache_commit_args;
+fa_status fa_cache_commit(const fa_cache_commit_args* args, cudaStream_t stream);
 
 /*
  * fa_cache_fork -- fork, free and give room, for the whole batch at once, in
- * place.  ref_counts (P) int32 counts the table entries that hold a page; a
- * page whose count is 0 is free.  Sequence z becomes a copy of sequence
- * source[z] as it was before the call: z itself (it stays), another one, or -1
- * (it is emptied); source NULL: all stay.  A copy shares the source's full
- * pages and gets its own copy (all L layers) of the partly filled one; what it
- * held before is released.  Then every sequence that is not emptied gets pages
- * for `room` more positions.  Pages are taken lowest first from those that
- * were free before the call, for sequences in order, columns in order; pages
- * released by a call can be handed out by the next one.  If they do not
- * suffice the last ones stay -1 (and a partly filled page uncopied), and
- * *missing (int32, may be NULL) is the number of pages that lacked, columns
- * past max_pages included; 0 otherwise.
+ * place.  A page whose count is 0 is free.  Sequence z becomes a copy of
+ * sequence source[z] as it was before the call: z itself (it stays), another
+ * one, or -1 (it is emptied).  A copy shares the source's full pages and gets
+ * its own copy (all L layers) of the partly filled one; what it held before is
+ * released.  Then every sequence that is not emptied gets pages for `room`
+ * more positions.  Pages are taken lowest first from those that were free
+ * before the call, for sequences in order, columns in order; pages released by
+ * a call can be handed out by the next one.  If they do not suffice the last
+ * ones stay -1 (and a partly filled page uncopied), and *missing is the number
+ * of pages that lacked, columns past max_pages included; 0 otherwise.
  *
  * Valid state: a row's entries are its ceil(len / page_size) pages, then
  * pages of room, then -1; a page with room to write belongs to one sequence.
- * fa_cache_fork keeps it so.  Z <= 8192.  workspace:
- * fa_cache_fork_workspace_size(Z, max_pages) bytes, 256-byte aligned.
+ * fa_cache_fork keeps it so.  A source outside -1 .. Z - 1 is recorded as
+ * FA_ERR_PAGE and the sequence stays.  Z <= 8192.
  */
-fa_status fa_cache_fork(void* k_cache, void* v_cache, int32_t* block_table, int32_t* seq_lens, int32_t* ref_counts,
-                        const int32_t* source, int32_t* missing, int Z, int L, int Hkv, int D, int P, int page_size,
-                        int max_pages, int room, int64_t table_stride, int64_t k_layer_stride, int64_t v_layer_stride,
-                        const fa_strides* skc, const fa_strides* svc, void* workspace, size_t workspace_bytes,
-                        cudaStream_t stream);
+typedef struct {
+    fa_paged_cache cache;
+    int32_t* ref_counts;          /* (P) table entries that hold each page */
+    const int32_t* source;        /* (Z), or NULL: all stay */
+    int32_t* missing;             /* one int32, or NULL */
+    void* workspace;              /* fa_cache_fork_workspace_size(Z, max_pages) bytes, 256-byte aligned */
+    size_t workspace_bytes;
+    int room;
+} fa_cache_fork_args;
+fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream);
 fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes);
 
 /*

@@ -19,22 +19,68 @@ def lib():
 PTR = 0x10000
 
 
+class Strides(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in ("b", "h", "n", "d")]
+
+
 def _st(b, h, n, d=1):
-    return ctypes.byref(fa.fa_strides(b, h, n, d))
+    return Strides(b, h, n, d)
 
 
-def _attend(lib, *, q=PTR, k=PTR, v=PTR, o=PTR, lse=PTR, table=PTR, lens=PTR, new=None, mask=None, Z=2, Hq=4, Hkv=2,
-            T=3, D=64, P=9, page=16, M=4, ts=4, ms=0, sq=None, sk=None, so=None, scale=0.1, dtype=0, ws=PTR,
+class Cache(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k", "v")] + [("sk", Strides), ("sv", Strides)] +
+                [(n, ctypes.c_int64) for n in ("k_layer", "v_layer")] +
+                [("table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("lens", ctypes.c_void_p)] +
+                [(n, ctypes.c_int) for n in ("Z", "L", "P", "Hkv", "page", "D", "M")])
+
+
+class Attend(ctypes.Structure):
+    _fields_ = [("cache", Cache), ("q", ctypes.c_void_p), ("o", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("sq", Strides), ("so", Strides), ("new", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("mask_stride", ctypes.c_int64), ("ws", ctypes.c_void_p), ("wsb", ctypes.c_size_t), ("Hq", ctypes.c_int),
+                ("T", ctypes.c_int), ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
+class Append(ctypes.Structure):
+    _fields_ = [("cache", Cache), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("sk", Strides), ("sv", Strides),
+                ("new", ctypes.c_void_p), ("T", ctypes.c_int)]
+
+
+class Commit(ctypes.Structure):
+    _fields_ = [("cache", Cache), ("path", ctypes.c_void_p), ("path_stride", ctypes.c_int64), ("kept", ctypes.c_void_p),
+                ("A", ctypes.c_int)]
+
+
+class Fork(ctypes.Structure):
+    _fields_ = [("cache", Cache), ("refs", ctypes.c_void_p), ("src", ctypes.c_void_p), ("miss", ctypes.c_void_p),
+                ("ws", ctypes.c_void_p), ("wsb", ctypes.c_size_t), ("room", ctypes.c_int)]
+
+
+def test_packed_blocks_have_the_structures_sizes():
+    import struct
+    from exact_attention_44_gb300 import paged
+    assert struct.calcsize(paged._CACHE) == ctypes.sizeof(Cache)
+    for pack, kind in ((paged._ATTEND, Attend), (paged._APPEND, Append), (paged._COMMIT, Commit), (paged._FORK, Fork)):
+        assert pack.__self__.size == ctypes.sizeof(kind)
+
+
+def _cache(kc=PTR, table=PTR, lens=PTR, Z=2, L=1, P=9, H=2, page=16, D=64, M=4, ts=4, kl=1 << 16, sc=None):
+    sc = sc or _st(H * page * D, page * D, D)
+    return Cache(kc, kc, sc, sc, kl, kl, table, ts, lens, Z, L, P, H, page, D, M)
+
+
+def _attend(lib, *, q=PTR, k=PTR, o=PTR, lse=PTR, table=PTR, lens=PTR, new=None, mask=None, Z=2, Hq=4, Hkv=2, T=3,
+            D=64, P=9, page=16, M=4, L=1, ts=4, ms=0, sq=None, sk=None, so=None, scale=0.1, dtype=0, ws=PTR,
             wsb=1 << 40):
-    sq = sq or _st(Hq * T * D, T * D, D)
-    sk = sk or _st(Hkv * page * D, page * D, D)
-    return lib.fa_fwd_paged(q, k, v, o, lse, table, lens, new, mask, Z, Hq, Hkv, T, D, P, page, M, ts, ms, sq, sk, sk,
-                            so or _st(Hq * T * D, T * D, D), scale, dtype, ws, wsb, None)
+    st = _st(Hq * T * D, T * D, D)
+    a = Attend(_cache(k, table, lens, Z, L, P, Hkv, page, D, M, ts, 1 << 16, sk), q, o, lse, sq or st, so or st, new, mask,
+               ms, ws, wsb, Hq, T, scale, dtype)
+    return lib.fa_fwd_paged(ctypes.addressof(a), None)
 
 
 @pytest.mark.parametrize("kw,code", [
     (dict(Z=-1), fa.FA_ERR_INVALID_ARG), (dict(T=-1), fa.FA_ERR_INVALID_ARG), (dict(Hq=3), fa.FA_ERR_INVALID_ARG),
-    (dict(Hkv=0), fa.FA_ERR_INVALID_ARG), (dict(P=-1), fa.FA_ERR_INVALID_ARG), (dict(M=-1), fa.FA_ERR_INVALID_ARG),
+    (dict(Hkv=0), fa.FA_ERR_INVALID_ARG), (dict(L=2), fa.FA_ERR_INVALID_ARG), (dict(P=-1), fa.FA_ERR_INVALID_ARG), (dict(M=-1), fa.FA_ERR_INVALID_ARG),
     (dict(ts=-4), fa.FA_ERR_INVALID_ARG), (dict(ms=-1), fa.FA_ERR_INVALID_ARG),
     (dict(scale=float("nan")), fa.FA_ERR_INVALID_ARG), (dict(scale=3e38), fa.FA_ERR_INVALID_ARG),
     (dict(q=None), fa.FA_ERR_INVALID_ARG), (dict(k=None), fa.FA_ERR_INVALID_ARG), (dict(o=None), fa.FA_ERR_INVALID_ARG),
@@ -56,11 +102,10 @@ def test_attention_arguments(lib, kw, code):
     assert _attend(lib, **kw) == code
 
 
-def _append(lib, *, k=PTR, kc=PTR, table=PTR, lens=PTR, new=None, Z=2, H=2, T=3, D=64, P=9, page=16, M=4, ts=4,
-            sk=None, sc=None):
-    sk = sk or _st(H * T * D, T * D, D)
-    sc = sc or _st(H * page * D, page * D, D)
-    return lib.fa_cache_append(k, k, kc, kc, table, lens, new, Z, H, T, D, P, page, M, ts, sk, sk, sc, sc, None)
+def _append(lib, *, k=PTR, T=3, new=None, sk=None, **kw):
+    c = _cache(**kw)
+    st = sk or _st(c.Hkv * T * c.D, T * c.D, c.D)
+    return lib.fa_cache_append(ctypes.addressof(Append(c, k, k, st, st, new, T)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -76,10 +121,8 @@ def test_append_arguments(lib, kw, code):
     assert _append(lib, **kw) == code
 
 
-def _commit(lib, *, kc=PTR, table=PTR, lens=PTR, path=PTR, kept=PTR, Z=2, L=2, H=2, A=3, D=64, P=9, page=16, M=4,
-            ts=4, ps=3, kl=1 << 16, sc=None):
-    sc = sc or _st(H * page * D, page * D, D)
-    return lib.fa_cache_commit(kc, kc, table, lens, path, kept, Z, L, H, A, D, P, page, M, ts, ps, kl, kl, sc, sc, None)
+def _commit(lib, *, path=PTR, kept=PTR, A=3, ps=3, L=2, **kw):
+    return lib.fa_cache_commit(ctypes.addressof(Commit(_cache(L=L, **kw), path, ps, kept, A)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -93,11 +136,8 @@ def test_commit_arguments(lib, kw, code):
     assert _commit(lib, **kw) == code
 
 
-def _fork(lib, *, kc=PTR, table=PTR, lens=PTR, refs=PTR, src=PTR, miss=None, Z=2, L=2, H=2, D=64, P=9, page=16, M=4,
-          room=1, ts=4, kl=1 << 16, sc=None, ws=PTR, wsb=1 << 40):
-    sc = sc or _st(H * page * D, page * D, D)
-    return lib.fa_cache_fork(kc, kc, table, lens, refs, src, miss, Z, L, H, D, P, page, M, room, ts, kl, kl, sc, sc, ws,
-                             wsb, None)
+def _fork(lib, *, refs=PTR, src=PTR, miss=None, room=1, ws=PTR, wsb=1 << 40, L=2, **kw):
+    return lib.fa_cache_fork(ctypes.addressof(Fork(_cache(L=L, **kw), refs, src, miss, ws, wsb, room)), None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -118,6 +158,8 @@ def test_workspace_sizes(lib):
     assert fa.fa_cache_fork_workspace_size(10, 100) >= 4 * 10 * 108
     n = ctypes.c_size_t()
     assert lib.fa_cache_fork_workspace_size(-1, 3, ctypes.byref(n)) == fa.FA_ERR_INVALID_ARG
+    for call in (lib.fa_fwd_paged, lib.fa_cache_append, lib.fa_cache_commit, lib.fa_cache_fork):
+        assert call(None, None) == fa.FA_ERR_INVALID_ARG
     assert lib.fa_fwd_paged_workspace_size(20, ctypes.byref(n)) == fa.FA_ERR_UNSUPPORTED
     assert lib.fa_fwd_paged_workspace_size(64, None) == fa.FA_ERR_INVALID_ARG
     assert fa.fa_status_string(fa.FA_ERR_PAGE) == "FA_ERR_PAGE"
