@@ -22,12 +22,12 @@ __device__ __forceinline__ void bad_page(uint32_t* status, uint32_t site) {
 }
 
 template <typename K, typename P>
-cudaError_t launch_dependent(K kernel, int64_t grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -38,94 +38,119 @@ cudaError_t launch_dependent(K kernel, int64_t grid, int threads, size_t smem, c
 
 // ------------------------------------------------------------ append --------
 // Row (z, t, h) of the new K and V, t < news[z], to position lens[z] + t.  A
-// thread moves one 16-byte piece of K and the same one of V; pieces of a row
-// are neighbours, then heads, then tokens.
-constexpr int APPEND_THREADS = 256;
+// group of up to 32 lanes takes a token: one block table entry for all of its
+// heads, then the 16-byte pieces of its K and V rows, four of each in flight a
+// lane.
+constexpr int APPEND_THREADS = 128;
 
 __global__ void __launch_bounds__(APPEND_THREADS) fa_cache_append_kernel(const AppendParams p) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int pieces = p.D / 8;
-    const uint32_t per_z = (uint32_t)p.T * p.H * pieces;  // < 2^31 (checked on the host)
-    const int z = blockIdx.y;
+    const int z = blockIdx.y, lane = threadIdx.x & (p.lanes - 1);
+    const int t = (int)((blockIdx.x * APPEND_THREADS + threadIdx.x) / p.lanes);
+    if (t >= p.T) return;
     const int len = max(ldi(p.lens + z), 0);
-    const int nl = p.news != nullptr ? min(ldi(p.news + z), p.T) : p.T;
-    const uint32_t i = blockIdx.x * APPEND_THREADS + threadIdx.x;
-    if (i >= per_z) return;
-    const uint32_t row = i / pieces, c = i - row * pieces;
-    const int t = (int)(row / p.H), h = (int)(row - (uint32_t)t * p.H);
+    const int nl = p.news != nullptr ? ldi(p.news + z) : p.T;
     if (t >= nl) return;
-    const int64_t pos = (int64_t)len + t;
-    const int64_t col = pos / p.page;
-    const int e = col < p.M ? ldi(p.table + z * p.st_z + col) : -1;
+    const uint32_t pos = (uint32_t)len + (uint32_t)t, col = pos / (uint32_t)p.page;  // below 2^32
+    const int e = col < (uint32_t)p.M ? ldi(p.table + z * p.st_z + col) : -1;
     if ((unsigned)e >= (unsigned)p.P) {
         bad_page(p.status, SITE_PAGE_APPEND);
         return;
     }
-    const int slot = (int)(pos - col * p.page);
-    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p.ks + z * p.ks_z + h * p.ks_h + t * p.ks_n + c * 8));
-    const uint4 b = __ldcg(reinterpret_cast<const uint4*>(p.vs + z * p.vs_z + h * p.vs_h + t * p.vs_n + c * 8));
-    *reinterpret_cast<uint4*>(p.k.base + e * p.k.p + h * p.k.h + slot * p.k.n + c * 8) = a;
-    *reinterpret_cast<uint4*>(p.v.base + e * p.v.p + h * p.v.h + slot * p.v.n + c * 8) = b;
-}
-
-// ------------------------------------------------------------ commit --------
-// Position lens[z] + path[z][i] to lens[z] + i for i < kept[z], in place.  One
-// thread takes a 16-byte piece through all of the path's steps: with the path
-// strictly increasing a step writes only where the same thread has already
-// read (position lens[z] + i is read by no step after i), so steps need no
-// barrier, and the reads of eight steps may go ahead of their writes.
-constexpr int COMMIT_THREADS = 256;
-
-__global__ void __launch_bounds__(COMMIT_THREADS) fa_cache_commit_kernel(const CommitParams p) {
-    ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
-    const int pieces = p.D / 8;
-    const uint32_t per_z = (uint32_t)p.L * 2 * p.H * pieces;  // < 2^31 (checked on the host)
-    const uint32_t i = blockIdx.x * COMMIT_THREADS + threadIdx.x;
-    const int z = blockIdx.y;
-    if (i >= per_z) return;
-    const uint32_t c = i % pieces;
-    uint32_t r = i / pieces;
-    const uint32_t h = r % p.H;
-    r /= p.H;
-    const bool is_v = r & 1u;
-    const uint32_t layer = r >> 1;
-    const CacheView& cache = is_v ? p.v : p.k;
-    uint16_t* base = cache.base + layer * cache.l + h * cache.h + c * 8;
-    const int64_t len = max(ldi(p.lens + z), 0), cap = (int64_t)p.M * p.page;
-    const int n = min(ldi(p.kept + z), p.A);
-    const int32_t* row = p.table + z * p.st_z;
-    auto at = [&](int64_t pos) -> uint16_t* {
-        if (pos < 0 || pos >= cap) return nullptr;
-        const int64_t col = pos / p.page;
-        const int e = ldi(row + col);
-        return (unsigned)e < (unsigned)p.P ? base + e * cache.p + (pos - col * p.page) * cache.n : nullptr;
-    };
-    constexpr int U = 8;
-    for (int s0 = 0; s0 < n; s0 += U) {
-        uint4 v[U];
-        uint16_t* to[U];
+    const int64_t slot = pos - col * (uint32_t)p.page;
+    const uint16_t* ks = p.ks + z * p.ks_z + t * p.ks_n;
+    const uint16_t* vs = p.vs + z * p.vs_z + t * p.vs_n;
+    uint16_t* kd = p.k.base + e * p.k.p + slot * p.k.n;
+    uint16_t* vd = p.v.base + e * p.v.p + slot * p.v.n;
+    const int shift = 31 - __clz(p.D / 8), n = p.H << shift;  // pieces of a row: a power of two
+    constexpr int U = 4;
+    for (int i0 = lane; i0 < n; i0 += U * p.lanes) {
+        uint4 a[U], b[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            to[u] = nullptr;
-            if (s0 + u < n) {
-                const int from = ldi(p.path + z * p.sp_z + s0 + u);
-                if (from != s0 + u) {
-                    const uint16_t* src = at(len + from);
-                    to[u] = at(len + s0 + u);
-                    if (src == nullptr || to[u] == nullptr) {
-                        bad_page(p.status, SITE_PAGE_COMMIT);
-                        to[u] = nullptr;
-                    } else {
-                        v[u] = __ldcg(reinterpret_cast<const uint4*>(src));
-                    }
-                }
+            const int i = i0 + u * p.lanes, h = i >> shift, c = (i & ((1 << shift) - 1)) * 8;
+            if (i < n) {
+                a[u] = __ldcg(reinterpret_cast<const uint4*>(ks + h * p.ks_h + c));
+                b[u] = __ldcg(reinterpret_cast<const uint4*>(vs + h * p.vs_h + c));
             }
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (to[u] != nullptr) *reinterpret_cast<uint4*>(to[u]) = v[u];
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * p.lanes, h = i >> shift, c = (i & ((1 << shift) - 1)) * 8;
+            if (i < n) {
+                *reinterpret_cast<uint4*>(kd + h * p.k.h + c) = a[u];
+                *reinterpret_cast<uint4*>(vd + h * p.v.h + c) = b[u];
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------ commit --------
+// Position lens[z] + path[z][i] to lens[z] + i for i < kept[z], in place.  A
+// CTA first turns a batch of steps into offsets within K and V; then one thread
+// takes a 16-byte piece (of a layer, K or V, head) through the steps: with the
+// path strictly increasing a step writes only where the same thread has
+// already read (position lens[z] + i is read by no step after i), so steps need
+// no barrier, and the reads of eight steps may go ahead of their writes.
+constexpr int COMMIT_THREADS = 256;
+constexpr int COMMIT_BATCH = 64;
+
+__global__ void __launch_bounds__(COMMIT_THREADS) fa_cache_commit_kernel(const CommitParams p) {
+    __shared__ int64_t move[2][2][COMMIT_BATCH];  // [K, V][from, to][step]; from -1: nothing to do
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int tid = threadIdx.x, z = blockIdx.y;
+    const int shift = 31 - __clz(p.D / 8);
+    const uint32_t per_z = ((uint32_t)p.L * 2 * p.H) << shift;  // < 2^31 (checked on the host)
+    const uint32_t i = blockIdx.x * COMMIT_THREADS + tid;
+    const uint32_t c = i & ((1u << shift) - 1);
+    uint32_t r = i >> shift;
+    const uint32_t h = r % p.H;
+    r /= p.H;
+    const int is_v = r & 1u;
+    const CacheView& cache = is_v ? p.v : p.k;
+    uint16_t* base = cache.base + (int64_t)(r >> 1) * cache.l + h * cache.h + c * 8;
+    const int n = min(ldi(p.kept + z), p.A);
+    const int len = max(ldi(p.lens + z), 0);
+    const int32_t* row = p.table + z * p.st_z;
+    for (int b0 = 0; b0 < n; b0 += COMMIT_BATCH) {
+        const int count = min(COMMIT_BATCH, n - b0);
+        if (b0 > 0) __syncthreads();
+        if (tid < 2 * count) {  // two threads a step: where it is, where it goes
+            const int step = tid >> 1, to = tid & 1;
+            const int from = ldi(p.path + z * p.sp_z + b0 + step), j = to ? b0 + step : from;
+            const int64_t pos = (int64_t)len + j;
+            int64_t k = -1, v = -1;
+            if (from != b0 + step) {
+                const uint32_t col = pos >= 0 && pos < (int64_t)p.M * p.page ? (uint32_t)pos / (uint32_t)p.page : 0u;
+                const int e = pos >= 0 && pos < (int64_t)p.M * p.page ? ldi(row + col) : -1;
+                if ((unsigned)e < (unsigned)p.P) {
+                    const int64_t slot = (uint32_t)pos - col * (uint32_t)p.page;
+                    k = e * p.k.p + slot * p.k.n;
+                    v = e * p.v.p + slot * p.v.n;
+                } else {
+                    bad_page(p.status, SITE_PAGE_COMMIT);
+                }
+            }
+            move[0][to][step] = k;
+            move[1][to][step] = v;
+        }
+        __syncthreads();
+        if (i >= per_z) continue;
+        constexpr int U = 8;
+        for (int s0 = 0; s0 < count; s0 += U) {
+            uint4 v[U];
+            bool go[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                go[u] = s0 + u < count && move[is_v][0][s0 + u] >= 0 && move[is_v][1][s0 + u] >= 0;
+                if (go[u]) v[u] = __ldcg(reinterpret_cast<const uint4*>(base + move[is_v][0][s0 + u]));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (go[u]) *reinterpret_cast<uint4*>(base + move[is_v][1][s0 + u]) = v[u];
+        }
     }
 }
 
@@ -148,8 +173,8 @@ __device__ __forceinline__ ForkWs fork_ws(const ForkParams& p) {
     w.first = w.len + p.Z;
     w.count = w.first + p.Z;
     w.off = w.count + p.Z;
-    w.tail = w.off + p.Z;         // 3 per sequence: from page, to page, rows (0: none)
-    w.found = w.tail + 3 * p.Z;   // pages found
+    w.tail = w.off + p.Z;         // list of tails: from page, to page, rows
+    w.found = w.tail + 3 * p.Z;   // pages found, tails
     w.pages = w.found + 2;
     return w;
 }
@@ -180,10 +205,12 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* sum) {
 
 __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const ForkParams p) {
     __shared__ int red[32];
+    __shared__ int tails;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const ForkWs w = fork_ws(p);
     const int tid = threadIdx.x;
+    if (tid == 0) tails = 0;
     const int cap = p.M * p.page;
     int wanted = 0, excess = 0;
     for (int z0 = 0; z0 < p.Z; z0 += PLAN_THREADS) {
@@ -235,22 +262,26 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
     }
     found = min(found, wanted);
     __syncthreads();
-    // tails: the partly filled last page of a source goes to the copy's first own page
+    // tails: the partly filled last page of a source goes to the copy's first own
+    // page (the list's order is of no account: no page is in it twice as a target,
+    // and no target is a source)
     for (int z = tid; z < p.Z; z += PLAN_THREADS) {
-        const int src = w.src[z], len = w.len[z], tail = len % p.page;
-        int rows = 0, from = 0, to = 0;
-        if (src >= 0 && src != z && tail > 0 && w.off[z] < found && w.count[z] > 0) {
-            from = ldi(p.table + src * p.st_z + len / p.page);
-            to = w.pages[w.off[z]];
-            if ((unsigned)from < (unsigned)p.P) rows = tail;
-            else bad_page(p.status, SITE_PAGE_FORK);
+        const int src = w.src[z], len = w.len[z], rows = len % p.page;
+        if (src < 0 || src == z || rows == 0 || w.off[z] >= found || w.count[z] == 0) continue;
+        const int from = ldi(p.table + src * p.st_z + len / p.page);
+        if ((unsigned)from < (unsigned)p.P) {
+            int32_t* t = w.tail + 3 * atomicAdd(&tails, 1);
+            t[0] = from;
+            t[1] = w.pages[w.off[z]];
+            t[2] = rows;
+        } else {
+            bad_page(p.status, SITE_PAGE_FORK);
         }
-        w.tail[3 * z] = from;
-        w.tail[3 * z + 1] = to;
-        w.tail[3 * z + 2] = rows;
     }
+    __syncthreads();
     if (tid == 0) {
         w.found[0] = found;
+        w.found[1] = tails;
         if (p.missing != nullptr) *p.missing = wanted - found + excess;
     }
 }
@@ -258,8 +289,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
 // Table, lengths and counts: a CTA takes `cols` columns of every row, reads
 // them all before it writes any (a source row may be rewritten in the same
 // call), and counts one reference less for what a changed row held and one
-// more for what it holds.  The other CTAs copy tails: rows of all heads of one
-// (sequence, layer, K or V) each.
+// more for what it holds.  The warps of the other CTAs copy tails, a (tail,
+// layer, K or V, head) at a time.
 constexpr int FORK_THREADS = 256;
 
 struct ForkApply {
@@ -303,66 +334,62 @@ __global__ void __launch_bounds__(FORK_THREADS) fa_cache_fork_apply_kernel(const
             for (int z = tid; z < p.Z; z += FORK_THREADS) p.lens[z] = ldi(w.len + z);
         return;
     }
-    const int pieces = p.D / 8;
-    const int64_t jobs = (int64_t)p.Z * p.L * 2;
-    for (int64_t j = blockIdx.x - a.table_ctas; j < jobs; j += gridDim.x - a.table_ctas) {
-        const int z = (int)(j / (2 * p.L)), r = (int)(j - (int64_t)z * 2 * p.L);
-        const int rows = ldi(w.tail + 3 * z + 2);
-        if (rows == 0) continue;
-        const int64_t from = ldi(w.tail + 3 * z), to = ldi(w.tail + 3 * z + 1);
-        const CacheView& cache = r & 1 ? p.v : p.k;
-        uint16_t* base = cache.base + (int64_t)(r >> 1) * cache.l;
-        for (int i = tid; i < p.H * rows * pieces; i += FORK_THREADS) {
-            const int c = i % pieces, row = i / pieces, h = row / rows, slot = row - h * rows;
-            const int64_t at = h * cache.h + slot * cache.n + c * 8;
-            *reinterpret_cast<uint4*>(base + to * cache.p + at) =
-                __ldcg(reinterpret_cast<const uint4*>(base + from * cache.p + at));
+    // a warp per (tail, layer, K or V, head)
+    const int shift = 31 - __clz(p.D / 8), lane = tid % 32, per_tail = p.L * 2 * p.H;
+    const int64_t jobs = (int64_t)ldi(w.found + 1) * per_tail;
+    const int64_t warps = (int64_t)(gridDim.x - a.table_ctas) * (FORK_THREADS / 32);
+    for (int64_t j = (int64_t)(blockIdx.x - a.table_ctas) * (FORK_THREADS / 32) + tid / 32; j < jobs; j += warps) {
+        const int i = (int)(j / per_tail), r = (int)(j - (int64_t)i * per_tail), lk = r / p.H, h = r - lk * p.H;
+        const int64_t from = ldi(w.tail + 3 * i), to = ldi(w.tail + 3 * i + 1);
+        const int n = ldi(w.tail + 3 * i + 2) << shift;
+        const CacheView& cache = lk & 1 ? p.v : p.k;
+        uint16_t* base = cache.base + (int64_t)(lk >> 1) * cache.l + h * cache.h;
+        constexpr int U = 8;
+        for (int i0 = lane; i0 < n; i0 += 32 * U) {
+            uint4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int x = i0 + 32 * u;
+                if (x < n)
+                    v[u] = __ldcg(reinterpret_cast<const uint4*>(base + from * cache.p + (x >> shift) * cache.n +
+                                                                 (x & ((1 << shift) - 1)) * 8));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int x = i0 + 32 * u;
+                if (x < n)
+                    *reinterpret_cast<uint4*>(base + to * cache.p + (x >> shift) * cache.n + (x & ((1 << shift) - 1)) * 8) = v[u];
+            }
         }
     }
 }
 
 }  // namespace
 
-cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream) {
-    const int64_t per_z = (int64_t)p.T * p.H * (p.D / 8);
-    const int64_t gx = (per_z + APPEND_THREADS - 1) / APPEND_THREADS;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)gx, (unsigned)p.Z);
-    cfg.blockDim = dim3(APPEND_THREADS);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_cache_append_kernel, p);
+cudaError_t launch_cache_append(AppendParams p, cudaStream_t stream) {
+    p.lanes = 1;
+    while (p.lanes < 32 && p.lanes < p.H * (p.D / 8)) p.lanes *= 2;
+    return launch_dependent(fa_cache_append_kernel, dim3((unsigned)(((int64_t)p.T * p.lanes + APPEND_THREADS - 1) / APPEND_THREADS), (unsigned)p.Z),
+                            APPEND_THREADS, 0, stream, p);
 }
 
 cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t stream) {
     const int64_t per_z = (int64_t)p.L * 2 * p.H * (p.D / 8);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((per_z + COMMIT_THREADS - 1) / COMMIT_THREADS), (unsigned)p.Z);
-    cfg.blockDim = dim3(COMMIT_THREADS);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa_cache_commit_kernel, p);
+    return launch_dependent(fa_cache_commit_kernel, dim3((unsigned)((per_z + COMMIT_THREADS - 1) / COMMIT_THREADS), (unsigned)p.Z),
+                            COMMIT_THREADS, 0, stream, p);
 }
 
 cudaError_t launch_cache_fork(const ForkParams& p, int sms, cudaStream_t stream) {
-    cudaError_t err = launch_dependent(fa_cache_fork_plan_kernel, 1, PLAN_THREADS, 0, stream, p);
+    cudaError_t err = launch_dependent(fa_cache_fork_plan_kernel, dim3(1), PLAN_THREADS, 0, stream, p);
     if (err != cudaSuccess) return err;
     ForkApply a{p, 1, 0};
-    // columns a CTA: as many as 32 KB of shared memory hold, but enough CTAs to spread the rows
-    a.cols = (int)(8192 / p.Z);
+    // columns a CTA: about two table entries a thread (32 KB of shared memory at most, Z <= 8192)
+    a.cols = 2 * FORK_THREADS / p.Z;
     a.cols = a.cols < 1 ? 1 : a.cols > 32 ? 32 : a.cols;
     a.table_ctas = p.M > 0 ? (p.M + a.cols - 1) / a.cols : 1;  // the first writes the lengths
-    const int64_t jobs = (int64_t)p.Z * p.L * 2;
-    const int64_t copies = p.source == nullptr ? 0 : jobs < 4 * sms ? jobs : 4 * sms;
-    return launch_dependent(fa_cache_fork_apply_kernel, a.table_ctas + copies, FORK_THREADS,
+    const int64_t jobs = ((int64_t)p.Z * p.L * 2 * p.H + FORK_THREADS / 32 - 1) / (FORK_THREADS / 32);  // at most
+    const int64_t copies = p.source == nullptr ? 0 : jobs < 8 * sms ? jobs : 8 * sms;
+    return launch_dependent(fa_cache_fork_apply_kernel, dim3((unsigned)(a.table_ctas + copies)), FORK_THREADS,
                             (size_t)p.Z * a.cols * sizeof(int), stream, a);
 }
 

@@ -21,6 +21,7 @@ struct AppendParams {
     int64_t st_z;
     const int32_t *lens, *news;     // news may be nullptr
     int Z, H, T, D, page, M, P;
+    int lanes;                      // of a token (set by the launch)
     uint32_t* status;
 };
 
@@ -46,11 +47,11 @@ struct ForkParams {
     uint32_t* status;
 };
 // per sequence: source, length after, first column to fill, columns to fill,
-// place in the page list; then the list of tails (3 each), their count and the
-// number of pages found; then the page list
+// place in the page list; the list of tails (3 each), the number of pages found
+// and of tails; the page list
 inline int64_t fork_workspace_ints(int64_t Z, int64_t M) { return 8 * Z + 2 + Z * M; }
 
-cudaError_t launch_cache_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_cache_append(AppendParams p, cudaStream_t stream);
 cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t stream);
 cudaError_t launch_cache_fork(const ForkParams& p, int sms, cudaStream_t stream);
 

@@ -332,7 +332,7 @@ fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
     fa_status st = check_cache(c, true);
     if (st != FA_OK) return st;
     if (c.Z > 8192 || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||
-        (int64_t)c.Hkv * c.page_size * (c.D / 8) > INT32_MAX)
+        (int64_t)c.L * 2 * c.Hkv > INT32_MAX || (int64_t)c.page_size * (c.D / 8) > INT32_MAX)
         return FA_ERR_UNSUPPORTED;
     if (c.Z == 0) return FA_OK;
     if ((st = check_cache_data(c, true)) != FA_OK) return st;
