@@ -21,6 +21,27 @@ enum PageSite : uint32_t {
     SITE_PAGE_FORK = 63,
 };
 
+// Division of 0 <= n < 2^31 by a positive divisor fixed for the launch, in four
+// instructions: with s = ceil(log2 d) and m = floor(2^32 (2^s - d) / d) + 1, the
+// quotient is (m n / 2^32 + n) / 2^s (Granlund and Montgomery 1994, figure 4.1).
+struct FastDiv {
+    uint32_t m = 1, s1 = 0, s2 = 0;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d) {
+        uint32_t s = 0;
+        while ((uint64_t(1) << s) < d) ++s;
+        m = (uint32_t)(((uint64_t(1) << 32) * ((uint64_t(1) << s) - d)) / d + 1);
+        s1 = s < 1 ? s : 1;
+        s2 = s > 0 ? s - 1 : 0;
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int operator()(int n) const {
+        const uint32_t t = __umulhi(m, (uint32_t)n);
+        return (int)((t + (((uint32_t)n - t) >> s1)) >> s2);
+    }
+#endif
+};
+
 // Attention over a paged cache.  Strides are in elements; the cache's are
 // (page, head, slot) with the head dim contiguous.
 struct PagedParams {
@@ -42,6 +63,7 @@ struct PagedParams {
     int words;                 // ceil(T / 32)
     int Z, Hq, Hkv, G, T;      // G = Hq / Hkv
     int page, M, P;            // slots a page, table columns, pages of the cache
+    FastDiv by_g, by_page, by_tile_rows, by_team;
     int cap;                   // M * page: positions a sequence can have
     int tile_rows;             // query rows of a tile (a row is a (token, head of the group) pair, heads innermost)
     int box_rows;              // positions a TMA box holds: gcd(page, positions a block)

@@ -250,6 +250,10 @@ fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
     // more teams than there can be blocks would find no work
     const int64_t blocks = (int64_t)Z * Hkv * cdiv(p.tiles, p.team) * cdiv(p.cap, bk);
     p.teams = (int)std::max<int64_t>(1, std::min<int64_t>(blocks, workers / p.team));
+    p.by_g = fa::FastDiv(G);
+    p.by_page = fa::FastDiv(p.page);
+    p.by_tile_rows = fa::FastDiv(p.tile_rows);
+    p.by_team = fa::FastDiv(p.team);
     p.cuts = static_cast<char*>(x.workspace) + paged_slot_bytes(D, f.sms);
     err = launch_paged(D, a, bf16);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("paged attention launch", err);

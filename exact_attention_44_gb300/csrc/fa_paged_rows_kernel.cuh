@@ -117,14 +117,14 @@ struct RowsLoader {
         const int k = j * T::KT + piece() * p.box_rows;
         there = piece() * p.box_rows < T::KT && k < g.len + g.nl;
         if (there) {
-            const int col = k / p.page;
+            const int col = p.by_page(k);
             page = ldi(p.table + (int64_t)g.z * p.st_z + col);
             slot = k - col * p.page;
         }
     }
     __device__ __forceinline__ void start(const PagedParams& p, const PagedWalk& walk, int worker) {
         w = walk;
-        more = paged_seg<T::KT>(p, w, g, worker);
+        more = paged_seg<T::KT>(p, w, g, worker, 0);
         if (more) {
             j = g.jb;
             request(p);
@@ -149,7 +149,7 @@ struct RowsLoader {
         }
         if (++j == g.je) {
             paged_next<T::KT>(p, w);
-            more = paged_seg<T::KT>(p, w, g, worker);
+            more = paged_seg<T::KT>(p, w, g, worker, 0);
             j = g.jb;
         }
         if (more) request(p);
@@ -207,11 +207,11 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, RowsTraits<D>::CTAS)
     bool ok = true;
 
     PagedSeg sg;
-    for (; ok && paged_seg<T::KT>(p, walk, sg, worker); paged_next<T::KT>(p, walk)) {
+    for (; ok && paged_seg<T::KT>(p, walk, sg, worker, 0); paged_next<T::KT>(p, walk)) {
         // Q fragments of the tile's rows (zeros past the live ones); a thread
         // holds rows lane / 4 and lane / 4 + 8
         auto q_row = [&](int r) -> const uint16_t* {
-            const int row = sg.row0 + r, t = row / p.G, h = sg.hk * p.G + row - t * p.G;
+            const int row = sg.row0 + r, t = p.by_g(row), h = sg.hk * p.G + row - t * p.G;
             return static_cast<const uint16_t*>(p.q) + (int64_t)sg.z * p.sq_z + h * p.sq_h + t * p.sq_n;
         };
         uint32_t qf[T::QREG ? KS : 1][4];
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, RowsTraits<D>::CTAS)
         for (int y = 0; y < 2; ++y) {
             m[y] = -INFINITY;
             l[y] = 0.f;
-            tok[y] = min((sg.row0 + y * 8 + lane / 4) / p.G, p.T - 1);
+            tok[y] = min(p.by_g(sg.row0 + y * 8 + lane / 4), p.T - 1);
         }
 
         for (int j = sg.jb; j < sg.je; ++j) {
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, RowsTraits<D>::CTAS)
                         make_float2(o[x][2 * y] * inv, o[x][2 * y + 1] * inv);
                 if (lane % 4 == 0) slot[p.tile_rows * D + r] = lse2;
             } else {
-                const int row = sg.row0 + r, t = row / p.G, h = sg.hk * p.G + row - t * p.G;
+                const int row = sg.row0 + r, t = p.by_g(row), h = sg.hk * p.G + row - t * p.G;
                 uint16_t* dst = static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + h * p.so_h + t * p.so_n;
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)

@@ -51,21 +51,21 @@ __device__ __forceinline__ int tile_blocks(const PagedParams& p, const SeqLen& s
     int end = s.len + s.nl;
     if (p.mask == nullptr) {
         const int last = min((mt + 1) * p.tile_rows, s.nl * p.G) - 1;
-        end = s.len + last / p.G + 1;
+        end = s.len + p.by_g(last) + 1;
     }
     return (end + BK - 1) / BK;
 }
 __device__ __forceinline__ int live_tiles(const PagedParams& p, const SeqLen& s) {
-    return (s.nl * p.G + p.tile_rows - 1) / p.tile_rows;
+    return p.by_tile_rows(s.nl * p.G + p.tile_rows - 1);
 }
 __device__ __forceinline__ int live_groups(const PagedParams& p, const SeqLen& s) {
-    return (live_tiles(p, s) + p.team - 1) / p.team;
+    return p.by_team(live_tiles(p, s) + p.team - 1);
 }
 // blocks of tile group gi: those of its last tile (a tile of a chain sees at
-// least what the one before it sees)
+// least what the one before it sees; tile_blocks stops at the live rows)
 template <int BK>
 __device__ __forceinline__ int group_blocks(const PagedParams& p, const SeqLen& s, int gi) {
-    return tile_blocks<BK>(p, s, min((gi + 1) * p.team, live_tiles(p, s)) - 1);
+    return tile_blocks<BK>(p, s, (gi + 1) * p.team - 1);
 }
 // blocks of all groups of one (sequence, kv head)
 template <int BK>
@@ -93,6 +93,7 @@ __device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
 struct PagedWalk {
     int z, hk, gi;   // tile group
     int jb;          // its first block in this range
+    int groups;      // of its sequence
     int64_t left;    // blocks left in the range
     SeqLen s;
 };
@@ -146,16 +147,16 @@ struct PagedFind {
     int z[RANGES], len[RANGES], nl[RANGES];
 };
 
-// Every thread of the CTA: where the range of team first + mine starts (RANGES
-// teams a CTA, mine the same in all threads of a warp), recorded for the merge
-// by the thread that `records`.  pads: some sequence has fewer than T new
-// tokens.
+// Where the range of team first + mine starts (RANGES teams a CTA, mine the same
+// in all threads of a warp), recorded for the merge by the thread that
+// `records`.  pads: some sequence has fewer than T new tokens.  Called by every
+// thread of the CTA; with up to 32 sequences the warps need not all call it.
 template <int BK, int RANGES>
 __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind<RANGES>* f, int first, int mine,
-                                                 bool records, bool& pads) {
+                                              bool records, bool& pads) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid % 32;
     const int c = first + mine;
-    PagedWalk w{-1, 0, 0, 0, 0, {0, 0}};
+    PagedWalk w{-1, 0, 0, 0, 0, 0, {0, 0}};
     PagedCuts cuts;
     int64_t before = 0;  // blocks before sequence w.z
     if (p.Z <= 32) {
@@ -238,6 +239,7 @@ __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind
         for (int64_t n; rem >= (n = group_blocks<BK>(p, w.s, w.gi)); ++w.gi) rem -= n;
         w.jb = (int)rem;
         w.left = cuts.start(c + 1) - cuts.start(c);
+        w.groups = live_groups(p, w.s);
     }
     if (records && c < p.teams)
         static_cast<PagedCut*>(p.cuts)[c] = PagedCut{w.z, w.hk, w.gi, w.jb, w.s.len, w.s.nl, cuts.rem, cuts.teams, cuts.q};
@@ -250,7 +252,7 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, PagedWalk& w) {
     w.left -= group_blocks<BK>(p, w.s, w.gi) - w.jb;
     w.jb = 0;
     if (w.left <= 0) return;
-    if (++w.gi < live_groups(p, w.s)) return;
+    if (++w.gi < w.groups) return;
     w.gi = 0;
     if (++w.hk < p.Hkv) return;
     w.hk = 0;
@@ -261,14 +263,15 @@ __device__ __forceinline__ void paged_next(const PagedParams& p, PagedWalk& w) {
         }
         w.s = seq_len(p, w.z);
     } while (w.s.nl == 0);
+    w.groups = live_groups(p, w.s);
 }
 
-// The next segment of a team's member at or after w's place (worker: its
-// number in the launch); false when the range is done.
+// The next segment of member `member` of a team at or after w's place (worker:
+// its number in the launch); false when the range is done.
 template <int BK>
-__device__ __forceinline__ bool paged_seg(const PagedParams& p, PagedWalk& w, PagedSeg& g, int worker) {
+__device__ __forceinline__ bool paged_seg(const PagedParams& p, PagedWalk& w, PagedSeg& g, int worker, int member) {
     for (; w.left > 0; paged_next<BK>(p, w)) {
-        const int mt = w.gi * p.team + worker % p.team;
+        const int mt = w.gi * p.team + member;
         g.row0 = mt * p.tile_rows;
         g.rows = min(p.tile_rows, w.s.nl * p.G - g.row0);
         if (g.rows <= 0) continue;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             acc.w += __shfl_xor_sync(0xffffffffu, acc.w, k);
         }
         if (!ok || sl != 0) continue;
-        const int row = row0 + r, t = row / p.G, h = hk * p.G + row - t * p.G;
+        const int row = row0 + r, t = p.by_g(row), h = hk * p.G + row - t * p.G;
         const float inv = den == 0.f ? 0.f : 1.f / den;  // (a NaN score reaches O)
         uint2 out;
         out.x = pack_pair<BF16>(acc.x * inv, acc.y * inv);

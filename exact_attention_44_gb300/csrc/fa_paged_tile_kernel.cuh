@@ -19,6 +19,8 @@
 // barriers' counts.  Every wait is bounded as in fa_fwd_kernel.cuh.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_fwd_kernel.cuh"
 #include "fa_paged_sched.cuh"
 
@@ -28,13 +30,62 @@ template <int D_>
 struct TileTraits : Traits<D_> {
     using Base = Traits<D_>;
     static constexpr int B_VFIX = Base::NUM_BARS;             // [2] V slot's rows behind the end zeroed
-    static constexpr int NUM_BARS = B_VFIX + 2;
+    static constexpr int SEGS = 4;                            // segments in the ring
+    static constexpr int B_SEGFULL = B_VFIX + 2;              // [SEGS] segment written (K producer)
+    static constexpr int B_SEGFREE = B_SEGFULL + SEGS;        // [SEGS] read by every other warp
+    static constexpr int NUM_BARS = B_SEGFREE + SEGS;
     static constexpr int OFF_MISC = Base::OFF_BAR + NUM_BARS * 8;
-    static constexpr int SMEM_USED = OFF_MISC + 16;
+    static constexpr int OFF_SEG = OFF_MISC + 16;
+    static constexpr int SEG_END = OFF_SEG + SEGS * 48;
+    // staging of the epilogue: 32 rows x 128 bytes a warp
+    static constexpr int OFF_STAGE = D_ >= 64 ? Base::OFF_OST : (SEG_END + 15) / 16 * 16;
+    static constexpr int SMEM_USED = D_ >= 64 ? SEG_END : OFF_STAGE + 4 * 4096;
     static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static __device__ __forceinline__ uint32_t bar_count(int i) {
+        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return Base::THREADS / 32 - 1;
+        if (i >= B_VFIX) return 1;
+        return Base::bar_count(i);
+    }
     static_assert((int)sizeof(PagedFind<1>) <= 2 * Base::HAND_ROWS * BM * 4, "the range search fits the hand-over area");
 };
+
+// The K producer's warp walks the range and hands the segments to the other
+// warps through a ring in shared memory, a few ahead of them.  (Every role
+// walking by itself cost registers -- 0.99 against 0.81 us a block in the
+// softmax loop -- and 24 warps doing the same arithmetic at the start of every
+// segment got in each other's way.)
+struct SegMsg {
+    int z, hk, jb, je, slot, len, nl, row0, rows, pad[3];  // je = 0: the end
+};
+template <int D, typename Bar>
+__device__ __forceinline__ void seg_put(volatile int* ring, const PagedSeg& g, bool have, uint32_t n, Bar bar) {
+    using T = TileTraits<D>;
+    volatile int* s = ring + (n % T::SEGS) * (sizeof(SegMsg) / 4);
+    if (threadIdx.x % 32 == 0) {
+        s[0] = g.z, s[1] = g.hk, s[2] = g.jb, s[3] = have ? g.je : 0, s[4] = g.slot;
+        s[5] = g.len, s[6] = g.nl, s[7] = g.row0, s[8] = g.rows;
+        ptx::mbar_arrive(bar(T::B_SEGFULL + n % T::SEGS));
+    }
+    __syncwarp();
+}
+// Segment n of the ring; ok: false when the wait ran out or another role gave
+// up.  Returns false at the end of the range.  WARP: the whole warp calls, else
+// its one active lane.
+template <int D, bool WARP, typename Bar>
+__device__ __forceinline__ bool seg_get(volatile const int* ring, PagedSeg& g, uint32_t n, Bar bar, const Ctl& ctl,
+                                        bool& ok) {
+    using T = TileTraits<D>;
+    const uint32_t full = bar(T::B_SEGFULL + n % T::SEGS), parity = (n / T::SEGS) & 1u;
+    ok = WARP ? warp_wait_phase(full, parity, ctl, SITE_SEG_FULL) : wait_phase(full, parity, ctl, SITE_SEG_FULL);
+    if (!ok) return false;
+    volatile const int* s = ring + (n % T::SEGS) * (sizeof(SegMsg) / 4);
+    g.z = s[0], g.hk = s[1], g.jb = s[2], g.je = s[3], g.slot = s[4];
+    g.len = s[5], g.nl = s[6], g.row0 = s[7], g.rows = s[8];
+    if (WARP) __syncwarp();
+    if (!WARP || threadIdx.x % 32 == 0) ptx::mbar_arrive(bar(T::B_SEGFREE + n % T::SEGS));
+    return g.je > 0;
+}
 
 // A block's boxes: lane b of the producer warp has the box of positions
 // kj * BN + b * rb .. (b * rb < BN), if the sequence has any of them.
@@ -47,7 +98,7 @@ __device__ __forceinline__ PageBox page_box(const PagedParams& p, const int32_t*
     PageBox b{p.P, 0, false};
     const int k = k0 + lane * rb;
     if (lane * rb < bn && k < end) {
-        const int col = k / p.page;
+        const int col = p.by_page(k);
         b.slot = k - col * p.page;
         b.page = ldi(row + col);
         b.there = true;
@@ -74,11 +125,13 @@ __device__ __forceinline__ void load_boxes(const PagedParams& p, PageBox b, cons
 
 template <int D>
 __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK, const PagedParams& p, PagedWalk w,
-                                 uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
+                                 volatile int* ring, uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int lane = threadIdx.x % 32;
-    const uint64_t pol_q = ptx::policy_evict_first(), pol_kv = ptx::policy_evict_last();
+    // K and V pass once (the members of a team read them at the same time) unless there are more groups
+    const uint64_t pol_q = ptx::policy_evict_first();
+    const uint64_t pol_kv = p.tiles > p.team ? ptx::policy_evict_last() : ptx::policy_evict_first();
     uint32_t qi = 0, ki = 0;
     bool ok = true, withheld = false;
     auto load_q = [&](const PagedSeg& sg) -> bool {
@@ -89,42 +142,56 @@ __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK,
             const uint32_t dst = sbase + T::OFF_Q + s * T::Q_BYTES;
             for (int c = 0; c < T::NCHUNK; ++c)
                 ptx::tma_load_4d(dst + c * (BM * T::SW), tmQ, bar(T::B_QFULL + s), c * T::SWE, sg.hk * p.G,
-                                 sg.row0 / p.G, sg.z, pol_q);
+                                 p.by_g(sg.row0), sg.z, pol_q);
         }
         __syncwarp();
         ++qi;
         return true;
     };
-    PagedSeg sg{}, nx{};
-    bool have = paged_seg<T::BN>(p, w, sg, (int)blockIdx.x);
-    if (have) ok = load_q(sg);
+    uint32_t nseg = 0;  // segments put into the ring
+    auto put = [&](const PagedSeg& sg, bool have) -> bool {
+        const uint32_t slot = nseg % T::SEGS;
+        if (nseg >= (uint32_t)T::SEGS &&
+            !warp_wait_phase(bar(T::B_SEGFREE + slot), (nseg / T::SEGS - 1) & 1u, ctl, SITE_SEG_FREE)) return false;
+        seg_put<D>(ring, sg, have, nseg, bar);
+        ++nseg;
+        return true;
+    };
+    const int member = (int)blockIdx.x - (int)(blockIdx.x / p.team) * p.team;
+    PagedSeg sg{};
+    bool have = paged_seg<T::BN>(p, w, sg, (int)blockIdx.x, member);
+    ok = put(sg, have);
+    bool first = true;
     while (ok && have) {
-        paged_next<T::BN>(p, w);
-        have = paged_seg<T::BN>(p, w, nx, (int)blockIdx.x);
+        const int jb = sg.jb, je = sg.je, hk = sg.hk, end = sg.len + sg.nl;
         const int32_t* row = p.table + (int64_t)sg.z * p.st_z;
-        const int end = sg.len + sg.nl;
-        PageBox b = page_box(p, row, sg.jb * T::BN, p.box_rows, T::BN, end, lane);
-        for (int j = sg.jb; j < sg.je; ++j) {
+        PageBox b = page_box(p, row, jb * T::BN, p.box_rows, T::BN, end, lane);
+        // the first tile's Q goes while its first table entries are on their way
+        if (first && !load_q(sg)) { ok = false; break; }
+        first = false;
+        for (int j = jb; j < je; ++j) {
             PageBox after = b;
-            if (j + 1 < sg.je) after = page_box(p, row, (j + 1) * T::BN, p.box_rows, T::BN, end, lane);
+            if (j + 1 < je) after = page_box(p, row, (j + 1) * T::BN, p.box_rows, T::BN, end, lane);
             const uint32_t s = ki & 1u;
             if (ki >= 2 && !warp_wait_phase(bar(T::B_SFULL + rslot<T::SR>(ki - 2)), rphase<T::SR>(ki - 2), ctl,
                                             SITE_K_EMPTY)) { ok = false; break; }
             if (p.inject_stall && blockIdx.x == 0 && !withheld) {
                 withheld = true;  // never issued: the S issuer's wait for this block must time out
             } else {
-                load_boxes<D>(p, b, tmK, sbase + T::OFF_K + s * T::KV_BYTES, bar(T::B_KFULL + s), sg.hk, p.box_rows,
+                load_boxes<D>(p, b, tmK, sbase + T::OFF_K + s * T::KV_BYTES, bar(T::B_KFULL + s), hk, p.box_rows,
                               lane, pol_kv);
             }
             ++ki;
             b = after;
-            const int q_at = T::Q_STAGES >= 2 ? sg.jb : sg.je - 1;
-            if (j == q_at && have && !load_q(nx)) {
-                ok = false;
-                break;
+            // the next segment, after the first K; its Q then if there are two Q slots,
+            // else after the last K
+            if (j == jb) {
+                paged_next<T::BN>(p, w);
+                have = paged_seg<T::BN>(p, w, sg, (int)blockIdx.x, member);
+                if (!put(sg, have)) { ok = false; break; }
             }
+            if (j == (T::Q_STAGES >= 2 ? jb : je - 1) && have && !load_q(sg)) { ok = false; break; }
         }
-        sg = nx;
     }
     if (!ok) {
         const uint64_t lim = ctl.limit_ns;
@@ -136,27 +203,32 @@ __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK,
 }
 
 template <int D>
-__device__ void tile_producer_v(const CUtensorMap* tmV, const PagedParams& p, PagedWalk w, uint32_t sbase,
+__device__ void tile_producer_v(const CUtensorMap* tmV, const PagedParams& p, volatile int* ring, uint32_t sbase,
                                 uint32_t bar0, const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int lane = threadIdx.x % 32;
-    const uint64_t pol_kv = ptx::policy_evict_last();
+    const uint64_t pol_kv = p.tiles > p.team ? ptx::policy_evict_last() : ptx::policy_evict_first();
     uint32_t vi = 0;
     bool ok = true;
-    PagedSeg sg;
-    for (; ok && paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w)) {
-        const int32_t* row = p.table + (int64_t)sg.z * p.st_z;
-        const int end = sg.len + sg.nl;
-        PageBox b = page_box(p, row, sg.jb * T::BN, p.box_rows, T::BN, end, lane);
-        for (int j = sg.jb; j < sg.je; ++j) {
+    for (uint32_t n = 0;; ++n) {
+        int jb, je, hk, end;
+        const int32_t* row;
+        {
+            PagedSeg sg;
+            if (!ok || !seg_get<D, true>(ring, sg, n, bar, ctl, ok)) break;
+            jb = sg.jb, je = sg.je, hk = sg.hk, end = sg.len + sg.nl;
+            row = p.table + (int64_t)sg.z * p.st_z;
+        }
+        PageBox b = page_box(p, row, jb * T::BN, p.box_rows, T::BN, end, lane);
+        for (int j = jb; j < je; ++j) {
             PageBox after = b;
-            if (j + 1 < sg.je) after = page_box(p, row, (j + 1) * T::BN, p.box_rows, T::BN, end, lane);
+            if (j + 1 < je) after = page_box(p, row, (j + 1) * T::BN, p.box_rows, T::BN, end, lane);
             const uint32_t s = vi & 1u;
             if (vi >= 2 && !warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(vi - 2)), rphase<T::SR>(vi - 2), ctl,
                                             SITE_V_EMPTY)) { ok = false; break; }
             const uint32_t dst = sbase + T::OFF_V + s * T::KV_BYTES;
-            load_boxes<D>(p, b, tmV, dst, bar(T::B_VFULL + s), sg.hk, p.box_rows, lane, pol_kv);
+            load_boxes<D>(p, b, tmV, dst, bar(T::B_VFULL + s), hk, p.box_rows, lane, pol_kv);
             ++vi;
             b = after;
             if ((j + 1) * T::BN > end) {
@@ -179,7 +251,7 @@ __device__ void tile_producer_v(const CUtensorMap* tmV, const PagedParams& p, Pa
 }
 
 template <int D, bool BF16>
-__device__ void tile_mma_qk(const PagedParams& p, PagedWalk w, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+__device__ void tile_mma_qk(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
                             const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -189,12 +261,17 @@ __device__ void tile_mma_qk(const PagedParams& p, PagedWalk w, uint32_t sbase, u
     const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16);
     uint32_t qi = 0, g = 0;
     bool ok = true;
-    PagedSeg sg;
-    for (; ok && paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w)) {
+    for (uint32_t n = 0;; ++n) {
+        int jb, je;
+        {
+            PagedSeg sg;
+            if (!ok || !seg_get<D, false>(ring, sg, n, bar, ctl, ok)) break;
+            jb = sg.jb, je = sg.je;
+        }
         const uint32_t qs = qi % T::Q_STAGES;
         if (!wait_phase(bar(T::B_QFULL + qs), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
         const uint32_t q_lo = q_lo0 + qs * (T::Q_BYTES >> 4);
-        for (int j = sg.jb; j < sg.je; ++j, ++g) {
+        for (int j = jb; j < je; ++j, ++g) {
             const uint32_t kb = g & 1u, r = rslot<T::SR>(g);
             if (!wait_phase(bar(T::B_KFULL + kb), (g >> 1) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
             if (g >= (uint32_t)T::SR && !wait_phase(bar(T::B_PVDONE + r), rphase<T::SR>(g - T::SR), ctl, SITE_S_FREE)) {
@@ -212,7 +289,7 @@ __device__ void tile_mma_qk(const PagedParams& p, PagedWalk w, uint32_t sbase, u
                             kk > 0 ? 1u : 0u);
             }
             ptx::tc_commit(bar(T::B_SFULL + r));
-            if (j == sg.je - 1) {
+            if (j == je - 1) {
                 ptx::tc_commit(bar(T::B_QEMPTY + qs));
                 ++qi;
             }
@@ -225,7 +302,7 @@ __device__ void tile_mma_qk(const PagedParams& p, PagedWalk w, uint32_t sbase, u
 }
 
 template <int D, bool BF16>
-__device__ void tile_mma_pv(const PagedParams& p, PagedWalk w, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+__device__ void tile_mma_pv(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
                             const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -234,22 +311,27 @@ __device__ void tile_mma_pv(const PagedParams& p, PagedWalk w, uint32_t sbase, u
     const uint32_t v_lo0 = ptx::smem_desc_lo(sbase + T::OFF_V, T::BN * T::SW);
     uint32_t g = 0, ntile = 0, fixes[2] = {0, 0};
     bool ok = true;
-    PagedSeg sg;
-    for (; ok && paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w), ++ntile) {
-        for (int j = sg.jb; j < sg.je; ++j, ++g) {
+    for (;; ++ntile) {
+        int jb, je, end;
+        {
+            PagedSeg sg;
+            if (!ok || !seg_get<D, false>(ring, sg, ntile, bar, ctl, ok)) break;
+            jb = sg.jb, je = sg.je, end = sg.len + sg.nl;
+        }
+        for (int j = jb; j < je; ++j, ++g) {
             const uint32_t vb = g & 1u, r = rslot<T::SR>(g);
-            if (j == sg.jb && ntile > 0 &&
+            if (j == jb && ntile > 0 &&
                 !wait_phase(bar(T::B_OFREE), (ntile - 1) & 1u, ctl, SITE_O_FREE)) { ok = false; break; }
             if (!wait_phase(bar(T::B_PFULL + r), rphase<T::SR>(g), ctl, SITE_P_FULL)) { ok = false; break; }
             if (!wait_phase(bar(T::B_VFULL + vb), (g >> 1) & 1u, ctl, SITE_V_FULL)) { ok = false; break; }
-            if ((j + 1) * T::BN > sg.len + sg.nl) {
+            if ((j + 1) * T::BN > end) {
                 const uint32_t n = vb == 0 ? fixes[0]++ : fixes[1]++;
                 if (!wait_phase(bar(T::B_VFIX + vb), n & 1u, ctl, SITE_V_FULL)) { ok = false; break; }
             }
             ptx::tc_fence_after();
             const uint32_t v_lo = v_lo0 + vb * (T::KV_BYTES >> 4);
             const uint32_t a_tmem = tmem + T::TM_S + r * T::BN;
-            const uint32_t acc0 = j > sg.jb ? 1u : 0u;
+            const uint32_t acc0 = j > jb ? 1u : 0u;
 #pragma unroll
             for (int kk = 0; kk < T::BN / 16; ++kk)
                 ptx::mma_ts(tmem + T::TM_O, a_tmem + kk * 8, ptx::desc64(v_lo + ((kk * 16 * T::SW) >> 4), HI), IDESC,
@@ -263,22 +345,10 @@ __device__ void tile_mma_pv(const PagedParams& p, PagedWalk w, uint32_t sbase, u
     }
 }
 
-// A walk in shared memory, for the warp that owns it.
-__device__ __forceinline__ PagedWalk walk_load(volatile const int* s) {
-    PagedWalk w;
-    w.z = s[0], w.hk = s[1], w.gi = s[2], w.jb = s[3];
-    w.left = (int64_t)(((uint64_t)(uint32_t)s[5] << 32) | (uint32_t)s[4]);
-    w.s = SeqLen{s[6], s[7]};
-    return w;
-}
-__device__ __forceinline__ void walk_store(volatile int* s, const PagedWalk& w) {
-    __syncwarp();
-    if (threadIdx.x % 32 == 0) {
-        s[0] = w.z, s[1] = w.hk, s[2] = w.gi, s[3] = w.jb;
-        s[4] = (int)(uint32_t)w.left, s[5] = (int)(uint32_t)((uint64_t)w.left >> 32);
-        s[6] = w.s.len, s[7] = w.s.nl;
-    }
-    __syncwarp();
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
 }
 
 // Which of positions k0 .. k0 + 31 new token t sees, as bits (row: its mask words, or nullptr).
@@ -300,7 +370,7 @@ __device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int len, int
 }
 
 template <int D, bool BF16>
-__device__ void tile_softmax(const PagedParams& p, volatile int* ws, uint32_t bar0, uint32_t tmem, float* hand, float* red,
+__device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t bar0, uint32_t tmem, float* hand, float* red,
                              int h, const Ctl& ctl) {
     using T = TileTraits<D>;
     constexpr int BN = T::BN, NG = T::NG, HC = BN / NG;
@@ -313,22 +383,17 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ws, uint32_t ba
     const uint64_t c2 = ptx::pack_f32x2(c, c);
     uint32_t step = 0, ntile = 0;
     for (;; ++ntile) {
-        // What the blocks need of the segment.  The walk itself stays in shared
-        // memory between segments: kept in registers it cost the loop below 20 %
-        // (0.99 against 0.81 us a block).
         int jb, je, len, nl, tok;
         bool idle;
         const uint32_t* bits_row;
         {
-            PagedWalk w = walk_load(ws);
             PagedSeg sg;
-            if (!paged_seg<BN>(p, w, sg, (int)blockIdx.x)) return;
+            bool ok;
+            if (!seg_get<D, true>(ring, sg, ntile, bar, ctl, ok)) return;
             jb = sg.jb, je = sg.je, len = sg.len, nl = sg.nl;
-            tok = min((sg.row0 + row) / p.G, p.T - 1);
+            tok = min(p.by_g(sg.row0 + row), p.T - 1);
             idle = quad * 32 >= sg.rows;  // none of the warp's rows holds a token
             bits_row = p.mask == nullptr ? nullptr : p.mask + sg.z * p.sm_z + (int64_t)tok * p.words;
-            paged_next<BN>(p, w);
-            walk_store(ws, w);
         }
         const int masked = len / BN;  // first block that holds a new token, or ends behind the sequence
         float m = -INFINITY, l = 0.f;
@@ -428,17 +493,20 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ws, uint32_t ba
 }
 
 template <int D, bool BF16>
-__device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, uint32_t tmem, const float* hand,
-                              bool pads, const Ctl& ctl) {
+__device__ void tile_epilogue(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+                              const float* hand, bool pads, const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int quad = (threadIdx.x / 32) % 4;
     const int row = quad * 32 + threadIdx.x % 32;
+    const int lane = threadIdx.x % 32;
     const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O;
+    const uint32_t stage = sbase + T::OFF_STAGE + (uint32_t)quad * 4096u;
     uint32_t step = 0, ntile = 0;
-    constexpr int CH = D >= 32 ? 32 : 16;
+    constexpr int CH = 16;  // columns a TMEM load
     PagedSeg sg;
-    for (; paged_seg<T::BN>(p, w, sg, (int)blockIdx.x); paged_next<T::BN>(p, w), ++ntile) {
+    bool ok;
+    for (; seg_get<D, true>(ring, sg, ntile, bar, ctl, ok); ++ntile) {
         step += sg.je - sg.jb;
         const uint32_t slot = ntile & 1u;
         if (!warp_wait_phase(bar(T::B_EPIFULL + slot), (ntile >> 1) & 1u, ctl, SITE_EPI_FULL)) return;
@@ -450,55 +518,78 @@ __device__ void tile_epilogue(const PagedParams& p, PagedWalk w, uint32_t bar0, 
         const uint32_t g = step - 1;
         if (!warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(g)), rphase<T::SR>(g), ctl, SITE_PV_DONE)) return;
         ptx::tc_fence_after();
-        const bool keep = row < sg.rows;
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
         const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        if (sg.slot >= 0) {
-            // a part: rows of O / l, then the base-2 log-sum-exps
-            float* part = p.scratch + (int64_t)sg.slot * p.slot_floats;
-            float4* mine = reinterpret_cast<float4*>(part + row * D);
-#pragma unroll 1
-            for (int i = 0; i < D / CH; ++i) {
+        // The warp's rows go out through its 4 KB of staging, 128 bytes of a row at
+        // a time: a thread fills its row's pieces (permuted against bank conflicts),
+        // then eight lanes write a row, so that a store instruction touches four
+        // lines instead of 32 (which took 2.5 us for a part of 128 rows).
+        const bool part = sg.slot >= 0;
+        float* slot_base = p.scratch + (int64_t)max(sg.slot, 0) * p.slot_floats;
+        if (row < sg.rows) {
+            const int grow = sg.row0 + row, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
+            if (part) slot_base[p.tile_rows * D + row] = lse2;
+            else if (p.lse != nullptr) p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
+        }
+        // where this lane writes: row 4 i + lane / 8 of the warp's, piece lane % 8
+        const int lr = lane / 8, lp = lane % 8;
+        auto out_row = [&](int i) -> uint8_t* {
+            const int r = quad * 32 + 4 * i + lr;
+            if (r >= sg.rows) return nullptr;
+            if (part) return reinterpret_cast<uint8_t*>(slot_base + (int64_t)r * D);
+            const int grow = sg.row0 + r, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
+            return reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h +
+                                              t * p.so_n);
+        };
+        // columns a round: 128 bytes of fp32 or of the output type (less for D < 64, 32)
+        auto round = [&](auto c_tag, int c0, bool last) {
+            constexpr int C = decltype(c_tag)::value;     // columns of this round
+            uint32_t w[32];
+            const int pieces = part ? C / 4 : C / 8;
+#pragma unroll
+            for (int i = 0; i < C / CH; ++i) {
                 uint32_t r[CH];
-                if constexpr (CH == 32) ptx::tmem_ld32(o_addr + i * CH, r);
-                else ptx::tmem_ld16(o_addr + i * CH, r);
-                if (keep) {
+                ptx::tmem_ld16(o_addr + c0 + i * CH, r);
+                if (part) {
 #pragma unroll
-                    for (int x = 0; x < CH / 4; ++x)
-                        mine[i * (CH / 4) + x] =
-                            make_float4(__uint_as_float(r[4 * x]) * inv, __uint_as_float(r[4 * x + 1]) * inv,
-                                        __uint_as_float(r[4 * x + 2]) * inv, __uint_as_float(r[4 * x + 3]) * inv);
+                    for (int x = 0; x < CH; ++x)
+                        if (i * CH + x < 32) w[i * CH + x] = __float_as_uint(__uint_as_float(r[x]) * inv);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < CH / 2; ++x)
+                        w[i * (CH / 2) + x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
                 }
             }
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(bar(T::B_OFREE));
-            if (keep) part[p.tile_rows * D + row] = lse2;
-            continue;
-        }
-        const int grow = sg.row0 + row, t = grow / p.G, hq = sg.hk * p.G + grow - t * p.G;
-        uint16_t* orow = static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h + t * p.so_n;
+            if (last) {
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(bar(T::B_OFREE));
+            }
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (x < pieces)
+                    ptx::st_shared_v4(stage + lane * 128 + ((x ^ (lane & 7)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+            __syncwarp();
+            const int bytes0 = part ? c0 * 4 : c0 * 2;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint8_t* dst = out_row(i);
+                const int r = 4 * i + lr;
+                if (dst != nullptr && lp < pieces)
+                    *reinterpret_cast<uint4*>(dst + bytes0 + lp * 16) = ld_shared_v4(stage + r * 128 + ((lp ^ (r & 7)) << 4));
+            }
+        };
+        if (part) {
+            constexpr int C = D < 32 ? D : 32;
 #pragma unroll 1
-        for (int i = 0; i < D / CH; ++i) {
-            uint32_t r[CH];
-            if constexpr (CH == 32) ptx::tmem_ld32(o_addr + i * CH, r);
-            else ptx::tmem_ld16(o_addr + i * CH, r);
-            if (keep) {
-#pragma unroll
-                for (int x = 0; x < CH / 8; ++x) {
-                    uint4 v;
-                    v.x = pack2<BF16>(__uint_as_float(r[8 * x]) * inv, __uint_as_float(r[8 * x + 1]) * inv);
-                    v.y = pack2<BF16>(__uint_as_float(r[8 * x + 2]) * inv, __uint_as_float(r[8 * x + 3]) * inv);
-                    v.z = pack2<BF16>(__uint_as_float(r[8 * x + 4]) * inv, __uint_as_float(r[8 * x + 5]) * inv);
-                    v.w = pack2<BF16>(__uint_as_float(r[8 * x + 6]) * inv, __uint_as_float(r[8 * x + 7]) * inv);
-                    *reinterpret_cast<uint4*>(orow + i * CH + 8 * x) = v;
-                }
-            }
+            for (int c0 = 0; c0 < D; c0 += C) round(std::integral_constant<int, C>{}, c0, c0 + C == D);
+        } else {
+            constexpr int C = D < 64 ? D : 64;
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += C) round(std::integral_constant<int, C>{}, c0, c0 + C == D);
         }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(bar(T::B_OFREE));
-        if (keep && p.lse != nullptr) p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
     }
-    if (pads) paged_fill<D>(p, (int)blockIdx.x * 4 + quad, (int)gridDim.x * 4);
+    if (ok && pads) paged_fill<D>(p, (int)blockIdx.x * 4 + quad, (int)gridDim.x * 4);
 }
 
 template <int D, bool BF16>
@@ -537,27 +628,29 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     const Ctl ctl{abort_flag, p.status, p.wait_limit_ns};
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    PagedFind<1>* find = reinterpret_cast<PagedFind<1>*>(hand);
-    bool pads;
-    const PagedWalk walk = paged_range<T::BN, 1>(p, find, (int)blockIdx.x / p.team, 0,
-                                                 threadIdx.x == 0 && blockIdx.x % p.team == 0, pads);
-    __syncthreads();  // (the search's area is the hand-over area of the roles)
+    volatile int* ring = reinterpret_cast<volatile int*>(smem + T::OFF_SEG);
+    PagedWalk walk{};
+    bool pads = false;
+    // With few sequences the K producer's warp finds the range by itself; else
+    // the CTA together.  (The search's area is the roles' hand-over area.)
+    if (p.Z > 32 || warp == 0 || warp > 3 + 4 * T::NG)
+        walk = paged_range<T::BN, 1>(p, reinterpret_cast<PagedFind<1>*>(hand), (int)blockIdx.x / p.team, 0,
+                                     threadIdx.x == 0 && blockIdx.x % p.team == 0, pads);
+    if (p.Z > 32) __syncthreads();
 
     constexpr int SOFTMAX_END = 4 + 4 * T::NG;
     if (warp == 0) {
-        tile_producer_qk<D>(&tmQ, &tmK, p, walk, sbase, bar0, ctl);
+        tile_producer_qk<D>(&tmQ, &tmK, p, walk, ring, sbase, bar0, ctl);
     } else if (warp == 3) {
-        tile_producer_v<D>(&tmV, p, walk, sbase, bar0, ctl);
+        tile_producer_v<D>(&tmV, p, ring, sbase, bar0, ctl);
     } else if (warp == 1) {
-        if (lane == 0) tile_mma_qk<D, BF16>(p, walk, sbase, bar0, tmem, ctl);
+        if (lane == 0) tile_mma_qk<D, BF16>(p, ring, sbase, bar0, tmem, ctl);
     } else if (warp == 2) {
-        if (lane == 0) tile_mma_pv<D, BF16>(p, walk, sbase, bar0, tmem, ctl);
+        if (lane == 0) tile_mma_pv<D, BF16>(p, ring, sbase, bar0, tmem, ctl);
     } else if (warp < SOFTMAX_END) {
-        volatile int* ws = reinterpret_cast<volatile int*>(smem + T::OFF_OST) + warp * 8;  // (no O staging here)
-        walk_store(ws, walk);
-        tile_softmax<D, BF16>(p, ws, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
+        tile_softmax<D, BF16>(p, ring, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
     } else {
-        tile_epilogue<D, BF16>(p, walk, bar0, tmem, hand, pads, ctl);
+        tile_epilogue<D, BF16>(p, ring, sbase, bar0, tmem, hand, pads, ctl);
     }
 
     ptx::tc_fence_before();

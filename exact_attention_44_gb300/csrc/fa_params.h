@@ -33,6 +33,8 @@ enum WaitSite : uint32_t {
     SITE_PEER_K = 17,
     SITE_PEER_V = 18,
     SITE_DRAIN = 19,
+    SITE_SEG_FULL = 50,     // paged tile kernel: the ring of segments
+    SITE_SEG_FREE = 51,
     // backward
     SITE_B_KV_FULL = 20,
     SITE_B_KV_EMPTY = 21,
