@@ -348,27 +348,42 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int tid = threadIdx.x;
-    const int per_cut = p.team * sub;
-    const int b = 1 + (int)blockIdx.x / per_cut, in = (int)blockIdx.x % per_cut, member = in / sub;
-    const int4* rec = reinterpret_cast<const int4*>(static_cast<const PagedCut*>(p.cuts) + b);
-    const int4 cut = __ldcg(rec), more = __ldcg(rec + 1);
-    const PagedCuts cuts{__ldcg(reinterpret_cast<const long long*>(rec + 2)), more.z, more.w};
-    if (cut.x < 0 || cut.w == 0) return;  // no such range, or it starts with a tile
-    const int z = cut.x, hk = cut.y, mt = cut.z * p.team + member;
-    const SeqLen s{more.x, more.y};
-    const int row0 = mt * p.tile_rows;
-    const int live = min(p.tile_rows, s.nl * p.G - row0);
-    if (live <= 0) return;
-    const int64_t t0 = cuts.start(b) - cut.w, t1 = t0 + tile_blocks<BK>(p, s, mt) - 1;
-    const int c0 = cuts.team_of(t0), c1 = cuts.team_of(t1);
-    if (b > c1) return;  // the cut is behind this tile's last block
-    const int parts = c1 - c0 + 1, shares = (c1 - c0) * sub, share = (live * W + shares - 1) / shares;
-    const int first = ((b - 1 - c0) * sub + in % sub) * share, last = min(first + share, live * W);
+    const int member = (int)(blockIdx.x / sub) % p.team;
+    // One warp works out the block's share for all (the arithmetic in every warp took
+    // longer than the loads): {first and last item, parts, z, kv head, row0, first slot}.
+    __shared__ int what[8];
+    if (tid < 32) {
+        const int b = 1 + (int)blockIdx.x / (p.team * sub);
+        const int4* rec = reinterpret_cast<const int4*>(static_cast<const PagedCut*>(p.cuts) + b);
+        const int4 cut = __ldcg(rec), more = __ldcg(rec + 1);
+        const PagedCuts cuts{__ldcg(reinterpret_cast<const long long*>(rec + 2)), more.z, more.w};
+        int first = 0, last = 0, parts = 0, c0 = 0;
+        const int mt = cut.z * p.team + member, row0 = mt * p.tile_rows;
+        const SeqLen s{more.x, more.y};
+        const int live = cut.x < 0 ? 0 : min(p.tile_rows, s.nl * p.G - row0);
+        if (live > 0 && cut.w > 0) {  // there is such a range, and it does not start with a tile
+            const int64_t t0 = cuts.start(b) - cut.w, t1 = t0 + tile_blocks<BK>(p, s, mt) - 1;
+            c0 = cuts.team_of(t0);
+            const int c1 = cuts.team_of(t1);
+            if (b <= c1) {  // (else the cut is behind this tile's last block)
+                parts = c1 - c0 + 1;
+                const int shares = (c1 - c0) * sub, share = (live * W + shares - 1) / shares;
+                first = ((b - 1 - c0) * sub + (int)blockIdx.x % sub) * share;
+                last = min(first + share, live * W);
+            }
+        }
+        if (tid == 0) {
+            what[0] = first, what[1] = last, what[2] = parts, what[3] = cut.x, what[4] = cut.y, what[5] = row0;
+            what[6] = 2 * (c0 * p.team + member);
+        }
+    }
+    __syncthreads();
+    const int first = what[0], last = what[1], parts = what[2];
     if (first >= last) return;
-    auto slot = [&](int i) -> const float* {
-        const int worker = (c0 + i) * p.team + member;
-        return p.scratch + (int64_t)(i == 0 ? 2 * worker + 1 : 2 * worker) * p.slot_floats;
-    };
+    const int z = what[3], hk = what[4], row0 = what[5];
+    // the first part is in slot 2 c + 1 of its worker, the others in slots 2 c
+    const float* base = p.scratch + (int64_t)what[6] * p.slot_floats;
+    auto slot = [&](int i) { return base + (i == 0 ? p.slot_floats : (int64_t)i * 2 * p.team * p.slot_floats); };
     int spl = 1;
     while (spl < 32 && spl < parts && (last - first) * spl * 2 <= NT) spl *= 2;
     const int sl = tid % spl;
@@ -395,13 +410,13 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             float top = mx;
 #pragma unroll
             for (int u = 0; u < U; ++u) top = fmaxf(top, l[u]);
-            const float a = mx == -INFINITY ? 0.f : exp2f(mx - top);
+            const float a = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
             mx = top;
             den *= a;
             acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float w = l[u] == -INFINITY ? 0.f : exp2f(l[u] - top);
+                const float w = l[u] == -INFINITY ? 0.f : ptx::ex2(l[u] - top);
                 den += w;
                 acc.x += w * v[u].x;
                 acc.y += w * v[u].y;
@@ -411,7 +426,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
         }
         for (int k = spl / 2; k > 0; k /= 2) {
             const float other = __shfl_xor_sync(0xffffffffu, mx, k), top = fmaxf(mx, other);
-            const float a = mx == -INFINITY ? 0.f : exp2f(mx - top);
+            const float a = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
             mx = top;
             den *= a;
             acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
