@@ -6,17 +6,21 @@ Objects and the shared library go to exact_attention_44_gb300/_build/ (git
 ignored).  A content hash of the sources, headers and flags is stored next to
 the library; an unchanged tree is not rebuilt.  --debug-checks builds a
 second library, _build/checks/libfa.so, whose forward kernels check every
-unit they decode against the launch's sizes (FA_DEBUG_CHECKS=1).
+unit they decode against the launch's sizes (FA_DEBUG_CHECKS=1).  Where torch
+is installed, the binding of the paged-cache calls (_paged_ext.so, a CPython
+extension over torch's headers) is built beside libfa.so with g++.
 """
 from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -24,6 +28,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libfa.so")
+EXT = os.path.join(BUILD, "_paged_ext.so")
 
 # (source, object, extra flags): the per-head-dim launchers are one source
 # each, compiled once per supported head dim
@@ -50,11 +55,25 @@ def _tree_hash(extra_flags: list[str]) -> str:
     h = hashlib.sha256()
     for d in (CSRC, INCLUDE):
         for name in sorted(os.listdir(d)):
-            if name.endswith((".cu", ".cuh", ".h")):
+            if name.endswith((".cu", ".cuh", ".h", ".cpp")):
                 with open(os.path.join(d, name), "rb") as f:
                     h.update(name.encode() + b"\0" + f.read())
     h.update(" ".join(FLAGS + extra_flags).encode())
     return h.hexdigest()
+
+
+def _ext_command(cc: str, out: str) -> list[str] | None:
+    """The command that builds the paged-cache binding, or None without torch (which is not imported)."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch = list(spec.submodule_search_locations)[0]
+    inc = os.path.join(torch, "include")
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", os.path.join(CSRC, "paged_ext.cpp"), "-o", out,
+            f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
+            f"-isystem{os.path.join(inc, 'torch', 'csrc', 'api', 'include')}",
+            f"-I{os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(cc))), 'include')}",
+            f"-L{os.path.join(torch, 'lib')}", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
@@ -71,7 +90,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     os.makedirs(build_dir, exist_ok=True)
     digest = _tree_hash(extra_flags)
     stamp = lib_path + ".hash"
-    if not force and os.path.exists(lib_path) and os.path.exists(stamp) and open(stamp).read() == digest:
+    have_torch = importlib.util.find_spec("torch") is not None
+    if not force and os.path.exists(lib_path) and os.path.exists(stamp) and open(stamp).read() == digest and (
+            debug_checks or not have_torch or os.path.exists(EXT)):
         return lib_path
     cc = nvcc()
     jobs = []
@@ -81,6 +102,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         jobs.append((src, obj, cmd))
+
+    ext_tmp = EXT + f".tmp{os.getpid()}"
+    ext = None if debug_checks else _ext_command(cc, ext_tmp)
+    if ext is not None:
+        jobs.append(("paged_ext.cpp", ext_tmp, ext))
 
     def run(job):
         src, obj, cmd = job
@@ -99,11 +125,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if failed:
         raise RuntimeError("libfa build failed")
     tmp = lib_path + f".tmp{os.getpid()}"
-    link = [cc, *ARCH, "-shared", "-o", tmp, *[obj for _, obj, _ in jobs]]
+    link = [cc, *ARCH, "-shared", "-o", tmp, *[obj for _, obj, _ in jobs if obj != ext_tmp]]
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"libfa link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, lib_path)
+    if ext is not None:
+        os.replace(ext_tmp, EXT)
     with open(stamp, "w") as f:
         f.write(digest)
     return lib_path

@@ -56,14 +56,6 @@ class Fork(ctypes.Structure):
                 ("ws", ctypes.c_void_p), ("wsb", ctypes.c_size_t), ("room", ctypes.c_int)]
 
 
-def test_packed_blocks_have_the_structures_sizes():
-    import struct
-    from exact_attention_44_gb300 import paged
-    assert struct.calcsize(paged._CACHE) == ctypes.sizeof(Cache)
-    for pack, kind in ((paged._ATTEND, Attend), (paged._APPEND, Append), (paged._COMMIT, Commit), (paged._FORK, Fork)):
-        assert pack.__self__.size == ctypes.sizeof(kind)
-
-
 def _cache(kc=PTR, table=PTR, lens=PTR, Z=2, L=1, P=9, H=2, page=16, D=64, M=4, ts=4, kl=1 << 16, sc=None):
     sc = sc or _st(H * page * D, page * D, D)
     return Cache(kc, kc, sc, sc, kl, kl, table, ts, lens, Z, L, P, H, page, D, M)
