@@ -205,14 +205,15 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* sum) {
 
 __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const ForkParams p) {
     __shared__ int red[32];
-    __shared__ int tails;
+    __shared__ int tails, excess;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const ForkWs w = fork_ws(p);
     const int tid = threadIdx.x;
-    if (tid == 0) tails = 0;
+    if (tid == 0) tails = excess = 0;
+    __syncthreads();
     const int cap = p.M * p.page;
-    int wanted = 0, excess = 0;
+    int wanted = 0;
     for (int z0 = 0; z0 < p.Z; z0 += PLAN_THREADS) {
         const int z = z0 + tid;
         int count = 0, over = 0;
@@ -237,9 +238,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
         int sum, off = block_scan(count, red, &sum);
         if (z < p.Z) w.off[z] = wanted + off;
         wanted += sum;
-        int unused = block_scan(over, red, &sum);
-        (void)unused;
-        excess += sum;
+        if (over > 0) atomicAdd(&excess, over);
     }
     // the first `wanted` pages with count 0
     int found = 0;

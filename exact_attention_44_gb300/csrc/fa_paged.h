@@ -67,6 +67,7 @@ struct PagedParams {
     int cap;                   // M * page: positions a sequence can have
     int tile_rows;             // query rows of a tile (a row is a (token, head of the group) pair, heads innermost)
     int box_rows;              // positions a TMA box holds: gcd(page, positions a block)
+    int snap;                  // tile groups of at most this many key blocks are not cut
     int tiles;                 // tiles of one (z, kv head): ceil(T * G / tile_rows)
     float scale_log2;          // scale * log2(e) (rows kernel: signed; tile kernel: its magnitude)
     int negate_s;              // tile kernel: the scale is negative

@@ -10,10 +10,11 @@
 // over the same key blocks, so that the blocks come from DRAM once and from L2
 // for the others.  The (tile group, key block) pairs, in the order sequence,
 // kv head, group, block, are laid end to end and cut into one equal range per
-// team, whatever the lengths are; a tile that a cut crosses leaves partial
-// results (O / l in fp32 and the base-2 log-sum-exp) in slots of the workspace,
-// two per worker, and fa_paged_merge_kernel joins them in the order of the
-// keys.  Nothing depends on timing: the same inputs give the same bits.
+// team, whatever the lengths are (a cut inside a group of at most p.snap blocks
+// moves to the group's end); a tile that a cut crosses leaves partial results
+// (O / l in fp32 and the base-2 log-sum-exp) in slots of the workspace, two per
+// worker, and fa_paged_merge_kernel joins them in the order of the keys.
+// Nothing depends on timing: the same inputs give the same bits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -105,6 +106,26 @@ struct PagedSeg {
     int len, nl;
     int row0, rows;  // first query row of the tile and its live rows
 };
+// On to the next tile group (sequences without new tokens have none).
+template <int BK>
+__device__ __forceinline__ void paged_next(const PagedParams& p, PagedWalk& w) {
+    w.left -= group_blocks<BK>(p, w.s, w.gi) - w.jb;
+    w.jb = 0;
+    if (w.left <= 0) return;
+    if (++w.gi < w.groups) return;
+    w.gi = 0;
+    if (++w.hk < p.Hkv) return;
+    w.hk = 0;
+    do {
+        if (++w.z >= p.Z) {
+            w.left = 0;
+            return;
+        }
+        w.s = seq_len(p, w.z);
+    } while (w.s.nl == 0);
+    w.groups = live_groups(p, w.s);
+}
+
 // Unsigned division that takes the 32-bit route where both fit: the 64-bit one
 // costs a few hundred cycles, which a short call would feel.
 __device__ __forceinline__ int64_t fast_div(int64_t a, int64_t b) {
@@ -240,30 +261,12 @@ __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind
         w.jb = (int)rem;
         w.left = cuts.start(c + 1) - cuts.start(c);
         w.groups = live_groups(p, w.s);
+        // a short group is not cut: the team before has it whole
+        if (w.jb > 0 && group_blocks<BK>(p, w.s, w.gi) <= p.snap) paged_next<BK>(p, w);
     }
     if (records && c < p.teams)
         static_cast<PagedCut*>(p.cuts)[c] = PagedCut{w.z, w.hk, w.gi, w.jb, w.s.len, w.s.nl, cuts.rem, cuts.teams, cuts.q};
     return w;
-}
-
-// On to the next tile group (sequences without new tokens have none).
-template <int BK>
-__device__ __forceinline__ void paged_next(const PagedParams& p, PagedWalk& w) {
-    w.left -= group_blocks<BK>(p, w.s, w.gi) - w.jb;
-    w.jb = 0;
-    if (w.left <= 0) return;
-    if (++w.gi < w.groups) return;
-    w.gi = 0;
-    if (++w.hk < p.Hkv) return;
-    w.hk = 0;
-    do {
-        if (++w.z >= p.Z) {
-            w.left = 0;
-            return;
-        }
-        w.s = seq_len(p, w.z);
-    } while (w.s.nl == 0);
-    w.groups = live_groups(p, w.s);
 }
 
 // The next segment of member `member` of a team at or after w's place (worker:
@@ -279,7 +282,8 @@ __device__ __forceinline__ bool paged_seg(const PagedParams& p, PagedWalk& w, Pa
         g.z = w.z;
         g.hk = w.hk;
         g.jb = w.jb;
-        g.je = own - w.jb <= w.left ? own : w.jb + (int)w.left;
+        const bool whole = own - w.jb <= w.left || group_blocks<BK>(p, w.s, w.gi) <= p.snap;
+        g.je = whole ? own : w.jb + (int)w.left;
         if (g.je <= g.jb) continue;
         g.slot = g.jb == 0 && g.je == own ? -1 : 2 * worker + (g.jb > 0 ? 0 : 1);
         g.len = w.s.len;
@@ -345,8 +349,9 @@ constexpr int PAGED_MERGE_THREADS = 128;
 template <int D, int BK, bool BF16>
 __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int sub) {
     constexpr int W = D / 4, NT = PAGED_MERGE_THREADS;
+    // (no early launch of the next kernel: its set-up would take issue slots from the merge, 187 against
+    // 194 us for 32 sequences x 64 drafted tokens)
     ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
     const int tid = threadIdx.x;
     const int member = (int)(blockIdx.x / sub) % p.team;
     // One warp works out the block's share for all (the arithmetic in every warp took
@@ -367,9 +372,13 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             const int c1 = cuts.team_of(t1);
             if (b <= c1) {  // (else the cut is behind this tile's last block)
                 parts = c1 - c0 + 1;
-                const int shares = (c1 - c0) * sub, share = (live * W + shares - 1) / shares;
-                first = ((b - 1 - c0) * sub + (int)blockIdx.x % sub) * share;
-                last = min(first + share, live * W);
+                // as many of the cut's blocks as have an item for every thread
+                const int cuts_in = c1 - c0, use = min(sub, (live * W + cuts_in * NT - 1) / (cuts_in * NT));
+                const int mine = (int)blockIdx.x % sub, shares = cuts_in * use, share = (live * W + shares - 1) / shares;
+                if (mine < use) {
+                    first = ((b - 1 - c0) * use + mine) * share;
+                    last = min(first + share, live * W);
+                }
             }
         }
         if (tid == 0) {
@@ -381,9 +390,10 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     const int first = what[0], last = what[1], parts = what[2];
     if (first >= last) return;
     const int z = what[3], hk = what[4], row0 = what[5];
-    // the first part is in slot 2 c + 1 of its worker, the others in slots 2 c
+    // the first part is in slot 2 c + 1 of its worker, the others in slots 2 c: offsets in
+    // floats, below 2^32 (two slots a worker, at most 1280 x 33 KB or 152 x 132 KB each)
     const float* base = p.scratch + (int64_t)what[6] * p.slot_floats;
-    auto slot = [&](int i) { return base + (i == 0 ? p.slot_floats : (int64_t)i * 2 * p.team * p.slot_floats); };
+    const uint32_t slot0 = (uint32_t)p.slot_floats, step = 2u * (uint32_t)p.team * slot0, lses = (uint32_t)(p.tile_rows * D);
     int spl = 1;
     while (spl < 32 && spl < parts && (last - first) * spl * 2 <= NT) spl *= 2;
     const int sl = tid % spl;
@@ -401,10 +411,11 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             for (int u = 0; u < U; ++u) {
                 l[u] = -INFINITY;
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (x0 + u * spl < parts) {
-                    const float* from = slot(x0 + u * spl);
-                    l[u] = __ldcg(from + p.tile_rows * D + r);
+                const int x = x0 + u * spl;
+                if (x < parts) {
+                    const float* from = base + (x == 0 ? slot0 : (uint32_t)x * step);
                     v[u] = __ldcg(reinterpret_cast<const float4*>(from) + i);
+                    l[u] = __ldcg(from + lses + r);
                 }
             }
             float top = mx;

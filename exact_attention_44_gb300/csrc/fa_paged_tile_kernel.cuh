@@ -37,9 +37,9 @@ struct TileTraits : Traits<D_> {
     static constexpr int OFF_MISC = Base::OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_SEG = OFF_MISC + 16;
     static constexpr int SEG_END = OFF_SEG + SEGS * 48;
-    // staging of the epilogue: 32 rows x 128 bytes a warp
+    // staging of the epilogue: 32 rows x 64 bytes a warp
     static constexpr int OFF_STAGE = D_ >= 64 ? Base::OFF_OST : (SEG_END + 15) / 16 * 16;
-    static constexpr int SMEM_USED = D_ >= 64 ? SEG_END : OFF_STAGE + 4 * 4096;
+    static constexpr int SMEM_USED = D_ >= 64 ? SEG_END : OFF_STAGE + 4 * 2048;
     static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     static __device__ __forceinline__ uint32_t bar_count(int i) {
@@ -56,15 +56,16 @@ struct TileTraits : Traits<D_> {
 // softmax loop -- and 24 warps doing the same arithmetic at the start of every
 // segment got in each other's way.)
 struct SegMsg {
-    int z, hk, jb, je, slot, len, nl, row0, rows, pad[3];  // je = 0: the end
+    int z, hk, jb, je, slot, len, nl, row0, rows, pads, unused[2];  // je = 0: the end
 };
 template <int D, typename Bar>
-__device__ __forceinline__ void seg_put(volatile int* ring, const PagedSeg& g, bool have, uint32_t n, Bar bar) {
+__device__ __forceinline__ void seg_put(volatile int* ring, const PagedSeg& g, bool have, bool pads,
+                                         uint32_t n, Bar bar) {
     using T = TileTraits<D>;
     volatile int* s = ring + (n % T::SEGS) * (sizeof(SegMsg) / 4);
     if (threadIdx.x % 32 == 0) {
         s[0] = g.z, s[1] = g.hk, s[2] = g.jb, s[3] = have ? g.je : 0, s[4] = g.slot;
-        s[5] = g.len, s[6] = g.nl, s[7] = g.row0, s[8] = g.rows;
+        s[5] = g.len, s[6] = g.nl, s[7] = g.row0, s[8] = g.rows, s[9] = pads;
         ptx::mbar_arrive(bar(T::B_SEGFULL + n % T::SEGS));
     }
     __syncwarp();
@@ -74,7 +75,7 @@ __device__ __forceinline__ void seg_put(volatile int* ring, const PagedSeg& g, b
 // its one active lane.
 template <int D, bool WARP, typename Bar>
 __device__ __forceinline__ bool seg_get(volatile const int* ring, PagedSeg& g, uint32_t n, Bar bar, const Ctl& ctl,
-                                        bool& ok) {
+                                        bool& ok, bool* pads = nullptr) {
     using T = TileTraits<D>;
     const uint32_t full = bar(T::B_SEGFULL + n % T::SEGS), parity = (n / T::SEGS) & 1u;
     ok = WARP ? warp_wait_phase(full, parity, ctl, SITE_SEG_FULL) : wait_phase(full, parity, ctl, SITE_SEG_FULL);
@@ -82,6 +83,7 @@ __device__ __forceinline__ bool seg_get(volatile const int* ring, PagedSeg& g, u
     volatile const int* s = ring + (n % T::SEGS) * (sizeof(SegMsg) / 4);
     g.z = s[0], g.hk = s[1], g.jb = s[2], g.je = s[3], g.slot = s[4];
     g.len = s[5], g.nl = s[6], g.row0 = s[7], g.rows = s[8];
+    if (pads != nullptr) *pads = s[9] != 0;
     if (WARP) __syncwarp();
     if (!WARP || threadIdx.x % 32 == 0) ptx::mbar_arrive(bar(T::B_SEGFREE + n % T::SEGS));
     return g.je > 0;
@@ -125,7 +127,7 @@ __device__ __forceinline__ void load_boxes(const PagedParams& p, PageBox b, cons
 
 template <int D>
 __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK, const PagedParams& p, PagedWalk w,
-                                 volatile int* ring, uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
+                                 bool pads, volatile int* ring, uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int lane = threadIdx.x % 32;
@@ -153,7 +155,7 @@ __device__ void tile_producer_qk(const CUtensorMap* tmQ, const CUtensorMap* tmK,
         const uint32_t slot = nseg % T::SEGS;
         if (nseg >= (uint32_t)T::SEGS &&
             !warp_wait_phase(bar(T::B_SEGFREE + slot), (nseg / T::SEGS - 1) & 1u, ctl, SITE_SEG_FREE)) return false;
-        seg_put<D>(ring, sg, have, nseg, bar);
+        seg_put<D>(ring, sg, have, pads, nseg, bar);
         ++nseg;
         return true;
     };
@@ -494,19 +496,18 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t 
 
 template <int D, bool BF16>
 __device__ void tile_epilogue(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
-                              const float* hand, bool pads, const Ctl& ctl) {
+                              const float* hand, const Ctl& ctl) {
     using T = TileTraits<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int quad = (threadIdx.x / 32) % 4;
     const int row = quad * 32 + threadIdx.x % 32;
     const int lane = threadIdx.x % 32;
     const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O;
-    const uint32_t stage = sbase + T::OFF_STAGE + (uint32_t)quad * 4096u;
+    const uint32_t stage = sbase + T::OFF_STAGE + (uint32_t)quad * 2048u;
     uint32_t step = 0, ntile = 0;
-    constexpr int CH = 16;  // columns a TMEM load
     PagedSeg sg;
-    bool ok;
-    for (; seg_get<D, true>(ring, sg, ntile, bar, ctl, ok); ++ntile) {
+    bool ok, pads = false;
+    for (; seg_get<D, true>(ring, sg, ntile, bar, ctl, ok, &pads); ++ntile) {
         step += sg.je - sg.jb;
         const uint32_t slot = ntile & 1u;
         if (!warp_wait_phase(bar(T::B_EPIFULL + slot), (ntile >> 1) & 1u, ctl, SITE_EPI_FULL)) return;
@@ -520,10 +521,10 @@ __device__ void tile_epilogue(const PagedParams& p, volatile int* ring, uint32_t
         ptx::tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
         const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        // The warp's rows go out through its 4 KB of staging, 128 bytes of a row at
-        // a time: a thread fills its row's pieces (permuted against bank conflicts),
-        // then eight lanes write a row, so that a store instruction touches four
-        // lines instead of 32 (which took 2.5 us for a part of 128 rows).
+        // The warp's rows go out through its staging, 64 bytes of a row at a time: a
+        // thread fills its row's pieces (permuted against bank conflicts), then PIECES
+        // lanes write a row, so that a store instruction touches eight lines instead of
+        // 32 (which took 2.5 us for a part of 128 rows).
         const bool part = sg.slot >= 0;
         float* slot_base = p.scratch + (int64_t)max(sg.slot, 0) * p.slot_floats;
         if (row < sg.rows) {
@@ -531,62 +532,56 @@ __device__ void tile_epilogue(const PagedParams& p, volatile int* ring, uint32_t
             if (part) slot_base[p.tile_rows * D + row] = lse2;
             else if (p.lse != nullptr) p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
         }
-        // where this lane writes: row 4 i + lane / 8 of the warp's, piece lane % 8
-        const int lr = lane / 8, lp = lane % 8;
-        auto out_row = [&](int i) -> uint8_t* {
-            const int r = quad * 32 + 4 * i + lr;
-            if (r >= sg.rows) return nullptr;
-            if (part) return reinterpret_cast<uint8_t*>(slot_base + (int64_t)r * D);
-            const int grow = sg.row0 + r, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
-            return reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h +
-                                              t * p.so_n);
-        };
-        // columns a round: 128 bytes of fp32 or of the output type (less for D < 64, 32)
-        auto round = [&](auto c_tag, int c0, bool last) {
-            constexpr int C = decltype(c_tag)::value;     // columns of this round
-            uint32_t w[32];
-            const int pieces = part ? C / 4 : C / 8;
+        // Columns c0 .. of the warp's rows, PIECES 16-byte pieces a row, are in w: write
+        // them out at byte `at` of each row.
+        auto write_out = [&](auto pieces, const uint32_t (&w)[16], int at) {
+            constexpr int PIECES = decltype(pieces)::value, RI = 32 / PIECES;  // rows an instruction
+            const int lr = lane / PIECES, lp = lane % PIECES;
+            __syncwarp();
 #pragma unroll
-            for (int i = 0; i < C / CH; ++i) {
-                uint32_t r[CH];
-                ptx::tmem_ld16(o_addr + c0 + i * CH, r);
+            for (int x = 0; x < PIECES; ++x)
+                ptx::st_shared_v4(stage + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2],
+                                  w[4 * x + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PIECES; ++i) {
+                const int rw = i * RI + lr, r = quad * 32 + rw;
+                if (r >= sg.rows) continue;
+                uint8_t* dst;
+                if (part) {
+                    dst = reinterpret_cast<uint8_t*>(slot_base + r * D);
+                } else {
+                    const int grow = sg.row0 + r, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
+                    dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h +
+                                                     t * p.so_n);
+                }
+                *reinterpret_cast<uint4*>(dst + at + lp * 16) = ld_shared_v4(stage + rw * 64 + ((lp ^ ((rw >> 1) & 3)) << 4));
+            }
+        };
+        constexpr int C = D < 32 ? D : 32;  // columns a round
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += C) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < C / 16; ++i) {
+                uint32_t r[16];
+                ptx::tmem_ld16(o_addr + c0 + i * 16, r);
+                if (i == C / 16 - 1 && c0 + C == D) {
+                    // all of O has been read: the MMA warp may overwrite it
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(bar(T::B_OFREE));
+                }
                 if (part) {
 #pragma unroll
-                    for (int x = 0; x < CH; ++x)
-                        if (i * CH + x < 32) w[i * CH + x] = __float_as_uint(__uint_as_float(r[x]) * inv);
+                    for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(__uint_as_float(r[x]) * inv);
+                    write_out(std::integral_constant<int, 4>{}, w, (c0 + i * 16) * 4);
                 } else {
 #pragma unroll
-                    for (int x = 0; x < CH / 2; ++x)
-                        w[i * (CH / 2) + x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
+                    for (int x = 0; x < 8; ++x)
+                        w[i * 8 + x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
                 }
             }
-            if (last) {
-                ptx::tc_fence_before();
-                ptx::mbar_arrive(bar(T::B_OFREE));
-            }
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (x < pieces)
-                    ptx::st_shared_v4(stage + lane * 128 + ((x ^ (lane & 7)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-            __syncwarp();
-            const int bytes0 = part ? c0 * 4 : c0 * 2;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                uint8_t* dst = out_row(i);
-                const int r = 4 * i + lr;
-                if (dst != nullptr && lp < pieces)
-                    *reinterpret_cast<uint4*>(dst + bytes0 + lp * 16) = ld_shared_v4(stage + r * 128 + ((lp ^ (r & 7)) << 4));
-            }
-        };
-        if (part) {
-            constexpr int C = D < 32 ? D : 32;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += C) round(std::integral_constant<int, C>{}, c0, c0 + C == D);
-        } else {
-            constexpr int C = D < 64 ? D : 64;
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += C) round(std::integral_constant<int, C>{}, c0, c0 + C == D);
+            if (!part) write_out(std::integral_constant<int, C / 8>{}, w, c0 * 2);
         }
     }
     if (ok && pads) paged_fill<D>(p, (int)blockIdx.x * 4 + quad, (int)gridDim.x * 4);
@@ -633,14 +628,14 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     bool pads = false;
     // With few sequences the K producer's warp finds the range by itself; else
     // the CTA together.  (The search's area is the roles' hand-over area.)
-    if (p.Z > 32 || warp == 0 || warp > 3 + 4 * T::NG)
+    if (p.Z > 32 || warp == 0)
         walk = paged_range<T::BN, 1>(p, reinterpret_cast<PagedFind<1>*>(hand), (int)blockIdx.x / p.team, 0,
                                      threadIdx.x == 0 && blockIdx.x % p.team == 0, pads);
     if (p.Z > 32) __syncthreads();
 
     constexpr int SOFTMAX_END = 4 + 4 * T::NG;
     if (warp == 0) {
-        tile_producer_qk<D>(&tmQ, &tmK, p, walk, ring, sbase, bar0, ctl);
+        tile_producer_qk<D>(&tmQ, &tmK, p, walk, pads, ring, sbase, bar0, ctl);
     } else if (warp == 3) {
         tile_producer_v<D>(&tmV, p, ring, sbase, bar0, ctl);
     } else if (warp == 1) {
@@ -650,7 +645,7 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     } else if (warp < SOFTMAX_END) {
         tile_softmax<D, BF16>(p, ring, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
     } else {
-        tile_epilogue<D, BF16>(p, ring, sbase, bar0, tmem, hand, pads, ctl);
+        tile_epilogue<D, BF16>(p, ring, sbase, bar0, tmem, hand, ctl);
     }
 
     ptx::tc_fence_before();
