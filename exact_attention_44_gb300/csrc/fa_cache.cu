@@ -6,6 +6,8 @@
 // are skipped and STATUS_PAGE is recorded.
 #include "fa_cache.h"
 
+#include <climits>
+
 #include "fa_paged.h"
 #include "fa_ptx.cuh"
 
@@ -205,12 +207,16 @@ __device__ __forceinline__ int block_scan(int v, int* red, int* sum) {
 
 __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const ForkParams p) {
     __shared__ int red[32];
-    __shared__ int tails, excess;
+    __shared__ int tails;
+    __shared__ unsigned long long excess;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const ForkWs w = fork_ws(p);
     const int tid = threadIdx.x;
-    if (tid == 0) tails = excess = 0;
+    if (tid == 0) {
+        tails = 0;
+        excess = 0;
+    }
     __syncthreads();
     const int cap = p.M * p.page;
     int wanted = 0;
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
         int sum, off = block_scan(count, red, &sum);
         if (z < p.Z) w.off[z] = wanted + off;
         wanted += sum;
-        if (over > 0) atomicAdd(&excess, over);
+        if (over > 0) atomicAdd(&excess, (unsigned long long)over);
     }
     // the first `wanted` pages with count 0
     int found = 0;
@@ -281,7 +287,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
     if (tid == 0) {
         w.found[0] = found;
         w.found[1] = tails;
-        if (p.missing != nullptr) *p.missing = wanted - found + excess;
+        if (p.missing != nullptr) *p.missing = (int)min((long long)wanted - found + (long long)excess, (long long)INT_MAX);
     }
 }
 

@@ -343,11 +343,14 @@ fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
     if (c.Z > 8192 || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||
         (int64_t)c.L * 2 * c.Hkv > INT32_MAX || (int64_t)c.page_size * (c.D / 8) > INT32_MAX)
         return FA_ERR_UNSUPPORTED;
-    if (c.Z == 0) return FA_OK;
+    if ((st = check_ints(x.missing, false)) != FA_OK) return st;
+    if (c.Z == 0) {  // nothing to do, and nothing lacks
+        const cudaError_t err = x.missing != nullptr ? cudaMemsetAsync(x.missing, 0, sizeof(int32_t), stream) : cudaSuccess;
+        return err == cudaSuccess ? FA_OK : fa::report_cuda("cache fork", err);
+    }
     if ((st = check_cache_data(c, true)) != FA_OK) return st;
     if ((st = check_ints(x.ref_counts, c.P > 0)) != FA_OK) return st;
     if ((st = check_ints(x.source, false)) != FA_OK) return st;
-    if ((st = check_ints(x.missing, false)) != FA_OK) return st;
     if (x.workspace == nullptr || misaligned(x.workspace, 256) ||
         x.workspace_bytes < (size_t)fa::fork_workspace_ints(c.Z, c.max_pages) * sizeof(int32_t))
         return FA_ERR_WORKSPACE;

@@ -205,6 +205,7 @@ __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind
         SeqLen s{0, 0};
         int64_t own = 0, v = 0;
         bool pad = false;
+#pragma unroll 4
         for (int z = tid; z < p.Z; z += nt) {
             s = seq_len(p, z);
             v = p.Hkv * head_blocks<BK>(p, s);

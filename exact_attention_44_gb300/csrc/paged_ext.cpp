@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -129,13 +130,31 @@ int cuda_device(const char* call, const at::Tensor& lead, std::initializer_list<
     return lead.get_device();
 }
 
-// The stream's handle: the given one (an int), or torch's current stream of the device.
-cudaStream_t stream_of(PyObject* o, int device) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream();
-    void* p = PyLong_AsVoidPtr(o);
-    if (p == nullptr && PyErr_Occurred()) throw python_error();
-    return static_cast<cudaStream_t>(p);
-}
+// The device and stream of a call: the given stream (its handle, an int), else
+// torch's current one.  What is allocated meanwhile belongs to that stream, and
+// the tensors of a call on another stream than the current one are kept from
+// reuse until that stream has passed the call.
+class Place {
+  public:
+    Place(PyObject* o, int device, std::initializer_list<const at::Tensor*> used)
+        : device_((c10::DeviceIndex)device), stream_(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device)) {
+        if (o == Py_None) return;
+        void* p = PyLong_AsVoidPtr(o);
+        if (p == nullptr && PyErr_Occurred()) throw python_error();
+        if (static_cast<cudaStream_t>(p) == stream_.stream()) return;
+        stream_ = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), (c10::DeviceIndex)device);
+        guard_.reset_stream(stream_);
+        for (const at::Tensor* t : used)
+            if (t != nullptr && t->has_storage())
+                c10::cuda::CUDACachingAllocator::recordStream(t->storage().data_ptr(), stream_);
+    }
+    cudaStream_t stream() const { return stream_.stream(); }
+
+  private:
+    c10::cuda::CUDAGuard device_;
+    c10::cuda::CUDAStream stream_;
+    c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 void check(fa_status st, const char* call) {
     if (st == FA_OK) return;
@@ -221,7 +240,7 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int want = PyObject_IsTrue(a[12]);
         if (want < 0) throw python_error();
         const int dev = cuda_device("fa_fwd_paged", q, {&k, &v, &table, &lens, o_arg, lse_arg, news, mask, ws_arg});
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const Place place(a[11], dev, {&q, &k, &v, &table, &lens, o_arg, lse_arg, news, mask, ws_arg});
         at::Tensor o = o_arg != nullptr ? *o_arg : at::empty(q.sizes(), q.options());
         at::Tensor lse, ws;
         if (lse_arg != nullptr) lse = *lse_arg;
@@ -245,8 +264,7 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x.Hq = to_int(Hq, "the heads");
         x.T = to_int(T, "T");
         x.scale = (float)scale;
-        const cudaStream_t stream = stream_of(a[11], dev);
-        check(unlocked([&] { return lib.fwd(&x, stream); }), "fa_fwd_paged");
+        check(unlocked([&] { return lib.fwd(&x, place.stream()); }), "fa_fwd_paged");
         PyObject* result = PyTuple_New(2);
         if (result == nullptr) throw python_error();
         PyTuple_SET_ITEM(result, 0, THPVariable_Wrap(o));
@@ -276,15 +294,14 @@ PyObject* cache_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
             type_error("k and v must have the cache's dtype");
         if (news != nullptr) check_ints(*news, "new_lens", {Z});
         const int dev = cuda_device("fa_cache_append", k, {&v, &kc, &vc, &table, &lens, news});
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const Place place(a[7], dev, {&k, &v, &kc, &vc, &table, &lens, news});
         x.k = k.data_ptr();
         x.v = v.data_ptr();
         x.sk = strides4(k);
         x.sv = strides4(v);
         x.new_lens = ints(news);
         x.T = to_int(k.size(2), "T");
-        const cudaStream_t stream = stream_of(a[7], dev);
-        check(unlocked([&] { return lib.append(&x, stream); }), "fa_cache_append");
+        check(unlocked([&] { return lib.append(&x, place.stream()); }), "fa_cache_append");
         Py_RETURN_NONE;
     });
 }
@@ -303,13 +320,12 @@ PyObject* cache_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
         fa_cache_commit_args x{};
         x.cache = cache_of(kc, vc, table, lens, Z, true);
         const int dev = cuda_device("fa_cache_commit", kc, {&vc, &table, &lens, &path, &kept});
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const Place place(a[6], dev, {&kc, &vc, &table, &lens, &path, &kept});
         x.accepted = ints(&path);
         x.accepted_stride = path.stride(0);
         x.accepted_lens = ints(&kept);
         x.A = to_int(path.size(1), "A");
-        const cudaStream_t stream = stream_of(a[6], dev);
-        check(unlocked([&] { return lib.commit(&x, stream); }), "fa_cache_commit");
+        check(unlocked([&] { return lib.commit(&x, place.stream()); }), "fa_cache_commit");
         Py_RETURN_NONE;
     });
 }
@@ -331,7 +347,7 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (missing != nullptr) check_ints(*missing, "missing", {1});
         x.room = int_arg(a[6], "room");
         const int dev = cuda_device("fa_cache_fork", kc, {&vc, &table, &lens, &refs, source, missing, ws_arg});
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const Place place(a[9], dev, {&kc, &vc, &table, &lens, &refs, source, missing, ws_arg});
         at::Tensor ws;
         if (ws_arg != nullptr) {
             ws = *ws_arg;
@@ -345,8 +361,7 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x.missing = ints(missing);
         x.workspace = ws.data_ptr();
         x.workspace_bytes = ws.nbytes();
-        const cudaStream_t stream = stream_of(a[9], dev);
-        check(unlocked([&] { return lib.fork(&x, stream); }), "fa_cache_fork");
+        check(unlocked([&] { return lib.fork(&x, place.stream()); }), "fa_cache_fork");
         Py_RETURN_NONE;
     });
 }

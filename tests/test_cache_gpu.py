@@ -302,3 +302,13 @@ def test_serving_run(dtype):
         assert torch.equal(buf["o"], o) and torch.equal(buf["lse"], lse)
     assert lens.tolist() == end
     fa.fa_device_status()
+
+
+def test_fork_counts_what_lacks_without_overflow():
+    import exact_attention_44_gb300 as fa
+    kc, vc, table, refs = fork_state(12, [5] * 64, 16, 1, 16, 1, 0, 2)
+    missing = i32([0])
+    fa.fa_cache_fork(kc.cuda(), vc.cuda(), table.cuda(), i32([5] * 64), i32(refs), room=2 ** 30, missing=missing)
+    assert missing.item() == 2 ** 31 - 1  # 64 x 2^26 pages, more than an int32 holds
+    fa.fa_cache_fork(kc.cuda(), vc.cuda(), table[:0].cuda(), i32([]), i32(refs), room=1, missing=missing)
+    assert missing.item() == 0

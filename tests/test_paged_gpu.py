@@ -373,3 +373,43 @@ def test_expanded_queries(T):
     a, la = fa.fa_fwd_paged(q.expand(3, 4, T, 64), *args)
     b, lb = fa.fa_fwd_paged(q.expand(3, 4, T, 64).contiguous(), *args)
     assert torch.equal(a, b) and torch.equal(la, lb)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_side_stream_keeps_what_it_uses(T):
+    # every tensor of the call, its workspace included, is dropped right after it; allocations on the
+    # current stream must not reuse their memory while the side stream, held up first, still needs it
+    import exact_attention_44_gb300 as fa
+    kc, vc, table, k, v = pu.make_cache(43, [500 + T] * 4, 4, 128, 16, "bf16")
+    q = torch.randn(4, 16, T, 128).bfloat16()
+    lens = torch.tensor([500] * 4, dtype=torch.int32)
+    want, wlse = fa.fa_fwd_paged(*[x.cuda() for x in (q, kc, vc, table, lens)])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    args = [x.cuda() for x in (q, kc, vc, table, lens)]
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    o, lse = fa.fa_fwd_paged(*args, stream=s)
+    sizes = [x.numel() * x.element_size() for x in args] + [fa.fa_fwd_paged_workspace_size(128)]
+    del args
+    junk = [torch.full((n,), 0x7f, dtype=torch.uint8, device="cuda") for n in sizes]
+    s.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(lse, wlse) and len(junk) == 6
+
+
+@pytest.mark.parametrize("T,G,tree", [(130, 4, True), (200, 3, False), (64, 8, True), (300, 2, True), (257, 5, False)])
+def test_teams_of_tiles(T, G, tree):
+    # several tiles of a kv head: teams of two to eight CTAs, the last tile ragged, sequences of all sizes
+    lens, new = [0, 700, 33, 1500], [T, T // 2, 1, T - 3]
+    seen = pu.random_tree(44, 4, T) if tree else None
+    check(44, lens, 2 * G, 2, T, 64, 32, "bf16", new=new, seen=seen)
+
+
+def test_many_sequences_of_all_lengths():
+    r = np.random.RandomState(45)
+    lens = np.concatenate([r.randint(0, 20, 200), r.randint(100, 900, 20), [2500]])
+    r.shuffle(lens)
+    check(45, list(lens), 4, 2, 1, 64, 16, "fp16")
+    check(46, list(lens[:60]), 8, 1, 9, 64, 16, "fp16", new=list(r.randint(0, 10, 60)))
