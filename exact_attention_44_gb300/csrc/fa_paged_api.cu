@@ -259,6 +259,7 @@ fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
     p.by_page = fa::FastDiv(p.page);
     p.by_tile_rows = fa::FastDiv(p.tile_rows);
     p.by_team = fa::FastDiv(p.team);
+    p.few = Z <= 32 && blocks < (int64_t(1) << 30);
     p.cuts = static_cast<char*>(x.workspace) + paged_slot_bytes(D, f.sms);
     err = launch_paged(D, a, bf16);
     return err == cudaSuccess ? FA_OK : fa::report_cuda("paged attention launch", err);

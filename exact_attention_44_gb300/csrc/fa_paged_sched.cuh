@@ -144,8 +144,8 @@ struct PagedCuts {
         return x < big ? (int)fast_div(x, q + 1) : rem + (int)fast_div(x - big, q);
     }
 };
-__device__ __forceinline__ PagedCuts paged_cuts(int64_t total, int teams) {
-    PagedCuts c{0, 0, (int)min((int64_t)teams, total)};
+__device__ __forceinline__ PagedCuts paged_cuts(const PagedParams& p, int64_t total) {
+    PagedCuts c{0, 0, (int)min((int64_t)p.teams, total)};
     if (total > 0) {
         c.q = fast_div(total, c.teams);
         c.rem = (int)(total - c.q * c.teams);
@@ -171,35 +171,44 @@ struct PagedFind {
 // Where the range of team first + mine starts (RANGES teams a CTA, mine the same
 // in all threads of a warp), recorded for the merge by the thread that
 // `records`.  pads: some sequence has fewer than T new tokens.  Called by every
-// thread of the CTA; with up to 32 sequences the warps need not all call it.
+// thread of the CTA; with few sequences (p.few) the warps need not all call it.
 template <int BK, int RANGES>
 __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind<RANGES>* f, int first, int mine,
                                               bool records, bool& pads) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid % 32;
     const int c = first + mine;
     PagedWalk w{-1, 0, 0, 0, 0, 0, {0, 0}};
-    PagedCuts cuts;
-    int64_t before = 0;  // blocks before sequence w.z
-    if (p.Z <= 32) {
-        // each warp by itself, one sequence a lane
+    PagedCuts cuts{0, 0, 0};
+    if (p.few) {
+        // Few sequences: each warp by itself, one sequence a lane, in 32 bits.  This
+        // stands between the launch and the first copy.
         SeqLen s{0, 0};
-        int64_t v = 0;
+        int per = 0;
         if (lane < p.Z) {
             s = seq_len(p, lane);
-            v = p.Hkv * head_blocks<BK>(p, s);
+            per = (int)head_blocks<BK>(p, s);
         }
         pads = __any_sync(0xffffffffu, lane < p.Z && s.nl < p.T);
-        int64_t x = v;
+        const int v = per * p.Hkv;
+        int x = v;
         for (int d = 1; d < 32; d *= 2) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            const int y = __shfl_up_sync(0xffffffffu, x, d);
             if (lane >= d) x += y;
         }
-        cuts = paged_cuts(__shfl_sync(0xffffffffu, x, 31), p.teams);
+        const int total = __shfl_sync(0xffffffffu, x, 31);
+        cuts = paged_cuts(p, total);
         if (c < cuts.teams) {
-            const int64_t lo = cuts.start(c);
+            const int lo = (int)cuts.start(c);
             w.z = __ffs(__ballot_sync(0xffffffffu, lo < x)) - 1;
-            before = __shfl_sync(0xffffffffu, x - v, w.z);
+            per = __shfl_sync(0xffffffffu, per, w.z);
             w.s = SeqLen{__shfl_sync(0xffffffffu, s.len, w.z), __shfl_sync(0xffffffffu, s.nl, w.z)};
+            int rem = lo - __shfl_sync(0xffffffffu, x - v, w.z);
+            w.hk = p.Hkv <= 32 ? __popc(__ballot_sync(0xffffffffu, (lane + 1) * (int64_t)per <= rem)) : rem / per;
+            rem -= w.hk * per;
+            for (int n; rem >= (n = group_blocks<BK>(p, w.s, w.gi)); ++w.gi) rem -= n;
+            w.jb = rem;
+            w.left = (int)cuts.start(c + 1) - lo;
+            w.groups = live_groups(p, w.s);
         }
     } else {
         SeqLen s{0, 0};
@@ -212,7 +221,7 @@ __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind
             own += v;
             pad |= s.nl < p.T;
         }
-        cuts = paged_cuts(block_sum(own, f->red), p.teams);
+        cuts = paged_cuts(p, block_sum(own, f->red));
         if (tid < RANGES) f->lo[tid] = first + tid < cuts.teams ? cuts.start(first + tid) : -1;
         pads = __syncthreads_or(pad);
         int64_t base = 0;
@@ -250,21 +259,18 @@ __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind
         if (c < cuts.teams) {
             w.z = f->z[mine];
             w.s = SeqLen{f->len[mine], f->nl[mine]};
-            before = f->z_before[mine];
+            int64_t rem = cuts.start(c) - f->z_before[mine];
+            const int64_t per = head_blocks<BK>(p, w.s);
+            w.hk = (int)fast_div(rem, per);
+            rem -= w.hk * per;
+            for (int64_t n; rem >= (n = group_blocks<BK>(p, w.s, w.gi)); ++w.gi) rem -= n;
+            w.jb = (int)rem;
+            w.left = cuts.start(c + 1) - cuts.start(c);
+            w.groups = live_groups(p, w.s);
         }
     }
-    if (c < cuts.teams) {
-        int64_t rem = cuts.start(c) - before;
-        const int64_t per = head_blocks<BK>(p, w.s);
-        w.hk = (int)fast_div(rem, per);
-        rem -= w.hk * per;
-        for (int64_t n; rem >= (n = group_blocks<BK>(p, w.s, w.gi)); ++w.gi) rem -= n;
-        w.jb = (int)rem;
-        w.left = cuts.start(c + 1) - cuts.start(c);
-        w.groups = live_groups(p, w.s);
-        // a short group is not cut: the team before has it whole
-        if (w.jb > 0 && group_blocks<BK>(p, w.s, w.gi) <= p.snap) paged_next<BK>(p, w);
-    }
+    // a short group is not cut: the team before has it whole
+    if (w.left > 0 && w.jb > 0 && group_blocks<BK>(p, w.s, w.gi) <= p.snap) paged_next<BK>(p, w);
     if (records && c < p.teams)
         static_cast<PagedCut*>(p.cuts)[c] = PagedCut{w.z, w.hk, w.gi, w.jb, w.s.len, w.s.nl, cuts.rem, cuts.teams, cuts.q};
     return w;
@@ -373,8 +379,9 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             const int c1 = cuts.team_of(t1);
             if (b <= c1) {  // (else the cut is behind this tile's last block)
                 parts = c1 - c0 + 1;
-                // as many of the cut's blocks as have an item for every thread
-                const int cuts_in = c1 - c0, use = min(sub, (live * W + cuts_in * NT - 1) / (cuts_in * NT));
+                // as many of the cut's blocks as leave a thread about four loads
+                const int cuts_in = c1 - c0, loads = cuts_in * NT * 4;
+                const int use = min(sub, (live * W * parts + loads - 1) / loads);
                 const int mine = (int)blockIdx.x % sub, shares = cuts_in * use, share = (live * W + shares - 1) / shares;
                 if (mine < use) {
                     first = ((b - 1 - c0) * use + mine) * share;

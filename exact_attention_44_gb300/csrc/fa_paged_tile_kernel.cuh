@@ -628,10 +628,10 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     bool pads = false;
     // With few sequences the K producer's warp finds the range by itself; else
     // the CTA together.  (The search's area is the roles' hand-over area.)
-    if (p.Z > 32 || warp == 0)
+    if (!p.few || warp == 0)
         walk = paged_range<T::BN, 1>(p, reinterpret_cast<PagedFind<1>*>(hand), (int)blockIdx.x / p.team, 0,
                                      threadIdx.x == 0 && blockIdx.x % p.team == 0, pads);
-    if (p.Z > 32) __syncthreads();
+    if (!p.few) __syncthreads();
 
     constexpr int SOFTMAX_END = 4 + 4 * T::NG;
     if (warp == 0) {
