@@ -37,13 +37,17 @@ struct TileTraits : Traits<D_> {
     static constexpr int OFF_MISC = Base::OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_SEG = OFF_MISC + 16;
     static constexpr int SEG_END = OFF_SEG + SEGS * 48;
-    // staging of the epilogue: 32 rows x 64 bytes a warp
+    // staging of the output: 32 rows x 32 bytes a softmax warp
     static constexpr int OFF_STAGE = D_ >= 64 ? Base::OFF_OST : (SEG_END + 15) / 16 * 16;
-    static constexpr int SMEM_USED = D_ >= 64 ? SEG_END : OFF_STAGE + 4 * 2048;
+    static constexpr int SMEM_USED = D_ >= 64 ? SEG_END : OFF_STAGE + 4 * Base::NG * 1024;
+    static_assert(D_ < 64 || 4 * Base::NG * 1024 <= BM * Base::SW, "the staging fits");
     static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    // four warps for the copies and products, then the softmax warps, which also write O
+    static constexpr int THREADS = 32 * (4 + 4 * Base::NG);
     static __device__ __forceinline__ uint32_t bar_count(int i) {
-        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return Base::THREADS / 32 - 1;
+        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return THREADS / 32 - 1;
+        if (i == Base::B_OFREE) return 4 * Base::NG;  // one arrival a warp
         if (i >= B_VFIX) return 1;
         return Base::bar_count(i);
     }
@@ -70,22 +74,34 @@ __device__ __forceinline__ void seg_put(volatile int* ring, const PagedSeg& g, b
     }
     __syncwarp();
 }
-// Segment n of the ring; ok: false when the wait ran out or another role gave
-// up.  Returns false at the end of the range.  WARP: the whole warp calls, else
-// its one active lane.
-template <int D, bool WARP, typename Bar>
-__device__ __forceinline__ bool seg_get(volatile const int* ring, PagedSeg& g, uint32_t n, Bar bar, const Ctl& ctl,
-                                        bool& ok, bool* pads = nullptr) {
-    using T = TileTraits<D>;
-    const uint32_t full = bar(T::B_SEGFULL + n % T::SEGS), parity = (n / T::SEGS) & 1u;
-    ok = WARP ? warp_wait_phase(full, parity, ctl, SITE_SEG_FULL) : wait_phase(full, parity, ctl, SITE_SEG_FULL);
-    if (!ok) return false;
-    volatile const int* s = ring + (n % T::SEGS) * (sizeof(SegMsg) / 4);
+template <int D>
+__device__ __forceinline__ void seg_read(volatile const int* ring, PagedSeg& g, uint32_t n) {
+    volatile const int* s = ring + (n % TileTraits<D>::SEGS) * (sizeof(SegMsg) / 4);
     g.z = s[0], g.hk = s[1], g.jb = s[2], g.je = s[3], g.slot = s[4];
     g.len = s[5], g.nl = s[6], g.row0 = s[7], g.rows = s[8];
-    if (pads != nullptr) *pads = s[9] != 0;
+}
+// WARP: the whole warp calls, else its one active lane.
+template <int D, bool WARP, typename Bar>
+__device__ __forceinline__ void seg_release(uint32_t n, Bar bar) {
     if (WARP) __syncwarp();
-    if (!WARP || threadIdx.x % 32 == 0) ptx::mbar_arrive(bar(T::B_SEGFREE + n % T::SEGS));
+    if (!WARP || threadIdx.x % 32 == 0) ptx::mbar_arrive(bar(TileTraits<D>::B_SEGFREE + n % TileTraits<D>::SEGS));
+}
+// Waits for segment n of the ring; false when the wait ran out or another role gave up.
+template <int D, bool WARP, typename Bar>
+__device__ __forceinline__ bool seg_wait(uint32_t n, Bar bar, const Ctl& ctl) {
+    using T = TileTraits<D>;
+    const uint32_t full = bar(T::B_SEGFULL + n % T::SEGS), parity = (n / T::SEGS) & 1u;
+    return WARP ? warp_wait_phase(full, parity, ctl, SITE_SEG_FULL) : wait_phase(full, parity, ctl, SITE_SEG_FULL);
+}
+// The next segment of a role that needs it no longer once it has read it; false
+// at the end of the range, or (ok false) when the wait ran out.
+template <int D, bool WARP, typename Bar>
+__device__ __forceinline__ bool seg_get(volatile const int* ring, PagedSeg& g, uint32_t n, Bar bar, const Ctl& ctl,
+                                        bool& ok) {
+    ok = seg_wait<D, WARP>(n, bar, ctl);
+    if (!ok) return false;
+    seg_read<D>(ring, g, n);
+    seg_release<D, WARP>(n, bar);
     return g.je > 0;
 }
 
@@ -371,9 +387,104 @@ __device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int len, int
     return bits;
 }
 
+// One softmax warp's share of a finished tile or part: its 32 rows, columns h *
+// D / NG .. of O / l in the output type, or in fp32 with the base-2
+// log-sum-exps for the merge.  They go out through the warp's staging, 32
+// bytes of a row at a time, permuted against bank conflicts: two lanes write a
+// row, so that a store instruction writes 16 full sectors instead of 32 halves.
 template <int D, bool BF16>
-__device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t bar0, uint32_t tmem, float* hand, float* red,
-                             int h, const Ctl& ctl) {
+__device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg& sg, uint32_t sbase, uint32_t bar0,
+                                            uint32_t tmem, const float* ls, float m, int h) {
+    using T = TileTraits<D>;
+    constexpr int COLS = D / T::NG;  // of this warp
+    const int lane = threadIdx.x % 32, quad = (threadIdx.x / 32) % 4, row = quad * 32 + lane;
+    const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O + h * COLS;
+    const uint32_t stage = sbase + T::OFF_STAGE + (uint32_t)(h * 4 + quad) * 1024u;
+    float l = 0.f;
+#pragma unroll
+    for (int g = 0; g < T::NG; ++g) l += ls[g * BM + row];
+    const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
+    const bool part = sg.slot >= 0, live = row < sg.rows;
+    float* slot_base = p.scratch + (int64_t)max(sg.slot, 0) * p.slot_floats;
+    auto o_row = [&](int r) -> uint16_t* {  // row r of the tile in O
+        const int grow = sg.row0 + r, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
+        return static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h + t * p.so_n + h * COLS;
+    };
+    if (h == 0 && live) {
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        if (part) {
+            slot_base[p.tile_rows * D + row] = lse2;
+        } else if (p.lse != nullptr) {
+            const int grow = sg.row0 + row, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
+            p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
+        }
+    }
+    if constexpr (COLS >= 16) {
+        // 32 bytes of each row, at byte `at` of the columns of this warp
+        auto write_out = [&](const uint32_t (&w)[8], int at) {
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                ptx::st_shared_v4(stage + lane * 32 + ((x ^ ((lane >> 2) & 1)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2],
+                                  w[4 * x + 3]);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int rw = i * 16 + lane / 2, lp = lane % 2, r = quad * 32 + rw;
+                if (r >= sg.rows) continue;
+                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(slot_base + r * D + h * COLS) : reinterpret_cast<uint8_t*>(o_row(r));
+                *reinterpret_cast<uint4*>(dst + at + lp * 16) = ld_shared_v4(stage + rw * 32 + ((lp ^ ((rw >> 2) & 1)) << 4));
+            }
+        };
+#pragma unroll 1
+        for (int c = 0; c < COLS; c += 16) {
+            uint32_t r[16], w[8];
+            ptx::tmem_ld16(o_addr + c, r);
+            if (c + 16 == COLS) {
+                // all of this warp's O has been read: the next tile may overwrite it
+                ptx::tc_fence_before();
+                ptx::mbar_arrive_warp(bar0 + 8u * T::B_OFREE);
+            }
+            if (part) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(__uint_as_float(r[half * 8 + x]) * inv);
+                    write_out(w, (c + half * 8) * 4);
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < 8; ++x)
+                    w[x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
+                write_out(w, c * 2);
+            }
+        }
+    } else {
+        uint32_t r[COLS];
+        if constexpr (COLS == 8) ptx::tmem_ld8(o_addr, r);
+        else ptx::tmem_ld4(o_addr, r);
+        ptx::tc_fence_before();
+        ptx::mbar_arrive_warp(bar0 + 8u * T::B_OFREE);
+        if (!live) return;
+        if (part) {
+#pragma unroll
+            for (int x = 0; x < COLS; x += 4)
+                *reinterpret_cast<float4*>(slot_base + row * D + h * COLS + x) =
+                    make_float4(__uint_as_float(r[x]) * inv, __uint_as_float(r[x + 1]) * inv,
+                                __uint_as_float(r[x + 2]) * inv, __uint_as_float(r[x + 3]) * inv);
+        } else {
+#pragma unroll
+            for (int x = 0; x < COLS; x += 4)
+                *reinterpret_cast<uint2*>(o_row(row) + x) =
+                    make_uint2(pack2<BF16>(__uint_as_float(r[x]) * inv, __uint_as_float(r[x + 1]) * inv),
+                               pack2<BF16>(__uint_as_float(r[x + 2]) * inv, __uint_as_float(r[x + 3]) * inv));
+        }
+    }
+}
+
+template <int D, bool BF16>
+__device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+                             float* hand, float* red, int h, const Ctl& ctl) {
     using T = TileTraits<D>;
     constexpr int BN = T::BN, NG = T::NG, HC = BN / NG;
     static_assert(HC == 32, "a thread holds 32 positions");
@@ -390,8 +501,9 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t 
         const uint32_t* bits_row;
         {
             PagedSeg sg;
-            bool ok;
-            if (!seg_get<D, true>(ring, sg, ntile, bar, ctl, ok)) return;
+            if (!seg_wait<D, true>(ntile, bar, ctl)) return;
+            seg_read<D>(ring, sg, ntile);  // (read again for the output: it is not kept in registers)
+            if (sg.je == 0) break;
             jb = sg.jb, je = sg.je, len = sg.len, nl = sg.nl;
             tok = min(p.by_g(sg.row0 + row), p.T - 1);
             idle = quad * 32 >= sg.rows;  // none of the warp's rows holds a token
@@ -407,6 +519,8 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t 
                 // (P of these rows stays what S left there: rows do not mix)
                 ptx::mbar_arrive(bar(T::B_RED + b));
                 ptx::mbar_arrive(bar(T::B_PFULL + r));
+                // not ahead of the others: an arrival for block step + 2 must not count for this one
+                if (!warp_wait_phase(bar(T::B_RED + b), ph, ctl, SITE_MAX_XCHG)) return;
                 ++step;
                 continue;
             }
@@ -486,105 +600,22 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t 
             l = l * alpha + (sl + sh);
             ++step;
         }
+        // The groups share m (the reference is the same for all) and add their l.
         const uint32_t slot = ntile & 1u;
-        if (!warp_wait_phase(bar(T::B_EPIEMPTY + slot), ((ntile >> 1) & 1u) ^ 1u, ctl, SITE_EPI_EMPTY)) return;
-        if (h == 0) hand[slot * T::HAND_ROWS * BM + row] = m;
-        hand[slot * T::HAND_ROWS * BM + (1 + h) * BM + row] = l;
+        float* ls = hand + slot * NG * BM;
+        ls[h * BM + row] = l;
         ptx::mbar_arrive(bar(T::B_EPIFULL + slot));
-    }
-}
-
-template <int D, bool BF16>
-__device__ void tile_epilogue(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
-                              const float* hand, const Ctl& ctl) {
-    using T = TileTraits<D>;
-    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    const int quad = (threadIdx.x / 32) % 4;
-    const int row = quad * 32 + threadIdx.x % 32;
-    const int lane = threadIdx.x % 32;
-    const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O;
-    const uint32_t stage = sbase + T::OFF_STAGE + (uint32_t)quad * 2048u;
-    uint32_t step = 0, ntile = 0;
-    PagedSeg sg;
-    bool ok, pads = false;
-    for (; seg_get<D, true>(ring, sg, ntile, bar, ctl, ok, &pads); ++ntile) {
-        step += sg.je - sg.jb;
-        const uint32_t slot = ntile & 1u;
         if (!warp_wait_phase(bar(T::B_EPIFULL + slot), (ntile >> 1) & 1u, ctl, SITE_EPI_FULL)) return;
-        const float m = hand[slot * T::HAND_ROWS * BM + row];
-        float l = 0.f;
-#pragma unroll
-        for (int g2 = 0; g2 < T::NG; ++g2) l += hand[slot * T::HAND_ROWS * BM + (1 + g2) * BM + row];
-        ptx::mbar_arrive(bar(T::B_EPIEMPTY + slot));
         const uint32_t g = step - 1;
         if (!warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(g)), rphase<T::SR>(g), ctl, SITE_PV_DONE)) return;
         ptx::tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
-        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        // The warp's rows go out through its staging, 64 bytes of a row at a time: a
-        // thread fills its row's pieces (permuted against bank conflicts), then PIECES
-        // lanes write a row, so that a store instruction touches eight lines instead of
-        // 32 (which took 2.5 us for a part of 128 rows).
-        const bool part = sg.slot >= 0;
-        float* slot_base = p.scratch + (int64_t)max(sg.slot, 0) * p.slot_floats;
-        if (row < sg.rows) {
-            const int grow = sg.row0 + row, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
-            if (part) slot_base[p.tile_rows * D + row] = lse2;
-            else if (p.lse != nullptr) p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
-        }
-        // Columns c0 .. of the warp's rows, PIECES 16-byte pieces a row, are in w: write
-        // them out at byte `at` of each row.
-        auto write_out = [&](auto pieces, const uint32_t (&w)[16], int at) {
-            constexpr int PIECES = decltype(pieces)::value, RI = 32 / PIECES;  // rows an instruction
-            const int lr = lane / PIECES, lp = lane % PIECES;
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < PIECES; ++x)
-                ptx::st_shared_v4(stage + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2],
-                                  w[4 * x + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < PIECES; ++i) {
-                const int rw = i * RI + lr, r = quad * 32 + rw;
-                if (r >= sg.rows) continue;
-                uint8_t* dst;
-                if (part) {
-                    dst = reinterpret_cast<uint8_t*>(slot_base + r * D);
-                } else {
-                    const int grow = sg.row0 + r, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
-                    dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h +
-                                                     t * p.so_n);
-                }
-                *reinterpret_cast<uint4*>(dst + at + lp * 16) = ld_shared_v4(stage + rw * 64 + ((lp ^ ((rw >> 1) & 3)) << 4));
-            }
-        };
-        constexpr int C = D < 32 ? D : 32;  // columns a round
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += C) {
-            uint32_t w[16];
-#pragma unroll
-            for (int i = 0; i < C / 16; ++i) {
-                uint32_t r[16];
-                ptx::tmem_ld16(o_addr + c0 + i * 16, r);
-                if (i == C / 16 - 1 && c0 + C == D) {
-                    // all of O has been read: the MMA warp may overwrite it
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(bar(T::B_OFREE));
-                }
-                if (part) {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(__uint_as_float(r[x]) * inv);
-                    write_out(std::integral_constant<int, 4>{}, w, (c0 + i * 16) * 4);
-                } else {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        w[i * 8 + x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
-                }
-            }
-            if (!part) write_out(std::integral_constant<int, C / 8>{}, w, c0 * 2);
-        }
+        PagedSeg sg;
+        seg_read<D>(ring, sg, ntile);
+        tile_output<D, BF16>(p, sg, sbase, bar0, tmem, ls, m, h);
+        seg_release<D, true>(ntile, bar);
     }
-    if (ok && pads) paged_fill<D>(p, (int)blockIdx.x * 4 + quad, (int)gridDim.x * 4);
+    if (ring[(ntile % T::SEGS) * (sizeof(SegMsg) / 4) + 9] != 0)  // pads, from the end's message
+        paged_fill<D>(p, (int)blockIdx.x * 4 * NG + (int)threadIdx.x / 32 - 4, (int)gridDim.x * 4 * NG);
 }
 
 template <int D, bool BF16>
@@ -633,7 +664,6 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
                                      threadIdx.x == 0 && blockIdx.x % p.team == 0, pads);
     if (!p.few) __syncthreads();
 
-    constexpr int SOFTMAX_END = 4 + 4 * T::NG;
     if (warp == 0) {
         tile_producer_qk<D>(&tmQ, &tmK, p, walk, pads, ring, sbase, bar0, ctl);
     } else if (warp == 3) {
@@ -642,10 +672,8 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
         if (lane == 0) tile_mma_qk<D, BF16>(p, ring, sbase, bar0, tmem, ctl);
     } else if (warp == 2) {
         if (lane == 0) tile_mma_pv<D, BF16>(p, ring, sbase, bar0, tmem, ctl);
-    } else if (warp < SOFTMAX_END) {
-        tile_softmax<D, BF16>(p, ring, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
     } else {
-        tile_epilogue<D, BF16>(p, ring, sbase, bar0, tmem, hand, ctl);
+        tile_softmax<D, BF16>(p, ring, sbase, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
     }
 
     ptx::tc_fence_before();
