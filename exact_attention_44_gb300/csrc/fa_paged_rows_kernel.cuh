@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(32 * ROWS_WARPS, RowsTraits<D>::CTAS)
                 float* slot = p.scratch + (int64_t)sg.slot * p.slot_floats;
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)
-                    *reinterpret_cast<float2*>(slot + r * D + 8 * x + 2 * (lane % 4)) =
+                    *reinterpret_cast<float2*>(slot + (x * p.tile_rows + r) * 8 + 2 * (lane % 4)) =
                         make_float2(o[x][2 * y] * inv, o[x][2 * y + 1] * inv);
                 if (lane % 4 == 0) slot[p.tile_rows * D + r] = lse2;
             } else {

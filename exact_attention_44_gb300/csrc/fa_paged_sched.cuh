@@ -345,7 +345,10 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 // the ranges of teams b - 1 and b.  If it falls inside a tile group, the
 // member's tile of it has its parts with the teams c0 (slot 2c + 1) and c0 + 1
 // .. c1 (slots 2c); the cuts inside the tile are c0 + 1 .. c1, and each of
-// their blocks merges one share of the tile's (row, four columns) items.  With
+// their blocks merges one share of the tile's (four columns, row) items.  A
+// part is [D / 8][tile_rows][8] floats of O / l, as both kernels' threads hold
+// it, then a log-sum-exp per row; items follow that order, so that a warp's
+// loads are contiguous.  With
 // lambda_s the base-2 log-sum-exp of part s and O_s its O / l,
 //     lambda = log2 sum_s 2^lambda_s,   O = sum_s 2^(lambda_s - lambda) O_s.
 // in one pass with a running maximum, so that a part's lambda and its O are one
@@ -391,13 +394,13 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
         }
         if (tid == 0) {
             what[0] = first, what[1] = last, what[2] = parts, what[3] = cut.x, what[4] = cut.y, what[5] = row0;
-            what[6] = 2 * (c0 * p.team + member);
+            what[6] = 2 * (c0 * p.team + member), what[7] = live;
         }
     }
     __syncthreads();
     const int first = what[0], last = what[1], parts = what[2];
     if (first >= last) return;
-    const int z = what[3], hk = what[4], row0 = what[5];
+    const int z = what[3], hk = what[4], row0 = what[5], live = what[7];
     // the first part is in slot 2 c + 1 of its worker, the others in slots 2 c: offsets in
     // floats, below 2^32 (two slots a worker, at most 1280 x 33 KB or 152 x 132 KB each)
     const float* base = p.scratch + (int64_t)what[6] * p.slot_floats;
@@ -408,7 +411,9 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     for (int i0 = first; i0 < last; i0 += NT / spl) {
         const int i = i0 + tid / spl;
         const bool ok = i < last;
-        const int r = ok ? i / W : 0, c = i % W;
+        // items: eight-column groups, in each the live rows, in each the two halves
+        const int kg = ok ? i / (2 * live) : 0, in = ok ? i - kg * 2 * live : 0, r = in / 2, c = 2 * kg + in % 2;
+        const int at = (kg * p.tile_rows + r) * 2 + in % 2;
         float mx = -INFINITY, den = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         constexpr int U = 4;
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
                 const int x = x0 + u * spl;
                 if (x < parts) {
                     const float* from = base + (x == 0 ? slot0 : (uint32_t)x * step);
-                    v[u] = __ldcg(reinterpret_cast<const float4*>(from) + i);
+                    v[u] = __ldcg(reinterpret_cast<const float4*>(from) + at);
                     l[u] = __ldcg(from + lses + r);
                 }
             }

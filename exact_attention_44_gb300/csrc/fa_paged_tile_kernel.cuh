@@ -389,9 +389,10 @@ __device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int len, int
 
 // One softmax warp's share of a finished tile or part: its 32 rows, columns h *
 // D / NG .. of O / l in the output type, or in fp32 with the base-2
-// log-sum-exps for the merge.  They go out through the warp's staging, 32
-// bytes of a row at a time, permuted against bank conflicts: two lanes write a
-// row, so that a store instruction writes 16 full sectors instead of 32 halves.
+// log-sum-exps for the merge.  A part's layout (eight columns of all rows after
+// one another) takes the registers as they are; O goes out through the warp's
+// staging, 32 bytes of a row at a time, permuted against bank conflicts: two
+// lanes write a row, so that a store instruction writes 16 full sectors.
 template <int D, bool BF16>
 __device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg& sg, uint32_t sbase, uint32_t bar0,
                                             uint32_t tmem, const float* ls, float m, int h) {
@@ -419,6 +420,12 @@ __device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg
             p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
         }
     }
+    auto part_store = [&](int c, const uint32_t* r) {  // four columns of this row
+        const int col = h * COLS + c;
+        *reinterpret_cast<float4*>(slot_base + ((col / 8) * p.tile_rows + row) * 8 + col % 8) =
+            make_float4(__uint_as_float(r[0]) * inv, __uint_as_float(r[1]) * inv, __uint_as_float(r[2]) * inv,
+                        __uint_as_float(r[3]) * inv);
+    };
     if constexpr (COLS >= 16) {
         // 32 bytes of each row, at byte `at` of the columns of this warp
         auto write_out = [&](const uint32_t (&w)[8], int at) {
@@ -432,13 +439,12 @@ __device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg
             for (int i = 0; i < 2; ++i) {
                 const int rw = i * 16 + lane / 2, lp = lane % 2, r = quad * 32 + rw;
                 if (r >= sg.rows) continue;
-                uint8_t* dst = part ? reinterpret_cast<uint8_t*>(slot_base + r * D + h * COLS) : reinterpret_cast<uint8_t*>(o_row(r));
-                *reinterpret_cast<uint4*>(dst + at + lp * 16) = ld_shared_v4(stage + rw * 32 + ((lp ^ ((rw >> 2) & 1)) << 4));
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(o_row(r)) + at + lp * 16) = ld_shared_v4(stage + rw * 32 + ((lp ^ ((rw >> 2) & 1)) << 4));
             }
         };
 #pragma unroll 1
         for (int c = 0; c < COLS; c += 16) {
-            uint32_t r[16], w[8];
+            uint32_t r[16];
             ptx::tmem_ld16(o_addr + c, r);
             if (c + 16 == COLS) {
                 // all of this warp's O has been read: the next tile may overwrite it
@@ -446,13 +452,11 @@ __device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg
                 ptx::mbar_arrive_warp(bar0 + 8u * T::B_OFREE);
             }
             if (part) {
+                if (live)
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-#pragma unroll
-                    for (int x = 0; x < 8; ++x) w[x] = __float_as_uint(__uint_as_float(r[half * 8 + x]) * inv);
-                    write_out(w, (c + half * 8) * 4);
-                }
+                    for (int x = 0; x < 16; x += 4) part_store(c + x, r + x);
             } else {
+                uint32_t w[8];
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
                     w[x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
@@ -468,10 +472,7 @@ __device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg
         if (!live) return;
         if (part) {
 #pragma unroll
-            for (int x = 0; x < COLS; x += 4)
-                *reinterpret_cast<float4*>(slot_base + row * D + h * COLS + x) =
-                    make_float4(__uint_as_float(r[x]) * inv, __uint_as_float(r[x + 1]) * inv,
-                                __uint_as_float(r[x + 2]) * inv, __uint_as_float(r[x + 3]) * inv);
+            for (int x = 0; x < COLS; x += 4) part_store(x, r + x);
         } else {
 #pragma unroll
             for (int x = 0; x < COLS; x += 4)
