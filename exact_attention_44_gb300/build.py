@@ -7,7 +7,7 @@ ignored).  A content hash of the sources, headers and flags is stored next to
 the library; an unchanged tree is not rebuilt.  --debug-checks builds a
 second library, _build/checks/libfa.so, whose forward kernels check every
 unit they decode against the launch's sizes (FA_DEBUG_CHECKS=1).  Where torch
-is installed, the binding of the paged-cache calls (_paged_ext.so, a CPython
+with CUDA is installed, the binding of the paged-cache calls (_paged_ext.so, a CPython
 extension over torch's headers) is built beside libfa.so with g++.
 """
 from __future__ import annotations
@@ -62,12 +62,23 @@ def _tree_hash(extra_flags: list[str]) -> str:
     return h.hexdigest()
 
 
-def _ext_command(cc: str, out: str) -> list[str] | None:
-    """The command that builds the paged-cache binding, or None without torch (which is not imported)."""
+def _torch_dir() -> str | None:
+    """Where torch with CUDA is installed (it is not imported), or None."""
     spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
-        return None
-    torch = list(spec.submodule_search_locations)[0]
+    for d in spec.submodule_search_locations or [] if spec is not None else []:
+        if os.path.exists(os.path.join(d, "lib", "libc10_cuda.so")):
+            return d
+    return None
+
+
+def _ext_stamp(torch: str) -> str:
+    """What the binding is tied to: this interpreter, and the torch whose headers it was built over."""
+    with open(os.path.join(torch, "version.py")) as f:
+        return sys.version + "\n" + torch + "\n" + f.read()
+
+
+def _ext_command(torch: str, cc: str, out: str) -> list[str]:
+    """The command that builds the paged-cache binding."""
     inc = os.path.join(torch, "include")
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", os.path.join(CSRC, "paged_ext.cpp"), "-o", out,
             f"-I{INCLUDE}", f"-I{sysconfig.get_paths()['include']}", f"-isystem{inc}",
@@ -90,9 +101,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     os.makedirs(build_dir, exist_ok=True)
     digest = _tree_hash(extra_flags)
     stamp = lib_path + ".hash"
-    have_torch = importlib.util.find_spec("torch") is not None
+    torch = None if debug_checks else _torch_dir()
+    if torch is not None:
+        digest += "\n" + _ext_stamp(torch)
     if not force and os.path.exists(lib_path) and os.path.exists(stamp) and open(stamp).read() == digest and (
-            debug_checks or not have_torch or os.path.exists(EXT)):
+            torch is None or os.path.exists(EXT)):
         return lib_path
     cc = nvcc()
     jobs = []
@@ -104,9 +117,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         jobs.append((src, obj, cmd))
 
     ext_tmp = EXT + f".tmp{os.getpid()}"
-    ext = None if debug_checks else _ext_command(cc, ext_tmp)
-    if ext is not None:
-        jobs.append(("paged_ext.cpp", ext_tmp, ext))
+    if torch is not None:
+        jobs.append(("paged_ext.cpp", ext_tmp, _ext_command(torch, cc, ext_tmp)))
 
     def run(job):
         src, obj, cmd = job
@@ -130,7 +142,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if r.returncode != 0:
         raise RuntimeError(f"libfa link failed:\n{r.stdout}{r.stderr}")
     os.replace(tmp, lib_path)
-    if ext is not None:
+    if torch is not None:
         os.replace(ext_tmp, EXT)
     with open(stamp, "w") as f:
         f.write(digest)
