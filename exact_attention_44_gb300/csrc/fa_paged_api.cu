@@ -347,7 +347,7 @@ fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
     if (x.room < 0) return FA_ERR_INVALID_ARG;
     fa_status st = check_cache(c, true);
     if (st != FA_OK) return st;
-    if (c.Z > 8192 || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||
+    if (c.Z > 8192 || c.P > (1 << 30) || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||
         (int64_t)c.L * 2 * c.Hkv > INT32_MAX || (int64_t)c.page_size * (c.D / 8) > INT32_MAX)
         return FA_ERR_UNSUPPORTED;
     if ((st = check_ints(x.missing, false)) != FA_OK) return st;

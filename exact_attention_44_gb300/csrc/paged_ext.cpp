@@ -174,6 +174,11 @@ fa_status unlocked(F&& fn) {
     return st;
 }
 
+// A workspace argument: its bytes are counted, so they must lie together.
+void check_workspace(const at::Tensor* t) {
+    if (t != nullptr && !t->is_contiguous()) value_error("workspace must be contiguous");
+}
+
 at::Tensor scratch(size_t bytes, const at::Tensor& like) {
     return at::empty({(int64_t)bytes}, like.options().dtype(at::kByte));
 }
@@ -239,6 +244,7 @@ PyObject* fwd_paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
         }
         const int want = PyObject_IsTrue(a[12]);
         if (want < 0) throw python_error();
+        check_workspace(ws_arg);
         const int dev = cuda_device("fa_fwd_paged", q, {&k, &v, &table, &lens, o_arg, lse_arg, news, mask, ws_arg});
         const Place place(a[11], dev, {&q, &k, &v, &table, &lens, o_arg, lse_arg, news, mask, ws_arg});
         at::Tensor o = o_arg != nullptr ? *o_arg : at::empty(q.sizes(), q.options());
@@ -346,6 +352,7 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (source != nullptr) check_ints(*source, "source", {Z});
         if (missing != nullptr) check_ints(*missing, "missing", {1});
         x.room = int_arg(a[6], "room");
+        check_workspace(ws_arg);
         const int dev = cuda_device("fa_cache_fork", kc, {&vc, &table, &lens, &refs, source, missing, ws_arg});
         const Place place(a[9], dev, {&kc, &vc, &table, &lens, &refs, source, missing, ws_arg});
         at::Tensor ws;

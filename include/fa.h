@@ -556,7 +556,7 @@ fa_status fa_cache_commit(const fa_cache_commit_args* args, cudaStream_t stream)
  * Valid state: a row's entries are its ceil(len / page_size) pages, then
  * pages of room, then -1; a page with room to write belongs to one sequence.
  * fa_cache_fork keeps it so.  A source outside -1 .. Z - 1 is recorded as
- * FA_ERR_PAGE and the sequence stays.  Z <= 8192.
+ * FA_ERR_PAGE and the sequence stays.  Z <= 8192, P and room <= 2^30, Z * max_pages < 2^31.
  */
 typedef struct {
     fa_paged_cache cache;

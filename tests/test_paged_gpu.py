@@ -78,6 +78,12 @@ def test_groups(Hq, Hkv, T):
     check(3, [70, 5, 129], Hq, Hkv, T, 64, 16, "fp16")
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(100, 1), (128, 1), (260, 2), (129, 1)])
+@pytest.mark.parametrize("T,D", [(1, 256), (2, 256), (3, 128)])
+def test_large_groups(Hq, Hkv, T, D):
+    check(34, [70, 5, 129, 400], Hq, Hkv, T, D, 16, "bf16")
+
+
 @pytest.mark.parametrize("T", [2, 17, 31, 32, 33, 64, 65, 100])
 @pytest.mark.parametrize("D,page", [(64, 16), (128, 32), (256, 48)])
 def test_trees(T, D, page):

@@ -1,6 +1,7 @@
 """The paged-cache entry points refuse bad arguments on the host, before anything is enqueued (no
 GPU needed), and the plain statement of fork's bookkeeping keeps its invariants."""
 import ctypes
+import importlib
 
 import numpy as np
 import pytest
@@ -140,6 +141,7 @@ def _fork(lib, *, refs=PTR, src=PTR, miss=None, room=1, ws=PTR, wsb=1 << 40, L=2
     (dict(src=PTR + 2), fa.FA_ERR_ALIGNMENT), (dict(miss=PTR + 2), fa.FA_ERR_ALIGNMENT),
     (dict(kl=4), fa.FA_ERR_ALIGNMENT), (dict(ws=None), fa.FA_ERR_WORKSPACE), (dict(wsb=16), fa.FA_ERR_WORKSPACE),
     (dict(ws=PTR + 8), fa.FA_ERR_WORKSPACE), (dict(Z=0), fa.FA_OK),
+    (dict(L=0, P=(1 << 30) + 1), fa.FA_ERR_UNSUPPORTED), (dict(room=(1 << 30) + 1), fa.FA_ERR_UNSUPPORTED),
 ])
 def test_fork_arguments(lib, kw, code):
     assert _fork(lib, **kw) == code
@@ -206,6 +208,29 @@ def test_python_cache_checks():
                        (lambda: fa.fa_cache_fork(kc, vc, tb, ln, torch.zeros(9, **i32)), ValueError)]:
         with pytest.raises(error):
             bad()
+
+
+def test_python_workspace_must_be_contiguous():
+    t, ws = _tensors(), torch.zeros(1, dtype=torch.uint8).expand(1 << 30)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        fa.fa_fwd_paged(**t, workspace=ws)
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        fa.fa_cache_fork(t["k_cache"], t["v_cache"], t["block_table"], t["seq_lens"], torch.zeros(9, dtype=torch.int32),
+                         workspace=ws)
+
+
+def test_binding_is_built_for_torch_with_cuda_only(tmp_path, monkeypatch):
+    from types import SimpleNamespace
+
+    b = importlib.import_module("exact_attention_44_gb300.build")
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: None)
+    assert b._torch_dir() is None
+    spec = SimpleNamespace(submodule_search_locations=[str(tmp_path)])
+    monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: spec)
+    assert b._torch_dir() is None
+    (tmp_path / "lib").mkdir()
+    (tmp_path / "lib" / "libc10_cuda.so").touch()
+    assert b._torch_dir() == str(tmp_path)
 
 
 # ------------------------------------------------------------- the plain statements
