@@ -64,6 +64,7 @@ struct PagedParams {
     int Z, Hq, Hkv, G, T;      // G = Hq / Hkv
     int page, M, P;            // slots a page, table columns, pages of the cache
     FastDiv by_g, by_page, by_tile_rows, by_team;
+    bool wide_o;               // every row of O starts at a multiple of 32 bytes
     bool few;                  // at most 32 sequences, and all block counts fit in 31 bits
     int cap;                   // M * page: positions a sequence can have
     int tile_rows;             // query rows of a tile (a row is a (token, head of the group) pair, heads innermost)

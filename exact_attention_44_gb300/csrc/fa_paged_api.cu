@@ -265,6 +265,8 @@ fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
     p.by_page = fa::FastDiv(p.page);
     p.by_tile_rows = fa::FastDiv(p.tile_rows);
     p.by_team = fa::FastDiv(p.team);
+    p.wide_o = !misaligned(x.o, 32) && (Z == 1 || p.so_z % 16 == 0) && (Hq == 1 || p.so_h % 16 == 0) &&
+               (T == 1 || p.so_n % 16 == 0);
     p.few = Z <= 32 && blocks < (int64_t(1) << 30);
     p.cuts = static_cast<char*>(x.workspace) + paged_slot_bytes(D, f.sms);
     err = launch_paged(D, a, bf16);

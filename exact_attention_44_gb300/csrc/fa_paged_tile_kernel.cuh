@@ -19,15 +19,20 @@
 // barriers' counts.  Every wait is bounded as in fa_fwd_kernel.cuh.
 //
 // What bounds it.  With one tile a kv head (up to 128 rows), DRAM: a block's K
-// and V are 64 KB at D = 128, 1.49 us of an SM's share of 6.7 TB/s, against 0.78
-// us that the chain S -> softmax -> P takes a block (as in the contiguous
-// forward; 1.06 us with 16-position pages, whose 32 boxes a block the copy unit
-// takes one after another).  With two tiles the two bounds meet: 32 sequences
-// of 4096-8192 positions x 64 tokens x 4 heads (848 MB, 207 GFLOP) take 187 us,
-// 4.5 TB/s and 1.1 PFLOP/s.  Short calls are bounded by the way from launch to
-// the first products (about 8 us: lengths, block table, first copies, first
-// block) and by the merge of the parts (about 7 us; 8 sequences of 500-3000 x
-// 32 tokens: 25 us in all, 10 us of DRAM time).
+// and V are 64 KB at D = 128, 1.49 us of an SM's share of 6.7 TB/s (1.31 us
+// measured), against 0.8 us that the chain S -> softmax -> P takes a block, as
+// in the contiguous forward (1.06 us with 16-position pages, whose 32 boxes a
+// block the copy unit takes one after another).  With two tiles the two bounds
+// meet: 32 sequences of 4096-8192 positions x 64 tokens x 4 heads (848 MB, 207
+// GFLOP) take 183 to 192 us, 4.5 TB/s and 1.1 PFLOP/s at 1.2 kW, where the clock
+// has fallen from 2.07 to 1.85 GHz (168 us with all pages in L2; a third slot
+// in the rings of K and V instead of Q's second changes nothing).  Between two
+// tiles a softmax warp loses 2.6 us (its last product 0.6, the output 1.2, the
+// next tile's first scores 0.5), which short contexts feel: 128 sequences of
+// 300-400 x 128 tokens x 4 heads take 187 us.  Short calls are bounded by the way
+// from launch to the first products (about 8 us: lengths, block table, first
+// copies, first block) and by the merge of the parts (about 6 us; 8 sequences of
+// 500-3000 x 32 tokens: 23 us in all, 10 us of DRAM time).
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
@@ -43,13 +48,10 @@ struct TileTraits : Traits<D_> {
     static constexpr int B_SEGFULL = B_VFIX + 2;              // [SEGS] segment written (K producer)
     static constexpr int B_SEGFREE = B_SEGFULL + SEGS;        // [SEGS] read by every other warp
     static constexpr int NUM_BARS = B_SEGFREE + SEGS;
-    static constexpr int OFF_MISC = Base::OFF_BAR + NUM_BARS * 8;
+    static constexpr int OFF_BAR = Base::OFF_OST;             // (O is not staged)
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int OFF_SEG = OFF_MISC + 16;
-    static constexpr int SEG_END = OFF_SEG + SEGS * 48;
-    // staging of the output: 32 rows x 32 bytes a softmax warp
-    static constexpr int OFF_STAGE = D_ >= 64 ? Base::OFF_OST : (SEG_END + 15) / 16 * 16;
-    static constexpr int SMEM_USED = D_ >= 64 ? SEG_END : OFF_STAGE + 4 * Base::NG * 1024;
-    static_assert(D_ < 64 || 4 * Base::NG * 1024 <= BM * Base::SW, "the staging fits");
+    static constexpr int SMEM_USED = OFF_SEG + SEGS * 48;
     static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     // four warps for the copies and products, then the softmax warps, which also write O
@@ -374,12 +376,6 @@ __device__ void tile_mma_pv(const PagedParams& p, volatile int* ring, uint32_t s
     }
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
 // Which of positions k0 .. k0 + 31 new token t sees, as bits (row: its mask words, or nullptr).
 __device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int len, int nl, const uint32_t* row, int t, int k0) {
     const int j0 = k0 - len;  // new token of the first position (negative: before the new tokens)
@@ -398,104 +394,100 @@ __device__ __forceinline__ uint32_t seen_bits(const PagedParams& p, int len, int
     return bits;
 }
 
-// One softmax warp's share of a finished tile or part: its 32 rows, columns h *
-// D / NG .. of O / l in the output type, or in fp32 with the base-2
-// log-sum-exps for the merge.  A part's layout (eight columns of all rows after
-// one another) takes the registers as they are; O goes out through the warp's
-// staging, 32 bytes of a row at a time, permuted against bank conflicts: two
-// lanes write a row, so that a store instruction writes 16 full sectors.
-template <int D, bool BF16>
-__device__ __forceinline__ void tile_output(const PagedParams& p, const PagedSeg& sg, uint32_t sbase, uint32_t bar0,
-                                            uint32_t tmem, const float* ls, float m, int h) {
+// 32 bytes, a whole sector, in one store.
+__device__ __forceinline__ void st_global_v8(void* to, const uint32_t* r) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void st_global_v4(void* to, const uint32_t* r) {
+    *reinterpret_cast<uint4*>(to) = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// One softmax warp's share of a finished tile or part: its 32 rows (one a
+// lane), columns h * D / NG .. of O / l in the output type, or in fp32 with the
+// base-2 log-sum-exps for the merge.  Both go out as the registers hold them,
+// 32 bytes of a row at a time.  What does not need O (the sums, the addresses)
+// comes before the wait for its last product, done(); false if that ran out.
+template <int D, bool BF16, typename Done>
+__device__ __forceinline__ bool tile_output(const PagedParams& p, const PagedSeg& sg, uint32_t bar0, uint32_t tmem,
+                                            const float* ls, float m, int h, Done done) {
     using T = TileTraits<D>;
-    constexpr int COLS = D / T::NG;  // of this warp
+    constexpr int COLS = D / T::NG, STEP = COLS < 32 ? COLS : 32;  // columns of this warp, and of a round
     const int lane = threadIdx.x % 32, quad = (threadIdx.x / 32) % 4, row = quad * 32 + lane;
     const uint32_t o_addr = tmem + ((uint32_t)(quad * 32) << 16) + T::TM_O + h * COLS;
-    const uint32_t stage = sbase + T::OFF_STAGE + (uint32_t)(h * 4 + quad) * 1024u;
     float l = 0.f;
 #pragma unroll
     for (int g = 0; g < T::NG; ++g) l += ls[g * BM + row];
     const float inv = l == 0.f ? 0.f : 1.f / l;  // nothing seen: O = 0, lse = -inf
     const bool part = sg.slot >= 0, live = row < sg.rows;
-    float* slot_base = p.scratch + (int64_t)max(sg.slot, 0) * p.slot_floats;
-    auto o_row = [&](int r) -> uint16_t* {  // row r of the tile in O
-        const int grow = sg.row0 + r, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
-        return static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h + t * p.so_n + h * COLS;
-    };
-    if (h == 0 && live) {
-        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
-        if (part) {
-            slot_base[p.tile_rows * D + row] = lse2;
-        } else if (p.lse != nullptr) {
-            const int grow = sg.row0 + row, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
-            p.lse[((int64_t)sg.z * p.Hq + hq) * p.T + t] = lse2 * 0.6931471805599453f;
-        }
-    }
-    auto part_store = [&](int c, const uint32_t* r) {  // four columns of this row
-        const int col = h * COLS + c;
-        *reinterpret_cast<float4*>(slot_base + ((col / 8) * p.tile_rows + row) * 8 + col % 8) =
-            make_float4(__uint_as_float(r[0]) * inv, __uint_as_float(r[1]) * inv, __uint_as_float(r[2]) * inv,
-                        __uint_as_float(r[3]) * inv);
-    };
-    if constexpr (COLS >= 16) {
-        // 32 bytes of each row, at byte `at` of the columns of this warp
-        auto write_out = [&](const uint32_t (&w)[8], int at) {
-            __syncwarp();
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                ptx::st_shared_v4(stage + lane * 32 + ((x ^ ((lane >> 2) & 1)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2],
-                                  w[4 * x + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int rw = i * 16 + lane / 2, lp = lane % 2, r = quad * 32 + rw;
-                if (r >= sg.rows) continue;
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(o_row(r)) + at + lp * 16) = ld_shared_v4(stage + rw * 32 + ((lp ^ ((rw >> 2) & 1)) << 4));
-            }
-        };
-#pragma unroll 1
-        for (int c = 0; c < COLS; c += 16) {
-            uint32_t r[16];
-            ptx::tmem_ld16(o_addr + c, r);
-            if (c + 16 == COLS) {
-                // all of this warp's O has been read: the next tile may overwrite it
-                ptx::tc_fence_before();
-                ptx::mbar_arrive_warp(bar0 + 8u * T::B_OFREE);
-            }
-            if (part) {
-                if (live)
-#pragma unroll
-                    for (int x = 0; x < 16; x += 4) part_store(c + x, r + x);
-            } else {
-                uint32_t w[8];
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-                    w[x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
-                write_out(w, c * 2);
-            }
-        }
+    uint8_t* dst;  // this lane's row: of O, or of the part's first column group
+    float* lse;
+    if (part) {
+        float* slot = p.scratch + (int64_t)sg.slot * p.slot_floats;
+        dst = reinterpret_cast<uint8_t*>(slot + ((h * COLS / 8) * p.tile_rows + row) * 8 + h * COLS % 8);
+        lse = slot + p.tile_rows * D + row;
     } else {
-        uint32_t r[COLS];
-        if constexpr (COLS == 8) ptx::tmem_ld8(o_addr, r);
-        else ptx::tmem_ld4(o_addr, r);
-        ptx::tc_fence_before();
-        ptx::mbar_arrive_warp(bar0 + 8u * T::B_OFREE);
-        if (!live) return;
+        const int grow = sg.row0 + row, t = p.by_g(grow), hq = sg.hk * p.G + grow - t * p.G;
+        dst = reinterpret_cast<uint8_t*>(static_cast<uint16_t*>(p.o) + (int64_t)sg.z * p.so_z + hq * p.so_h + t * p.so_n + h * COLS);
+        lse = p.lse == nullptr ? nullptr : p.lse + ((int64_t)sg.z * p.Hq + hq) * p.T + t;
+    }
+    if (h == 0 && live && lse != nullptr) {
+        const float lse2 = l == 0.f ? -INFINITY : m + log2f(l);
+        *lse = part ? lse2 : lse2 * 0.6931471805599453f;
+    }
+    if (!done()) return false;
+    ptx::tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += STEP) {
+        uint32_t r[STEP];
+        __syncwarp();
+        if constexpr (STEP == 32) ptx::tmem_ld32(o_addr + c, r);
+        else if constexpr (STEP == 16) ptx::tmem_ld16(o_addr + c, r);
+        else if constexpr (STEP == 8) ptx::tmem_ld8(o_addr + c, r);
+        else ptx::tmem_ld4(o_addr + c, r);
+        if (c + STEP == COLS) {
+            // all of this warp's O has been read: the next tile may overwrite it
+            ptx::tc_fence_before();
+            ptx::mbar_arrive_warp(bar0 + 8u * T::B_OFREE);
+        }
+        if (!live) continue;
         if (part) {
 #pragma unroll
-            for (int x = 0; x < COLS; x += 4) part_store(x, r + x);
-        } else {
+            for (int x = 0; x < STEP; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * inv);
+            if constexpr (STEP >= 8) {
 #pragma unroll
-            for (int x = 0; x < COLS; x += 4)
-                *reinterpret_cast<uint2*>(o_row(row) + x) =
-                    make_uint2(pack2<BF16>(__uint_as_float(r[x]) * inv, __uint_as_float(r[x + 1]) * inv),
-                               pack2<BF16>(__uint_as_float(r[x + 2]) * inv, __uint_as_float(r[x + 3]) * inv));
+                for (int x = 0; x < STEP; x += 8) st_global_v8(dst + ((c + x) / 8 * p.tile_rows) * 32, r + x);
+            } else {
+                st_global_v4(dst, r);
+            }
+        } else {
+            uint32_t w[STEP / 2];
+#pragma unroll
+            for (int x = 0; x < STEP / 2; ++x)
+                w[x] = pack2<BF16>(__uint_as_float(r[2 * x]) * inv, __uint_as_float(r[2 * x + 1]) * inv);
+            if constexpr (STEP >= 16) {
+#pragma unroll
+                for (int x = 0; x < STEP / 2; x += 8) {
+                    if (p.wide_o) {
+                        st_global_v8(dst + c * 2 + x * 4, w + x);
+                    } else {
+                        st_global_v4(dst + c * 2 + x * 4, w + x);
+                        st_global_v4(dst + c * 2 + x * 4 + 16, w + x + 4);
+                    }
+                }
+            } else if constexpr (STEP == 8) {
+                st_global_v4(dst, w);
+            } else {
+                *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+            }
         }
     }
+    return true;
 }
 
 template <int D, bool BF16>
-__device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+__device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t bar0, uint32_t tmem,
                              float* hand, float* red, int h, const Ctl& ctl) {
     using T = TileTraits<D>;
     constexpr int BN = T::BN, NG = T::NG, HC = BN / NG;
@@ -618,12 +610,13 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t 
         ls[h * BM + row] = l;
         ptx::mbar_arrive(bar(T::B_EPIFULL + slot));
         if (!warp_wait_phase(bar(T::B_EPIFULL + slot), (ntile >> 1) & 1u, ctl, SITE_EPI_FULL)) return;
-        const uint32_t g = step - 1;
-        if (!warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(g)), rphase<T::SR>(g), ctl, SITE_PV_DONE)) return;
-        ptx::tc_fence_after();
         PagedSeg sg;
         seg_read<D>(ring, sg, ntile);
-        tile_output<D, BF16>(p, sg, sbase, bar0, tmem, ls, m, h);
+        const bool written = tile_output<D, BF16>(p, sg, bar0, tmem, ls, m, h, [&]() {
+            const uint32_t g = step - 1;
+            return warp_wait_phase(bar(T::B_PVDONE + rslot<T::SR>(g)), rphase<T::SR>(g), ctl, SITE_PV_DONE);
+        });
+        if (!written) return;
         seg_release<D, true>(ntile, bar);
     }
     if (ring[(ntile % T::SEGS) * (sizeof(SegMsg) / 4) + 9] != 0)  // pads, from the end's message
@@ -685,7 +678,7 @@ __global__ void __launch_bounds__(TileTraits<D>::THREADS, 1)
     } else if (warp == 2) {
         if (lane == 0) tile_mma_pv<D, BF16>(p, ring, sbase, bar0, tmem, ctl);
     } else {
-        tile_softmax<D, BF16>(p, ring, sbase, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
+        tile_softmax<D, BF16>(p, ring, bar0, tmem, hand, red, (warp - 4) / 4, ctl);
     }
 
     ptx::tc_fence_before();

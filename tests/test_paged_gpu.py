@@ -370,6 +370,23 @@ def test_cache_without_pages_holds_nothing(T):
     assert fa.fa_device_status()[0] == 0 and (o == 0).all() and torch.isneginf(lse).all()
 
 
+@pytest.mark.parametrize("D", [16, 64, 128, 256])
+@pytest.mark.parametrize("T", [1, 40])
+def test_outputs_off_32_byte_boundaries(D, T):
+    import exact_attention_44_gb300 as fa
+    kc, vc, table, k, v = pu.make_cache(42, [340, 1040], 2, D, 16, "bf16")
+    args = [kc.cuda(), vc.cuda(), table.cuda(), torch.tensor([300 - T, 1040 - T], dtype=torch.int32, device="cuda")]
+    q = torch.randn((2, 8, T, D), generator=torch.Generator().manual_seed(43)).bfloat16().cuda()
+    want, wl = fa.fa_fwd_paged(q, *args)
+    big = torch.full((2, 8, T, D + 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    odd = torch.full((2, 8, T, D + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    for whole, o in ((big, big[..., 8:8 + D]), (odd, odd[..., :D])):  # base, strides at odd multiples of 16 bytes
+        got, lse = fa.fa_fwd_paged(q, *args, o)
+        assert got.data_ptr() == o.data_ptr() and torch.equal(o, want) and torch.equal(lse, wl)
+        edge = torch.cat([whole[..., :o.storage_offset()], whole[..., o.storage_offset() + D:]], -1)
+        assert bool((edge == 7.0).all())
+
+
 @pytest.mark.parametrize("T", [1, 40])
 def test_expanded_queries(T):
     import exact_attention_44_gb300 as fa
