@@ -56,7 +56,7 @@ static cudaError_t launch_tile(const PagedLaunch& a) {
     if (err != cudaSuccess) return err;
     Dependent d((unsigned)(a.params.team * a.params.teams), T::THREADS, T::SMEM_BYTES, a.stream);
     err = cudaLaunchKernelEx(&d.cfg, kernel, *a.tmQ, *a.tmK, *a.tmV, a.params);
-    return err == cudaSuccess ? launch_merge<T::BN, BF16>(a, FA_HEAD_DIM == 256 ? 8 : 16) : err;
+    return err == cudaSuccess ? launch_merge<T::BN, BF16>(a, 8) : err;
 }
 
 #define FA_CAT2(a, b) a##b

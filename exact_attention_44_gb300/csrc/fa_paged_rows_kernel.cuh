@@ -19,6 +19,15 @@
 //   * the products run on mma.sync m16n8k16: 16 rows are far too few for a
 //     128-row tcgen05 tile (fa_paged_tile_kernel.cuh takes the calls with more
 //     rows), and Q, S, P and O stay in registers.
+// Measured: 64 sequences of 256-4096 positions, one token, 32 query heads on 8 of
+// D = 128 (572 MB): 91 us without the merge, 6.3 TB/s, 94 % of a plain copy's
+// rate; two of 30000-32768, 16 heads of D = 64 (257 MB): 41.7 us, 6.2 TB/s.  Two
+// CTAs of four warps an SM (231 registers a thread) have rings of 192 KB, two
+// thirds of them in flight at a time.  One sequence of 1024: 6.2 us, the way from
+// launch to lengths, table entry, copies and one block a warp.  The merge adds 4
+// to 5 us to each.  At D = 256 there is room for one CTA an SM, and the tile
+// kernel is level or better from one row on: there this kernel has only the
+// groups of more than 128 query heads.
 // What a page holds behind the sequence's last position has no effect: its
 // scores are masked, and its V rows are zeroed in shared memory (0 · NaN would
 // reach O).  Waits for copies are bounded as in fa_fwd_kernel.cuh.

@@ -345,7 +345,7 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 // the ranges of teams b - 1 and b.  If it falls inside a tile group, the
 // member's tile of it has its parts with the teams c0 (slot 2c + 1) and c0 + 1
 // .. c1 (slots 2c); the cuts inside the tile are c0 + 1 .. c1, and each of
-// their blocks merges one share of the tile's (four columns, row) items.  A
+// their blocks merges one share of the tile's (eight columns, row) items.  A
 // part is [D / 8][tile_rows][8] floats of O / l, as both kernels' threads hold
 // it, then a log-sum-exp per row; items follow that order, so that a warp's
 // loads are contiguous.  With
@@ -354,11 +354,30 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
 // in one pass with a running maximum, so that a part's lambda and its O are one
 // round of loads; with few items up to 32 neighbouring lanes share one, split
 // the parts and join by shuffles.
+// What bounds it is latency: a launch behind the kernel that writes the parts,
+// one round of loads for the cut, one or two for the parts, which lie in L2.  It
+// takes 4 to 5 us of a call on either kernel (2 MB of parts: one sequence of 1024,
+// 128 parts a tile; 14 MB: 8 sequences x 32 tokens).  Blocks a cut, each with a
+// share of the tile: one in the rows kernel (two: 10.5 -> 10.7 us for one sequence
+// of 1024, 45.7 -> 46.7 for two of 30000), 8 in the tile kernel, whose parts are
+// eight times as large (1 / 4 / 8 / 16: 36.1 / 23.6 / 21.7 / 23.0 us for 8 sequences
+// x 32 tokens).  Eight columns an item rather than four: half the index arithmetic,
+// 23.0 -> 21.7 and 11.1 -> 10.5 us.  The loads of four parts in flight a thread: with
+// two, whose 48 registers leave room for a block beside those of the rows kernel,
+// 10.5 -> 11.0 and 21.7 -> 22.4, but 97.8 -> 96.2 for 64 sequences of 256-4096.
 constexpr int PAGED_MERGE_THREADS = 128;
+
+// Eight floats, a whole sector, through L2.
+__device__ __forceinline__ void ld_part(const float* from, float (&v)[8]) {
+    asm volatile("ld.global.cg.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "l"(from)
+                 : "memory");
+}
 
 template <int D, int BK, bool BF16>
 __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(const PagedParams p, int sub) {
-    constexpr int W = D / 4, NT = PAGED_MERGE_THREADS;
+    constexpr int W = D / 8, NT = PAGED_MERGE_THREADS;
     // (no early launch of the next kernel: its set-up would take issue slots from the merge, 187 against
     // 194 us for 32 sequences x 64 drafted tokens)
     ptx::grid_dependency_wait();
@@ -411,23 +430,23 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
     for (int i0 = first; i0 < last; i0 += NT / spl) {
         const int i = i0 + tid / spl;
         const bool ok = i < last;
-        // items: eight-column groups, in each the live rows, in each the two halves
-        const int kg = ok ? i / (2 * live) : 0, in = ok ? i - kg * 2 * live : 0, r = in / 2, c = 2 * kg + in % 2;
-        const int at = (kg * p.tile_rows + r) * 2 + in % 2;
-        float mx = -INFINITY, den = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        // items: eight-column groups, in each the live rows
+        const int kg = ok ? i / live : 0, r = ok ? i - kg * live : 0, at = (kg * p.tile_rows + r) * 8;
+        float mx = -INFINITY, den = 0.f, acc[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) acc[y] = 0.f;
         constexpr int U = 4;
         for (int x0 = sl; ok && x0 < parts; x0 += U * spl) {
-            float l[U];
-            float4 v[U];
+            float l[U], v[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 l[u] = -INFINITY;
-                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int y = 0; y < 8; ++y) v[u][y] = 0.f;
                 const int x = x0 + u * spl;
                 if (x < parts) {
                     const float* from = base + (x == 0 ? slot0 : (uint32_t)x * step);
-                    v[u] = __ldcg(reinterpret_cast<const float4*>(from) + at);
+                    ld_part(from + at, v[u]);
                     l[u] = __ldcg(from + lses + r);
                 }
             }
@@ -437,15 +456,14 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             const float a = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
             mx = top;
             den *= a;
-            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) acc[y] *= a;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const float w = l[u] == -INFINITY ? 0.f : ptx::ex2(l[u] - top);
                 den += w;
-                acc.x += w * v[u].x;
-                acc.y += w * v[u].y;
-                acc.z += w * v[u].z;
-                acc.w += w * v[u].w;
+#pragma unroll
+                for (int y = 0; y < 8; ++y) acc[y] += w * v[u][y];
             }
         }
         for (int k = spl / 2; k > 0; k /= 2) {
@@ -453,21 +471,20 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
             const float a = mx == -INFINITY ? 0.f : ptx::ex2(mx - top);
             mx = top;
             den *= a;
-            acc = make_float4(acc.x * a, acc.y * a, acc.z * a, acc.w * a);
             den += __shfl_xor_sync(0xffffffffu, den, k);
-            acc.x += __shfl_xor_sync(0xffffffffu, acc.x, k);
-            acc.y += __shfl_xor_sync(0xffffffffu, acc.y, k);
-            acc.z += __shfl_xor_sync(0xffffffffu, acc.z, k);
-            acc.w += __shfl_xor_sync(0xffffffffu, acc.w, k);
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+                acc[y] *= a;
+                acc[y] += __shfl_xor_sync(0xffffffffu, acc[y], k);
+            }
         }
         if (!ok || sl != 0) continue;
         const int row = row0 + r, t = p.by_g(row), h = hk * p.G + row - t * p.G;
         const float inv = den == 0.f ? 0.f : 1.f / den;  // (a NaN score reaches O)
-        uint2 out;
-        out.x = pack_pair<BF16>(acc.x * inv, acc.y * inv);
-        out.y = pack_pair<BF16>(acc.z * inv, acc.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.o) + (int64_t)z * p.so_z + h * p.so_h + t * p.so_n + 4 * c) = out;
-        if (c == 0 && p.lse != nullptr)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + (int64_t)z * p.so_z + h * p.so_h + t * p.so_n + 8 * kg) =
+            make_uint4(pack_pair<BF16>(acc[0] * inv, acc[1] * inv), pack_pair<BF16>(acc[2] * inv, acc[3] * inv),
+                       pack_pair<BF16>(acc[4] * inv, acc[5] * inv), pack_pair<BF16>(acc[6] * inv, acc[7] * inv));
+        if (kg == 0 && p.lse != nullptr)
             p.lse[((int64_t)z * p.Hq + h) * p.T + t] = den == 0.f ? -INFINITY : (mx + log2f(den)) * 0.6931471805599453f;
     }
 }

@@ -31,8 +31,8 @@
 // next tile's first scores 0.5), which short contexts feel: 128 sequences of
 // 300-400 x 128 tokens x 4 heads take 187 us.  Short calls are bounded by the way
 // from launch to the first products (about 8 us: lengths, block table, first
-// copies, first block) and by the merge of the parts (about 6 us; 8 sequences of
-// 500-3000 x 32 tokens: 23 us in all, 10 us of DRAM time).
+// copies, first block) and by the merge of the parts (about 5 us; 8 sequences of
+// 500-3000 x 32 tokens: 21.7 us in all, 10 us of DRAM time).
 #pragma once
 
 #include "fa_fwd_kernel.cuh"
