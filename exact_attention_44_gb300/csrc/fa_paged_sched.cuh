@@ -276,12 +276,20 @@ __device__ __forceinline__ PagedWalk paged_range(const PagedParams& p, PagedFind
     return w;
 }
 
+// The tile of a group that a member takes: in turn from the first and from the
+// last, so that the chain's longer later tiles do not all fall to one member (a
+// group counts as many blocks as its last tile has: prompts of 1024 tokens, 4 x 16
+// heads of D = 128, 49.6 -> 39.3 us).
+__device__ __forceinline__ int member_tile(const PagedParams& p, int hk, int gi, int member) {
+    return gi * p.team + ((hk + gi) & 1 ? p.team - 1 - member : member);
+}
+
 // The next segment of member `member` of a team at or after w's place (worker:
 // its number in the launch); false when the range is done.
 template <int BK>
 __device__ __forceinline__ bool paged_seg(const PagedParams& p, PagedWalk& w, PagedSeg& g, int worker, int member) {
     for (; w.left > 0; paged_next<BK>(p, w)) {
-        const int mt = w.gi * p.team + member;
+        const int mt = member_tile(p, w.hk, w.gi, member);
         g.row0 = mt * p.tile_rows;
         g.rows = min(p.tile_rows, w.s.nl * p.G - g.row0);
         if (g.rows <= 0) continue;
@@ -392,7 +400,7 @@ __global__ void __launch_bounds__(PAGED_MERGE_THREADS) fa_paged_merge_kernel(con
         const int4 cut = __ldcg(rec), more = __ldcg(rec + 1);
         const PagedCuts cuts{__ldcg(reinterpret_cast<const long long*>(rec + 2)), more.z, more.w};
         int first = 0, last = 0, parts = 0, c0 = 0;
-        const int mt = cut.z * p.team + member, row0 = mt * p.tile_rows;
+        const int mt = member_tile(p, cut.y, cut.z, member), row0 = mt * p.tile_rows;
         const SeqLen s{more.x, more.y};
         const int live = cut.x < 0 ? 0 : min(p.tile_rows, s.nl * p.G - row0);
         if (live > 0 && cut.w > 0) {  // there is such a range, and it does not start with a tile

@@ -422,6 +422,12 @@ def test_side_stream_keeps_what_it_uses(T):
     assert torch.equal(o, want) and torch.equal(lse, wlse) and len(junk) == 6
 
 
+@pytest.mark.parametrize("T,G,D", [(1100, 1, 64), (520, 3, 128), (700, 2, 256)])
+def test_prompts_from_scratch(T, G, D):
+    # the tiles of a team have very different numbers of key blocks; groups of uneven sizes
+    check(45, [0, 3, 130], 2 * G, 2, T, D, 16, "fp16", new=[T, T - 9, T // 3])
+
+
 @pytest.mark.parametrize("T,G,tree", [(130, 4, True), (200, 3, False), (64, 8, True), (300, 2, True), (257, 5, False)])
 def test_teams_of_tiles(T, G, tree):
     # several tiles of a kv head: teams of two to eight CTAs, the last tile ragged, sequences of all sizes
