@@ -2,7 +2,6 @@
 // fa_cache_commit, fa_cache_fork): argument validation, the choice of kernel,
 // launch.
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
 #include <utility>
 

@@ -422,6 +422,27 @@ def test_side_stream_keeps_what_it_uses(T):
     assert torch.equal(o, want) and torch.equal(lse, wlse) and len(junk) == 6
 
 
+def test_two_streams_at_once():
+    import exact_attention_44_gb300 as fa
+    jobs = []
+    for n, (T, D, lens) in enumerate(((1, 128, [3000, 70, 900]), (60, 64, [40, 2000, 333]))):
+        kc, vc, table, k, v = pu.make_cache(46 + n, [x + T for x in lens], 2, D, 16, "bf16")
+        q = torch.randn((3, 8, T, D), generator=torch.Generator().manual_seed(n)).bfloat16().cuda()
+        args = (q, kc.cuda(), vc.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        ws = torch.empty(fa.fa_fwd_paged_workspace_size(D), dtype=torch.uint8, device="cuda")
+        jobs.append((args, dict(workspace=ws), fa.fa_fwd_paged(*args), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, (args, kw, _, stream) in enumerate(jobs):
+            with torch.cuda.stream(stream):
+                got[i].append(fa.fa_fwd_paged(*args, **kw))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status()[0] == 0
+    for (_, _, (o, lse), _), runs in zip(jobs, got):
+        assert all(torch.equal(a, o) and torch.equal(b, lse) for a, b in runs)
+
+
 @pytest.mark.parametrize("T,G,D", [(1100, 1, 64), (520, 3, 128), (700, 2, 256)])
 def test_prompts_from_scratch(T, G, D):
     # the tiles of a team have very different numbers of key blocks; groups of uneven sizes
