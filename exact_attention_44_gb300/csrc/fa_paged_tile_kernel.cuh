@@ -29,7 +29,7 @@
 // in the rings of K and V instead of Q's second changes nothing).  Between two
 // tiles a softmax warp loses 2.6 us (its last product 0.6, the output 1.2, the
 // next tile's first scores 0.5), which short contexts feel: 128 sequences of
-// 300-400 x 128 tokens x 4 heads take 187 us.  Short calls are bounded by the way
+// 300-400 x 128 tokens x 4 heads take 183 us.  Short calls are bounded by the way
 // from launch to the first products (about 8 us: lengths, block table, first
 // copies, first block) and by the merge of the parts (about 5 us; 8 sequences of
 // 500-3000 x 32 tokens: 21.7 us in all, 10 us of DRAM time).
