@@ -18,6 +18,13 @@
 // Warps whose 32 rows hold no token skip the softmax and only keep the
 // barriers' counts.  Every wait is bounded as in fa_fwd_kernel.cuh.
 //
+// Rows of a tile that hold no token (behind the last new token, and behind
+// tile_rows where the group does not divide 128: there Q's slot is whatever
+// shared memory held before) go through the products and the softmax of their
+// warp, but must not decide anything for it: when O is rescaled, the lanes of
+// the live rows move their reference too, and P is rounded against another one.
+// So their reference is +inf from the first block on: they never ask for it.
+//
 // What bounds it.  With one tile a kv head (up to 128 rows), DRAM: a block's K
 // and V are 64 KB at D = 128, 1.49 us of an SM's share of 6.7 TB/s (1.31 us
 // measured), against 0.8 us that the chain S -> softmax -> P takes a block, as
@@ -560,7 +567,7 @@ __device__ void tile_softmax(const PagedParams& p, volatile int* ring, uint32_t 
             };
             if (j == jb) {
                 if (!warp_wait_phase(bar(T::B_RED + b), ph, ctl, SITE_MAX_XCHG)) return;
-                m = block_max();
+                m = row < ring[(ntile % T::SEGS) * (sizeof(SegMsg) / 4) + 8] ? block_max() : INFINITY;
             }
             constexpr int NP = HC / 2;
             uint32_t pk[NP];
