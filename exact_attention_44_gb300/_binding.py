@@ -513,7 +513,9 @@ def fa_fwd_splitkv_raw(q_ptr: int, k_ptr: int, v_ptr: int, o_ptr: int, lse_ptr: 
 
 
 def fa_device_status(stream=None) -> tuple[int, int]:
-    """Synchronise the stream, read and clear the device status word: (code, raw word)."""
+    """Synchronise the stream, read and clear the device's first recorded error: (code, raw word).
+
+    FA_ERR_PAGE is kept apart from the other codes, which are reported before it."""
     import torch
 
     if stream is None:

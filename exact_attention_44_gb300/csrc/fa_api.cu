@@ -22,7 +22,11 @@
 
 namespace {
 
-__device__ uint32_t g_fa_status;  // first device-side error of any launch on this device
+// First device-side errors of the launches on this device: [0] a wait that ran
+// out or a failed check, [1] a bad page of the paged cache (fa::PAGE_WORD).  Two
+// words, because a bad page is met in calls that otherwise do their work, and
+// must not hide that a later kernel gave up.
+__device__ uint32_t g_fa_status[2];
 
 constexpr int kMaxDevices = 64;
 
@@ -1081,11 +1085,13 @@ fa_status fa_lse_merge(int nparts, const void* const* o_parts, const float* cons
 
 fa_status fa_device_status(cudaStream_t stream, uint32_t* detail) {
     if (cudaStreamSynchronize(stream) != cudaSuccess) return FA_ERR_CUDA;
-    uint32_t word = 0;
-    if (cudaMemcpyFromSymbol(&word, g_fa_status, sizeof(word)) != cudaSuccess) return FA_ERR_CUDA;
+    uint32_t words[2] = {0, 0};
+    if (cudaMemcpyFromSymbol(words, g_fa_status, sizeof(words)) != cudaSuccess) return FA_ERR_CUDA;
+    const int which = words[0] != 0 ? 0 : fa::PAGE_WORD;  // the other one is left for the next call
+    const uint32_t word = words[which];
     if (word != 0) {
         const uint32_t zero = 0;
-        if (cudaMemcpyToSymbol(g_fa_status, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
+        if (cudaMemcpyToSymbol(g_fa_status, &zero, sizeof(zero), which * sizeof(zero)) != cudaSuccess) return FA_ERR_CUDA;
     }
     if (detail) *detail = word;
     return word == 0 ? FA_OK : (fa_status)(word & 0xFFu);

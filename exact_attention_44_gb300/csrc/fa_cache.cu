@@ -20,7 +20,7 @@ namespace {
 __device__ __forceinline__ int ldi(const int32_t* p) { return __ldcg(p); }
 
 __device__ __forceinline__ void bad_page(uint32_t* status, uint32_t site) {
-    atomicCAS(status, 0u, STATUS_PAGE | (site << 8) | ((blockIdx.x & 0xFFFFu) << 16));
+    atomicCAS(status + PAGE_WORD, 0u, STATUS_PAGE | (site << 8) | ((blockIdx.x & 0xFFFFu) << 16));
 }
 
 template <typename K, typename P>

@@ -12,8 +12,9 @@
 namespace fa {
 
 constexpr uint32_t STATUS_PAGE = 8;  // FA_ERR_PAGE: a block table entry outside the cache was needed
+constexpr int PAGE_WORD = 1;         // its place behind the status word of waits and checks, which it must not hide
 
-// Where a bad page was met; recorded in bits 8-15 of the device status word.
+// Where a bad page was met; recorded in bits 8-15 of its status word.
 enum PageSite : uint32_t {
     SITE_PAGE_ATTENTION = 60,
     SITE_PAGE_APPEND = 61,

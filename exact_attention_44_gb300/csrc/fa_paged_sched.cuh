@@ -334,7 +334,7 @@ __device__ __forceinline__ void paged_fill(const PagedParams& p, int warp, int w
 }
 
 __device__ __forceinline__ void record_bad_page(uint32_t* status, uint32_t site) {
-    atomicCAS(status, 0u, STATUS_PAGE | (site << 8) | ((blockIdx.x & 0xFFFFu) << 16));
+    atomicCAS(status + PAGE_WORD, 0u, STATUS_PAGE | (site << 8) | ((blockIdx.x & 0xFFFFu) << 16));
 }
 
 template <bool BF16>

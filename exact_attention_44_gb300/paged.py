@@ -8,12 +8,16 @@ a block table (Z, max_pages) int32 names the page of every page_size positions
 of each sequence, -1 where it has none; seq_lens (Z) int32 holds the positions
 that each sequence has.  One step of speculative decoding:
 
-    fa_cache_fork(k, v, table, lens, refs, room=T, missing=missing)   # pages for T more positions
+    fa_cache_fork(k, v, table, lens, refs, source, room=T, missing=missing)   # pages for T more positions
     for layer in ...:
-        fa_cache_append(k_new, v_new, k[layer], v[layer], table, lens)
-        o, lse = fa_fwd_paged(q, k[layer], v[layer], table, lens, tree_mask=mask)
-    fa_cache_commit(k, v, table, lens, accepted, accepted_lens)       # all layers
+        fa_cache_append(k_new, v_new, k[layer], v[layer], table, lens, new_lens=new)
+        o, lse = fa_fwd_paged(q, k[layer], v[layer], table, lens, new_lens=new, tree_mask=mask)
+    fa_cache_commit(k, v, table, lens, accepted, accepted_lens)               # all layers
     lens += accepted_lens
+
+new is T for every sequence that goes on; one that has ended keeps source -1, new
+0 and accepted_lens 0 until it is used again (it has no pages, and a row for it
+would be recorded as FA_ERR_PAGE).
 
 Everything is argument marshalling: the work, the lengths and the page
 bookkeeping stay on the device, and no call synchronises.

@@ -84,7 +84,7 @@ typedef struct {
  *
  * Ownership: the caller owns every buffer and must keep them alive until the
  * stream reaches this work.  The library allocates no device memory per call;
- * it keeps one 4-byte status word per device for device-side errors.
+ * it keeps two 4-byte status words per device for device-side errors.
  *
  * Errors: argument errors return FA_ERR_INVALID_ARG / FA_ERR_UNSUPPORTED /
  * FA_ERR_ALIGNMENT synchronously and enqueue nothing; a failed launch returns
@@ -365,15 +365,19 @@ const char* fa_status_string(fa_status status);
 
 /*
  * fa_device_status -- synchronise `stream`, then read and clear the current
- * device's status word.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT (a bounded
+ * device's first recorded error.  Returns FA_OK, FA_ERR_DEVICE_TIMEOUT (a bounded
  * mbarrier wait inside a kernel gave up and the kernel exited cleanly),
  * FA_ERR_DEVICE_CHECK (only in a library built with debug index checks,
  * `python -m exact_attention_44_gb300.build --debug-checks`: a role of the
  * forward kernel found a unit outside the launch's sizes, recorded it and
- * stopped; the wait site field then names the role), or FA_ERR_CUDA if the
- * synchronisation itself failed.  When `detail` is not
- * NULL it receives the raw word: bits 0-7 the code, 8-15 the wait site,
- * 16-31 the CTA index that gave up first.
+ * stopped; the wait site field then names the role), FA_ERR_PAGE (a call on a
+ * paged cache needed a page that is not there, or a fork's source is no
+ * sequence; the call did the rest of its work; site 60 attention, 61 append, 62
+ * commit, 63 fork), or FA_ERR_CUDA if the synchronisation itself failed.  When
+ * `detail` is not NULL it receives the raw word: bits 0-7 the code, 8-15 the
+ * wait site, 16-31 the CTA index that gave up first.  The first FA_ERR_PAGE is
+ * kept apart from the other codes, which are reported before it: one call
+ * reports and clears one of the two.
  */
 fa_status fa_device_status(cudaStream_t stream, uint32_t* detail);
 
@@ -457,7 +461,9 @@ fa_status fa_fwd_schedule(int Z, int Hq, int Hkv, int Nq, int Nkv, int D, int ca
  * must be ordered.  A needed table entry outside 0 .. P - 1 is never followed:
  * its positions read as zeros (attention) or are skipped (the others), and
  * FA_ERR_PAGE is recorded (fa_device_status).  Lengths are clamped to what the
- * table can hold; a cache without pages (P = 0) holds nothing.
+ * table can hold; a cache without pages (P = 0) holds nothing.  A sequence that
+ * has been emptied has no pages for new tokens: pass new_lens 0 for it, and -1
+ * as its source, until it is used again.
  */
 typedef struct {
     void* k;                      /* (L, P, Hkv, page_size, D), 16-bit elements */
