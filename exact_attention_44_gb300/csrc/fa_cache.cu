@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(COMMIT_THREADS) fa_cache_commit_kernel(const C
 constexpr int PLAN_THREADS = 1024;
 
 struct ForkWs {
-    int32_t *src, *len, *first, *count, *off, *tail, *found, *pages;
+    int32_t *src, *len, *first, *count, *off, *from, *tail, *found, *pages;
 };
 __device__ __forceinline__ ForkWs fork_ws(const ForkParams& p) {
     ForkWs w;
@@ -183,7 +183,8 @@ __device__ __forceinline__ ForkWs fork_ws(const ForkParams& p) {
     w.first = w.len + p.Z;
     w.count = w.first + p.Z;
     w.off = w.count + p.Z;
-    w.tail = w.off + p.Z;         // list of tails: from page, to page, rows
+    w.from = w.off + p.Z;
+    w.tail = w.from + p.Z;        // list of tails: from page, to page, rows
     w.found = w.tail + 3 * p.Z;   // pages found, tails
     w.pages = w.found + 2;
     return w;
@@ -239,12 +240,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
             }
             const int len = src >= 0 ? min(max(ldi(p.lens + src), 0), cap) : 0;
             const int need = src >= 0 ? (int)(((int64_t)len + p.room + p.page - 1) / p.page) : 0;
-            int first = src == z ? (len + p.page - 1) / p.page : len / p.page;
+            const int full = len / p.page, rows = len - full * p.page;
+            const int from = rows > 0 ? ldi(p.table + src * p.st_z + full) : -1;  // (full < M)
+            int first = full + (src == z && rows > 0);
             if (src == z)
                 while (first < min(need, p.M) && ldi(p.table + z * p.st_z + first) >= 0) ++first;  // room it has
-            count = max(0, min(need, p.M) - first);
-            over = max(0, need - p.M);
+            // The rows of a partly filled page that is not in the table are lost (a call that
+            // ran short has left it uncopied).  No page can bring them back: what they and
+            // all behind them need goes on lacking, in copies too.
+            const bool lost = rows > 0 && (unsigned)from >= (unsigned)p.P;
+            count = lost ? 0 : max(0, min(need, p.M) - first);
+            over = lost ? need - full : max(0, need - p.M);
+            if (lost && src != z) bad_page(p.status, SITE_PAGE_FORK);
             w.src[z] = src;
+            w.from[z] = from;
             w.len[z] = len;
             w.first[z] = first;
             w.count[z] = count;
@@ -279,23 +288,20 @@ __global__ void __launch_bounds__(PLAN_THREADS) fa_cache_fork_plan_kernel(const 
     // page (the list's order is of no account: no page is in it twice as a target,
     // and no target is a source)
     for (int z = tid; z < p.Z; z += PLAN_THREADS) {
-        const int src = w.src[z], len = w.len[z], rows = len % p.page;
+        const int src = w.src[z], rows = w.len[z] % p.page;
         if (src < 0 || src == z || rows == 0 || w.off[z] >= found || w.count[z] == 0) continue;
-        const int from = ldi(p.table + src * p.st_z + len / p.page);
-        if ((unsigned)from < (unsigned)p.P) {
-            int32_t* t = w.tail + 3 * atomicAdd(&tails, 1);
-            t[0] = from;
-            t[1] = w.pages[w.off[z]];
-            t[2] = rows;
-        } else {
-            bad_page(p.status, SITE_PAGE_FORK);
-        }
+        int32_t* t = w.tail + 3 * atomicAdd(&tails, 1);
+        t[0] = w.from[z];
+        t[1] = w.pages[w.off[z]];
+        t[2] = rows;
     }
     __syncthreads();
     if (tid == 0) {
-        w.found[0] = found;
-        w.found[1] = tails;
-        if (p.missing != nullptr) *p.missing = (int)min((long long)wanted - found + (long long)excess, (long long)INT_MAX);
+        const long long lack = (long long)wanted - found + (long long)excess;
+        const bool none = p.whole && lack > 0;
+        w.found[0] = none ? -1 : found;
+        w.found[1] = none ? 0 : tails;
+        if (p.missing != nullptr) *p.missing = (int)min(lack, (long long)INT_MAX);
     }
 }
 
@@ -321,6 +327,7 @@ __global__ void __launch_bounds__(FORK_THREADS) fa_cache_fork_apply_kernel(const
     if ((int)blockIdx.x < a.table_ctas) {
         const int c0 = blockIdx.x * a.cols, nc = min(a.cols, p.M - c0), n = p.Z * a.cols;
         const int found = ldi(w.found);
+        if (found < 0) return;  // all or nothing, and pages lack
         for (int i = tid; i < n; i += FORK_THREADS) {
             const int z = i / a.cols, c = i - z * a.cols;
             old[i] = c < nc ? ldi(p.table + z * p.st_z + c0 + c) : -1;

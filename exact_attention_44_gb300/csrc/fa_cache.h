@@ -43,13 +43,15 @@ struct ForkParams {
     const int32_t* source;          // nullptr: every sequence stays
     int32_t* missing;               // or nullptr
     int Z, L, H, D, page, M, P, room;
+    int whole;                      // all or nothing
     int32_t* ws;                    // fork_workspace_ints(Z, M)
     uint32_t* status;
 };
 // per sequence: source, length after, first column to fill, columns to fill,
-// place in the page list; the list of tails (3 each), the number of pages found
-// and of tails; the page list
-inline int64_t fork_workspace_ints(int64_t Z, int64_t M) { return 8 * Z + 2 + Z * M; }
+// place in the page list, partly filled page of the source; the list of tails (3
+// each), the number of pages found (-1: nothing is to be changed) and of tails;
+// the page list
+inline int64_t fork_workspace_ints(int64_t Z, int64_t M) { return 9 * Z + 2 + Z * M; }
 
 cudaError_t launch_cache_append(AppendParams p, cudaStream_t stream);
 cudaError_t launch_cache_commit(const CommitParams& p, cudaStream_t stream);

@@ -349,7 +349,7 @@ fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
     if (args == nullptr) return FA_ERR_INVALID_ARG;
     const fa_cache_fork_args& x = *args;
     const fa_paged_cache& c = x.cache;
-    if (x.room < 0) return FA_ERR_INVALID_ARG;
+    if (x.room < 0 || (x.all_or_nothing != 0 && x.all_or_nothing != 1)) return FA_ERR_INVALID_ARG;
     fa_status st = check_cache(c, true);
     if (st != FA_OK) return st;
     if (c.Z > 8192 || c.P > (1 << 30) || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||
@@ -379,6 +379,7 @@ fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
     p.source = x.source;
     p.missing = x.missing;
     p.Z = c.Z, p.L = c.L, p.H = c.Hkv, p.D = c.D, p.page = c.page_size, p.M = c.max_pages, p.P = c.P, p.room = x.room;
+    p.whole = x.all_or_nothing;
     p.ws = static_cast<int32_t*>(x.workspace);
     p.status = f.status;
     err = fa::launch_cache_fork(p, f.sms, stream);

@@ -336,9 +336,9 @@ PyObject* cache_commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (k_cache, v_cache, block_table, seq_lens, ref_counts, source, room, missing, workspace, stream)
+// (k_cache, v_cache, block_table, seq_lens, ref_counts, source, room, missing, workspace, stream, all_or_nothing)
 PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!expect(n, 10)) return nullptr;
+    if (!expect(n, 11)) return nullptr;
     return guarded([&]() -> PyObject* {
         const at::Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache");
         const at::Tensor &table = tensor(a[2], "block_table"), &lens = tensor(a[3], "seq_lens");
@@ -352,6 +352,8 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (source != nullptr) check_ints(*source, "source", {Z});
         if (missing != nullptr) check_ints(*missing, "missing", {1});
         x.room = int_arg(a[6], "room");
+        x.all_or_nothing = PyObject_IsTrue(a[10]);
+        if (x.all_or_nothing < 0) throw python_error();
         check_workspace(ws_arg);
         const int dev = cuda_device("fa_cache_fork", kc, {&vc, &table, &lens, &refs, source, missing, ws_arg});
         const Place place(a[9], dev, {&kc, &vc, &table, &lens, &refs, source, missing, ws_arg});

@@ -8,13 +8,14 @@ a block table (Z, max_pages) int32 names the page of every page_size positions
 of each sequence, -1 where it has none; seq_lens (Z) int32 holds the positions
 that each sequence has.  One step of speculative decoding:
 
-    fa_cache_fork(k, v, table, lens, refs, source, room=T, missing=missing)   # pages for T more positions
+    fa_cache_fork(k, v, table, lens, refs, source, room=T, missing=missing, all_or_nothing=True)  # room for T more
     for layer in ...:
         fa_cache_append(k_new, v_new, k[layer], v[layer], table, lens, new_lens=new)
         o, lse = fa_fwd_paged(q, k[layer], v[layer], table, lens, new_lens=new, tree_mask=mask)
     fa_cache_commit(k, v, table, lens, accepted, accepted_lens)               # all layers
     lens += accepted_lens
 
+If missing is not 0 the fork has changed nothing: free sequences and fork again.
 new is T for every sequence that goes on; one that has ended keeps source -1, new
 0 and accepted_lens 0 until it is used again (it has no pages, and a row for it
 would be recorded as FA_ERR_PAGE).
@@ -127,7 +128,7 @@ def fa_cache_fork_workspace_size(Z: int, max_pages: int) -> int:
 
 
 def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=None, *, room: int = 0, missing=None,
-                  workspace=None, stream=None) -> None:
+                  workspace=None, stream=None, all_or_nothing: bool = False) -> None:
     """Fork, free and give room to the sequences of a cache, in place (libfa's fa_cache_fork).
 
     source: (Z) int32, which sequence (as it was before the call) each one
@@ -136,10 +137,14 @@ def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=No
     int32, counts the table entries of a page; 0 is free) and get their own copy
     of the partly filled one, in every layer of the caches.  Then every sequence
     that is not emptied gets pages for `room` more positions.  missing: (1)
-    int32, receives how many pages lacked (0: none).  workspace: a CUDA uint8
-    tensor of fa_cache_fork_workspace_size(Z, max_pages) bytes; one is allocated
-    when omitted.
+    int32, receives how many pages lacked (0: none).  all_or_nothing: if pages
+    lack nothing is changed, so that sequences can be freed and the same call made
+    again; otherwise the call does what it can, and a copy whose partly filled
+    page lacked has lost the rows in it (`missing` counts it in every later call,
+    until it is replaced or emptied).  workspace: a CUDA uint8 tensor of
+    fa_cache_fork_workspace_size(Z, max_pages) bytes; one is allocated when
+    omitted.
     """
     ext = _ext if _bound is not None and _bound is _binding._lib else _calls()
     ext.cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source, room, missing, workspace,
-                   None if stream is None else stream.cuda_stream)
+                   None if stream is None else stream.cuda_stream, all_or_nothing)

@@ -555,13 +555,22 @@ fa_status fa_cache_commit(const fa_cache_commit_args* args, cudaStream_t stream)
  * released.  Then every sequence that is not emptied gets pages for `room`
  * more positions.  Pages are taken lowest first from those that were free
  * before the call, for sequences in order, columns in order; pages released by
- * a call can be handed out by the next one.  If they do not suffice the last
- * ones stay -1 (and a partly filled page uncopied), and *missing is the number
- * of pages that lacked, columns past max_pages included; 0 otherwise.
+ * a call can be handed out by the next one.  *missing is the number of pages
+ * that lacked, columns past max_pages included; 0 if they sufficed.  If pages
+ * lack, then
+ *   all_or_nothing 1: nothing is changed but *missing, so that the caller can
+ *     free sequences (with one call) and make the same call again;
+ *   all_or_nothing 0: the call does what it can.  The last pages stay -1.  Where
+ *     that is the partly filled page of a copy, the copy has lost its rows in
+ *     it, for good if the source does not stay: positions there read as zeros
+ *     (FA_ERR_PAGE), neither the sequence nor a copy of it gets pages any more,
+ *     and every call counts the pages that it would need from there on in
+ *     *missing, until it becomes a copy of another sequence or is emptied.
  *
  * Valid state: a row's entries are its ceil(len / page_size) pages, then
  * pages of room, then -1; a page with room to write belongs to one sequence.
- * fa_cache_fork keeps it so.  A source outside -1 .. Z - 1 is recorded as
+ * fa_cache_fork keeps it so as long as all_or_nothing is set or no pages lack.
+ * A source outside -1 .. Z - 1 is recorded as
  * FA_ERR_PAGE and the sequence stays.  Z <= 8192, P and room <= 2^30, Z * max_pages < 2^31.
  */
 typedef struct {
@@ -572,6 +581,7 @@ typedef struct {
     void* workspace;              /* fa_cache_fork_workspace_size(Z, max_pages) bytes, 256-byte aligned */
     size_t workspace_bytes;
     int room;
+    int all_or_nothing;           /* 1: if pages lack nothing is changed; 0: what can be done is */
 } fa_cache_fork_args;
 fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream);
 fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes);
