@@ -186,8 +186,8 @@ at::Tensor scratch(size_t bytes, const at::Tensor& like) {
 template <typename F>
 PyObject* guarded(F&& fn) {
     HANDLE_TH_ERRORS
-    if (lib.fwd == nullptr) throw Refused{PyExc_ImportError, "libfa is not loaded"};
     try {
+        if (lib.fwd == nullptr) throw Refused{PyExc_ImportError, "libfa is not loaded"};
         return fn();
     } catch (const Refused& r) {
         PyErr_SetString(r.type, r.text.c_str());
