@@ -8,7 +8,10 @@ the library; an unchanged tree is not rebuilt.  --debug-checks builds a
 second library, _build/checks/libfa.so, whose forward kernels check every
 unit they decode against the launch's sizes (FA_DEBUG_CHECKS=1).  Where torch
 with CUDA is installed, the binding of the paged-cache calls (_paged_ext.so, a CPython
-extension over torch's headers) is built beside libfa.so with g++.
+extension over torch's headers) is built beside libfa.so with g++, under a hash of
+its own.  The library does not need it: if it cannot be compiled, the compiler's
+output is printed, the library is built all the same, and the paged-cache calls of
+the package raise ImportError.
 """
 from __future__ import annotations
 
@@ -51,15 +54,43 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: libfa needs the CUDA 13 toolkit to build")
 
 
-def _tree_hash(extra_flags: list[str]) -> str:
+def _hash(files: list[str], flags: list[str]) -> str:
     h = hashlib.sha256()
-    for d in (CSRC, INCLUDE):
-        for name in sorted(os.listdir(d)):
-            if name.endswith((".cu", ".cuh", ".h", ".cpp")):
-                with open(os.path.join(d, name), "rb") as f:
-                    h.update(name.encode() + b"\0" + f.read())
-    h.update(" ".join(FLAGS + extra_flags).encode())
+    for path in files:
+        with open(path, "rb") as f:
+            h.update(os.path.basename(path).encode() + b"\0" + f.read())
+    h.update(" ".join(flags).encode())
     return h.hexdigest()
+
+
+def _sources(folder: str, *endings: str) -> list[str]:
+    return [os.path.join(folder, name) for name in sorted(os.listdir(folder)) if name.endswith(endings)]
+
+
+def _tree_hash(extra_flags: list[str]) -> str:
+    """Of what libfa.so is made of."""
+    return _hash(_sources(CSRC, ".cu", ".cuh", ".h") + _sources(INCLUDE, ".h"), FLAGS + extra_flags)
+
+
+def _ext_hash(torch: str) -> str:
+    """Of what the binding is made of and tied to."""
+    return _hash([os.path.join(CSRC, "paged_ext.cpp")] + _sources(INCLUDE, ".h"),
+                 [*_ext_command(torch, "nvcc", EXT), _ext_stamp(torch)])
+
+
+def _fresh(product: str, digest: str) -> bool:
+    """Whether the product is there, and was made from what has this hash."""
+    stamp = product + ".hash"
+    if not (os.path.exists(product) and os.path.exists(stamp)):
+        return False
+    with open(stamp) as f:
+        return f.read() == digest
+
+
+def _install(tmp: str, product: str, digest: str) -> None:
+    os.replace(tmp, product)
+    with open(product + ".hash", "w") as f:
+        f.write(digest)
 
 
 def _torch_dir() -> str | None:
@@ -100,52 +131,55 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         lib_path = os.path.join(build_dir, "libfa.so")
     os.makedirs(build_dir, exist_ok=True)
     digest = _tree_hash(extra_flags)
-    stamp = lib_path + ".hash"
+    need_lib = force or not _fresh(lib_path, digest)
     torch = None if debug_checks else _torch_dir()
-    if torch is not None:
-        digest += "\n" + _ext_stamp(torch)
-    if not force and os.path.exists(lib_path) and os.path.exists(stamp) and open(stamp).read() == digest and (
-            torch is None or os.path.exists(EXT)):
+    ext_digest = "" if torch is None else _ext_hash(torch)
+    need_ext = torch is not None and (force or not _fresh(EXT, ext_digest))
+    if not need_lib and not need_ext:
         return lib_path
     cc = nvcc()
-    jobs = []
-    for src, obj_name, unit_flags in UNITS:
+    jobs = []  # (compiler, source, output, command)
+    for src, obj_name, unit_flags in UNITS if need_lib else []:
         obj = os.path.join(build_dir, obj_name)
         cmd = [cc, *FLAGS, *unit_flags, *extra_flags, "-c", os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        jobs.append((src, obj, cmd))
-
+        jobs.append(("nvcc", src, obj, cmd))
+    objects = [obj for _, _, obj, _ in jobs]
     ext_tmp = EXT + f".tmp{os.getpid()}"
-    if torch is not None:
-        jobs.append(("paged_ext.cpp", ext_tmp, _ext_command(torch, cc, ext_tmp)))
+    if need_ext:
+        jobs.append(("g++", "paged_ext.cpp", ext_tmp, _ext_command(torch, cc, ext_tmp)))
 
     def run(job):
-        src, obj, cmd = job
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        return os.path.basename(obj), r
+        try:
+            r = subprocess.run(job[3], capture_output=True, text=True)
+            return r.returncode == 0, r.stdout + r.stderr
+        except OSError as e:  # no such compiler
+            return False, f"{e}\n"
 
     with cf.ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
         results = list(ex.map(run, jobs))
-    failed = False
-    for src, r in results:
-        if r.returncode != 0:
-            failed = True
-            sys.stderr.write(f"--- nvcc failed on {src}\n{r.stdout}{r.stderr}\n")
-        elif verbose and (r.stdout or r.stderr):
-            sys.stderr.write(f"--- {src}\n{r.stdout}{r.stderr}\n")
-    if failed:
+    failed = set()
+    for (compiler, src, out, _), (ok, text) in zip(jobs, results):
+        if not ok:
+            failed.add(out)
+            sys.stderr.write(f"--- {compiler} failed on {src}\n{text}\n")
+        elif verbose and text:
+            sys.stderr.write(f"--- {os.path.basename(out)}\n{text}\n")
+    if ext_tmp in failed:
+        sys.stderr.write("the paged-cache binding was not built: fa_fwd_paged and the fa_cache_* calls will raise ImportError\n")
+        if os.path.exists(EXT):  # of other sources, or of another torch
+            os.remove(EXT)
+    elif need_ext:
+        _install(ext_tmp, EXT, ext_digest)
+    if failed.intersection(objects):
         raise RuntimeError("libfa build failed")
-    tmp = lib_path + f".tmp{os.getpid()}"
-    link = [cc, *ARCH, "-shared", "-o", tmp, *[obj for _, obj, _ in jobs if obj != ext_tmp]]
-    r = subprocess.run(link, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"libfa link failed:\n{r.stdout}{r.stderr}")
-    os.replace(tmp, lib_path)
-    if torch is not None:
-        os.replace(ext_tmp, EXT)
-    with open(stamp, "w") as f:
-        f.write(digest)
+    if need_lib:
+        tmp = lib_path + f".tmp{os.getpid()}"
+        r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objects], capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"libfa link failed:\n{r.stdout}{r.stderr}")
+        _install(tmp, lib_path, digest)
     return lib_path
 
 
