@@ -350,6 +350,7 @@ fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream) {
     const fa_cache_fork_args& x = *args;
     const fa_paged_cache& c = x.cache;
     if (x.room < 0 || (x.all_or_nothing != 0 && x.all_or_nothing != 1)) return FA_ERR_INVALID_ARG;
+    if (x.all_or_nothing && x.missing == nullptr) return FA_ERR_INVALID_ARG;  // whether it happened could not be told
     fa_status st = check_cache(c, true);
     if (st != FA_OK) return st;
     if (c.Z > 8192 || c.P > (1 << 30) || x.room > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX ||

@@ -351,9 +351,11 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
         check_ints(refs, "ref_counts", {x.cache.P});
         if (source != nullptr) check_ints(*source, "source", {Z});
         if (missing != nullptr) check_ints(*missing, "missing", {1});
+        const int whole = PyObject_IsTrue(a[10]);
+        if (whole < 0) throw python_error();
+        if (whole && missing == nullptr) value_error("all_or_nothing needs missing, which says whether anything was done");
         x.room = int_arg(a[6], "room");
-        x.all_or_nothing = PyObject_IsTrue(a[10]);
-        if (x.all_or_nothing < 0) throw python_error();
+        x.all_or_nothing = whole;
         check_workspace(ws_arg);
         const int dev = cuda_device("fa_cache_fork", kc, {&vc, &table, &lens, &refs, source, missing, ws_arg});
         const Place place(a[9], dev, {&kc, &vc, &table, &lens, &refs, source, missing, ws_arg});

@@ -577,7 +577,7 @@ typedef struct {
     fa_paged_cache cache;
     int32_t* ref_counts;          /* (P) table entries that hold each page */
     const int32_t* source;        /* (Z), or NULL: all stay */
-    int32_t* missing;             /* one int32, or NULL */
+    int32_t* missing;             /* one int32, or NULL (not with all_or_nothing) */
     void* workspace;              /* fa_cache_fork_workspace_size(Z, max_pages) bytes, 256-byte aligned */
     size_t workspace_bytes;
     int room;

@@ -89,6 +89,37 @@ def test_short_then_freed_then_retried():
     assert pool.lens.tolist() == [20, 30, 5, 0]
 
 
+def test_captured_call_is_made_again_once_pages_are_free():
+    import exact_attention_44_gb300 as fa
+    pool = Pool(7, LENS, 16, 0, 8)
+    source, missing = i32([1, 0, 2, 3]), i32([-1])
+    ws = torch.empty(fa.fa_cache_fork_workspace_size(4, 8), dtype=torch.uint8, device="cuda")
+    assert pool.fork([0, 1, 2, 3], 0, True) == 0  # (one call in the context before any capture)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            fa.fa_cache_fork(pool.k, pool.v, pool.table, pool.lens, pool.refs, source, room=1, missing=missing,
+                             workspace=ws, all_or_nothing=True)
+    torch.cuda.synchronize()
+    state = [pool.table, pool.lens, pool.refs, pool.k, pool.v]
+    before = [x.clone() for x in state]
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert missing.item() == 3 and all(torch.equal(a, b) for a, b in zip(state, before))
+    assert pool.fork([0, 1, 2, -1], 0, True) == 0
+    source.copy_(i32([1, 0, 2, -1]))
+    want = fu.fork(*pool.plain, [1, 0, 2, -1], 1, 16, True)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert missing.item() == 0
+    assert [pool.table.tolist(), pool.lens.tolist(), pool.refs.tolist()] == list(want[:3])
+    pool.rows = [pool.rows[1], pool.rows[0], pool.rows[2], pool.rows[3]]
+    pool.check_rows()
+    assert fa.fa_device_status()[0] == 0
+
+
 def test_enough_pages_all_or_nothing_is_the_same_call():
     for source in (None, [3, 0, 0, -1], [0, 1, 2, 3]):
         a, b = Pool(3, LENS, 16, 40, 8), Pool(3, LENS, 16, 40, 8)

@@ -3,6 +3,8 @@ keeps every row of an all-or-nothing run; the flag of such a call is checked."""
 import ctypes
 
 import numpy as np
+import pytest
+import torch
 
 import exact_attention_44_gb300 as fa
 import fork_util as fu
@@ -41,7 +43,12 @@ def test_flag_is_refused_unless_0_or_1_and_reads_as_off_where_it_is_not_set():
     lib = fa.load()
     # (the flag takes the place of padding: a zeroed structure without it has the same size and reads as 0)
     assert ctypes.sizeof(ForkWhole) == ctypes.sizeof(Fork) and ForkWhole.all_or_nothing.offset == Fork.room.offset + 4
-    for flag, code in ((2, fa.FA_ERR_INVALID_ARG), (-1, fa.FA_ERR_INVALID_ARG), (0, fa.FA_ERR_WORKSPACE),
-                       (1, fa.FA_ERR_WORKSPACE)):
-        x = ForkWhole(cache=_cache(), refs=PTR, src=PTR, ws=None, all_or_nothing=flag)
+    for flag, miss, code in ((2, PTR, fa.FA_ERR_INVALID_ARG), (-1, PTR, fa.FA_ERR_INVALID_ARG),
+                             (0, PTR, fa.FA_ERR_WORKSPACE), (0, None, fa.FA_ERR_WORKSPACE),
+                             (1, PTR, fa.FA_ERR_WORKSPACE), (1, None, fa.FA_ERR_INVALID_ARG)):
+        x = ForkWhole(cache=_cache(), refs=PTR, src=PTR, miss=miss, ws=None, all_or_nothing=flag)
         assert lib.fa_cache_fork(ctypes.addressof(x), None) == code
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    cache = torch.zeros(9, 2, 16, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="all_or_nothing needs missing"):
+        fa.fa_cache_fork(cache, cache, z(2, 4), z(2), z(9), all_or_nothing=True)
