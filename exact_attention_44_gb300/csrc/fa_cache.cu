@@ -43,9 +43,10 @@ cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cuda
 // group of up to 32 lanes takes a token: one block table entry for all of its
 // heads, then the 16-byte pieces of its K and V rows, four of each in flight a
 // lane.  (A thread a piece, each with its own table entry, took 17.5 us where
-// this takes 8.8: five prompts of up to 2011 tokens, 8 heads of D = 128, 62 MB read
-// and written, 7.0 TB/s with what the L2 cache keeps.)  One token for each of 64
-// sequences: 2.0 us, a launch and three dependent loads.
+// this takes 8.8 to 9.5: five prompts of up to 2011 tokens, 8 heads of D = 128, 62 MB
+// read and written, repeated in a graph, where the L2 cache keeps part; 12.6 on new
+// inputs, 4.9 TB/s.)  One token for each of 64 sequences: 2.1 us in a graph, 3.0 a
+// call, a launch and three dependent loads.
 constexpr int APPEND_THREADS = 128;
 
 __global__ void __launch_bounds__(APPEND_THREADS) fa_cache_append_kernel(const AppendParams p) {
@@ -98,8 +99,9 @@ __global__ void __launch_bounds__(APPEND_THREADS) fa_cache_append_kernel(const A
 // path strictly increasing a step writes only where the same thread has
 // already read (position lens[z] + i is read by no step after i), so steps need
 // no barrier, and the reads of eight steps may go ahead of their writes.  64
-// sequences x 9 tokens x 16 layers x 8 heads of D = 128 (33.6 MB): 7.2 us, 4.7 TB/s
-// (16.5 with table look-ups in every thread); 4 sequences x 5 tokens: 2.8 us.
+// sequences x 9 tokens x 16 layers x 8 heads of D = 128 (33.6 MB): 9.0 us on new
+// inputs, 3.7 TB/s, 7.2 to 8.0 repeated in a graph (16.5 with table look-ups in every
+// thread); 4 sequences x 5 tokens: 2.8 to 3.1 us.
 constexpr int COMMIT_THREADS = 256;
 constexpr int COMMIT_BATCH = 64;
 
@@ -167,8 +169,10 @@ __global__ void __launch_bounds__(COMMIT_THREADS) fa_cache_commit_kernel(const C
 // its own, and which pages those are -- the lowest ones whose count is 0, in
 // the order of sequences and columns (so the result does not depend on
 // timing).  The second rewrites the table and counts, and copies the partly
-// filled pages.  Bounded by latency: 6.2 us for 8 beams over 16 layers, 8.5 us for a
-// batch of 96, about half for each kernel.  One cluster of eight CTAs with
+// filled pages.  Bounded by latency in small pools: 6.3 us for 8 beams over 16 layers,
+// 8.1 to 8.8 us for a batch of 96, about half for each kernel; a page of room that a
+// sequence still has costs a dependent load, and used pages in front of the free ones
+// 22 us per 100 000.  One cluster of eight CTAs with
 // barriers between the phases instead took 14.0 and 22.4 us: too few loads in
 // flight for the table and the tails.
 constexpr int PLAN_THREADS = 1024;

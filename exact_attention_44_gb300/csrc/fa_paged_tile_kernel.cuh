@@ -31,7 +31,8 @@
 // in the contiguous forward (1.06 us with 16-position pages, whose 32 boxes a
 // block the copy unit takes one after another).  With two tiles the two bounds
 // meet: 32 sequences of 4096-8192 positions x 64 tokens x 4 heads (848 MB, 207
-// GFLOP) take 183 to 192 us, 4.5 TB/s and 1.1 PFLOP/s at 1.2 kW, where the clock
+// GFLOP) take 188 to 195 us a call (175 to 192 as one input repeated in a graph),
+// 4.4 TB/s and 1.08 PFLOP/s at 1.2 kW, where the clock
 // has fallen from 2.07 to 1.85 GHz (168 us with all pages in L2; a third slot
 // in the rings of K and V instead of Q's second changes nothing).  Between two
 // tiles a softmax warp loses 2.6 us (its last product 0.6, the output 1.2, the
@@ -39,7 +40,7 @@
 // 300-400 x 128 tokens x 4 heads take 183 us.  Short calls are bounded by the way
 // from launch to the first products (about 8 us: lengths, block table, first
 // copies, first block) and by the merge of the parts (about 5 us; 8 sequences of
-// 500-3000 x 32 tokens: 21.7 us in all, 10 us of DRAM time).
+// 500-3000 x 32 tokens: 22.0 us in all, 10 us of DRAM time).
 #pragma once
 
 #include "fa_fwd_kernel.cuh"

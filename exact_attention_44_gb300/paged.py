@@ -82,7 +82,10 @@ def fa_fwd_paged(q, k_cache, v_cache, block_table, seq_lens, o=None, lse=None, *
     (default T).  tree_mask: int32 bit words, (T, ceil(T/32)) for all sequences
     or (Z, T, ceil(T/32)): bit j of token t's words says that t sees new token
     j; None is a chain (t sees 0 .. t).  Every new token sees all earlier
-    positions.  Tokens that see nothing or do not exist get o = 0, lse = -inf.
+    positions.  Tokens that see nothing or do not exist get o = 0, lse = -inf
+    (what q holds for the latter does not matter).  Sums are fp32; the
+    probabilities are cast to the input type before the product with V, as in
+    fa_fwd.
     workspace: a CUDA uint8 tensor of fa_fwd_paged_workspace_size(D) bytes;
     one is allocated when omitted.  Returns (o, lse), lse (Z, Hq, T) fp32 or
     None, without synchronising.

@@ -485,12 +485,13 @@ typedef struct {
  *
  * Every new token sees all positions before seq_lens[z].  With query head hq
  * on kv head hq / (Hq / Hkv), O and lse are softmax attention over the seen
- * positions (fp32 sums, lse natural).  A token that sees nothing, and a token
+ * positions (fp32 sums, lse natural; the probabilities are cast to the input
+ * type before the product with V, as in fa_fwd).  A token that sees nothing, and a token
  * t >= new_lens[z], gets O = 0 and lse = -inf.  What a page holds behind the
  * last position is never used.  A new token's K that a query does not see has
  * no effect on it whatever it holds; its V must be finite (the products weigh
  * it with 0).  Hq % Hkv == 0.  Results are bitwise reproducible for the same
- * arguments and lengths.
+ * arguments and lengths, and do not depend on q of tokens t >= new_lens[z].
  */
 typedef struct {
     fa_paged_cache cache;
