@@ -210,13 +210,13 @@ fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
 
     const bool bf16 = x.dtype == FA_DTYPE_BF16;
     // Up to 16 rows of a (sequence, kv head) run on the rows kernel up to D = 128, the
-    // others on the tile kernel, which needs a whole group in a tile.  Both sides (calls
-    // repeated in a graph), rows against tile kernel: 16 rows, 16 sequences of 1000-4000, Hkv 8: 35.0 / 36.1 us at
-    // D 128, 21.9 / 30.1 at D 64, 19.2 / 28.6 at D 16; 4 rows, 64 sequences of 256-4096,
-    // D 128: 96 / 101; 12 to 16 rows of one sequence of 1024, D 128: 13.9 / 13.4, 14.7 /
-    // 13.4; 32 rows (two tiles of 16): 178 / 106.  At D = 256, where the rows kernel has
-    // four warps an SM: 4 rows 22.7 / 19.8, 8 rows 25.1 / 19.9, 1 row 98.5 / 98.8 and
-    // 13.8 / 15.0.
+    // others on the tile kernel, which needs a whole group in a tile.  Both sides, rows
+    // against tile kernel, repeated in a graph: 16 rows, 16 sequences of 1000-4000, Hkv 8:
+    // 35.0 / 36.1 us at D 128, 21.9 / 30.1 at D 64, 19.2 / 28.6 at D 16; 4 rows, 64
+    // sequences of 256-4096, D 128: 96 / 101; 12 to 16 rows of one sequence of 1024, D 128:
+    // 13.9 / 13.4, 14.7 / 13.4; 32 rows (two tiles of 16): 178 / 106.  At D = 256, where the
+    // rows kernel has four warps an SM: 4 rows 22.7 / 19.8, 8 rows 25.1 / 19.9, 1 row 98.5 /
+    // 98.8 and 13.8 / 15.0.
     a.tiles = G <= 128 && (D == 256 || T * (int64_t)G > 16);
     CUtensorMap mq{}, mk{}, mv{};
     int bk, workers;

@@ -142,11 +142,11 @@ def fa_cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source=No
     that is not emptied gets pages for `room` more positions.  missing: (1)
     int32, receives how many pages lacked (0: none).  all_or_nothing: if pages
     lack nothing is changed, so that sequences can be freed and the same call made
-    again (it needs `missing`); otherwise the call does what it can, and a copy whose partly filled
-    page lacked has lost the rows in it (`missing` counts it in every later call,
-    until it is replaced or emptied).  workspace: a CUDA uint8 tensor of
-    fa_cache_fork_workspace_size(Z, max_pages) bytes; one is allocated when
-    omitted.
+    again (it needs `missing`); otherwise the call does what it can, and a copy
+    whose partly filled page lacked has lost the rows in it (`missing` counts it in
+    every later call, until it is replaced or emptied).  workspace: a CUDA uint8
+    tensor of fa_cache_fork_workspace_size(Z, max_pages) bytes; one is allocated
+    when omitted.
     """
     ext = _ext if _bound is not None and _bound is _binding._lib else _calls()
     ext.cache_fork(k_cache, v_cache, block_table, seq_lens, ref_counts, source, room, missing, workspace,

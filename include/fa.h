@@ -486,8 +486,8 @@ typedef struct {
  * Every new token sees all positions before seq_lens[z].  With query head hq
  * on kv head hq / (Hq / Hkv), O and lse are softmax attention over the seen
  * positions (fp32 sums, lse natural; the probabilities are cast to the input
- * type before the product with V, as in fa_fwd).  A token that sees nothing, and a token
- * t >= new_lens[z], gets O = 0 and lse = -inf.  What a page holds behind the
+ * type before the product with V, as in fa_fwd).  A token that sees nothing, and
+ * a token t >= new_lens[z], gets O = 0 and lse = -inf.  What a page holds behind the
  * last position is never used.  A new token's K that a query does not see has
  * no effect on it whatever it holds; its V must be finite (the products weigh
  * it with 0).  Hq % Hkv == 0.  Results are bitwise reproducible for the same
@@ -566,13 +566,14 @@ fa_status fa_cache_commit(const fa_cache_commit_args* args, cudaStream_t stream)
  *     it, for good if the source does not stay: positions there read as zeros
  *     (FA_ERR_PAGE), neither the sequence nor a copy of it gets pages any more,
  *     and every call counts the pages that it would need from there on in
- *     *missing, until it becomes a copy of another sequence or is emptied.
+ *     *missing (so that an all_or_nothing call does nothing), until it becomes a
+ *     copy of another sequence or is emptied.
  *
  * Valid state: a row's entries are its ceil(len / page_size) pages, then
  * pages of room, then -1; a page with room to write belongs to one sequence.
  * fa_cache_fork keeps it so as long as all_or_nothing is set or no pages lack.
- * A source outside -1 .. Z - 1 is recorded as
- * FA_ERR_PAGE and the sequence stays.  Z <= 8192, P and room <= 2^30, Z * max_pages < 2^31.
+ * A source outside -1 .. Z - 1 is recorded as FA_ERR_PAGE and the sequence
+ * stays.  Z <= 8192, P and room <= 2^30, Z * max_pages < 2^31.
  */
 typedef struct {
     fa_paged_cache cache;

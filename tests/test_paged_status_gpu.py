@@ -81,7 +81,7 @@ def test_steps_after_an_ended_sequence_record_nothing():
         alive = torch.where(source < 0, torch.zeros_like(alive), alive[source.clamp(min=0).long()])
         source = torch.where(alive > 0, source, torch.full_like(source, -1))
         new = alive * T
-        fa.fa_cache_fork(k, v, table, lens, refs, source, room=T, missing=missing)
+        fa.fa_cache_fork(k, v, table, lens, refs, source, room=T, missing=missing, all_or_nothing=True)
         for i in range(2):
             fa.fa_cache_append(rows, rows, k[i], v[i], table, lens, new_lens=new)
             o, lse = fa.fa_fwd_paged(q, k[i], v[i], table, lens, new_lens=new)
