@@ -56,6 +56,14 @@ _SIGNATURES = {
     "fa_cache_fork": (ctypes.c_int, [ctypes.c_void_p] * 2),
     "fa_fwd_paged_workspace_size": (ctypes.c_int, [ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]),
     "fa_cache_fork_workspace_size": (ctypes.c_int, [ctypes.c_int] * 2 + [ctypes.POINTER(ctypes.c_size_t)]),
+    "fa_rope_frequencies": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "fa_rope_turns": (ctypes.c_int, [ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p]),
+    "fa_rope": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_append_rope": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_score": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_evict": (ctypes.c_int, [ctypes.c_void_p] * 2),
+    "fa_cache_score_workspace_size": (ctypes.c_int, [ctypes.POINTER(ctypes.c_size_t)]),
+    "fa_cache_evict_workspace_size": (ctypes.c_int, [ctypes.c_int] * 5 + [ctypes.POINTER(ctypes.c_size_t)]),
     "fa_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "fa_device_status": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ctypes.c_uint32)]),
     "fa_fwd_plan": (ctypes.c_int, [ctypes.c_int] * 8 + [ctypes.POINTER(ctypes.c_int64)] * 2 +

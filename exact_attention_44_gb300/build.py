@@ -38,10 +38,12 @@ EXT = os.path.join(BUILD, "_paged_ext.so")
 FWD_DIMS = (16, 32, 64, 128, 256)
 BWD_DIMS = (16, 32, 64, 128, 256)
 UNITS = ([(src, src.replace(".cu", ".o"), []) for src in ("fa_api.cu", "fa_lse_merge.cu", "fa_noalloc.cu",
-                                                           "fa_paged_api.cu", "fa_cache.cu")] +
+                                                           "fa_paged_api.cu", "fa_cache.cu", "fa_budget_api.cu",
+                                                           "fa_rope.cu", "fa_evict.cu")] +
          [("fa_fwd_dim.cu", f"fa_fwd_d{d}.o", [f"-DFA_HEAD_DIM={d}"]) for d in FWD_DIMS] +
          [("fa_bwd_dim.cu", f"fa_bwd_d{d}.o", [f"-DFA_HEAD_DIM={d}"]) for d in BWD_DIMS] +
-         [("fa_paged_dim.cu", f"fa_paged_d{d}.o", [f"-DFA_HEAD_DIM={d}"]) for d in FWD_DIMS])
+         [("fa_paged_dim.cu", f"fa_paged_d{d}.o", [f"-DFA_HEAD_DIM={d}"]) for d in FWD_DIMS] +
+         [("fa_score_dim.cu", f"fa_score_d{d}.o", [f"-DFA_HEAD_DIM={d}"]) for d in FWD_DIMS])
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
                 "--expt-relaxed-constexpr", f"-I{INCLUDE}", f"-I{CSRC}"]

@@ -8,35 +8,13 @@
 
 #include <climits>
 
+#include "fa_cache.cuh"
 #include "fa_paged.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
 
 namespace {
-
-// Small integers through L2: the kernels are programmatic dependents (see
-// fa_paged_sched.cuh), and fork rewrites tables in place.
-__device__ __forceinline__ int ldi(const int32_t* p) { return __ldcg(p); }
-
-__device__ __forceinline__ void bad_page(uint32_t* status, uint32_t site) {
-    atomicCAS(status + PAGE_WORD, 0u, STATUS_PAGE | (site << 8) | ((blockIdx.x & 0xFFFFu) << 16));
-}
-
-template <typename K, typename P>
-cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const P& p) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
-}
 
 // ------------------------------------------------------------ append --------
 // Row (z, t, h) of the new K and V, t < news[z], to position lens[z] + t.  A

@@ -1,0 +1,439 @@
+// Cutting the sequences of a paged cache back to a budget: of each (layer, sequence, kv
+// head) the positions with the highest scores stay, in their order, and move together.
+//
+// Three kernels.  The first, a CTA a (layer, sequence, head), selects: a radix selection
+// of the n-th highest score (three passes over 11, 11 and 10 bits of the keys), then the
+// list of the positions that stay.  The second, one CTA, does the books: pages that are
+// rewritten but shared with other sequences are replaced by free ones, lowest first in
+// the order of sequences and columns (so the result does not depend on timing).  The
+// third moves the rows, in place, and writes tables, counts and lengths.
+//
+// What bounds it is the rows that move: 8 D bytes each, against 4 to 12 bytes of
+// selection a position.
+#include "fa_evict.h"
+
+#include <climits>
+
+#include "fa_cache.cuh"
+#include "fa_paged.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+struct EvictWs {
+    int32_t *target, *own, *off, *lack, *before, *after, *pages, *first, *idx;
+};
+__device__ __forceinline__ EvictWs evict_ws(const EvictParams& p) {
+    EvictWs w;
+    const int64_t zm = (int64_t)p.Z * p.M;
+    w.target = p.ws;
+    w.own = w.target + p.Z;
+    w.off = w.own + p.Z;
+    w.lack = w.off + p.Z;
+    w.before = w.lack + 1;
+    w.after = w.before + zm;
+    w.pages = w.after + zm;
+    w.first = w.pages + zm;
+    w.idx = w.first + (int64_t)p.L * p.Z * p.H;
+    return w;
+}
+
+// What a sequence is cut to; -1: it stays as it is.
+__device__ __forceinline__ int cut_to(const EvictParams& p, int z, int len) {
+    int n = p.budget;
+    if (p.keep != nullptr) {
+        const int k = ldi(p.keep + z);
+        if (k < 0) return -1;
+        n = min(n, k);
+    }
+    return len > n ? n : -1;
+}
+__device__ __forceinline__ int held_len(const EvictParams& p, int z) { return min(max(ldi(p.lens + z), 0), p.P > 0 ? p.M * p.page : 0); }
+
+// ------------------------------------------------------------ select --------
+constexpr int SELECT_THREADS = 256;
+constexpr int SELECT_WARPS = SELECT_THREADS / 32;
+constexpr int BINS = 2048;
+
+// Unsigned keys in the order of the scores; -0 is 0, a NaN is above everything.
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (x != x) return 0xffffffffu;
+    const uint32_t b = __float_as_uint(x == 0.f ? 0.f : x);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(SELECT_THREADS) fa_evict_select_kernel(const EvictParams p, int held) {
+    extern __shared__ uint32_t keys_held[];  // the candidates' keys, if they fit
+    __shared__ int hist[BINS];
+    __shared__ int red[SELECT_WARPS], red2[SELECT_WARPS], found[2], first_moved;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const EvictWs w = evict_ws(p);
+    const int h = blockIdx.x, z = blockIdx.y, l = blockIdx.z;
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    const int len = held_len(p, z), target = cut_to(p, z, len);
+    if (h == 0 && l == 0) {
+        if (tid == 0) w.target[z] = target;
+        if (target >= 0)
+            for (int c = tid; c < p.M; c += SELECT_THREADS) w.before[(int64_t)z * p.M + c] = ldi(p.table + z * p.st_z + c);
+    }
+    if (target < 0) return;
+    const int64_t unit = ((int64_t)l * p.Z + z) * p.H + h;
+    const int front = min(p.first, target), back = min(p.recent, target - front);
+    const int n = len - back - front, m = target - back - front;  // candidates, and how many of them stay: m < n
+    const float* from = p.scores + l * p.ss_l + z * p.ss_z + h * p.ss_h + front;
+    const bool fits = n <= held;
+    if (fits)
+        for (int i = tid; i < n; i += SELECT_THREADS) keys_held[i] = score_key(__ldcg(from + i));
+    auto key = [&](int i) { return fits ? keys_held[i] : score_key(__ldcg(from + i)); };
+
+    // the m-th highest key: its bits from the top, 11, 11 and 10 at a time; `want` is how
+    // many keys with these upper bits stay
+    uint32_t prefix = 0;
+    int want = m;
+    if (m > 0)
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+            const uint32_t above = pass == 0 ? 0u : ~0u << (shift + bits);
+            for (int i = tid; i < BINS; i += SELECT_THREADS) hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < n; i += SELECT_THREADS) {
+                const uint32_t k = key(i);
+                if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+            }
+            __syncthreads();
+            // a thread sums BINS / SELECT_THREADS bins, the highest first
+            constexpr int B = BINS / SELECT_THREADS;
+            const int top = BINS - 1 - tid * B;
+            int mine = 0;
+            for (int b = 0; b < B; ++b) mine += hist[top - b];
+            int x = mine;
+            for (int d = 1; d < 32; d *= 2) {
+                const int y = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += y;
+            }
+            if (lane == 31) red[warp] = x;
+            __syncthreads();
+            for (int i = 0; i < warp; ++i) x += red[i];
+            if (x >= want && x - mine < want) {  // one thread
+                int before = x - mine, b = 0;
+                while (before + hist[top - b] < want) before += hist[top - b++];
+                found[0] = top - b;
+                found[1] = want - before;
+            }
+            __syncthreads();
+            prefix |= (uint32_t)found[0] << shift;
+            want = found[1];
+        }
+    __syncthreads();
+    // Keys above the prefix stay, and of those equal to it the first `want`.  A warp takes
+    // a contiguous share of the candidates.
+    const int share = ((n + SELECT_WARPS - 1) / SELECT_WARPS + 31) / 32 * 32;
+    const int i0 = min(warp * share, n), i1 = min(i0 + share, n);
+    int higher = 0, equal = 0;
+    if (m > 0)
+        for (int i = i0; i < i1; i += 32) {
+            const bool in = i + lane < i1;
+            const uint32_t k = in ? key(i + lane) : 0u;
+            higher += __popc(__ballot_sync(0xffffffffu, in && k > prefix));
+            equal += __popc(__ballot_sync(0xffffffffu, in && k == prefix));
+        }
+    if (lane == 0) {
+        red[warp] = higher;
+        red2[warp] = equal;
+    }
+    if (tid == 0) first_moved = target;
+    __syncthreads();
+    int to = front, ties = want;  // where this warp's first one goes, and how many equal ones are left for it
+    for (int i = 0; i < warp; ++i) {
+        to += red[i] + min(ties, red2[i]);
+        ties -= min(ties, red2[i]);
+    }
+    int32_t* idx = w.idx + unit * p.budget;
+    int moved = target;
+    if (m > 0)
+        for (int i = i0; i < i1; i += 32) {
+            const bool in = i + lane < i1;
+            const uint32_t k = in ? key(i + lane) : 0u;
+            const uint32_t hi = __ballot_sync(0xffffffffu, in && k > prefix), eq = __ballot_sync(0xffffffffu, in && k == prefix);
+            const uint32_t below = (1u << lane) - 1;
+            const bool stays = in && (k > prefix || (k == prefix && __popc(eq & below) < ties));
+            if (stays) {
+                const int at = to + __popc(hi & below) + min(ties, __popc(eq & below));
+                idx[at] = front + i + lane;
+                if (at != front + i + lane) moved = min(moved, at);
+            }
+            to += __popc(hi) + min(ties, __popc(eq));
+            ties -= min(ties, __popc(eq));
+        }
+    for (int i = tid; i < front; i += SELECT_THREADS) idx[i] = i;
+    for (int i = tid; i < back; i += SELECT_THREADS) idx[front + m + i] = len - back + i;
+    if (tid == 0 && back > 0) moved = min(moved, front + m);  // (len - back > front + m)
+    for (int d = 16; d > 0; d /= 2) moved = min(moved, __shfl_xor_sync(0xffffffffu, moved, d));
+    if (lane == 0) atomicMin(&first_moved, moved);
+    __syncthreads();
+    if (tid == 0) w.first[unit] = first_moved;
+}
+
+// ------------------------------------------------------------ plan ----------
+constexpr int EVICT_PLAN_THREADS = 1024;
+
+// exclusive prefix sum over the CTA; total in *sum
+__device__ __forceinline__ int cta_scan(int v, int* red, int* sum) {
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    int x = v;
+    for (int d = 1; d < 32; d *= 2) {
+        const int y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int y = lane < (int)blockDim.x / 32 ? red[lane] : 0;
+        for (int d = 1; d < 32; d *= 2) {
+            const int u = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += u;
+        }
+        red[lane] = y;
+    }
+    __syncthreads();
+    *sum = red[31];
+    return x - v + (warp > 0 ? red[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(EVICT_PLAN_THREADS) fa_evict_plan_kernel(const EvictParams p) {
+    __shared__ int red[32];
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const EvictWs w = evict_ws(p);
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    constexpr int WARPS = EVICT_PLAN_THREADS / 32;
+    // a warp a sequence: its first page that is rewritten, and how many from there on are shared
+    for (int z = warp; z < p.Z; z += WARPS) {
+        const int target = ldi(w.target + z);
+        int count = 0, own = 0;
+        if (target >= 0) {
+            int first = target;
+            for (int i = lane; i < p.L * p.H; i += 32) {
+                const int l = i / p.H, h = i - l * p.H;
+                first = min(first, ldi(w.first + ((int64_t)l * p.Z + z) * p.H + h));
+            }
+            for (int d = 16; d > 0; d /= 2) first = min(first, __shfl_xor_sync(0xffffffffu, first, d));
+            own = first / p.page;
+            const int need = (target + p.page - 1) / p.page;
+            for (int c = own + lane; c < need; c += 32) {
+                const int e = ldi(w.before + (int64_t)z * p.M + c);
+                count += (unsigned)e < (unsigned)p.P && ldi(p.refs + e) > 1;
+            }
+            for (int d = 16; d > 0; d /= 2) count += __shfl_xor_sync(0xffffffffu, count, d);
+        }
+        if (lane == 0) {
+            w.own[z] = own;
+            w.off[z] = count;
+        }
+    }
+    __syncthreads();
+    int wanted = 0;
+    for (int z0 = 0; z0 < p.Z; z0 += EVICT_PLAN_THREADS) {
+        const int z = z0 + tid;
+        int sum, off = cta_scan(z < p.Z ? ldi(w.off + z) : 0, red, &sum);
+        if (z < p.Z) w.off[z] = wanted + off;
+        wanted += sum;
+    }
+    // the first `wanted` pages with count 0
+    int found = 0;
+    for (int p0 = 0; p0 < p.P && found < wanted; p0 += 4 * EVICT_PLAN_THREADS) {
+        const int i = p0 + 4 * tid;
+        int c[4], k = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            c[u] = i + u < p.P ? ldi(p.refs + i + u) : 1;
+            k += c[u] == 0;
+        }
+        int sum, at = found + cta_scan(k, red, &sum);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (c[u] == 0) {
+                if (at < wanted) w.pages[at] = i + u;
+                ++at;
+            }
+        found += sum;
+    }
+    const int lack = max(0, wanted - found);
+    if (tid == 0) {
+        *w.lack = lack;
+        *p.missing = lack;
+    }
+    __syncthreads();
+    if (lack > 0) return;
+    // the rows as they will be
+    for (int z = warp; z < p.Z; z += WARPS) {
+        const int target = ldi(w.target + z);
+        if (target < 0) continue;
+        const int own = ldi(w.own + z), need = (target + p.page - 1) / p.page;
+        int off = ldi(w.off + z);
+        for (int c0 = 0; c0 < need; c0 += 32) {
+            const int c = c0 + lane, e = c < need ? ldi(w.before + (int64_t)z * p.M + c) : -1;
+            const bool shared = c >= own && (unsigned)e < (unsigned)p.P && ldi(p.refs + e) > 1;
+            const uint32_t all = __ballot_sync(0xffffffffu, shared);
+            if (c < need) w.after[(int64_t)z * p.M + c] = shared ? ldi(w.pages + off + __popc(all & ((1u << lane) - 1))) : e;
+            off += __popc(all);
+        }
+    }
+}
+
+// ------------------------------------------------------------ move ----------
+// Row idx[i] to row i of each (layer, sequence, head), K and V, and its score.  idx[i] >=
+// i increases with i, so what a row overwrites is read by no later row: within a CTA the
+// rows go in chunks whose reads come before their writes, and the reads of the next chunk
+// go ahead of the writes of this one.
+constexpr int MOVE_THREADS = 256;
+
+struct EvictMove {
+    EvictParams p;
+    int table_ctas;
+};
+
+__global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const EvictMove a) {
+    const EvictParams& p = a.p;
+    constexpr int U = 8;
+    __shared__ int64_t where[2][2][MOVE_THREADS];  // [chunk parity][from, to][row]; from -1: it stays
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const EvictWs w = evict_ws(p);
+    const int tid = threadIdx.x;
+    if (ldi(w.lack) > 0) return;
+    if ((int)blockIdx.x < a.table_ctas) {  // the books
+        for (int z = blockIdx.x; z < p.Z; z += a.table_ctas) {
+            const int target = ldi(w.target + z);
+            if (target < 0) continue;
+            const int need = (target + p.page - 1) / p.page;
+            for (int c = tid; c < p.M; c += MOVE_THREADS) {
+                const int was = ldi(w.before + (int64_t)z * p.M + c);
+                const int now = c < need ? ldi(w.after + (int64_t)z * p.M + c) : -1;
+                if (now == was) continue;
+                if ((unsigned)was < (unsigned)p.P) atomicAdd(p.refs + was, -1);
+                if (now >= 0) atomicAdd(p.refs + now, 1);
+                p.table[z * p.st_z + c] = now;
+            }
+            if (tid == 0) p.lens[z] = target;
+        }
+        return;
+    }
+    // a CTA a unit: (layer, sequence, head, K or V or the scores)
+    const int64_t unit3 = (int64_t)blockIdx.x - a.table_ctas, unit = unit3 / 3;
+    const int kind = (int)(unit3 - unit * 3);
+    const int h = (int)(unit % p.H), z = (int)(unit / p.H % p.Z), l = (int)(unit / p.H / p.Z);
+    const int target = ldi(w.target + z);
+    if (target < 0) return;
+    const int32_t *idx = w.idx + unit * p.budget, *before = w.before + (int64_t)z * p.M, *after = w.after + (int64_t)z * p.M;
+    if (kind == 2) {
+        float* s = p.scores + l * p.ss_l + z * p.ss_z + h * p.ss_h;
+        for (int i0 = ldi(w.first + unit); i0 < target; i0 += U * MOVE_THREADS) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * MOVE_THREADS + tid;
+                if (i < target) v[u] = __ldcg(s + ldi(idx + i));
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = i0 + u * MOVE_THREADS + tid;
+                if (i < target) s[i] = v[u];
+            }
+        }
+        return;
+    }
+    const CacheView& cache = kind == 0 ? p.k : p.v;
+    uint16_t* base = cache.base + l * cache.l + h * cache.h;
+    const int per = p.D / 8, side = MOVE_THREADS / per, rows = U * side;  // lanes a row, rows at a time, rows a chunk
+    const int row = tid / per, piece = (tid - row * per) * 8;
+    const int start = min(ldi(w.own + z) * p.page, target);
+    const int unmoved = ldi(w.first + unit);
+    bool bad = false;
+    // rows of a chunk: at most U * 32 (D = 64: 256); for D < 64 in turns of MOVE_THREADS
+    auto find = [&](int i0, int half) {
+        const int i = i0 + tid;
+        int64_t from = -1, to = -1;
+        if (tid < rows && i < target) {
+            const int j = i < unmoved ? i : ldi(idx + i);
+            const int cf = j / p.page, ct = i / p.page;
+            const int ef = ldi(before + cf), et = ldi(after + ct);
+            if (j != i || ef != et) {
+                if ((unsigned)ef < (unsigned)p.P && (unsigned)et < (unsigned)p.P) {
+                    from = ef * cache.p + (j - cf * p.page) * cache.n;
+                    to = et * cache.p + (i - ct * p.page) * cache.n;
+                } else {
+                    bad = true;
+                }
+            }
+        }
+        where[half][0][tid] = from;
+        where[half][1][tid] = to;
+    };
+    const int chunk = min(rows, MOVE_THREADS);
+    uint4 now[U], then[U];
+    auto load = [&](int half, uint4 (&v)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = u * side + row;
+            if (r < chunk && where[half][0][r] >= 0) v[u] = __ldcg(reinterpret_cast<const uint4*>(base + where[half][0][r] + piece));
+        }
+    };
+    auto store = [&](int half, const uint4 (&v)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = u * side + row;
+            if (r < chunk && where[half][0][r] >= 0) *reinterpret_cast<uint4*>(base + where[half][1][r] + piece) = v[u];
+        }
+    };
+    if (start < target) {
+        find(start, 0);
+        __syncthreads();
+        load(0, now);
+    }
+    int half = 0;
+    for (int i0 = start; i0 < target; i0 += chunk) {
+        const bool more = i0 + chunk < target;
+        if (more) find(i0 + chunk, half ^ 1);
+        __syncthreads();  // this chunk has been read, and the places of the next are there
+        if (more) load(half ^ 1, then);
+        store(half, now);
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = then[u];
+        half ^= 1;
+        __syncthreads();  // the places of this chunk may be overwritten
+    }
+    if (bad) bad_page(p.status, SITE_PAGE_EVICT);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_evict(const EvictParams& p, int sms, cudaStream_t stream) {
+    // keys of up to 8192 candidates are held in shared memory
+    const int64_t cap = (int64_t)p.M * p.page;
+    const int held = (int)(cap < 8192 ? cap : 8192);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.H, (unsigned)p.Z, (unsigned)p.L);
+    cfg.blockDim = dim3(SELECT_THREADS);
+    cfg.dynamicSmemBytes = (size_t)held * sizeof(uint32_t);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, fa_evict_select_kernel, p, held);
+    if (err != cudaSuccess) return err;
+    err = launch_dependent(fa_evict_plan_kernel, dim3(1), EVICT_PLAN_THREADS, 0, stream, p);
+    if (err != cudaSuccess) return err;
+    const EvictMove a{p, p.Z < sms ? p.Z : sms};
+    const int64_t units = (int64_t)p.L * p.Z * p.H * 3;
+    return launch_dependent(fa_evict_move_kernel, dim3((unsigned)(a.table_ctas + units)), MOVE_THREADS, 0, stream, a);
+}
+
+}  // namespace fa

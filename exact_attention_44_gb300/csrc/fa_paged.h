@@ -20,6 +20,8 @@ enum PageSite : uint32_t {
     SITE_PAGE_APPEND = 61,
     SITE_PAGE_COMMIT = 62,
     SITE_PAGE_FORK = 63,
+    SITE_PAGE_SCORE = 64,
+    SITE_PAGE_EVICT = 65,
 };
 
 // Division of 0 <= n < 2^31 by a positive divisor fixed for the launch, in four

@@ -1,0 +1,218 @@
+// Rotary positions: the first R elements of a row are R / 2 pairs -- (i, i + R / 2),
+// or (2 i, 2 i + 1) interleaved -- and pair i of a row at position p turns by the
+// angle p f_i:
+//     (a, b) -> factor (a cos - b sin, a sin + b cos),
+// the rest of the row stays.  The gradient is the turn back, times the same factor.
+// With a cache (fa_cache_append_rope) the turned K rows and the V rows go to their
+// slots through the block table.
+//
+// The angle.  p f in fp32 would be off by p 2^-24 radians (0.06 at a million), so f is
+// given in turns as a 64-bit fixed-point fraction and the product with the integer p
+// is taken modulo a whole turn by letting it wrap: what is left is exact but for f's
+// own rounding, p 2^-65 turns.  Its upper 32 bits go to sincospi.
+//
+// What bounds it is reading and writing each row once.  A thread takes 8 pairs (two
+// 16-byte pieces) of a token through some of its heads, so that a sine and cosine serve
+// several heads, with the loads of four heads in flight.
+#include "fa_rope.h"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_cache.cuh"
+#include "fa_paged.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr int ROPE_THREADS = 128;
+
+template <bool BF16>
+__device__ __forceinline__ float2 widen(uint32_t w) {
+    if constexpr (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <bool BF16>
+__device__ __forceinline__ uint32_t narrow(float lo, float hi) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// V pairs as a thread holds them: V = 8, two 16-byte pieces; V = 1, two elements in
+// the low halves of a word each.
+template <int V>
+struct Pairs {
+    uint4 a, b;
+};
+template <>
+struct Pairs<1> {
+    uint32_t a, b;
+};
+// `from` and `apart`: the first element of the piece, and of its second half
+template <int V>
+__device__ __forceinline__ Pairs<V> load_pairs(const uint16_t* from, int apart) {
+    Pairs<V> x;
+    if constexpr (V == 8) {
+        x.a = __ldcg(reinterpret_cast<const uint4*>(from));
+        x.b = __ldcg(reinterpret_cast<const uint4*>(from + apart));
+    } else {
+        x.a = __ldcg(from);
+        x.b = __ldcg(from + apart);
+    }
+    return x;
+}
+template <int V>
+__device__ __forceinline__ void store_pairs(uint16_t* to, int apart, const Pairs<V>& x) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<uint4*>(to) = x.a;
+        *reinterpret_cast<uint4*>(to + apart) = x.b;
+    } else {
+        to[0] = (uint16_t)x.a;
+        to[apart] = (uint16_t)x.b;
+    }
+}
+template <bool BF16, bool INTER, int V>
+__device__ __forceinline__ void turn(Pairs<V>& x, const float (&c)[V], const float (&s)[V]) {
+    if constexpr (V == 1) {
+        const float a = widen<BF16>(x.a).x, b = widen<BF16>(x.b).x;
+        const uint32_t w = narrow<BF16>(fmaf(a, c[0], -(b * s[0])), fmaf(a, s[0], b * c[0]));
+        x.a = w & 0xffffu;
+        x.b = w >> 16;
+    } else {
+        uint32_t w[8] = {x.a.x, x.a.y, x.a.z, x.a.w, x.b.x, x.b.y, x.b.z, x.b.w};
+        if constexpr (INTER) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 p = widen<BF16>(w[i]);
+                w[i] = narrow<BF16>(fmaf(p.x, c[i], -(p.y * s[i])), fmaf(p.x, s[i], p.y * c[i]));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = widen<BF16>(w[i]), b = widen<BF16>(w[i + 4]);
+                w[i] = narrow<BF16>(fmaf(a.x, c[2 * i], -(b.x * s[2 * i])), fmaf(a.y, c[2 * i + 1], -(b.y * s[2 * i + 1])));
+                w[i + 4] = narrow<BF16>(fmaf(a.x, s[2 * i], b.x * c[2 * i]), fmaf(a.y, s[2 * i + 1], b.y * c[2 * i + 1]));
+            }
+        }
+        x.a = make_uint4(w[0], w[1], w[2], w[3]);
+        x.b = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
+
+template <bool BF16, bool INTER, int V, bool CACHE>
+__global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const RopeParams p) {
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int pieces = p.D / (2 * V), turning = p.R / (2 * V);  // pieces: a power of two
+    const int z = blockIdx.z, piece = threadIdx.x & (pieces - 1);
+    const int n = (int)(((int64_t)blockIdx.x * ROPE_THREADS + threadIdx.x) / pieces);
+    if (n >= p.N) return;
+    int64_t slot = 0;
+    int page = -1;
+    uint32_t position = (uint32_t)n;
+    if constexpr (CACHE) {
+        const int nl = p.news != nullptr ? ldi(p.news + z) : p.N;
+        if (n >= nl) return;
+        position += (uint32_t)max(ldi(p.lens + z), 0);  // below 2^32: the slot
+        const uint32_t col = position / (uint32_t)p.page;
+        page = col < (uint32_t)p.M ? ldi(p.table + z * p.st_z + col) : -1;
+        slot = position - col * (uint32_t)p.page;
+        if ((unsigned)page >= (unsigned)p.P) {
+            bad_page(p.status, SITE_PAGE_APPEND);
+            page = -1;
+        }
+    }
+    int64_t at = position;
+    if (p.positions != nullptr) at = ldi(p.positions + z * p.pos_z + n);
+    const bool turns = piece < turning;
+    float c[V], s[V];
+    if (turns) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint64_t f = (uint64_t)__ldcg(reinterpret_cast<const long long*>(p.turns + piece * V + i));
+            // the fraction of a turn, then in half turns for sincospi
+            const int32_t frac = (int32_t)(uint32_t)((f * (uint64_t)at) >> 32);
+            sincospif((float)frac * 0x1p-31f, &s[i], &c[i]);
+            c[i] *= p.cos_factor;
+            s[i] *= p.sin_factor;
+        }
+    }
+    // where a piece starts, and its second half
+    const int first = INTER || !turns ? piece * 2 * V : piece * V;
+    const int apart = INTER || !turns ? V : p.R / 2;
+    const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, p.Hq + p.Hk + (CACHE ? p.Hk : 0));
+    constexpr int U = 4;
+    for (int h = h0; h < h1; h += U) {
+        Pairs<V> x[U];
+        uint16_t* to[U];
+        bool rope[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = h + u;
+            to[u] = nullptr;
+            if (i >= h1) continue;
+            const uint16_t* from;
+            if (i < p.Hq) {
+                from = p.q + z * p.q_z + i * p.q_h + n * p.q_n;
+                if (turns || !p.q_in_place) to[u] = p.qo + z * p.qo_z + i * p.qo_h + n * p.qo_n;
+                rope[u] = turns;
+            } else if (i < p.Hq + p.Hk) {
+                from = p.k + z * p.k_z + (i - p.Hq) * p.k_h + n * p.k_n;
+                if constexpr (CACHE) {
+                    if (page >= 0) to[u] = p.kc.base + page * p.kc.p + (i - p.Hq) * p.kc.h + slot * p.kc.n;
+                } else if (turns || !p.k_in_place) {
+                    to[u] = p.ko + z * p.ko_z + (i - p.Hq) * p.ko_h + n * p.ko_n;
+                }
+                rope[u] = turns;
+            } else {
+                from = p.v + z * p.v_z + (i - p.Hq - p.Hk) * p.v_h + n * p.v_n;
+                if (page >= 0) to[u] = p.vc.base + page * p.vc.p + (i - p.Hq - p.Hk) * p.vc.h + slot * p.vc.n;
+                rope[u] = false;
+            }
+            if (to[u] != nullptr) {
+                x[u] = load_pairs<V>(from + first, apart);
+                to[u] += first;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (to[u] != nullptr) {
+                if (rope[u]) turn<BF16, INTER, V>(x[u], c, s);
+                store_pairs<V>(to[u], apart, x[u]);
+            }
+    }
+}
+
+template <bool BF16, bool INTER, int V>
+cudaError_t launch_v(RopeParams p, bool cache, int sms, cudaStream_t stream) {
+    const int heads = p.Hq + p.Hk * (cache ? 2 : 1);
+    const int64_t threads = (int64_t)p.N * (p.D / (2 * V));
+    const int64_t blocks = (threads + ROPE_THREADS - 1) / ROPE_THREADS;
+    // few tokens: fewer heads a thread, so that there are threads for every SM
+    p.heads = 4;
+    while (p.heads > 1 && blocks * p.Z * ((heads + p.heads - 1) / p.heads) < sms) p.heads /= 2;
+    const dim3 grid((unsigned)blocks, (unsigned)((heads + p.heads - 1) / p.heads), (unsigned)p.Z);
+    return cache ? launch_dependent(fa_rope_kernel<BF16, INTER, V, true>, grid, ROPE_THREADS, 0, stream, p)
+                 : launch_dependent(fa_rope_kernel<BF16, INTER, V, false>, grid, ROPE_THREADS, 0, stream, p);
+}
+template <bool BF16, bool INTER>
+cudaError_t launch_layout(const RopeParams& p, bool cache, int sms, cudaStream_t stream) {
+    // 16-byte pieces hold 8 pairs of one half: R a multiple of 16; other R go pair by pair
+    return p.R % 16 == 0 ? launch_v<BF16, INTER, 8>(p, cache, sms, stream) : launch_v<BF16, INTER, 1>(p, cache, sms, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, bool bf16, bool interleaved, bool cache, int sms, cudaStream_t stream) {
+    if (bf16) return interleaved ? launch_layout<true, true>(p, cache, sms, stream) : launch_layout<true, false>(p, cache, sms, stream);
+    return interleaved ? launch_layout<false, true>(p, cache, sms, stream) : launch_layout<false, false>(p, cache, sms, stream);
+}
+
+}  // namespace fa

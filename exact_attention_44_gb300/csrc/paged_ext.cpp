@@ -1,5 +1,5 @@
-// Python binding of the paged-cache entry points: argument checks and
-// marshalling only.  A decode step makes two or three of these calls a layer,
+// Python binding of the paged-cache entry points and of rotary positions: argument
+// checks and marshalling only.  A decode step makes two or three of these calls a layer,
 // each a few microseconds of GPU time; through ctypes and Python the host side
 // of one took 7 to 16 us, so it is a CPython extension over torch's tensors.
 // The functions of libfa are handed over by address (bind), so the extension
@@ -8,6 +8,7 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/ops/empty_strided.h>
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -30,6 +31,12 @@ struct Library {
     decltype(&fa_cache_commit) commit = nullptr;
     decltype(&fa_cache_fork) fork = nullptr;
     decltype(&fa_cache_fork_workspace_size) fork_size = nullptr;
+    decltype(&fa_rope) rope = nullptr;
+    decltype(&fa_cache_append_rope) append_rope = nullptr;
+    decltype(&fa_cache_score) score = nullptr;
+    decltype(&fa_cache_score_workspace_size) score_size = nullptr;
+    decltype(&fa_cache_evict) evict = nullptr;
+    decltype(&fa_cache_evict_workspace_size) evict_size = nullptr;
     PyObject* error = nullptr;  // the package's FaError
 } lib;
 
@@ -377,11 +384,265 @@ PyObject* cache_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (FaError, the addresses of the six entry points)
+fa_dtype dtype_of(const at::Tensor& t, const char* call) {
+    if (t.scalar_type() == at::kBFloat16) return FA_DTYPE_BF16;
+    if (t.scalar_type() == at::kHalf) return FA_DTYPE_F16;
+    type_error(std::string(call) + " takes float16 or bfloat16 tensors");
+}
+float float_arg(PyObject* o) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw python_error();
+    return (float)x;
+}
+int flag_arg(PyObject* o) {
+    const int x = PyObject_IsTrue(o);
+    if (x < 0) throw python_error();
+    return x;
+}
+// The frequencies' pairs.
+int pairs_of(const at::Tensor& turns) {
+    if (turns.scalar_type() != at::kLong || turns.dim() != 1 || !turns.is_contiguous())
+        value_error("turns must be a contiguous int64 tensor of rotary_dim / 2 entries (fa_rope_turns)");
+    return to_int(2 * turns.size(0), "rotary_dim");
+}
+// (N,) for all sequences or (Z, N); the stride between sequences
+int64_t positions_stride(const at::Tensor& t, int64_t Z, int64_t N) {
+    if (t.dim() == 1) {
+        check_ints(t, "positions", {N});
+        return 0;
+    }
+    check_ints(t, "positions", {Z, N});
+    return t.stride(0);
+}
+void check_out(const at::Tensor* out, const at::Tensor& like, const char* name) {
+    if (out != nullptr && (out->sizes() != like.sizes() || out->scalar_type() != like.scalar_type()))
+        value_error(std::string(name) + " must match its input's shape and dtype");
+}
+// A tensor for the outputs of `like`: its layout if that is dense with the last dimension contiguous.
+at::Tensor out_like(const at::Tensor& like) {
+    const bool keep = like.is_non_overlapping_and_dense() && (like.size(3) <= 1 || like.stride(3) == 1);
+    return keep ? at::empty_strided(like.sizes(), like.strides(), like.options()) : at::empty(like.sizes(), like.options());
+}
+
+// (q, k, turns, positions, interleaved, inverse, factor, q_out, k_out, stream)
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 10)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &turns = tensor(a[2], "turns");
+        const at::Tensor *k = maybe_tensor(a[1], "k"), *pos = maybe_tensor(a[3], "positions");
+        const at::Tensor *qo_arg = maybe_tensor(a[7], "q_out"), *ko_arg = maybe_tensor(a[8], "k_out");
+        if (q.dim() != 4) value_error("q must be 4-D (Z, H, N, D)");
+        fa_rope_args x{};
+        x.dtype = dtype_of(q, "fa_rope");
+        if (k != nullptr) {
+            if (k->dim() != 4 || k->size(0) != q.size(0) || k->size(2) != q.size(2) || k->size(3) != q.size(3))
+                value_error("k must be (Z, Hk, N, D) like q, got " + shape_of(k->sizes()) + " for " + shape_of(q.sizes()));
+            if (k->scalar_type() != q.scalar_type()) type_error("q and k must share one dtype");
+        } else if (ko_arg != nullptr) {
+            value_error("k_out without k");
+        }
+        check_out(qo_arg, q, "q_out");
+        if (k != nullptr) check_out(ko_arg, *k, "k_out");
+        x.rotary_dim = pairs_of(turns);
+        if (pos != nullptr) x.positions_stride = positions_stride(*pos, q.size(0), q.size(2));
+        x.interleaved = flag_arg(a[4]);
+        x.inverse = flag_arg(a[5]);
+        x.factor = float_arg(a[6]);
+        const int dev = cuda_device("fa_rope", q, {k, &turns, pos, qo_arg, ko_arg});
+        const Place place(a[9], dev, {&q, k, &turns, pos, qo_arg, ko_arg});
+        const at::Tensor qo = qo_arg != nullptr ? *qo_arg : out_like(q);
+        at::Tensor ko;
+        if (k != nullptr) ko = ko_arg != nullptr ? *ko_arg : out_like(*k);
+        x.q = q.data_ptr();
+        x.q_out = qo.data_ptr();
+        x.sq = strides4(q);
+        x.sq_out = strides4(qo);
+        if (k != nullptr) {
+            x.k = k->data_ptr();
+            x.k_out = ko.data_ptr();
+            x.sk = strides4(*k);
+            x.sk_out = strides4(ko);
+            x.Hk = to_int(k->size(1), "the heads");
+        }
+        x.positions = ints(pos);
+        x.turns = static_cast<const int64_t*>(turns.data_ptr());
+        x.Z = to_int(q.size(0), "the batch");
+        x.Hq = to_int(q.size(1), "the heads");
+        x.N = to_int(q.size(2), "the rows");
+        x.D = to_int(q.size(3), "the head dim");
+        check(unlocked([&] { return lib.rope(&x, place.stream()); }), "fa_rope");
+        PyObject* result = PyTuple_New(2);
+        if (result == nullptr) throw python_error();
+        PyTuple_SET_ITEM(result, 0, THPVariable_Wrap(qo));
+        if (ko.defined()) PyTuple_SET_ITEM(result, 1, THPVariable_Wrap(ko));
+        else PyTuple_SET_ITEM(result, 1, (Py_INCREF(Py_None), Py_None));
+        return result;
+    });
+}
+
+// (q, k, v, k_cache, v_cache, block_table, seq_lens, turns, positions, new_lens, interleaved, factor, q_out, stream)
+PyObject* cache_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 14)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+        const at::Tensor &kc = tensor(a[3], "k_cache"), &vc = tensor(a[4], "v_cache");
+        const at::Tensor &table = tensor(a[5], "block_table"), &lens = tensor(a[6], "seq_lens"), &turns = tensor(a[7], "turns");
+        const at::Tensor *pos = maybe_tensor(a[8], "positions"), *news = maybe_tensor(a[9], "new_lens");
+        const at::Tensor* qo_arg = maybe_tensor(a[12], "q_out");
+        if (q.dim() != 4) value_error("q must be 4-D (Z, Hq, T, D)");
+        if (k.dim() != 4 || k.sizes() != v.sizes())
+            value_error("k and v must both be (Z, Hkv, T, D), got " + shape_of(k.sizes()) + ", " + shape_of(v.sizes()));
+        const int64_t Z = k.size(0), T = k.size(2);
+        fa_cache_append_rope_args x{};
+        x.cache = cache_of(kc, vc, table, lens, Z, false);
+        if (x.cache.Hkv != k.size(1) || x.cache.D != k.size(3))
+            value_error("k and v must both be (Z, " + std::to_string(x.cache.Hkv) + ", T, " + std::to_string(x.cache.D) +
+                        "), got " + shape_of(k.sizes()));
+        if (q.size(0) != Z || q.size(2) != T || q.size(3) != k.size(3))
+            value_error("q must be (Z, Hq, T, D) of k's tokens, got " + shape_of(q.sizes()) + " for " + shape_of(k.sizes()));
+        x.dtype = dtype_of(q, "fa_cache_append_rope");
+        if (k.scalar_type() != kc.scalar_type() || v.scalar_type() != kc.scalar_type() || q.scalar_type() != kc.scalar_type())
+            type_error("q, k and v must have the cache's dtype");
+        if (news != nullptr) check_ints(*news, "new_lens", {Z});
+        check_out(qo_arg, q, "q_out");
+        x.rotary_dim = pairs_of(turns);
+        if (pos != nullptr) x.positions_stride = positions_stride(*pos, Z, T);
+        x.interleaved = flag_arg(a[10]);
+        x.factor = float_arg(a[11]);
+        const int dev = cuda_device("fa_cache_append_rope", q, {&k, &v, &kc, &vc, &table, &lens, &turns, pos, news, qo_arg});
+        const Place place(a[13], dev, {&q, &k, &v, &kc, &vc, &table, &lens, &turns, pos, news, qo_arg});
+        const at::Tensor qo = qo_arg != nullptr ? *qo_arg : out_like(q);
+        x.q = q.data_ptr();
+        x.q_out = qo.data_ptr();
+        x.k = k.data_ptr();
+        x.v = v.data_ptr();
+        x.sq = strides4(q);
+        x.sq_out = strides4(qo);
+        x.sk = strides4(k);
+        x.sv = strides4(v);
+        x.new_lens = ints(news);
+        x.positions = ints(pos);
+        x.turns = static_cast<const int64_t*>(turns.data_ptr());
+        x.Hq = to_int(q.size(1), "the heads");
+        x.T = to_int(T, "T");
+        check(unlocked([&] { return lib.append_rope(&x, place.stream()); }), "fa_cache_append_rope");
+        return THPVariable_Wrap(qo);
+    });
+}
+
+// Scores: (..., positions) float32, the positions contiguous and at least the table's.
+void check_scores(const at::Tensor& t, std::initializer_list<int64_t> shape, const fa_paged_cache& c) {
+    const at::IntArrayRef want(shape);
+    if (t.scalar_type() != at::kFloat) type_error("scores must be float32");
+    if (t.dim() != (int64_t)want.size() + 1 || t.sizes().slice(0, want.size()) != want)
+        value_error("scores must be " + shape_of(want) + " and the positions, got " + shape_of(t.sizes()));
+    const int64_t cap = (int64_t)c.max_pages * c.page_size;
+    if (t.size(-1) < cap) value_error("scores must have a place for each of " + std::to_string(cap) + " positions");
+    if (t.size(-1) > 1 && t.stride(-1) != 1) value_error("scores' last dimension must be contiguous");
+}
+
+// (q, lse, k_cache, block_table, seq_lens, scores, new_lens, scale, decay, workspace, stream)
+PyObject* cache_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 11)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &lse = tensor(a[1], "lse"), &kc = tensor(a[2], "k_cache");
+        const at::Tensor &table = tensor(a[3], "block_table"), &lens = tensor(a[4], "seq_lens"), &scores = tensor(a[5], "scores");
+        const at::Tensor *news = maybe_tensor(a[6], "new_lens"), *ws_arg = maybe_tensor(a[9], "workspace");
+        if (q.dim() != 4) value_error("q must be 4-D (Z, Hq, T, D)");
+        const int64_t Z = q.size(0), D = q.size(3);
+        fa_cache_score_args x{};
+        x.cache = cache_of(kc, kc, table, lens, Z, false);
+        if (x.cache.D != D)
+            value_error("head dims differ: q has " + std::to_string(D) + ", the cache " + std::to_string(x.cache.D));
+        x.dtype = dtype_of(q, "fa_cache_score");
+        if (kc.scalar_type() != q.scalar_type()) type_error("q and the cache must share one dtype");
+        if (lse.scalar_type() != at::kFloat || lse.dim() != 3 || lse.sizes() != q.sizes().slice(0, 3) || !lse.is_contiguous())
+            value_error("lse must be a contiguous float32 (Z, Hq, T) tensor");
+        if (news != nullptr) check_ints(*news, "new_lens", {Z});
+        check_scores(scores, {Z, (int64_t)x.cache.Hkv}, x.cache);
+        x.scale = a[7] == Py_None ? (float)(1.0 / std::sqrt((double)D)) : float_arg(a[7]);
+        x.decay = float_arg(a[8]);
+        check_workspace(ws_arg);
+        const int dev = cuda_device("fa_cache_score", q, {&lse, &kc, &table, &lens, &scores, news, ws_arg});
+        const Place place(a[10], dev, {&q, &lse, &kc, &table, &lens, &scores, news, ws_arg});
+        at::Tensor ws;
+        if (ws_arg != nullptr) {
+            ws = *ws_arg;
+        } else {
+            size_t bytes = 0;
+            check(lib.score_size(&bytes), "fa_cache_score");
+            ws = scratch(bytes, q);
+        }
+        x.q = q.data_ptr();
+        x.lse = static_cast<const float*>(lse.data_ptr());
+        x.scores = static_cast<float*>(scores.data_ptr());
+        x.score_seq = scores.stride(0);
+        x.score_head = scores.stride(1);
+        x.sq = strides4(q);
+        x.new_lens = ints(news);
+        x.workspace = ws.data_ptr();
+        x.workspace_bytes = ws.nbytes();
+        x.Hq = to_int(q.size(1), "the heads");
+        x.T = to_int(q.size(2), "T");
+        check(unlocked([&] { return lib.score(&x, place.stream()); }), "fa_cache_score");
+        Py_RETURN_NONE;
+    });
+}
+
+// (k_cache, v_cache, block_table, seq_lens, ref_counts, scores, budget, missing, keep, first, recent, workspace, stream)
+PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 13)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache");
+        const at::Tensor &table = tensor(a[2], "block_table"), &lens = tensor(a[3], "seq_lens");
+        const at::Tensor &refs = tensor(a[4], "ref_counts"), &scores = tensor(a[5], "scores"), &missing = tensor(a[7], "missing");
+        const at::Tensor *keep = maybe_tensor(a[8], "keep"), *ws_arg = maybe_tensor(a[11], "workspace");
+        if (lens.dim() != 1) value_error("seq_lens must be (Z)");
+        const int64_t Z = lens.size(0);
+        fa_cache_evict_args x{};
+        x.cache = cache_of(kc, vc, table, lens, Z, true);
+        check_ints(refs, "ref_counts", {x.cache.P});
+        check_ints(missing, "missing", {1});
+        if (keep != nullptr) check_ints(*keep, "keep", {Z});
+        const bool layers = kc.dim() == 5;
+        if (layers) check_scores(scores, {(int64_t)x.cache.L, Z, (int64_t)x.cache.Hkv}, x.cache);
+        else check_scores(scores, {Z, (int64_t)x.cache.Hkv}, x.cache);
+        x.budget = int_arg(a[6], "budget");
+        x.first = int_arg(a[9], "first");
+        x.recent = int_arg(a[10], "recent");
+        check_workspace(ws_arg);
+        const int dev = cuda_device("fa_cache_evict", kc, {&vc, &table, &lens, &refs, &scores, &missing, keep, ws_arg});
+        const Place place(a[12], dev, {&kc, &vc, &table, &lens, &refs, &scores, &missing, keep, ws_arg});
+        at::Tensor ws;
+        if (ws_arg != nullptr) {
+            ws = *ws_arg;
+        } else {
+            size_t bytes = 0;
+            const int64_t cap = (int64_t)x.cache.max_pages * x.cache.page_size;
+            const int budget = x.budget < cap ? x.budget : (int)cap;
+            check(lib.evict_size(x.cache.L, x.cache.Z, x.cache.Hkv, x.cache.max_pages, budget, &bytes), "fa_cache_evict");
+            ws = scratch(bytes, kc);
+        }
+        x.ref_counts = ints(&refs);
+        x.scores = static_cast<float*>(scores.data_ptr());
+        x.score_layer = layers ? scores.stride(0) : 0;
+        x.score_seq = scores.stride(layers ? 1 : 0);
+        x.score_head = scores.stride(layers ? 2 : 1);
+        x.keep = ints(keep);
+        x.missing = ints(&missing);
+        x.workspace = ws.data_ptr();
+        x.workspace_bytes = ws.nbytes();
+        check(unlocked([&] { return lib.evict(&x, place.stream()); }), "fa_cache_evict");
+        Py_RETURN_NONE;
+    });
+}
+
+// (FaError, the addresses of the entry points)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (!expect(n, 7)) return nullptr;
-    void* p[6];
-    for (int i = 0; i < 6; ++i) {
+    constexpr int COUNT = 12;
+    if (!expect(n, COUNT + 1)) return nullptr;
+    void* p[COUNT];
+    for (int i = 0; i < COUNT; ++i) {
         p[i] = PyLong_AsVoidPtr(a[1 + i]);
         if (p[i] == nullptr) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
@@ -397,6 +658,12 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     lib.commit = reinterpret_cast<decltype(lib.commit)>(p[3]);
     lib.fork = reinterpret_cast<decltype(lib.fork)>(p[4]);
     lib.fork_size = reinterpret_cast<decltype(lib.fork_size)>(p[5]);
+    lib.rope = reinterpret_cast<decltype(lib.rope)>(p[6]);
+    lib.append_rope = reinterpret_cast<decltype(lib.append_rope)>(p[7]);
+    lib.score = reinterpret_cast<decltype(lib.score)>(p[8]);
+    lib.score_size = reinterpret_cast<decltype(lib.score_size)>(p[9]);
+    lib.evict = reinterpret_cast<decltype(lib.evict)>(p[10]);
+    lib.evict_size = reinterpret_cast<decltype(lib.evict_size)>(p[11]);
     Py_RETURN_NONE;
 }
 
@@ -406,6 +673,10 @@ PyMethodDef methods[] = {
     {"cache_append", reinterpret_cast<PyCFunction>(cache_append), METH_FASTCALL, nullptr},
     {"cache_commit", reinterpret_cast<PyCFunction>(cache_commit), METH_FASTCALL, nullptr},
     {"cache_fork", reinterpret_cast<PyCFunction>(cache_fork), METH_FASTCALL, nullptr},
+    {"rope", reinterpret_cast<PyCFunction>(rope), METH_FASTCALL, nullptr},
+    {"cache_append_rope", reinterpret_cast<PyCFunction>(cache_append_rope), METH_FASTCALL, nullptr},
+    {"cache_score", reinterpret_cast<PyCFunction>(cache_score), METH_FASTCALL, nullptr},
+    {"cache_evict", reinterpret_cast<PyCFunction>(cache_evict), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged_ext", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

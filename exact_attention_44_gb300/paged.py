@@ -53,7 +53,8 @@ def _calls():
             spec.loader.exec_module(ext)
             _ext = ext
         names = ("fa_fwd_paged", "fa_fwd_paged_workspace_size", "fa_cache_append", "fa_cache_commit", "fa_cache_fork",
-                 "fa_cache_fork_workspace_size")
+                 "fa_cache_fork_workspace_size", "fa_rope", "fa_cache_append_rope", "fa_cache_score",
+                 "fa_cache_score_workspace_size", "fa_cache_evict", "fa_cache_evict_workspace_size")
         _ext.bind(FaError, *[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names])
         _bound = lib
     return _ext

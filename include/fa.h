@@ -588,6 +588,154 @@ typedef struct {
 fa_status fa_cache_fork(const fa_cache_fork_args* args, cudaStream_t stream);
 fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes);
 
+/* ------------------------------------------------------------ rotary positions ---
+ * The first rotary_dim elements of a row are rotary_dim / 2 pairs: (i, i + rotary_dim /
+ * 2), or (2 i, 2 i + 1) if interleaved.  Pair i of a row at position p turns by p
+ * inv_freq[i] radians,
+ *     (a, b) -> factor (a cos - b sin, a sin + b cos),
+ * in fp32, rounded once; the rest of the row stays as it is.
+ *
+ * The angles are exact at any position: frequencies are given as turns a position in
+ * units of 2^-64 (an integer that wraps after a whole turn), which fa_rope_turns makes of
+ * radians a position; the angle of position p is then off by at most p inv_freq 2^-52
+ * radians.
+ *
+ * fa_rope_frequencies -- the usual frequencies, base^(-2 i / rotary_dim), host only, for
+ * a context that is `stretch` times as long as the one they were made for:
+ *   FA_ROPE_PLAIN   as they are (stretch is not used)
+ *   FA_ROPE_LINEAR  all divided by stretch
+ *   FA_ROPE_BASE    base times stretch^(rotary_dim / (rotary_dim - 2)): the slowest pair
+ *                   is stretched, the fastest stays
+ *   FA_ROPE_RAMP    pairs that turn at most `slow` times over `context` positions divided
+ *                   by stretch, those that turn at least `fast` times as they are, linear
+ *                   in the number of turns between (factor may then be above 1)
+ * scaling NULL is {FA_ROPE_PLAIN, 10000}.
+ */
+#define FA_ROPE_PLAIN 0
+#define FA_ROPE_LINEAR 1
+#define FA_ROPE_BASE 2
+#define FA_ROPE_RAMP 3
+typedef struct {
+    int kind;
+    double base, stretch, context, slow, fast;
+} fa_rope_scaling;
+fa_status fa_rope_frequencies(int rotary_dim, const fa_rope_scaling* scaling, double* inv_freq);
+/* Host only: turns a position in units of 2^-64 of `pairs` finite frequencies. */
+fa_status fa_rope_turns(int pairs, const double* inv_freq, int64_t* turns);
+
+/*
+ * fa_rope -- turn the rows of q and k (either may have no heads).  inverse 1 turns back
+ * (still times factor): the gradient of the same call.  Outputs may be the inputs (same
+ * pointer and strides); they must not overlap them, or each other, otherwise.  Any even
+ * rotary_dim up to D; D in {16, 32, 64, 128, 256}; fp16 / bf16; strides as for fa_fwd,
+ * inputs of stride 0 included.  Z and Hq + Hk <= 65535, N <= 2^30.
+ */
+typedef struct {
+    const void* q;                /* (Z, Hq, N, D) */
+    const void* k;                /* (Z, Hk, N, D) */
+    void* q_out;                  /* written */
+    void* k_out;
+    fa_strides sq, sk, sq_out, sk_out;
+    const int32_t* positions;     /* (Z, N), rows positions_stride apart (0: one for all); NULL: 0 .. N - 1 */
+    int64_t positions_stride;
+    const int64_t* turns;         /* (rotary_dim / 2) on the device */
+    int Z, Hq, Hk, N, D, rotary_dim;
+    int interleaved, inverse;
+    float factor;                 /* finite */
+    int dtype;                    /* fa_dtype */
+} fa_rope_args;
+fa_status fa_rope(const fa_rope_args* args, cudaStream_t stream);
+
+/*
+ * fa_cache_append_rope -- fa_cache_append with rotary positions: k rows are turned on
+ * their way into the cache, v rows moved unchanged, and the q rows of the same tokens
+ * turned to q_out (which may be q).  Token t of sequence z, t < new_lens[z], goes to slot
+ * position seq_lens[z] + t; the position that it turns by is positions[z][t], or NULL:
+ * that slot position (a cache from which positions were evicted needs its own).  Rows of
+ * q_out of tokens t >= new_lens[z] are left as they were.  q is turned even where a
+ * token's page is missing.  Results are those of fa_rope and fa_cache_append, bit by bit.
+ */
+typedef struct {
+    fa_paged_cache cache;         /* one layer, L = 1 */
+    const void* q;                /* (Z, Hq, T, D) */
+    void* q_out;
+    const void* k;                /* (Z, Hkv, T, D) */
+    const void* v;
+    fa_strides sq, sq_out, sk, sv;
+    const int32_t* new_lens;      /* NULL: T each */
+    const int32_t* positions;     /* (Z, T), rows positions_stride apart; or NULL */
+    int64_t positions_stride;
+    const int64_t* turns;
+    int Hq, T, rotary_dim, interleaved;
+    float factor;
+    int dtype;
+} fa_cache_append_rope_args;
+fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream_t stream);
+
+/*
+ * fa_cache_score -- the attention weight that the positions of a cache (one layer) have
+ * received, after fa_fwd_paged with the same seq_lens, new_lens, q and scale (chain rule:
+ * new token t sees positions up to seq_lens[z] + t) has left its lse:
+ *     scores[z][hk][j] = decay scores[z][hk][j]
+ *                        + sum over tokens t and heads h of the group that see j of
+ *                          exp(q k_j scale - lse[z][h][t]),
+ * where positions j >= seq_lens[z] had no score yet (0), and with decay 0 none had,
+ * whatever is there.  Scores of positions behind the new tokens are left as they were.  A
+ * token that is drafted but not kept should not count: call it after fa_cache_commit with
+ * the rows of the accepted tokens.  To let only the last W tokens of a prompt speak, pass
+ * their q and lse and seq_lens less W.  Only the cache's k is read (v may be NULL).  A
+ * row whose lse is -inf adds nothing; what q, lse and a page hold behind the last token
+ * has no effect.  Sums are fp32, in an order that depends on the sizes only (bitwise
+ * reproducible).
+ */
+typedef struct {
+    fa_paged_cache cache;
+    const void* q;                /* (Z, Hq, T, D) */
+    const float* lse;             /* (Z, Hq, T) contiguous */
+    float* scores;                /* (Z, Hkv, >= max_pages * page_size), positions contiguous */
+    int64_t score_seq, score_head; /* elements from a sequence, a head to the next */
+    fa_strides sq;
+    const int32_t* new_lens;      /* NULL: T each */
+    void* workspace;              /* fa_cache_score_workspace_size() bytes, 256-byte aligned */
+    size_t workspace_bytes;
+    int Hq, T;
+    float scale, decay;           /* finite */
+    int dtype;
+} fa_cache_score_args;
+fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream);
+fa_status fa_cache_score_workspace_size(size_t* bytes);
+
+/*
+ * fa_cache_evict -- cut sequences back: sequence z, if it has more than n = min(budget,
+ * keep[z]) positions (keep NULL: budget; a negative keep[z]: it stays as it is), keeps n.
+ * Of each layer and kv head these are the first `first`, the last `recent` (as far as n
+ * goes, `first` first) and of the others those with the highest scores (ties: the lowest
+ * position; a NaN is above everything).  They keep their order and become positions 0 ..
+ * n - 1, their scores with them; seq_lens[z] becomes n, and the pages behind are released,
+ * room included.  All layers lie in one call, since they share the block table.
+ *
+ * A page that would be written but that other sequences hold too (ref_counts above 1) is
+ * replaced by a free one, lowest first in the order of sequences and columns, from those
+ * that were free before the call; a shared page in front of the first row that moves, in
+ * any layer or head, stays shared.  *missing is the number of pages that lacked; if it is
+ * not 0 nothing else is changed.  Rows whose page is not in the cache are recorded as
+ * FA_ERR_PAGE and skipped.  Valid state before is valid state after (see fa_cache_fork).
+ * L <= 65535, P <= 2^30, Z * max_pages < 2^31, L * Z * Hkv < 2^29.
+ */
+typedef struct {
+    fa_paged_cache cache;
+    int32_t* ref_counts;          /* (P) */
+    float* scores;                /* (L, Z, Hkv, >= max_pages * page_size), positions contiguous */
+    int64_t score_layer, score_seq, score_head;
+    const int32_t* keep;          /* (Z), or NULL */
+    int32_t* missing;             /* one int32 */
+    void* workspace;              /* fa_cache_evict_workspace_size(...) bytes, 256-byte aligned */
+    size_t workspace_bytes;
+    int budget, first, recent;
+} fa_cache_evict_args;
+fa_status fa_cache_evict(const fa_cache_evict_args* args, cudaStream_t stream);
+fa_status fa_cache_evict_workspace_size(int L, int Z, int Hkv, int max_pages, int budget, size_t* bytes);
+
 /*
  * Test hooks for the failure-detection path; not for production use.
  *
