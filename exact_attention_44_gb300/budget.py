@@ -1,7 +1,7 @@
 """Rotary positions, and a paged cache that is held to a budget (libfa's fa_rope,
 fa_cache_append_rope, fa_cache_score and fa_cache_evict).
 
-A model keeps the frequencies of its rotary positions as turns on the device:
+A model keeps the frequencies of its rotary positions as turns, on the host:
 
     turns = fa_rope_turns(fa_rope_frequencies(rotary_dim))
     q, k = fa_rope(q, k, turns)                       # or rotary(...), with autograd
@@ -63,11 +63,11 @@ def fa_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str 
     return out
 
 
-def fa_rope_turns(inv_freq, device="cuda"):
-    """The frequencies (radians a position, a 1-D tensor) as fa_rope takes them: an int64 tensor on `device`.
+def fa_rope_turns(inv_freq):
+    """The frequencies (radians a position, a 1-D tensor) as fa_rope takes them: an int64 tensor on the host.
 
     Turns a position in units of 2^-64, which wrap after a whole turn, so that angles are
-    exact at any position.  Made once for a model, on the host.
+    exact at any position.  Made once for a model; calls pass them on as launch arguments.
     """
     import torch
 
@@ -78,7 +78,7 @@ def fa_rope_turns(inv_freq, device="cuda"):
     rc = _binding.load().fa_rope_turns(f.numel(), f.data_ptr(), out.data_ptr())
     if rc != FA_OK:
         raise FaError(rc, "fa_rope_turns")
-    return out.to(device)
+    return out
 
 
 def fa_rope(q, k, turns, positions=None, *, interleaved: bool = False, inverse: bool = False, factor: float = 1.0,

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "fa.h"
 #include "fa_checks.h"
@@ -28,7 +29,6 @@ fa_status check_rope(int D, int rotary_dim, int interleaved, float factor, int d
 }
 fa_status check_turns(const void* turns, const void* positions, int64_t positions_stride) {
     if (turns == nullptr || positions_stride < 0) return FA_ERR_INVALID_ARG;
-    if (misaligned(turns, 8)) return FA_ERR_ALIGNMENT;
     return check_ints(positions, false);
 }
 bool same_place(const void* a, const fa_strides& sa, const void* b, const fa_strides& sb) {
@@ -117,7 +117,7 @@ fa_status fa_rope(const fa_rope_args* args, cudaStream_t stream) {
     p.k_in_place = same_place(x.k, x.sk, x.k_out, x.sk_out);
     p.positions = x.positions;
     p.pos_z = x.positions_stride;
-    p.turns = x.turns;
+    std::memcpy(p.turns, x.turns, (size_t)x.rotary_dim / 2 * sizeof(int64_t));  // (at most 128: D is 256 at most)
     p.Z = x.Z, p.Hq = x.Hq, p.Hk = x.Hk, p.N = x.N, p.D = x.D, p.R = x.rotary_dim;
     p.cos_factor = x.factor;
     p.sin_factor = x.inverse ? -x.factor : x.factor;
@@ -158,7 +158,7 @@ fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream
     p.q_in_place = same_place(x.q, x.sq, x.q_out, x.sq_out);
     p.positions = x.positions;
     p.pos_z = x.positions_stride;
-    p.turns = x.turns;
+    std::memcpy(p.turns, x.turns, (size_t)x.rotary_dim / 2 * sizeof(int64_t));  // (at most 128: D is 256 at most)
     p.Z = c.Z, p.Hq = x.Hq, p.Hk = c.Hkv, p.N = x.T, p.D = c.D, p.R = x.rotary_dim;
     p.cos_factor = p.sin_factor = x.factor;
     p.kc = view(c.k, c.sk, 0);

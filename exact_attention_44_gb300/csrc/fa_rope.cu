@@ -13,7 +13,10 @@
 //
 // What bounds it is reading and writing each row once.  A thread takes 8 pairs (two
 // 16-byte pieces) of a token through some of its heads, so that a sine and cosine serve
-// several heads, with the loads of four heads in flight.
+// several heads; the loads go out before the sines are worked out.  671 MB (32 + 8 heads of
+// D = 128, 32768 tokens): 98 us, 6.8 TB/s, a plain copy's rate.  The turns come with the
+// launch's arguments: read from one place in global memory by every warp, through L2,
+// they took 367 us (one L2 slice serves them all).  One token: 1.9 us.
 #include "fa_rope.h"
 
 #include <cuda_bf16.h>
@@ -106,14 +109,17 @@ __device__ __forceinline__ void turn(Pairs<V>& x, const float (&c)[V], const flo
     }
 }
 
-template <bool BF16, bool INTER, int V, bool CACHE>
-__global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const RopeParams p) {
+// U: heads whose loads a thread has in flight
+template <bool BF16, bool INTER, int V, bool CACHE, int U>
+__global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const __grid_constant__ RopeParams p) {
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    const int pieces = p.D / (2 * V), turning = p.R / (2 * V);  // pieces: a power of two
-    const int z = blockIdx.z, piece = threadIdx.x & (pieces - 1);
-    const int n = (int)(((int64_t)blockIdx.x * ROPE_THREADS + threadIdx.x) / pieces);
-    if (n >= p.N) return;
+    // pieces of a row: a power of two
+    const int shift = 31 - __clz(p.D / (2 * V)), turning = p.R / (2 * V);
+    const int piece = threadIdx.x & ((1 << shift) - 1), token = threadIdx.x >> shift;
+    const int z = blockIdx.z * ((ROPE_THREADS >> shift) >> p.token_shift) + (token >> p.token_shift);
+    const int n = (int)(blockIdx.x << p.token_shift) + (token & ((1 << p.token_shift) - 1));
+    if (n >= p.N || z >= p.Z) return;
     int64_t slot = 0;
     int page = -1;
     uint32_t position = (uint32_t)n;
@@ -132,27 +138,17 @@ __global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const RopeParams 
     int64_t at = position;
     if (p.positions != nullptr) at = ldi(p.positions + z * p.pos_z + n);
     const bool turns = piece < turning;
-    float c[V], s[V];
-    if (turns) {
+    uint64_t f[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const uint64_t f = (uint64_t)__ldcg(reinterpret_cast<const long long*>(p.turns + piece * V + i));
-            // the fraction of a turn, then in half turns for sincospi
-            const int32_t frac = (int32_t)(uint32_t)((f * (uint64_t)at) >> 32);
-            sincospif((float)frac * 0x1p-31f, &s[i], &c[i]);
-            c[i] *= p.cos_factor;
-            s[i] *= p.sin_factor;
-        }
-    }
+    for (int i = 0; i < V; ++i) f[i] = (uint64_t)p.turns[turns ? piece * V + i : 0];
     // where a piece starts, and its second half
     const int first = INTER || !turns ? piece * 2 * V : piece * V;
     const int apart = INTER || !turns ? V : p.R / 2;
     const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, p.Hq + p.Hk + (CACHE ? p.Hk : 0));
-    constexpr int U = 4;
-    for (int h = h0; h < h1; h += U) {
-        Pairs<V> x[U];
-        uint16_t* to[U];
-        bool rope[U];
+    Pairs<V> x[U];
+    uint16_t* to[U];
+    bool rope[U];
+    auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = h + u;
@@ -176,16 +172,27 @@ __global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const RopeParams 
                 if (page >= 0) to[u] = p.vc.base + page * p.vc.p + (i - p.Hq - p.Hk) * p.vc.h + slot * p.vc.n;
                 rope[u] = false;
             }
-            if (to[u] != nullptr) {
-                x[u] = load_pairs<V>(from + first, apart);
-                to[u] += first;
-            }
+            x[u] = load_pairs<V>(from + first, apart);
         }
+    };
+    load(h0);
+    // the angles while the first rows are on their way
+    float c[V], s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        // the fraction of a turn, in half turns for sincospi
+        const int32_t frac = (int32_t)(uint32_t)((f[i] * (uint64_t)at) >> 32);
+        sincospif((float)frac * 0x1p-31f, &s[i], &c[i]);
+        c[i] *= p.cos_factor;
+        s[i] *= p.sin_factor;
+    }
+    for (int h = h0; h < h1; h += U) {
+        if (h > h0) load(h);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (to[u] != nullptr) {
                 if (rope[u]) turn<BF16, INTER, V>(x[u], c, s);
-                store_pairs<V>(to[u], apart, x[u]);
+                store_pairs<V>(to[u] + first, apart, x[u]);
             }
     }
 }
@@ -193,14 +200,27 @@ __global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const RopeParams 
 template <bool BF16, bool INTER, int V>
 cudaError_t launch_v(RopeParams p, bool cache, int sms, cudaStream_t stream) {
     const int heads = p.Hq + p.Hk * (cache ? 2 : 1);
-    const int64_t threads = (int64_t)p.N * (p.D / (2 * V));
-    const int64_t blocks = (threads + ROPE_THREADS - 1) / ROPE_THREADS;
-    // few tokens: fewer heads a thread, so that there are threads for every SM
-    p.heads = 4;
-    while (p.heads > 1 && blocks * p.Z * ((heads + p.heads - 1) / p.heads) < sms) p.heads /= 2;
-    const dim3 grid((unsigned)blocks, (unsigned)((heads + p.heads - 1) / p.heads), (unsigned)p.Z);
-    return cache ? launch_dependent(fa_rope_kernel<BF16, INTER, V, true>, grid, ROPE_THREADS, 0, stream, p)
-                 : launch_dependent(fa_rope_kernel<BF16, INTER, V, false>, grid, ROPE_THREADS, 0, stream, p);
+    const int tokens = ROPE_THREADS / (p.D / (2 * V));  // of a CTA: of several sequences if they have few
+    p.token_shift = 0;
+    while ((1 << p.token_shift) < tokens && (1 << p.token_shift) < p.N) ++p.token_shift;
+    const int64_t x = ((int64_t)p.N + (1 << p.token_shift) - 1) >> p.token_shift;
+    const int64_t zs = tokens >> p.token_shift, z = (p.Z + zs - 1) / zs;
+    auto blocks = [&](int n) { return x * z * ((heads + n - 1) / n); };
+    auto launch = [&](auto with_cache, auto without, int n) {
+        p.heads = n;
+        const dim3 grid((unsigned)x, (unsigned)((heads + n - 1) / n), (unsigned)z);
+        return launch_dependent(cache ? with_cache : without, grid, ROPE_THREADS, 0, stream, p);
+    };
+    // Eight heads a thread, all in flight, where that leaves 16 CTAs an SM (98 against 108
+    // us for 40 heads x 32768 tokens of D = 128, 40 against 47 for the cache's 48 x 10055),
+    // else four (13.3 / 10.6 us for 32 x 4096), and with few tokens fewer, so that there
+    // are CTAs for every SM.
+    if constexpr (V == 8)
+        if (blocks(8) >= 16 * (int64_t)sms)
+            return launch(fa_rope_kernel<BF16, INTER, V, true, 8>, fa_rope_kernel<BF16, INTER, V, false, 8>, 8);
+    int n = 4;
+    while (n > 1 && blocks(n) < sms) n /= 2;
+    return launch(fa_rope_kernel<BF16, INTER, V, true, 4>, fa_rope_kernel<BF16, INTER, V, false, 4>, n);
 }
 template <bool BF16, bool INTER>
 cudaError_t launch_layout(const RopeParams& p, bool cache, int sms, cudaStream_t stream) {

@@ -18,9 +18,10 @@ struct RopeParams {
     bool q_in_place, k_in_place;     // elements that do not turn stay where they are
     const int32_t* positions;        // nullptr: the row's index (a cache: its slot)
     int64_t pos_z;
-    const int64_t* turns;            // (R / 2) turns a position in units of 2^-64
+    int64_t turns[128];              // (R / 2) turns a position in units of 2^-64
     int Z, Hq, Hk, N, D, R;
     int heads;                       // of a thread (set by the launch)
+    int token_shift;                 // log2 of the tokens of a sequence that a CTA takes (set by the launch)
     float cos_factor, sin_factor;    // factor; its sign turns back
     // a cache (fa_cache_append_rope): k and v rows go to their slots
     CacheView kc, vc;

@@ -401,8 +401,8 @@ int flag_arg(PyObject* o) {
 }
 // The frequencies' pairs.
 int pairs_of(const at::Tensor& turns) {
-    if (turns.scalar_type() != at::kLong || turns.dim() != 1 || !turns.is_contiguous())
-        value_error("turns must be a contiguous int64 tensor of rotary_dim / 2 entries (fa_rope_turns)");
+    if (turns.scalar_type() != at::kLong || turns.dim() != 1 || !turns.is_contiguous() || !turns.device().is_cpu())
+        value_error("turns must be a contiguous int64 tensor of rotary_dim / 2 entries on the host (fa_rope_turns)");
     return to_int(2 * turns.size(0), "rotary_dim");
 }
 // (N,) for all sequences or (Z, N); the stride between sequences
@@ -448,8 +448,8 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x.interleaved = flag_arg(a[4]);
         x.inverse = flag_arg(a[5]);
         x.factor = float_arg(a[6]);
-        const int dev = cuda_device("fa_rope", q, {k, &turns, pos, qo_arg, ko_arg});
-        const Place place(a[9], dev, {&q, k, &turns, pos, qo_arg, ko_arg});
+        const int dev = cuda_device("fa_rope", q, {k, pos, qo_arg, ko_arg});
+        const Place place(a[9], dev, {&q, k, pos, qo_arg, ko_arg});
         const at::Tensor qo = qo_arg != nullptr ? *qo_arg : out_like(q);
         at::Tensor ko;
         if (k != nullptr) ko = ko_arg != nullptr ? *ko_arg : out_like(*k);
@@ -509,8 +509,8 @@ PyObject* cache_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (pos != nullptr) x.positions_stride = positions_stride(*pos, Z, T);
         x.interleaved = flag_arg(a[10]);
         x.factor = float_arg(a[11]);
-        const int dev = cuda_device("fa_cache_append_rope", q, {&k, &v, &kc, &vc, &table, &lens, &turns, pos, news, qo_arg});
-        const Place place(a[13], dev, {&q, &k, &v, &kc, &vc, &table, &lens, &turns, pos, news, qo_arg});
+        const int dev = cuda_device("fa_cache_append_rope", q, {&k, &v, &kc, &vc, &table, &lens, pos, news, qo_arg});
+        const Place place(a[13], dev, {&q, &k, &v, &kc, &vc, &table, &lens, pos, news, qo_arg});
         const at::Tensor qo = qo_arg != nullptr ? *qo_arg : out_like(q);
         x.q = q.data_ptr();
         x.q_out = qo.data_ptr();

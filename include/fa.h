@@ -597,7 +597,9 @@ fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes);
  *
  * The angles are exact at any position: frequencies are given as turns a position in
  * units of 2^-64 (an integer that wraps after a whole turn), which fa_rope_turns makes of
- * radians a position; the angle of position p is then off by at most p inv_freq 2^-52
+ * radians a position.  They travel with the launch as its arguments, from a host array
+ * that need not outlive the call (a captured graph keeps those that it was captured
+ * with).  The angle of position p is then off by at most p inv_freq 2^-52
  * radians.
  *
  * fa_rope_frequencies -- the usual frequencies, base^(-2 i / rotary_dim), host only, for
@@ -638,7 +640,7 @@ typedef struct {
     fa_strides sq, sk, sq_out, sk_out;
     const int32_t* positions;     /* (Z, N), rows positions_stride apart (0: one for all); NULL: 0 .. N - 1 */
     int64_t positions_stride;
-    const int64_t* turns;         /* (rotary_dim / 2) on the device */
+    const int64_t* turns;         /* (rotary_dim / 2) on the HOST, read during the call */
     int Z, Hq, Hk, N, D, rotary_dim;
     int interleaved, inverse;
     float factor;                 /* finite */
@@ -665,7 +667,7 @@ typedef struct {
     const int32_t* new_lens;      /* NULL: T each */
     const int32_t* positions;     /* (Z, T), rows positions_stride apart; or NULL */
     int64_t positions_stride;
-    const int64_t* turns;
+    const int64_t* turns;         /* (rotary_dim / 2) on the HOST, read during the call */
     int Hq, T, rotary_dim, interleaved;
     float factor;
     int dtype;

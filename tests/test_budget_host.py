@@ -38,11 +38,11 @@ def test_frequencies(lib):
 
 def test_turns_are_exact_fractions(lib):
     f = torch.tensor([2 * math.pi / 4, 2 * math.pi, -2 * math.pi / 8, 0.0, 2 * math.pi * 5.5, 1.0, 1e-4], dtype=torch.float64)
-    t = fa.fa_rope_turns(f, "cpu").tolist()
+    t = fa.fa_rope_turns(f).tolist()
     assert t[:4] == [1 << 62, 0, -(1 << 61), 0]
     # 5.5 turns in 53 bits, in radians and then in turns: half a turn but for 5.5 x 2^-52 of one
     assert abs(abs(t[4]) - (1 << 63)) <= 5.5 * 2.0 ** (64 - 52)
-    assert fa.fa_rope_turns(torch.tensor([math.pi], dtype=torch.float64), "cpu").item() == -(1 << 63)  # (half a turn either way)
+    assert fa.fa_rope_turns(torch.tensor([math.pi], dtype=torch.float64)).item() == -(1 << 63)  # (half a turn either way)
     # the product with any position wraps to the same fraction, off by p 2^-65 turns and the frequency's rounding
     from fractions import Fraction
     two_pi = Fraction(6283185307179586476925286766559005768394, 10 ** 39)
@@ -51,7 +51,7 @@ def test_turns_are_exact_fractions(lib):
             got = Fraction((t[i] * p) % (1 << 64), 1 << 64)
             d = (got - Fraction(f[i].item()) * p / two_pi) % 1
             assert min(d, 1 - d) <= abs(p) * (Fraction(1, 2 ** 65) + Fraction(f[i].item()) * Fraction(1, 2 ** 54))
-    assert fa.fa_rope_turns(torch.tensor([0.5]), "cpu").dtype == torch.int64  # float32 frequencies too
+    assert fa.fa_rope_turns(torch.tensor([0.5])).dtype == torch.int64  # float32 frequencies too
 
 
 def test_frequency_refusals(lib):
@@ -136,7 +136,7 @@ I, U, A, W, OK = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_ERR_ALIGNME
     (dict(Z=-1), I), (dict(Hq=-1), I), (dict(N=-1), I), (dict(R=0), I), (dict(R=7), I), (dict(R=66), I), (dict(inter=2), I),
     (dict(inverse=-1), I), (dict(factor=math.nan), I), (dict(factor=math.inf), I), (dict(q=None), I), (dict(ko=None), I),
     (dict(turns=None), I), (dict(ps=-1), I), (dict(so=_st(0, 192, 64)), I), (dict(D=96), U), (dict(dtype=2), U),
-    (dict(Z=65536), U), (dict(Hq=65535), U), (dict(N=(1 << 30) + 1), U), (dict(q=PTR + 8), A), (dict(turns=PTR + 4), A),
+    (dict(Z=65536), U), (dict(Hq=65535), U), (dict(N=(1 << 30) + 1), U), (dict(q=PTR + 8), A), 
     (dict(pos=PTR + 2), A), (dict(so=_st(768, 190, 64)), A), (dict(so=_st(768, 192, 64, 2)), A),
     (dict(Z=0), OK), (dict(N=0), OK), (dict(Hq=0, Hk=0), OK),
 ])
@@ -153,7 +153,7 @@ def test_rope_arguments(lib, kw, code):
     (dict(T=-1), I), (dict(Hq=-1), I), (dict(L=2), I), (dict(R=80), I), (dict(inter=3), I), (dict(factor=-math.inf), I),
     (dict(q=None), I), (dict(v=None), I), (dict(kc=None), I), (dict(turns=None), I), (dict(lens=None), I),
     (dict(sc=_st(0, 1024, 64)), I), (dict(dtype=-1), U), (dict(D=40), U), (dict(page=24), U), (dict(T=(1 << 30) + 1), U),
-    (dict(k=PTR + 2), A), (dict(new=PTR + 1), A), (dict(pos=PTR + 1), A), (dict(turns=PTR + 1), A),
+    (dict(k=PTR + 2), A), (dict(new=PTR + 1), A), (dict(pos=PTR + 1), A),
     (dict(Z=0), OK), (dict(T=0), OK),
 ])
 def test_append_rope_arguments(lib, kw, code):
