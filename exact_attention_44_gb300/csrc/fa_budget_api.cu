@@ -175,7 +175,10 @@ fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream
 
 fa_status fa_cache_score_workspace_size(size_t* bytes) {
     if (bytes == nullptr) return FA_ERR_INVALID_ARG;
-    *bytes = 256;
+    fa::DeviceFacts f;
+    const cudaError_t err = fa::device_facts(&f);
+    if (err != cudaSuccess) return fa::report_cuda("device query", err);
+    *bytes = fa::score_workspace_bytes(f.sms);
     return FA_OK;
 }
 
@@ -186,7 +189,9 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
     if (x.Hq < 0 || c.Hkv < 1 || x.T < 0 || x.Hq % c.Hkv != 0 || c.L != 1 || x.score_seq < 0 || x.score_head < 0)
         return FA_ERR_INVALID_ARG;
     if (x.dtype != FA_DTYPE_F16 && x.dtype != FA_DTYPE_BF16) return FA_ERR_UNSUPPORTED;
-    if (!std::isfinite(x.scale) || !std::isfinite(x.decay)) return FA_ERR_INVALID_ARG;
+    float magnitude = 0.f;
+    int negative = 0;
+    if (!fa::split_scale(x.scale, &magnitude, &negative) || !std::isfinite(x.decay)) return FA_ERR_INVALID_ARG;
     fa_status st = check_cache(c, false);
     if (st != FA_OK) return st;
     const int G = x.Hq / c.Hkv;
@@ -201,12 +206,10 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
     // rows of scores must not fold together
     if ((c.Hkv > 1 && x.score_head < cap) || (c.Z > 1 && x.score_seq < cap)) return FA_ERR_INVALID_ARG;
     if (x.workspace == nullptr || misaligned(x.workspace, 256)) return FA_ERR_WORKSPACE;
-    size_t bytes = 0;
-    if ((st = fa_cache_score_workspace_size(&bytes)) != FA_OK) return st;
-    if (x.workspace_bytes < bytes) return FA_ERR_WORKSPACE;
     fa::DeviceFacts f;
     const cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
+    if (x.workspace_bytes < fa::score_workspace_bytes(f.sms)) return FA_ERR_WORKSPACE;
     fa::ScoreLaunch a{};
     fa::ScoreParams& p = a.params;
     p.q = static_cast<const uint16_t*>(x.q);
@@ -226,9 +229,36 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
     p.by_page = fa::FastDiv(p.page);
     p.scale = x.scale, p.decay = x.decay;
     p.status = f.status;
+    p.wait_limit_ns = f.wait_limit_ns;
+    p.inject_stall = f.inject_stall;
     a.sms = f.sms;
     a.stream = stream;
-    return launch_score(c.D, a, x.dtype == FA_DTYPE_BF16);
+    const bool bf16 = x.dtype == FA_DTYPE_BF16;
+    const fa::ScoreTileFacts tile = fa::score_tile_facts(c.D);
+    // More than 16 rows of a (sequence, kv head) run on the tile kernel, which needs a
+    // whole group in a tile.
+    a.tiles = G <= tile.rows && (int64_t)x.T * G > 16;
+    CUtensorMap mq{}, mk{};
+    if (a.tiles) {
+        while (G << (p.token_shift + 1) <= tile.rows) ++p.token_shift;
+        p.tokens = 1 << p.token_shift;
+        p.tile_rows = p.tokens * G;
+        p.tile_cols = (int)cdiv(p.tile_rows, tile.step) * tile.step;
+        p.box_rows = fa::paged_box_rows(c.page_size, 128);
+        const fa::PagedMapDim dq[3] = {{x.Hq, x.sq.h, G}, {x.T, x.sq.n, p.tokens}, {c.Z, x.sq.b, 1}};
+        const fa::PagedMapDim dk[3] = {{c.page_size, c.sk.n, p.box_rows}, {c.Hkv, c.sk.h, 1}, {c.P, c.sk.b, 1}};
+        if (fa::make_paged_map(&mq, x.q, bf16, c.D, dq) != CUDA_SUCCESS ||
+            fa::make_paged_map(&mk, c.k, bf16, c.D, dk) != CUDA_SUCCESS)
+            return FA_ERR_CUDA;
+        a.tmQ = &mq;
+        a.tmK = &mk;
+        // with one tile a unit there is nothing to cut
+        if (x.T > p.tokens) {
+            p.parts = static_cast<float*>(x.workspace);
+            p.cuts = static_cast<char*>(x.workspace) + fa::score_slot_bytes(f.sms);
+        }
+    }
+    return launch_score(c.D, a, bf16);
 }
 
 fa_status fa_cache_evict_workspace_size(int L, int Z, int Hkv, int max_pages, int budget, size_t* bytes) {

@@ -1,4 +1,4 @@
-// Argument checks that the paged-cache entry points share (host only).
+// Argument checks and tensor maps that the paged-cache entry points share (host only).
 #pragma once
 
 #include <cuda_runtime_api.h>
@@ -8,6 +8,7 @@
 
 #include "fa.h"
 #include "fa_cache.h"
+#include "fa_paged.h"
 
 namespace fa {
 
@@ -71,4 +72,38 @@ inline CacheView view(void* base, const fa_strides& s, int64_t layer) {
 }
 
 }  // namespace checks
+
+// 4-D tensor map with the head dim innermost (dims: D, then `dims` outermost
+// last) and boxes of one swizzle chunk x the given extents.
+struct PagedMapDim {
+    int64_t extent, stride;  // stride in elements
+    int box;
+};
+inline CUresult make_paged_map(CUtensorMap* map, const void* ptr, bool bf16, int D, const PagedMapDim (&dims)[3]) {
+    const int swe = D < 64 ? D : 64;
+    const CUtensorMapSwizzle sw = swe == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+                                  : swe == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                              : CU_TENSOR_MAP_SWIZZLE_32B;
+    cuuint64_t ext[4] = {(cuuint64_t)D, 0, 0, 0}, str[3];
+    cuuint32_t box[4] = {(cuuint32_t)swe, 0, 0, 0}, ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 3; ++i) {
+        ext[i + 1] = (cuuint64_t)dims[i].extent;
+        // a dimension of extent 1 is never stepped along; give it a harmless stride
+        str[i] = dims[i].extent > 1 ? (cuuint64_t)dims[i].stride * 2 : (cuuint64_t)D * 2;
+        box[i + 1] = (cuuint32_t)dims[i].box;
+    }
+    const auto fn = tensor_map_encoder();
+    if (fn == nullptr) return CUDA_ERROR_NOT_SUPPORTED;
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr),
+              ext, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+// Largest box of whole page rows that tiles a block of `bn` positions.
+inline int paged_box_rows(int page, int bn) {
+    int r = 16;
+    while (r < bn && page % (2 * r) == 0) r *= 2;
+    return r;
+}
+
 }  // namespace fa

@@ -41,39 +41,6 @@ size_t paged_slot_bytes(int D, int sms) {
 }
 size_t paged_workspace_bytes(int D, int sms) { return paged_slot_bytes(D, sms) + 48 * kMaxTeams; }
 
-// 4-D tensor map with the head dim innermost (dims: D, then `dims` outermost
-// last) and boxes of one swizzle chunk x the given extents.
-struct MapDim {
-    int64_t extent, stride;  // stride in elements
-    int box;
-};
-CUresult make_paged_map(CUtensorMap* map, const void* ptr, bool bf16, int D, const MapDim (&dims)[3]) {
-    const int swe = D < 64 ? D : 64;
-    const CUtensorMapSwizzle sw = swe == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
-                                  : swe == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                              : CU_TENSOR_MAP_SWIZZLE_32B;
-    cuuint64_t ext[4] = {(cuuint64_t)D, 0, 0, 0}, str[3];
-    cuuint32_t box[4] = {(cuuint32_t)swe, 0, 0, 0}, ones[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 3; ++i) {
-        ext[i + 1] = (cuuint64_t)dims[i].extent;
-        // a dimension of extent 1 is never stepped along; give it a harmless stride
-        str[i] = dims[i].extent > 1 ? (cuuint64_t)dims[i].stride * 2 : (cuuint64_t)D * 2;
-        box[i + 1] = (cuuint32_t)dims[i].box;
-    }
-    const auto fn = fa::tensor_map_encoder();
-    if (fn == nullptr) return CUDA_ERROR_NOT_SUPPORTED;
-    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr),
-              ext, str, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-}
-
-// Largest box of whole page rows that tiles a block of `bn` positions.
-int box_rows_for(int page, int bn) {
-    int r = 16;
-    while (r < bn && page % (2 * r) == 0) r *= 2;
-    return r;
-}
-
 cudaError_t launch_paged(int D, const fa::PagedLaunch& a, bool bf16) {
     switch (D) {
         case 16: return fa::launch_paged_d16(a, bf16);
@@ -171,8 +138,8 @@ fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
         p.scale_log2 = c;
         p.negate_s = negate;
         p.slot_floats = slot_floats(128, D);
-        const MapDim dq[3] = {{Hq, x.sq.h, G}, {T, x.sq.n, tokens}, {Z, x.sq.b, 1}};
-        if (make_paged_map(&mq, x.q, bf16, D, dq) != CUDA_SUCCESS) return FA_ERR_CUDA;
+        const fa::PagedMapDim dq[3] = {{Hq, x.sq.h, G}, {T, x.sq.n, tokens}, {Z, x.sq.b, 1}};
+        if (fa::make_paged_map(&mq, x.q, bf16, D, dq) != CUDA_SUCCESS) return FA_ERR_CUDA;
         a.tmQ = &mq;
     } else {
         const RowsFacts rf = rows_facts(D);
@@ -182,13 +149,13 @@ fa_status fa_fwd_paged(const fa_fwd_paged_args* args, cudaStream_t stream) {
         p.scale_log2 = negate ? -c : c;
         p.slot_floats = slot_floats(16, D);
     }
-    p.box_rows = box_rows_for(p.page, bk);
+    p.box_rows = fa::paged_box_rows(p.page, bk);
     if (P > 0) {
         const fa_strides &sk = cache.sk, &sv = cache.sv;
-        const MapDim dk[3] = {{p.page, sk.n, p.box_rows}, {Hkv, sk.h, 1}, {P, sk.b, 1}};
-        const MapDim dv[3] = {{p.page, sv.n, p.box_rows}, {Hkv, sv.h, 1}, {P, sv.b, 1}};
-        if (make_paged_map(&mk, cache.k, bf16, D, dk) != CUDA_SUCCESS ||
-            make_paged_map(&mv, cache.v, bf16, D, dv) != CUDA_SUCCESS)
+        const fa::PagedMapDim dk[3] = {{p.page, sk.n, p.box_rows}, {Hkv, sk.h, 1}, {P, sk.b, 1}};
+        const fa::PagedMapDim dv[3] = {{p.page, sv.n, p.box_rows}, {Hkv, sv.h, 1}, {P, sv.b, 1}};
+        if (fa::make_paged_map(&mk, cache.k, bf16, D, dk) != CUDA_SUCCESS ||
+            fa::make_paged_map(&mv, cache.v, bf16, D, dv) != CUDA_SUCCESS)
             return FA_ERR_CUDA;
     }
     a.tmK = &mk;

@@ -3,7 +3,9 @@
 #ifndef FA_HEAD_DIM
 #error "compile with -DFA_HEAD_DIM=<16|32|64|128|256>"
 #endif
+#include "fa_launch.h"
 #include "fa_score_rows_kernel.cuh"
+#include "fa_score_tile_kernel.cuh"
 
 #include <algorithm>
 
@@ -20,9 +22,35 @@ static cudaError_t launch_rows(const ScoreLaunch& a) {
                             32 * SCORE_WARPS, 0, a.stream, p);
 }
 
+template <bool BF16>
+static cudaError_t launch_tiles(const ScoreLaunch& a) {
+    using T = ScoreTile<FA_HEAD_DIM>;
+    static_assert(T::BR == score_tile_facts(FA_HEAD_DIM).rows && T::KB == score_tile_facts(FA_HEAD_DIM).block &&
+                  T::NCG * T::CW <= score_tile_facts(FA_HEAD_DIM).step, "the host's facts");
+    static_assert(sizeof(scoret::Cut) == 48 && T::KB <= 256, "workspace");
+    auto kernel = fa_score_tile_kernel<FA_HEAD_DIM, BF16>;
+    static std::atomic<uint64_t> configured{0};  // context the opt-in shared memory size was set in
+    cudaError_t err = set_smem_for_context(kernel, T::SMEM_BYTES, configured);
+    if (err != cudaSuccess) return err;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.sms);
+    cfg.blockDim = dim3(T::THREADS);
+    cfg.dynamicSmemBytes = T::SMEM_BYTES;
+    cfg.stream = a.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kernel, *a.tmQ, *a.tmK, a.params);
+    if (err != cudaSuccess || a.params.parts == nullptr || a.sms < 2) return err;
+    return launch_dependent(fa_score_merge_kernel<FA_HEAD_DIM>, dim3((unsigned)(a.sms - 1)), T::KB, 0, a.stream, a.params);
+}
+
 #define FA_CAT2(a, b) a##b
 #define FA_CAT(a, b) FA_CAT2(a, b)
 cudaError_t FA_CAT(launch_score_d, FA_HEAD_DIM)(const ScoreLaunch& a, bool bf16) {
+    if (a.tiles) return bf16 ? launch_tiles<true>(a) : launch_tiles<false>(a);
     const bool one = (int64_t)a.params.T * a.params.G <= 8;
     if (bf16) return one ? launch_rows<true, 1>(a) : launch_rows<true, 2>(a);
     return one ? launch_rows<false, 1>(a) : launch_rows<false, 2>(a);

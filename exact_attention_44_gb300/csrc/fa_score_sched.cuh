@@ -35,10 +35,12 @@ struct ScoreFind {
 
 // The place of range first + mine of `ranges` (RANGES of them a CTA, mine the same in
 // all threads of a warp).  count(s): steps of a sequence.  Called by every thread of
-// the CTA.
+// the CTA; with up to 32 sequences the warps need not all call it.  *start: the first
+// step of the range, *all: the steps of all sequences.
 template <int RANGES, typename Count>
 __device__ __forceinline__ ScorePlace score_place(const ScoreParams& p, ScoreFind<RANGES>* f, int first, int mine,
-                                                  int ranges, Count count) {
+                                                  int ranges, Count count, int64_t* start = nullptr,
+                                                  int64_t* all = nullptr) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid % 32, c = first + mine;
     ScorePlace w{0, {0, 0}, 0, 0};
     auto cut = [&](int64_t total, int i, int64_t& lo, int64_t& n) {
@@ -48,6 +50,12 @@ __device__ __forceinline__ ScorePlace score_place(const ScoreParams& p, ScoreFin
         const int64_t rem = total - q * ranges;
         lo = q * i + (i < rem ? i : rem);
         n = i < ranges ? q + (i < rem) : 0;
+    };
+    auto report = [&](int64_t lo, int64_t total) {
+        if (start != nullptr) {
+            *start = lo;
+            *all = total;
+        }
     };
     if (p.Z <= 32) {  // each warp by itself, one sequence a lane
         ScoreLen s{0, 0};
@@ -62,7 +70,9 @@ __device__ __forceinline__ ScorePlace score_place(const ScoreParams& p, ScoreFin
             if (lane >= d) x += y;
         }
         int64_t lo;
-        cut(__shfl_sync(0xffffffffu, x, 31), c, lo, w.left);
+        const int64_t total = __shfl_sync(0xffffffffu, x, 31);
+        cut(total, c, lo, w.left);
+        report(lo, total);
         if (w.left > 0) {
             w.z = __ffs(__ballot_sync(0xffffffffu, lo < x)) - 1;
             w.at = lo - __shfl_sync(0xffffffffu, x - v, w.z);
@@ -78,6 +88,7 @@ __device__ __forceinline__ ScorePlace score_place(const ScoreParams& p, ScoreFin
     int64_t total = 0, lo;
     for (int i = 0; i < nt / 32; ++i) total += f->red[i];
     cut(total, c, lo, w.left);
+    report(lo, total);
     if (tid < RANGES) {
         int64_t l, n;
         cut(total, first + tid, l, n);

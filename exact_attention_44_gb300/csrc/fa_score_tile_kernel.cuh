@@ -1,0 +1,567 @@
+// The weight that cached positions receive from many query rows (a chunk of a prompt, the
+// last tokens of one, the accepted tokens of a batch): see fa_score_rows_kernel.cuh.
+//
+// Sᵀ = K Qᵀ on tcgen05 with the positions as the rows of the product, so that a position
+// is a lane of tensor memory and one thread's: the weights that it receives are summed in
+// that thread's registers, tile after tile of query rows, and nothing is exchanged until
+// the position's tiles are done.  A query row's lse is a column's, read from shared memory
+// as a broadcast.  A unit of work is a block of KB positions of one (sequence, kv head):
+// its K stays in shared memory while the tiles of up to BR query rows that see it stream
+// by.  Units are laid end to end, counted in tiles, and cut into one equal range a CTA
+// (fa_score_sched.cuh); a unit that a cut crosses leaves its sums in slots of the
+// workspace, and fa_score_merge_kernel joins them in order.
+//
+// Roles: warp 0 walks the range, hands the units on and loads K through the block table
+// (a lane a box of rows); warp 1 issues the products; warp 2 stages the lse; warp 3 loads
+// Q; sixteen warps take the exponentials: a quarter of the lanes each (a warp reaches only
+// its own quarter of tensor memory), of one half of the positions, of a group of columns.
+// Every wait is bounded as in fa_fwd_kernel.cuh.
+#pragma once
+
+#include "fa_fwd_kernel.cuh"
+#include "fa_score_sched.cuh"
+
+namespace fa {
+
+template <int D_>
+struct ScoreTile {
+    static constexpr int D = D_;
+    static constexpr int BR = D == 256 ? 64 : 128;       // query rows of a tile, at most
+    static constexpr int KH = D == 256 ? 1 : 2;          // products of 128 positions a tile
+    static constexpr int KB = 128 * KH;                  // positions of a unit
+    static constexpr int SWE = D < 64 ? D : 64;          // elements of a swizzled row chunk
+    static constexpr int SW = SWE * 2;
+    static constexpr int NCHUNK = D / SWE;
+    static constexpr uint32_t SWIZZLE_CODE = SW == 128 ? 2u : SW == 64 ? 4u : 6u;
+    static constexpr int HALF_BYTES = 128 * D * 2;
+    static constexpr int K_BYTES = KH * HALF_BYTES;
+    static constexpr int Q_BYTES = BR * D * 2;
+    static constexpr int K_STAGES = 2;
+    static constexpr int Q_STAGES = D >= 128 ? 2 : 4;
+    static constexpr int SR = 512 / (KH * BR) < 4 ? 512 / (KH * BR) : 4;  // score slots in tensor memory
+    static constexpr int WARPS = 16;                     // of the exponentials
+    static constexpr int NCG = WARPS / 4 / KH;           // column groups
+    static constexpr int CW = BR / NCG < 32 ? BR / NCG : 32;  // columns a thread takes at a time
+    static constexpr int THREADS = 32 * (4 + WARPS);
+    static constexpr int SEGS = 4;
+    static constexpr int OFF_K = 0;
+    static constexpr int OFF_Q = OFF_K + K_STAGES * K_BYTES;
+    static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;      // [SR][BR] -lse log2 e
+    static constexpr int OFF_LAST = OFF_LSE + SR * BR * 4;          // [SR][BR] last position seen
+    static constexpr int OFF_SUM = OFF_LAST + SR * BR * 4;          // [2][NCG][KB]
+    static constexpr int OFF_SEG = OFF_SUM + 2 * NCG * KB * 4;
+    static constexpr int OFF_BAR = OFF_SEG + SEGS * 48;
+    static constexpr int B_KFULL = 0;
+    static constexpr int B_KEMPTY = B_KFULL + K_STAGES;
+    static constexpr int B_QFULL = B_KEMPTY + K_STAGES;
+    static constexpr int B_QEMPTY = B_QFULL + Q_STAGES;
+    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // product done (commit)
+    static constexpr int B_SEMPTY = B_SFULL + SR;         // score slot and lse slot read (a warp each)
+    static constexpr int B_LFULL = B_SEMPTY + SR;         // lse staged
+    static constexpr int B_SEGFULL = B_LFULL + SR;
+    static constexpr int B_SEGFREE = B_SEGFULL + SEGS;
+    static constexpr int B_SUM = B_SEGFREE + SEGS;        // [2] the groups' sums are there
+    static constexpr int B_DRAIN = B_SUM + 2;
+    static constexpr int NUM_BARS = B_DRAIN + 1;
+    static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+    static constexpr int SMEM_USED = OFF_MISC + 16;
+    // >= 120 KB keeps one CTA per SM, so no CTA ever waits on another's TMEM
+    static constexpr int SMEM_BYTES = (SMEM_USED + 1024) > 120 * 1024 ? SMEM_USED + 1024 : 120 * 1024;
+    static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+    static_assert(SR * KH * BR <= 512, "tensor memory budget");
+    static __device__ __forceinline__ uint32_t bar_count(int i) {
+        if (i >= B_SEMPTY && i < B_SEMPTY + SR) return WARPS;
+        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 3 + WARPS;
+        if (i >= B_SUM && i < B_SUM + 2) return WARPS;
+        return 1;
+    }
+};
+
+namespace scoret {
+
+// A unit's part in a range: tiles i0 .. i1 - 1 of those that see its block.
+struct Unit {
+    int z, hk, j, i0, i1, slot, len, nl;  // i1 = 0: the end; slot -1: all of the unit's tiles
+};
+
+// Tiles of a sequence's rows, and which of them is the first that sees block j: the one
+// with token j KB - len.
+template <int D>
+struct Shape {
+    using T = ScoreTile<D>;
+    int nb, nt, lag;  // blocks, tiles, ceil(len / tokens)
+    __device__ __forceinline__ Shape(const ScoreParams& p, const ScoreLen& s) {
+        nb = (s.len + s.nl + T::KB - 1) / T::KB;
+        nt = (s.nl + p.tokens - 1) >> p.token_shift;
+        lag = (s.len + p.tokens - 1) >> p.token_shift;
+        if (s.nl == 0) {
+            nt = 1;                       // only the scores so far
+            lag = 0x7fffffff;
+            if (p.decay == 1.f) nb = 0;   // which stay as they are
+        }
+    }
+    // r = KB / tokens tiles from a block to the next
+    __device__ __forceinline__ int first(const ScoreParams& p, int j) const {
+        return (int)max((int64_t)0, (int64_t)j * (T::KB >> p.token_shift) - lag);
+    }
+    __device__ __forceinline__ int64_t before(const ScoreParams& p, int j) const {  // tiles of blocks 0 .. j - 1
+        const int64_t r = T::KB >> p.token_shift, j0 = lag / r + 1;  // the first block with first() > 0
+        int64_t n = (int64_t)j * nt;
+        if (j > j0) n -= r * ((int64_t)(j - 1) * j - j0 * (j0 - 1)) / 2 - (int64_t)lag * (j - j0);
+        return n;
+    }
+};
+
+// Where a range starts, for the merge.
+struct alignas(16) Cut {
+    int z, hk, j, skip;   // tiles of the unit in front of the range
+    int tiles, len, end, pad;
+    int64_t start, total; // in tiles
+};
+
+}  // namespace scoret
+
+template <int D>
+struct ScoreWalk {
+    using T = ScoreTile<D>;
+    ScorePlace w;
+    int hk, j, i;  // the next tile: of the unit's, counted from first()
+    __device__ __forceinline__ void start(const ScoreParams& p, const ScorePlace& place) {
+        w = place;
+        if (w.left == 0) return;
+        const scoret::Shape<D> s(p, w.s);
+        const int64_t per = s.before(p, s.nb);
+        hk = (int)(w.at / per);
+        const int64_t rem = w.at - hk * per;
+        int lo = 0, hi = s.nb;  // before(lo) <= rem < before(hi)
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) / 2;
+            if (s.before(p, mid) <= rem) lo = mid;
+            else hi = mid;
+        }
+        j = lo;
+        i = (int)(rem - s.before(p, lo));
+    }
+    // the next unit of the range; false at its end
+    __device__ __forceinline__ bool next(const ScoreParams& p, scoret::Unit& u) {
+        if (w.left == 0) return false;
+        const scoret::Shape<D> s(p, w.s);
+        const int first = s.first(p, j), tiles = s.nt - first;
+        u.z = w.z, u.hk = hk, u.j = j, u.len = w.s.len, u.nl = w.s.nl;
+        u.i0 = first + i;
+        const int n = (int)min((int64_t)(tiles - i), w.left);
+        u.i1 = u.i0 + n;
+        u.slot = i == 0 && n == tiles ? -1 : 2 * (int)blockIdx.x + (i > 0 ? 0 : 1);
+        w.left -= n;
+        i = 0;
+        if (w.left > 0 && ++j == s.nb) {
+            j = 0;
+            if (++hk == p.Hkv) {
+                hk = 0;
+                do w.s = score_len(p, ++w.z);
+                while (scoret::Shape<D>(p, w.s).nb == 0);
+            }
+        }
+        return true;
+    }
+};
+
+namespace scoret {
+
+template <int D, typename Bar>
+__device__ __forceinline__ void put(volatile int* ring, const Unit& u, uint32_t n, Bar bar) {
+    using T = ScoreTile<D>;
+    volatile int* s = ring + (n % T::SEGS) * 12;
+    if (threadIdx.x % 32 == 0) {
+        s[0] = u.z, s[1] = u.hk, s[2] = u.j, s[3] = u.i0, s[4] = u.i1, s[5] = u.slot, s[6] = u.len, s[7] = u.nl;
+        ptx::mbar_arrive(bar(T::B_SEGFULL + n % T::SEGS));
+    }
+    __syncwarp();
+}
+// The n-th unit, for a whole warp (WARP) or its one active lane; false at the end, or (ok
+// false) when the wait ran out.
+template <int D, bool WARP, typename Bar>
+__device__ __forceinline__ bool get(volatile const int* ring, Unit& u, uint32_t n, Bar bar, const Ctl& ctl, bool& ok) {
+    using T = ScoreTile<D>;
+    const uint32_t full = bar(T::B_SEGFULL + n % T::SEGS), parity = (n / T::SEGS) & 1u;
+    ok = WARP ? warp_wait_phase(full, parity, ctl, SITE_SEG_FULL) : wait_phase(full, parity, ctl, SITE_SEG_FULL);
+    if (!ok) return false;
+    volatile const int* s = ring + (n % T::SEGS) * 12;
+    u.z = s[0], u.hk = s[1], u.j = s[2], u.i0 = s[3], u.i1 = s[4], u.slot = s[5], u.len = s[6], u.nl = s[7];
+    if (WARP) __syncwarp();
+    if (!WARP || threadIdx.x % 32 == 0) ptx::mbar_arrive(bar(T::B_SEGFREE + n % T::SEGS));
+    return u.i1 > 0;
+}
+
+template <int D>
+__device__ void walk_and_load_k(const CUtensorMap* tmK, const ScoreParams& p, ScoreWalk<D> walk, volatile int* ring,
+                                uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
+    using T = ScoreTile<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int lane = threadIdx.x % 32;
+    // K passes once where all rows are one tile; else the units of a head are not far apart
+    const uint64_t policy = ptx::policy_evict_first();
+    uint32_t n = 0, ki = 0;
+    bool ok = true, withheld = false, have = true;
+    while (ok && have) {
+        Unit u{};
+        have = walk.next(p, u);
+        if (n >= (uint32_t)T::SEGS &&
+            !warp_wait_phase(bar(T::B_SEGFREE + n % T::SEGS), (n / T::SEGS - 1) & 1u, ctl, SITE_SEG_FREE)) {
+            ok = false;
+            break;
+        }
+        if (!have) u.i1 = 0;
+        put<D>(ring, u, n++, bar);
+        if (!have) break;
+        // lane b: the box of positions j KB + b box_rows ..
+        const int end = u.len + u.nl, k0 = u.j * T::KB + lane * p.box_rows;
+        const bool there = lane * p.box_rows < T::KB && k0 < end;
+        int page = p.P, slot = 0;
+        if (there) {
+            const int col = p.by_page(k0);
+            slot = k0 - col * p.page;
+            page = ldi(p.table + (int64_t)u.z * p.st_z + col);
+            if ((unsigned)page >= (unsigned)p.P) {
+                bad_page(p.status, SITE_PAGE_SCORE);
+                page = p.P;  // outside the map: zeros
+            }
+        }
+        const uint32_t s = ki % T::K_STAGES, ph = (ki / T::K_STAGES) & 1u;
+        if (!warp_wait_phase(bar(T::B_KEMPTY + s), ph ^ 1u, ctl, SITE_K_EMPTY)) { ok = false; break; }
+        if (p.inject_stall && blockIdx.x == 0 && !withheld) {
+            withheld = true;  // never issued: the wait for this block must time out
+        } else {
+            const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there));
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(T::B_KFULL + s), boxes * p.box_rows * T::SW * T::NCHUNK);
+            __syncwarp();
+            if (there) {
+                const int r = lane * p.box_rows;
+                const uint32_t dst = sbase + T::OFF_K + s * T::K_BYTES + (r / 128) * T::HALF_BYTES + (r % 128) * T::SW;
+                for (int c = 0; c < T::NCHUNK; ++c)
+                    ptx::tma_load_4d(dst + c * (128 * T::SW), tmK, bar(T::B_KFULL + s), c * T::SWE, slot, u.hk, page, policy);
+            }
+        }
+        ++ki;
+    }
+    if (!ok)
+        for (uint32_t i = ki > (uint32_t)T::K_STAGES ? ki - T::K_STAGES : 0; i < ki; ++i)
+            drain_phase(bar(T::B_KFULL + i % T::K_STAGES), (i / T::K_STAGES) & 1u, withheld ? ctl.limit_ns / 64 : ctl.limit_ns);
+}
+
+// A tile's Q is loaded unless it is the one before (blocks of a head whose rows are one tile).
+template <int D>
+__device__ void load_q(const CUtensorMap* tmQ, const ScoreParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0,
+                       const Ctl& ctl) {
+    using T = ScoreTile<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const uint64_t policy = ptx::policy_evict_last();
+    uint32_t qi = 0;
+    bool ok = true;
+    int z = -1, hk = -1, tile = -1;
+    Unit u;
+    for (uint32_t n = 0; get<D, false>(ring, u, n, bar, ctl, ok); ++n) {
+        for (int i = u.i0; i < u.i1; ++i) {
+            if (z == u.z && hk == u.hk && tile == i) continue;
+            z = u.z, hk = u.hk, tile = i;
+            const uint32_t s = qi % T::Q_STAGES, ph = (qi / T::Q_STAGES) & 1u;
+            if (!wait_phase(bar(T::B_QEMPTY + s), ph ^ 1u, ctl, SITE_Q_EMPTY)) { ok = false; break; }
+            ptx::mbar_arrive_expect_tx(bar(T::B_QFULL + s), (uint32_t)p.tile_rows * T::SW * T::NCHUNK);
+            const uint32_t dst = sbase + T::OFF_Q + s * T::Q_BYTES;
+            for (int c = 0; c < T::NCHUNK; ++c)
+                ptx::tma_load_4d(dst + c * (T::BR * T::SW), tmQ, bar(T::B_QFULL + s), c * T::SWE, u.hk * p.G,
+                                 i << p.token_shift, u.z, policy);
+            ++qi;
+        }
+        if (!ok) break;
+    }
+    if (!ok)
+        for (uint32_t i = qi > (uint32_t)T::Q_STAGES ? qi - T::Q_STAGES : 0; i < qi; ++i)
+            drain_phase(bar(T::B_QFULL + i % T::Q_STAGES), (i / T::Q_STAGES) & 1u, ctl.limit_ns);
+}
+
+template <int D, bool BF16>
+__device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
+                         const Ctl& ctl) {
+    using T = ScoreTile<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const uint32_t IDESC = ptx::idesc_f16(128, p.tile_cols, BF16, false, false);
+    constexpr uint32_t HI = ptx::smem_desc_hi(8 * T::SW, T::SWIZZLE_CODE);
+    const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16), q_lo0 = ptx::smem_desc_lo(sbase + T::OFF_Q, 16);
+    uint32_t g = 0, qi = 0;  // tiles, Q tiles
+    bool ok = true, held = false;  // held: a Q tile that the next unit may use again
+    int z = -1, hk = -1, tile = -1;
+    Unit u;
+    for (uint32_t n = 0; get<D, false>(ring, u, n, bar, ctl, ok); ++n) {
+        const uint32_t ks = n % T::K_STAGES;
+        for (int i = u.i0; i < u.i1; ++i, ++g) {
+            if (z != u.z || hk != u.hk || tile != i) {
+                if (held) ptx::tc_commit(bar(T::B_QEMPTY + (qi - 1) % T::Q_STAGES));
+                if (!wait_phase(bar(T::B_QFULL + qi % T::Q_STAGES), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
+                ++qi;
+                z = u.z, hk = u.hk, tile = i;
+                held = true;
+            }
+            if (i == u.i0 && !wait_phase(bar(T::B_KFULL + ks), (n / T::K_STAGES) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
+            const uint32_t r = g % T::SR;
+            if (!wait_phase(bar(T::B_SEMPTY + r), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t q_lo = q_lo0 + ((qi - 1) % T::Q_STAGES) * (T::Q_BYTES >> 4);
+#pragma unroll
+            for (int h = 0; h < T::KH; ++h) {
+                const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + h * T::HALF_BYTES) >> 4);
+                const uint32_t d = tmem + (r * T::KH + h) * T::BR;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
+                    ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
+                                ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
+                }
+            }
+            ptx::tc_commit(bar(T::B_SFULL + r));
+            if (i + 1 < u.i1) {  // another tile follows for certain
+                ptx::tc_commit(bar(T::B_QEMPTY + (qi - 1) % T::Q_STAGES));
+                held = false;
+            }
+        }
+        if (!ok) break;
+        ptx::tc_commit(bar(T::B_KEMPTY + ks));
+    }
+    if (!ok) {
+        ptx::tc_commit(bar(T::B_DRAIN));
+        drain_phase(bar(T::B_DRAIN), 0u, ctl.limit_ns);
+    }
+}
+
+// Each tile's lse and the last position that each of its rows sees, a warp.  A row that
+// does not count (no token, nothing seen) sees nothing; columns behind the tile's rows are
+// products with zeros.  A tile all of whose rows see all of the block needs no comparisons.
+template <int D>
+__device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, const Ctl& ctl) {
+    using T = ScoreTile<D>;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int lane = threadIdx.x % 32;
+    constexpr int N = T::BR / 32;
+    uint32_t g = 0;
+    bool ok = true;
+    Unit u;
+    for (uint32_t n = 0; get<D, true>(ring, u, n, bar, ctl, ok); ++n)
+        for (int i = u.i0; i < u.i1; ++i, ++g) {
+            const int row0 = i * p.tile_rows, rows = u.nl * p.G;
+            float v[N];
+            int last[N];
+            bool plain = true;
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const int c = x * 32 + lane, row = row0 + c, t = p.by_g(row), h = u.hk * p.G + row - t * p.G;
+                v[x] = -INFINITY;
+                last[x] = -1;
+                if (c < p.tile_rows) {
+                    float l = -INFINITY;
+                    if (row < rows) l = __ldcg(p.lse + ((int64_t)u.z * p.Hq + h) * p.T + t);
+                    if (l != -INFINITY) {
+                        v[x] = -l * 1.4426950408889634f;
+                        last[x] = u.len + t;
+                    }
+                    plain &= last[x] >= (u.j + 1) * T::KB - 1;
+                }
+            }
+            const uint32_t r = g % T::SR;
+            if (!warp_wait_phase(bar(T::B_SEMPTY + r), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return;
+            plain = __all_sync(0xffffffffu, plain);
+            float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
+            int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                ls[x * 32 + lane] = v[x];
+                la[x * 32 + lane] = plain ? 0x7fffffff : last[x];
+            }
+            ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
+        }
+}
+
+template <int D>
+__device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, uint32_t tmem, const Ctl& ctl) {
+    using T = ScoreTile<D>;
+    constexpr int CW = T::CW;
+    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+    const int w = threadIdx.x / 32 - 4, lane = threadIdx.x % 32;
+    const int quad = w % 4, half = w / 4 % T::KH, cg = w / 4 / T::KH;
+    const int key = half * 128 + quad * 32 + lane;
+    const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
+    const float c = p.scale * 1.4426950408889634f;
+    const uint64_t c2 = ptx::pack_f32x2(c, c);
+    const int cols = p.tile_cols / T::NCG;  // of a group: a multiple of CW
+    float* sums = reinterpret_cast<float*>(smem + T::OFF_SUM);
+    uint32_t g = 0;
+    bool ok = true;
+    Unit u;
+    for (uint32_t n = 0; get<D, true>(ring, u, n, bar, ctl, ok); ++n) {
+        const int pos = u.j * T::KB + key;
+        float* score = p.scores + (int64_t)u.z * p.ss_z + u.hk * p.ss_h + pos;
+        float old = 0.f;
+        if (cg == 0 && u.slot < 0 && p.decay != 0.f && pos < u.len) old = __ldcg(score) * p.decay;
+        uint64_t sum0 = ptx::pack_f32x2(0.f, 0.f), sum1 = sum0;
+        for (int i = u.i0; i < u.i1; ++i, ++g) {
+            const uint32_t r = g % T::SR, ph = (g / T::SR) & 1u;
+            if (!warp_wait_phase(bar(T::B_LFULL + r), ph, ctl, SITE_EPI_FULL)) return;
+            if (!warp_wait_phase(bar(T::B_SFULL + r), ph, ctl, SITE_S_FULL)) return;
+            ptx::tc_fence_after();
+            const uint32_t s_addr = tmem + lane_addr + (r * T::KH + half) * T::BR + cg * cols;
+            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (r * T::BR + cg * cols) * 4);
+            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (r * T::BR + cg * cols) * 4);
+            const bool plain = la[0].x == 0x7fffffff;
+            for (int c0 = 0; c0 < cols; c0 += CW) {
+                uint32_t s[CW];
+                if constexpr (CW == 32) ptx::tmem_ld32(s_addr + c0, s);
+                else ptx::tmem_ld16(s_addr + c0, s);
+                if (c0 + CW == cols) ptx::tc_fence_before();
+#pragma unroll
+                for (int x = 0; x < CW; x += 4) {
+                    const float4 l = ls[(c0 + x) / 4];
+                    float a[4];
+                    ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2,
+                                                 ptx::pack_f32x2(l.x, l.y)), a[0], a[1]);
+                    ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), c2,
+                                                 ptx::pack_f32x2(l.z, l.w)), a[2], a[3]);
+                    if (!plain) {
+                        const int4 t = la[(c0 + x) / 4];
+                        a[0] = pos <= t.x ? a[0] : -INFINITY;
+                        a[1] = pos <= t.y ? a[1] : -INFINITY;
+                        a[2] = pos <= t.z ? a[2] : -INFINITY;
+                        a[3] = pos <= t.w ? a[3] : -INFINITY;
+                    }
+                    sum0 = ptx::fadd2(sum0, ptx::pack_f32x2(ptx::ex2(a[0]), ptx::ex2(a[1])));
+                    sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
+                }
+            }
+            ptx::mbar_arrive_warp(bar(T::B_SEMPTY + r));
+        }
+        float s0, s1, s2, s3;
+        ptx::unpack_f32x2(sum0, s0, s1);
+        ptx::unpack_f32x2(sum1, s2, s3);
+        // the groups' sums, in order; the slot's parity and this wait keep a warp from
+        // writing where another has not read yet
+        float* mine = sums + (n & 1u) * T::NCG * T::KB + key;
+        mine[cg * T::KB] = (s0 + s1) + (s2 + s3);
+        ptx::mbar_arrive_warp(bar(T::B_SUM + (n & 1u)));
+        if (!warp_wait_phase(bar(T::B_SUM + (n & 1u)), (n >> 1) & 1u, ctl, SITE_MAX_XCHG)) return;
+        if (cg == 0) {
+            float all = mine[0];
+#pragma unroll
+            for (int x = 1; x < T::NCG; ++x) all += mine[x * T::KB];
+            if (u.slot >= 0) p.parts[(int64_t)u.slot * T::KB + key] = all;
+            else if (pos < u.len + u.nl) *score = old + all;
+        }
+    }
+}
+
+}  // namespace scoret
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(ScoreTile<D>::THREADS, 1)
+    fa_score_tile_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                         const __grid_constant__ ScoreParams p) {
+    using T = ScoreTile<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = ptx::smem_addr(smem), bar0 = sbase + T::OFF_BAR;
+    volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + T::OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + T::OFF_MISC + 4);
+    volatile int* ring = reinterpret_cast<volatile int*>(smem + T::OFF_SEG);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < T::NUM_BARS; ++i) ptx::mbar_init(bar0 + 8u * i, T::bar_count(i));
+        *abort_flag = 0;
+        ptx::fence_mbar_init();
+        ptx::prefetch_tmap(&tmQ);
+        ptx::prefetch_tmap(&tmK);
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
+        ptx::tmem_relinquish();
+    }
+    // rows of Q's slots behind the tile's: zeros (no copy writes them)
+    if (p.tile_rows < p.tile_cols) {
+        constexpr int PR = T::SW / 16;
+        const int n = (p.tile_cols - p.tile_rows) * PR;
+        for (int i = threadIdx.x; i < n * T::Q_STAGES * T::NCHUNK; i += T::THREADS)
+            ptx::st_shared_v4(sbase + T::OFF_Q + (i / n) * (T::BR * T::SW) + p.tile_rows * T::SW + (i % n) * 16, 0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const Ctl ctl{abort_flag, p.status, p.wait_limit_ns};
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    // (the search's area is that of the sums)
+    auto* find = reinterpret_cast<ScoreFind<1>*>(smem + T::OFF_SUM);
+    static_assert(sizeof(ScoreFind<1>) <= 2 * T::NCG * T::KB * 4, "the range search fits the sums' area");
+    auto count = [&](const ScoreLen& s) {
+        const scoret::Shape<D> x(p, s);
+        return x.before(p, x.nb) * p.Hkv;
+    };
+    ScoreWalk<D> walk{};
+    if (p.Z > 32 || warp == 0) {
+        int64_t start, total;
+        const ScorePlace place = score_place<1>(p, find, (int)blockIdx.x, 0, (int)gridDim.x, count, &start, &total);
+        walk.start(p, place);
+        if (p.parts != nullptr && threadIdx.x == 0) {
+            scoret::Cut cut{};
+            cut.z = -1;
+            if (place.left > 0) {
+                const scoret::Shape<D> s(p, place.s);
+                cut = scoret::Cut{place.z, walk.hk, walk.j, walk.i, s.nt - s.first(p, walk.j), place.s.len,
+                                  place.s.len + place.s.nl, 0, start, total};
+            }
+            static_cast<scoret::Cut*>(p.cuts)[blockIdx.x] = cut;
+        }
+    }
+    if (p.Z > 32) __syncthreads();
+
+    if (warp == 0) scoret::walk_and_load_k<D>(&tmK, p, walk, ring, sbase, bar0, ctl);
+    else if (warp == 1) { if (lane == 0) scoret::multiply<D, BF16>(p, ring, sbase, bar0, tmem, ctl); }
+    else if (warp == 2) scoret::stage_lse<D>(p, ring, smem, bar0, ctl);
+    else if (warp == 3) { if (lane == 0) scoret::load_q<D>(&tmQ, p, ring, sbase, bar0, ctl); }
+    else scoret::weigh<D>(p, ring, smem, bar0, tmem, ctl);
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Block b - 1 looks at the cut between ranges b - 1 and b.  If it is the first one inside
+// its unit, the unit's parts -- slot 2 c + 1 of the range c that it starts in, slots 2 c
+// of the following ones -- are added in order.
+template <int D>
+__global__ void __launch_bounds__(ScoreTile<D>::KB) fa_score_merge_kernel(const ScoreParams p) {
+    using T = ScoreTile<D>;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
+    const int b = 1 + (int)blockIdx.x, ranges = (int)gridDim.x + 1;
+    const scoret::Cut* at = static_cast<const scoret::Cut*>(p.cuts) + b;
+    const int4 u = __ldcg(reinterpret_cast<const int4*>(at)), v = __ldcg(reinterpret_cast<const int4*>(at) + 1);
+    if (u.x < 0 || u.w == 0) return;  // no such range, or it starts with a unit
+    const int64_t start = __ldcg(reinterpret_cast<const long long*>(at) + 4), total = __ldcg(reinterpret_cast<const long long*>(at) + 5);
+    const int64_t q = total / ranges, rem = total - q * ranges;
+    auto range_of = [&](int64_t x) {  // the range of tile x
+        const int64_t big = (q + 1) * rem;
+        return (int)(x < big ? x / (q + 1) : rem + (x - big) / q);
+    };
+    const int64_t t0 = start - u.w;
+    const int c0 = range_of(t0), c1 = range_of(t0 + v.x - 1);
+    if (b != c0 + 1) return;
+    const int key = threadIdx.x, pos = u.z * T::KB + key;
+    if (pos >= v.z) return;
+    float all = __ldcg(p.parts + (int64_t)(2 * c0 + 1) * T::KB + key);
+    for (int c = c0 + 1; c <= c1; ++c) all += __ldcg(p.parts + (int64_t)(2 * c) * T::KB + key);
+    float* score = p.scores + (int64_t)u.x * p.ss_z + u.y * p.ss_h + pos;
+    *score = (p.decay != 0.f && pos < v.y ? __ldcg(score) * p.decay : 0.f) + all;
+}
+
+}  // namespace fa
