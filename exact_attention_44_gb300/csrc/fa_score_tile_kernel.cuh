@@ -13,8 +13,9 @@
 //
 // Roles: warp 0 walks the range, hands the units on and loads K through the block table
 // (a lane a box of rows); warp 1 issues the products; warp 2 stages the lse; warp 3 loads
-// Q; sixteen warps take the exponentials: a quarter of the lanes each (a warp reaches only
-// its own quarter of tensor memory), of one half of the positions, of a group of columns.
+// Q; eight warps take the exponentials: a quarter of the lanes each (a warp reaches only
+// its own quarter of tensor memory), of one half of the positions (D = 256: of a group of
+// columns).
 // Every wait is bounded as in fa_fwd_kernel.cuh.
 #pragma once
 
@@ -39,26 +40,28 @@ struct ScoreTile {
     static constexpr int K_STAGES = 2;
     static constexpr int Q_STAGES = D >= 128 ? 2 : 4;
     static constexpr int SR = 512 / (KH * BR) < 4 ? 512 / (KH * BR) : 4;  // score slots in tensor memory
-    static constexpr int WARPS = 16;                     // of the exponentials
+    static constexpr int WARPS = 8;                      // of the exponentials
+    static constexpr int LR = 4;                         // lse slots
     static constexpr int NCG = WARPS / 4 / KH;           // column groups
-    static constexpr int CW = BR / NCG < 32 ? BR / NCG : 32;  // columns a thread takes at a time
+    static constexpr int CW = 32;                        // columns a thread takes at a time
     static constexpr int THREADS = 32 * (4 + WARPS);
     static constexpr int SEGS = 4;
     static constexpr int OFF_K = 0;
     static constexpr int OFF_Q = OFF_K + K_STAGES * K_BYTES;
-    static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;      // [SR][BR] -lse log2 e
-    static constexpr int OFF_LAST = OFF_LSE + SR * BR * 4;          // [SR][BR] last position seen
-    static constexpr int OFF_SUM = OFF_LAST + SR * BR * 4;          // [2][NCG][KB]
+    static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;      // [LR][BR] -lse log2 e
+    static constexpr int OFF_LAST = OFF_LSE + LR * BR * 4;          // [LR][BR] last position seen
+    static constexpr int OFF_SUM = OFF_LAST + LR * BR * 4;          // [2][NCG][KB]
     static constexpr int OFF_SEG = OFF_SUM + 2 * NCG * KB * 4;
     static constexpr int OFF_BAR = OFF_SEG + SEGS * 48;
     static constexpr int B_KFULL = 0;
     static constexpr int B_KEMPTY = B_KFULL + K_STAGES;
     static constexpr int B_QFULL = B_KEMPTY + K_STAGES;
     static constexpr int B_QEMPTY = B_QFULL + Q_STAGES;
-    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // product done (commit)
-    static constexpr int B_SEMPTY = B_SFULL + SR;         // score slot and lse slot read (a warp each)
-    static constexpr int B_LFULL = B_SEMPTY + SR;         // lse staged
-    static constexpr int B_SEGFULL = B_LFULL + SR;
+    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // [SR][KH] product done (commit)
+    static constexpr int B_SEMPTY = B_SFULL + SR * KH;    // [SR][KH] scores read (its warps)
+    static constexpr int B_LFULL = B_SEMPTY + SR * KH;    // [LR] lse staged
+    static constexpr int B_LEMPTY = B_LFULL + LR;         // [LR] lse read (every warp)
+    static constexpr int B_SEGFULL = B_LEMPTY + LR;
     static constexpr int B_SEGFREE = B_SEGFULL + SEGS;
     static constexpr int B_SUM = B_SEGFREE + SEGS;        // [2] the groups' sums are there
     static constexpr int B_DRAIN = B_SUM + 2;
@@ -70,7 +73,8 @@ struct ScoreTile {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
     static_assert(SR * KH * BR <= 512, "tensor memory budget");
     static __device__ __forceinline__ uint32_t bar_count(int i) {
-        if (i >= B_SEMPTY && i < B_SEMPTY + SR) return WARPS;
+        if (i >= B_SEMPTY && i < B_SEMPTY + SR * KH) return WARPS / KH;
+        if (i >= B_LEMPTY && i < B_LEMPTY + LR) return WARPS;
         if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 3 + WARPS;
         if (i >= B_SUM && i < B_SUM + 2) return WARPS;
         return 1;
@@ -304,11 +308,11 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
             }
             if (i == u.i0 && !wait_phase(bar(T::B_KFULL + ks), (n / T::K_STAGES) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
             const uint32_t r = g % T::SR;
-            if (!wait_phase(bar(T::B_SEMPTY + r), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
-            ptx::tc_fence_after();
             const uint32_t q_lo = q_lo0 + ((qi - 1) % T::Q_STAGES) * (T::Q_BYTES >> 4);
 #pragma unroll
             for (int h = 0; h < T::KH; ++h) {
+                if (!wait_phase(bar(T::B_SEMPTY + r * T::KH + h), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
+                ptx::tc_fence_after();
                 const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + h * T::HALF_BYTES) >> 4);
                 const uint32_t d = tmem + (r * T::KH + h) * T::BR;
 #pragma unroll
@@ -317,8 +321,9 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
                     ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
                                 ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
                 }
+                ptx::tc_commit(bar(T::B_SFULL + r * T::KH + h));
             }
-            ptx::tc_commit(bar(T::B_SFULL + r));
+            if (!ok) break;
             if (i + 1 < u.i1) {  // another tile follows for certain
                 ptx::tc_commit(bar(T::B_QEMPTY + (qi - 1) % T::Q_STAGES));
                 held = false;
@@ -333,57 +338,121 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
     }
 }
 
-// Each tile's lse and the last position that each of its rows sees, a warp.  A row that
-// does not count (no token, nothing seen) sees nothing; columns behind the tile's rows are
-// products with zeros.  A tile all of whose rows see all of the block needs no comparisons.
+// Each tile's lse and the last position that each of its rows sees, a warp, the loads two
+// tiles ahead.  A row that does not count (no token, nothing seen) sees nothing; columns
+// behind the tile's rows are products with zeros.  A tile all of whose rows see all of the
+// block needs no comparisons.
 template <int D>
 __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, const Ctl& ctl) {
     using T = ScoreTile<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int lane = threadIdx.x % 32;
     constexpr int N = T::BR / 32;
-    uint32_t g = 0;
+    struct Tile {
+        float l[N];
+        int j, i, len;
+        bool there;
+    };
+    uint32_t n = 0, g = 0;
     bool ok = true;
-    Unit u;
-    for (uint32_t n = 0; get<D, true>(ring, u, n, bar, ctl, ok); ++n)
-        for (int i = u.i0; i < u.i1; ++i, ++g) {
-            const int row0 = i * p.tile_rows, rows = u.nl * p.G;
-            float v[N];
-            int last[N];
-            bool plain = true;
+    Unit u{};
+    u.i0 = u.i1 = 0;
+    auto fetch = [&](Tile& t) {
+        t.there = ok && (u.i0 < u.i1 || (n == 0 || u.i1 > 0 ? get<D, true>(ring, u, n++, bar, ctl, ok) : false));
+        if (!t.there) return;
+        t.j = u.j, t.i = u.i0++, t.len = u.len;
+        const int row0 = t.i * p.tile_rows, rows = u.nl * p.G;
 #pragma unroll
-            for (int x = 0; x < N; ++x) {
-                const int c = x * 32 + lane, row = row0 + c, t = p.by_g(row), h = u.hk * p.G + row - t * p.G;
-                v[x] = -INFINITY;
-                last[x] = -1;
-                if (c < p.tile_rows) {
-                    float l = -INFINITY;
-                    if (row < rows) l = __ldcg(p.lse + ((int64_t)u.z * p.Hq + h) * p.T + t);
-                    if (l != -INFINITY) {
-                        v[x] = -l * 1.4426950408889634f;
-                        last[x] = u.len + t;
-                    }
-                    plain &= last[x] >= (u.j + 1) * T::KB - 1;
-                }
-            }
-            const uint32_t r = g % T::SR;
-            if (!warp_wait_phase(bar(T::B_SEMPTY + r), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return;
-            plain = __all_sync(0xffffffffu, plain);
-            float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
-            int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
-#pragma unroll
-            for (int x = 0; x < N; ++x) {
-                ls[x * 32 + lane] = v[x];
-                la[x * 32 + lane] = plain ? 0x7fffffff : last[x];
-            }
-            ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
+        for (int x = 0; x < N; ++x) {
+            const int c = x * 32 + lane, row = row0 + c, tok = p.by_g(row), h = u.hk * p.G + row - tok * p.G;
+            t.l[x] = -INFINITY;
+            if (c < p.tile_rows && row < rows) t.l[x] = __ldcg(p.lse + ((int64_t)u.z * p.Hq + h) * p.T + tok);
         }
+    };
+    auto finish = [&](const Tile& t) -> bool {
+        float v[N];
+        int last[N];
+        bool plain = true;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const int c = x * 32 + lane;
+            const bool counts = t.l[x] != -INFINITY;
+            v[x] = counts ? -t.l[x] * 1.4426950408889634f : -INFINITY;
+            last[x] = counts ? t.len + p.by_g(t.i * p.tile_rows + c) : -1;
+            plain &= c >= p.tile_rows || last[x] >= (t.j + 1) * T::KB - 1;
+        }
+        const uint32_t r = g % T::LR;
+        if (!warp_wait_phase(bar(T::B_LEMPTY + r), ((g / T::LR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
+        plain = __all_sync(0xffffffffu, plain);
+        float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
+        int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            ls[x * 32 + lane] = v[x];
+            la[x * 32 + lane] = plain ? 0x7fffffff : last[x];
+        }
+        ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
+        ++g;
+        return true;
+    };
+    Tile a, b;
+    fetch(a);
+    fetch(b);
+    while (a.there) {
+        if (!finish(a)) return;
+        fetch(a);
+        if (!b.there) break;
+        if (!finish(b)) return;
+        fetch(b);
+    }
+}
+
+// The weights of 32 columns of a position's scores, added to two pairs of sums.
+template <bool MASKED>
+__device__ __forceinline__ void add32(const uint32_t (&s)[32], const float4* ls, const int4* la, int pos, uint64_t c2,
+                                      uint64_t& sum0, uint64_t& sum1) {
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+        const float4 l = ls[x / 4];
+        float a[4];
+        ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2,
+                                     ptx::pack_f32x2(l.x, l.y)), a[0], a[1]);
+        ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), c2,
+                                     ptx::pack_f32x2(l.z, l.w)), a[2], a[3]);
+        if constexpr (MASKED) {
+            const int4 t = la[x / 4];
+            a[0] = pos <= t.x ? a[0] : -INFINITY;
+            a[1] = pos <= t.y ? a[1] : -INFINITY;
+            a[2] = pos <= t.z ? a[2] : -INFINITY;
+            a[3] = pos <= t.w ? a[3] : -INFINITY;
+        }
+        sum0 = ptx::fadd2(sum0, ptx::pack_f32x2(ptx::ex2(a[0]), ptx::ex2(a[1])));
+        sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
+    }
+}
+// Those of `cols` columns from s_addr: 32 are on their way while the 32 before are used.
+template <bool MASKED>
+__device__ __forceinline__ void take(uint32_t s_addr, int cols, const float4* ls, const int4* la, int pos, uint64_t c2,
+                                     uint64_t& sum0, uint64_t& sum1) {
+    uint32_t s[32], next[32];
+    ptx::tmem_ld32_issue(s_addr, s);
+    for (int c0 = 0; c0 < cols; c0 += 64) {
+        ptx::tmem_wait_ld();
+        ptx::reg_fence32(s);
+        if (c0 + 32 < cols) ptx::tmem_ld32_issue(s_addr + c0 + 32, next);
+        add32<MASKED>(s, ls + c0 / 4, la + c0 / 4, pos, c2, sum0, sum1);
+        if (c0 + 32 >= cols) break;
+        ptx::tmem_wait_ld();
+        ptx::reg_fence32(next);
+        if (c0 + 64 < cols) ptx::tmem_ld32_issue(s_addr + c0 + 64, s);
+        add32<MASKED>(next, ls + c0 / 4 + 8, la + c0 / 4 + 8, pos, c2, sum0, sum1);
+    }
 }
 
 template <int D>
 __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, uint32_t tmem, const Ctl& ctl) {
     using T = ScoreTile<D>;
-    constexpr int CW = T::CW;
+    static_assert(T::CW == 32, "a tensor memory load");
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int w = threadIdx.x / 32 - 4, lane = threadIdx.x % 32;
     const int quad = w % 4, half = w / 4 % T::KH, cg = w / 4 / T::KH;
@@ -403,53 +472,38 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
         if (cg == 0 && u.slot < 0 && p.decay != 0.f && pos < u.len) old = __ldcg(score) * p.decay;
         uint64_t sum0 = ptx::pack_f32x2(0.f, 0.f), sum1 = sum0;
         for (int i = u.i0; i < u.i1; ++i, ++g) {
-            const uint32_t r = g % T::SR, ph = (g / T::SR) & 1u;
-            if (!warp_wait_phase(bar(T::B_LFULL + r), ph, ctl, SITE_EPI_FULL)) return;
-            if (!warp_wait_phase(bar(T::B_SFULL + r), ph, ctl, SITE_S_FULL)) return;
-            ptx::tc_fence_after();
+            const uint32_t r = g % T::SR, lr = g % T::LR, full = bar(T::B_SFULL + r * T::KH + half);
+            if (!warp_wait_phase(bar(T::B_LFULL + lr), (g / T::LR) & 1u, ctl, SITE_EPI_FULL)) return;
             const uint32_t s_addr = tmem + lane_addr + (r * T::KH + half) * T::BR + cg * cols;
-            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (r * T::BR + cg * cols) * 4);
-            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (r * T::BR + cg * cols) * 4);
+            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (lr * T::BR + cg * cols) * 4);
+            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (lr * T::BR + cg * cols) * 4);
             const bool plain = la[0].x == 0x7fffffff;
-            for (int c0 = 0; c0 < cols; c0 += CW) {
-                uint32_t s[CW];
-                if constexpr (CW == 32) ptx::tmem_ld32(s_addr + c0, s);
-                else ptx::tmem_ld16(s_addr + c0, s);
-                if (c0 + CW == cols) ptx::tc_fence_before();
-#pragma unroll
-                for (int x = 0; x < CW; x += 4) {
-                    const float4 l = ls[(c0 + x) / 4];
-                    float a[4];
-                    ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2,
-                                                 ptx::pack_f32x2(l.x, l.y)), a[0], a[1]);
-                    ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), c2,
-                                                 ptx::pack_f32x2(l.z, l.w)), a[2], a[3]);
-                    if (!plain) {
-                        const int4 t = la[(c0 + x) / 4];
-                        a[0] = pos <= t.x ? a[0] : -INFINITY;
-                        a[1] = pos <= t.y ? a[1] : -INFINITY;
-                        a[2] = pos <= t.z ? a[2] : -INFINITY;
-                        a[3] = pos <= t.w ? a[3] : -INFINITY;
-                    }
-                    sum0 = ptx::fadd2(sum0, ptx::pack_f32x2(ptx::ex2(a[0]), ptx::ex2(a[1])));
-                    sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
-                }
-            }
-            ptx::mbar_arrive_warp(bar(T::B_SEMPTY + r));
+            if (!warp_wait_phase(full, (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
+            ptx::tc_fence_after();
+            // (all columns see all of the block, or comparisons: two loops, so that the
+            // first has none -- 6.9 instructions a weight in one loop with both)
+            if (plain) take<false>(s_addr, cols, ls, la, pos, c2, sum0, sum1);
+            else take<true>(s_addr, cols, ls, la, pos, c2, sum0, sum1);
+            ptx::tc_fence_before();
+            ptx::mbar_arrive_warp(bar(T::B_SEMPTY + r * T::KH + half));
+            ptx::mbar_arrive_warp(bar(T::B_LEMPTY + lr));
         }
         float s0, s1, s2, s3;
         ptx::unpack_f32x2(sum0, s0, s1);
         ptx::unpack_f32x2(sum1, s2, s3);
-        // the groups' sums, in order; the slot's parity and this wait keep a warp from
-        // writing where another has not read yet
-        float* mine = sums + (n & 1u) * T::NCG * T::KB + key;
-        mine[cg * T::KB] = (s0 + s1) + (s2 + s3);
-        ptx::mbar_arrive_warp(bar(T::B_SUM + (n & 1u)));
-        if (!warp_wait_phase(bar(T::B_SUM + (n & 1u)), (n >> 1) & 1u, ctl, SITE_MAX_XCHG)) return;
-        if (cg == 0) {
-            float all = mine[0];
+        float all = (s0 + s1) + (s2 + s3);
+        if constexpr (T::NCG > 1) {
+            // the groups' sums, in order; the slot's parity and this wait keep a warp from
+            // writing where another has not read yet
+            float* mine = sums + (n & 1u) * T::NCG * T::KB + key;
+            mine[cg * T::KB] = all;
+            ptx::mbar_arrive_warp(bar(T::B_SUM + (n & 1u)));
+            if (!warp_wait_phase(bar(T::B_SUM + (n & 1u)), (n >> 1) & 1u, ctl, SITE_MAX_XCHG)) return;
+            all = mine[0];
 #pragma unroll
             for (int x = 1; x < T::NCG; ++x) all += mine[x * T::KB];
+        }
+        if (cg == 0) {
             if (u.slot >= 0) p.parts[(int64_t)u.slot * T::KB + key] = all;
             else if (pos < u.len + u.nl) *score = old + all;
         }
