@@ -12,12 +12,14 @@
 // workspace, and fa_score_merge_kernel joins them in order.
 //
 // Roles: warp 0 walks the range, hands the units on and loads K through the block table
-// (a lane a box of rows); warp 1 issues the products; warp 2 stages the lse; warp 3 loads
-// Q; eight warps take the exponentials: a quarter of the lanes each (a warp reaches only
-// its own quarter of tensor memory), of one half of the positions (D = 256: of a group of
-// columns).
+// (a lane a box of rows) and Q; warps 1 and 3 issue the products of a half of the positions
+// each (one thread's instructions took longer than the products); warp 2 stages the lse;
+// sixteen warps take the exponentials: a quarter of the lanes each (a warp reaches only its
+// own quarter of tensor memory), of one half of the positions, of a group of columns.
 // Every wait is bounded as in fa_fwd_kernel.cuh.
 #pragma once
+
+#include <climits>
 
 #include "fa_fwd_kernel.cuh"
 #include "fa_score_sched.cuh"
@@ -40,32 +42,29 @@ struct ScoreTile {
     static constexpr int K_STAGES = 2;
     static constexpr int Q_STAGES = D >= 128 ? 2 : 4;
     static constexpr int SR = 512 / (KH * BR) < 4 ? 512 / (KH * BR) : 4;  // score slots in tensor memory
-    static constexpr int WARPS = 8;                      // of the exponentials
-    static constexpr int LR = 4;                         // lse slots
+    static constexpr int WARPS = 16;                     // of the exponentials
     static constexpr int NCG = WARPS / 4 / KH;           // column groups
-    static constexpr int CW = 32;                        // columns a thread takes at a time
+    static constexpr int CW = 16;                        // columns a thread takes at a time
     static constexpr int THREADS = 32 * (4 + WARPS);
     static constexpr int SEGS = 4;
     static constexpr int OFF_K = 0;
     static constexpr int OFF_Q = OFF_K + K_STAGES * K_BYTES;
-    static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;      // [LR][BR] -lse log2 e
-    static constexpr int OFF_LAST = OFF_LSE + LR * BR * 4;          // [LR][BR] last position seen
-    static constexpr int OFF_SUM = OFF_LAST + LR * BR * 4;          // [2][NCG][KB]
+    static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;      // [SR][BR] -lse log2 e
+    static constexpr int OFF_LAST = OFF_LSE + SR * BR * 4;          // [SR][BR] last position seen
+    static constexpr int OFF_SUM = OFF_LAST + SR * BR * 4;          // [2][NCG][KB]
     static constexpr int OFF_SEG = OFF_SUM + 2 * NCG * KB * 4;
     static constexpr int OFF_BAR = OFF_SEG + SEGS * 48;
     static constexpr int B_KFULL = 0;
     static constexpr int B_KEMPTY = B_KFULL + K_STAGES;
     static constexpr int B_QFULL = B_KEMPTY + K_STAGES;
     static constexpr int B_QEMPTY = B_QFULL + Q_STAGES;
-    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // [SR][KH] product done (commit)
-    static constexpr int B_SEMPTY = B_SFULL + SR * KH;    // [SR][KH] scores read (its warps)
-    static constexpr int B_LFULL = B_SEMPTY + SR * KH;    // [LR] lse staged
-    static constexpr int B_LEMPTY = B_LFULL + LR;         // [LR] lse read (every warp)
-    static constexpr int B_SEGFULL = B_LEMPTY + LR;
+    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // [SR][KH] product done (commit), lse staged
+    static constexpr int B_SEMPTY = B_SFULL + SR * KH;    // [SR][KH] scores and lse read (its warps)
+    static constexpr int B_SEGFULL = B_SEMPTY + SR * KH;
     static constexpr int B_SEGFREE = B_SEGFULL + SEGS;
     static constexpr int B_SUM = B_SEGFREE + SEGS;        // [2] the groups' sums are there
-    static constexpr int B_DRAIN = B_SUM + 2;
-    static constexpr int NUM_BARS = B_DRAIN + 1;
+    static constexpr int B_DRAIN = B_SUM + 2;             // [KH]
+    static constexpr int NUM_BARS = B_DRAIN + KH;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_USED = OFF_MISC + 16;
     // >= 120 KB keeps one CTA per SM, so no CTA ever waits on another's TMEM
@@ -74,8 +73,9 @@ struct ScoreTile {
     static_assert(SR * KH * BR <= 512, "tensor memory budget");
     static __device__ __forceinline__ uint32_t bar_count(int i) {
         if (i >= B_SEMPTY && i < B_SEMPTY + SR * KH) return WARPS / KH;
-        if (i >= B_LEMPTY && i < B_LEMPTY + LR) return WARPS;
-        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 3 + WARPS;
+        if (i >= B_SFULL && i < B_SFULL + SR * KH) return 2;
+        if ((i >= B_KEMPTY && i < B_KEMPTY + K_STAGES) || (i >= B_QEMPTY && i < B_QEMPTY + Q_STAGES)) return KH;
+        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 1 + KH + WARPS;
         if (i >= B_SUM && i < B_SUM + 2) return WARPS;
         return 1;
     }
@@ -100,7 +100,7 @@ struct Shape {
         lag = (s.len + p.tokens - 1) >> p.token_shift;
         if (s.nl == 0) {
             nt = 1;                       // only the scores so far
-            lag = 0x7fffffff;
+            lag = INT_MAX;
             if (p.decay == 1.f) nb = 0;   // which stay as they are
         }
     }
@@ -197,16 +197,18 @@ __device__ __forceinline__ bool get(volatile const int* ring, Unit& u, uint32_t 
     return u.i1 > 0;
 }
 
+// A tile's Q is loaded unless it is the one before (blocks of a head whose rows are one tile).
 template <int D>
-__device__ void walk_and_load_k(const CUtensorMap* tmK, const ScoreParams& p, ScoreWalk<D> walk, volatile int* ring,
-                                uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
+__device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, const ScoreParams& p, ScoreWalk<D> walk,
+                              volatile int* ring, uint32_t sbase, uint32_t bar0, const Ctl& ctl) {
     using T = ScoreTile<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int lane = threadIdx.x % 32;
     // K passes once where all rows are one tile; else the units of a head are not far apart
-    const uint64_t policy = ptx::policy_evict_first();
-    uint32_t n = 0, ki = 0;
+    const uint64_t policy = ptx::policy_evict_first(), policy_q = ptx::policy_evict_last();
+    uint32_t n = 0, ki = 0, qi = 0;
     bool ok = true, withheld = false, have = true;
+    int z = -1, hk = -1, tile = -1;  // of the last Q
     while (ok && have) {
         Unit u{};
         have = walk.next(p, u);
@@ -247,46 +249,34 @@ __device__ void walk_and_load_k(const CUtensorMap* tmK, const ScoreParams& p, Sc
             }
         }
         ++ki;
-    }
-    if (!ok)
-        for (uint32_t i = ki > (uint32_t)T::K_STAGES ? ki - T::K_STAGES : 0; i < ki; ++i)
-            drain_phase(bar(T::B_KFULL + i % T::K_STAGES), (i / T::K_STAGES) & 1u, withheld ? ctl.limit_ns / 64 : ctl.limit_ns);
-}
-
-// A tile's Q is loaded unless it is the one before (blocks of a head whose rows are one tile).
-template <int D>
-__device__ void load_q(const CUtensorMap* tmQ, const ScoreParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0,
-                       const Ctl& ctl) {
-    using T = ScoreTile<D>;
-    auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    const uint64_t policy = ptx::policy_evict_last();
-    uint32_t qi = 0;
-    bool ok = true;
-    int z = -1, hk = -1, tile = -1;
-    Unit u;
-    for (uint32_t n = 0; get<D, false>(ring, u, n, bar, ctl, ok); ++n) {
         for (int i = u.i0; i < u.i1; ++i) {
             if (z == u.z && hk == u.hk && tile == i) continue;
             z = u.z, hk = u.hk, tile = i;
-            const uint32_t s = qi % T::Q_STAGES, ph = (qi / T::Q_STAGES) & 1u;
-            if (!wait_phase(bar(T::B_QEMPTY + s), ph ^ 1u, ctl, SITE_Q_EMPTY)) { ok = false; break; }
-            ptx::mbar_arrive_expect_tx(bar(T::B_QFULL + s), (uint32_t)p.tile_rows * T::SW * T::NCHUNK);
-            const uint32_t dst = sbase + T::OFF_Q + s * T::Q_BYTES;
-            for (int c = 0; c < T::NCHUNK; ++c)
-                ptx::tma_load_4d(dst + c * (T::BR * T::SW), tmQ, bar(T::B_QFULL + s), c * T::SWE, u.hk * p.G,
-                                 i << p.token_shift, u.z, policy);
+            const uint32_t qs = qi % T::Q_STAGES;
+            if (!warp_wait_phase(bar(T::B_QEMPTY + qs), ((qi / T::Q_STAGES) & 1u) ^ 1u, ctl, SITE_Q_EMPTY)) { ok = false; break; }
+            if (lane == 0) {
+                ptx::mbar_arrive_expect_tx(bar(T::B_QFULL + qs), (uint32_t)p.tile_rows * T::SW * T::NCHUNK);
+                const uint32_t dst = sbase + T::OFF_Q + qs * T::Q_BYTES;
+                for (int c = 0; c < T::NCHUNK; ++c)
+                    ptx::tma_load_4d(dst + c * (T::BR * T::SW), tmQ, bar(T::B_QFULL + qs), c * T::SWE, u.hk * p.G,
+                                     i << p.token_shift, u.z, policy_q);
+            }
+            __syncwarp();
             ++qi;
         }
-        if (!ok) break;
     }
-    if (!ok)
+    if (!ok) {
         for (uint32_t i = qi > (uint32_t)T::Q_STAGES ? qi - T::Q_STAGES : 0; i < qi; ++i)
             drain_phase(bar(T::B_QFULL + i % T::Q_STAGES), (i / T::Q_STAGES) & 1u, ctl.limit_ns);
+        for (uint32_t i = ki > (uint32_t)T::K_STAGES ? ki - T::K_STAGES : 0; i < ki; ++i)
+            drain_phase(bar(T::B_KFULL + i % T::K_STAGES), (i / T::K_STAGES) & 1u, withheld ? ctl.limit_ns / 64 : ctl.limit_ns);
+    }
 }
 
+// The products of one half of a unit's positions.
 template <int D, bool BF16>
 __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
-                         const Ctl& ctl) {
+                         int half, const Ctl& ctl) {
     using T = ScoreTile<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const uint32_t IDESC = ptx::idesc_f16(128, p.tile_cols, BF16, false, false);
@@ -309,21 +299,17 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
             if (i == u.i0 && !wait_phase(bar(T::B_KFULL + ks), (n / T::K_STAGES) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
             const uint32_t r = g % T::SR;
             const uint32_t q_lo = q_lo0 + ((qi - 1) % T::Q_STAGES) * (T::Q_BYTES >> 4);
+            if (!wait_phase(bar(T::B_SEMPTY + r * T::KH + half), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
+            ptx::tc_fence_after();
+            const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + half * T::HALF_BYTES) >> 4);
+            const uint32_t d = tmem + (r * T::KH + half) * T::BR;
 #pragma unroll
-            for (int h = 0; h < T::KH; ++h) {
-                if (!wait_phase(bar(T::B_SEMPTY + r * T::KH + h), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
-                ptx::tc_fence_after();
-                const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + h * T::HALF_BYTES) >> 4);
-                const uint32_t d = tmem + (r * T::KH + h) * T::BR;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
-                    ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
-                                ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
-                }
-                ptx::tc_commit(bar(T::B_SFULL + r * T::KH + h));
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
+                ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
+                            ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
             }
-            if (!ok) break;
+            ptx::tc_commit(bar(T::B_SFULL + r * T::KH + half));
             if (i + 1 < u.i1) {  // another tile follows for certain
                 ptx::tc_commit(bar(T::B_QEMPTY + (qi - 1) % T::Q_STAGES));
                 held = false;
@@ -333,8 +319,8 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
         ptx::tc_commit(bar(T::B_KEMPTY + ks));
     }
     if (!ok) {
-        ptx::tc_commit(bar(T::B_DRAIN));
-        drain_phase(bar(T::B_DRAIN), 0u, ctl.limit_ns);
+        ptx::tc_commit(bar(T::B_DRAIN + half));
+        drain_phase(bar(T::B_DRAIN + half), 0u, ctl.limit_ns);
     }
 }
 
@@ -353,45 +339,60 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
         int j, i, len;
         bool there;
     };
+    // this lane's columns: row c of a tile is head c % G of token c / G
+    int tok[N];
+    int64_t off[N];
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+        const int c = x * 32 + lane;
+        tok[x] = c < p.tile_rows ? p.by_g(c) : INT_MAX;
+        off[x] = c < p.tile_rows ? (int64_t)(c - tok[x] * p.G) * p.T + tok[x] : 0;
+    }
     uint32_t n = 0, g = 0;
     bool ok = true;
     Unit u{};
-    u.i0 = u.i1 = 0;
+    const float* from = p.lse;
     auto fetch = [&](Tile& t) {
-        t.there = ok && (u.i0 < u.i1 || (n == 0 || u.i1 > 0 ? get<D, true>(ring, u, n++, bar, ctl, ok) : false));
-        if (!t.there) return;
+        if (u.i0 == u.i1) {
+            t.there = ok && (n == 0 || u.i1 > 0) && get<D, true>(ring, u, n++, bar, ctl, ok);
+            if (!t.there) return;
+            from = p.lse + ((int64_t)u.z * p.Hq + u.hk * p.G) * p.T;
+        }
+        t.there = true;
         t.j = u.j, t.i = u.i0++, t.len = u.len;
-        const int row0 = t.i * p.tile_rows, rows = u.nl * p.G;
+        const int t0 = t.i << p.token_shift, left = u.nl - t0;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-            const int c = x * 32 + lane, row = row0 + c, tok = p.by_g(row), h = u.hk * p.G + row - tok * p.G;
             t.l[x] = -INFINITY;
-            if (c < p.tile_rows && row < rows) t.l[x] = __ldcg(p.lse + ((int64_t)u.z * p.Hq + h) * p.T + tok);
+            if (tok[x] < left) t.l[x] = __ldcg(from + off[x] + t0);
         }
     };
     auto finish = [&](const Tile& t) -> bool {
         float v[N];
         int last[N];
         bool plain = true;
+        const int last0 = t.len + (t.i << p.token_shift), need = (t.j + 1) * T::KB - 1;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-            const int c = x * 32 + lane;
             const bool counts = t.l[x] != -INFINITY;
             v[x] = counts ? -t.l[x] * 1.4426950408889634f : -INFINITY;
-            last[x] = counts ? t.len + p.by_g(t.i * p.tile_rows + c) : -1;
-            plain &= c >= p.tile_rows || last[x] >= (t.j + 1) * T::KB - 1;
+            last[x] = counts ? last0 + tok[x] : -1;
+            plain &= tok[x] == INT_MAX || last[x] >= need;
         }
-        const uint32_t r = g % T::LR;
-        if (!warp_wait_phase(bar(T::B_LEMPTY + r), ((g / T::LR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
         plain = __all_sync(0xffffffffu, plain);
+        const uint32_t r = g % T::SR;
+#pragma unroll
+        for (int h = 0; h < T::KH; ++h)
+            if (!warp_wait_phase(bar(T::B_SEMPTY + r * T::KH + h), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
         float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
         int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
             ls[x * 32 + lane] = v[x];
-            la[x * 32 + lane] = plain ? 0x7fffffff : last[x];
+            la[x * 32 + lane] = plain ? INT_MAX : last[x];
         }
-        ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
+        __syncwarp();
+        if (lane < T::KH) ptx::mbar_arrive(bar(T::B_SFULL + r * T::KH + lane));
         ++g;
         return true;
     };
@@ -407,12 +408,12 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
     }
 }
 
-// The weights of 32 columns of a position's scores, added to two pairs of sums.
+// The weights of 16 columns of a position's scores, added to two pairs of sums.
 template <bool MASKED>
-__device__ __forceinline__ void add32(const uint32_t (&s)[32], const float4* ls, const int4* la, int pos, uint64_t c2,
+__device__ __forceinline__ void add16(const uint32_t (&s)[16], const float4* ls, const int4* la, int pos, uint64_t c2,
                                       uint64_t& sum0, uint64_t& sum1) {
 #pragma unroll
-    for (int x = 0; x < 32; x += 4) {
+    for (int x = 0; x < 16; x += 4) {
         const float4 l = ls[x / 4];
         float a[4];
         ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2,
@@ -430,29 +431,29 @@ __device__ __forceinline__ void add32(const uint32_t (&s)[32], const float4* ls,
         sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
     }
 }
-// Those of `cols` columns from s_addr: 32 are on their way while the 32 before are used.
+// Those of `cols` columns from s_addr: 16 are on their way while the 16 before are used.
 template <bool MASKED>
 __device__ __forceinline__ void take(uint32_t s_addr, int cols, const float4* ls, const int4* la, int pos, uint64_t c2,
                                      uint64_t& sum0, uint64_t& sum1) {
-    uint32_t s[32], next[32];
-    ptx::tmem_ld32_issue(s_addr, s);
-    for (int c0 = 0; c0 < cols; c0 += 64) {
+    uint32_t s[16], next[16];
+    ptx::tmem_ld16_issue(s_addr, s);
+    for (int c0 = 0; c0 < cols; c0 += 32) {
         ptx::tmem_wait_ld();
-        ptx::reg_fence32(s);
-        if (c0 + 32 < cols) ptx::tmem_ld32_issue(s_addr + c0 + 32, next);
-        add32<MASKED>(s, ls + c0 / 4, la + c0 / 4, pos, c2, sum0, sum1);
-        if (c0 + 32 >= cols) break;
+        ptx::reg_fence16(s);
+        if (c0 + 16 < cols) ptx::tmem_ld16_issue(s_addr + c0 + 16, next);
+        add16<MASKED>(s, ls + c0 / 4, la + c0 / 4, pos, c2, sum0, sum1);
+        if (c0 + 16 >= cols) break;
         ptx::tmem_wait_ld();
-        ptx::reg_fence32(next);
-        if (c0 + 64 < cols) ptx::tmem_ld32_issue(s_addr + c0 + 64, s);
-        add32<MASKED>(next, ls + c0 / 4 + 8, la + c0 / 4 + 8, pos, c2, sum0, sum1);
+        ptx::reg_fence16(next);
+        if (c0 + 32 < cols) ptx::tmem_ld16_issue(s_addr + c0 + 32, s);
+        add16<MASKED>(next, ls + c0 / 4 + 4, la + c0 / 4 + 4, pos, c2, sum0, sum1);
     }
 }
 
 template <int D>
 __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, uint32_t tmem, const Ctl& ctl) {
     using T = ScoreTile<D>;
-    static_assert(T::CW == 32, "a tensor memory load");
+    static_assert(T::CW == 16, "a tensor memory load");
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int w = threadIdx.x / 32 - 4, lane = threadIdx.x % 32;
     const int quad = w % 4, half = w / 4 % T::KH, cg = w / 4 / T::KH;
@@ -472,21 +473,19 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
         if (cg == 0 && u.slot < 0 && p.decay != 0.f && pos < u.len) old = __ldcg(score) * p.decay;
         uint64_t sum0 = ptx::pack_f32x2(0.f, 0.f), sum1 = sum0;
         for (int i = u.i0; i < u.i1; ++i, ++g) {
-            const uint32_t r = g % T::SR, lr = g % T::LR, full = bar(T::B_SFULL + r * T::KH + half);
-            if (!warp_wait_phase(bar(T::B_LFULL + lr), (g / T::LR) & 1u, ctl, SITE_EPI_FULL)) return;
+            const uint32_t r = g % T::SR;
             const uint32_t s_addr = tmem + lane_addr + (r * T::KH + half) * T::BR + cg * cols;
-            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (lr * T::BR + cg * cols) * 4);
-            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (lr * T::BR + cg * cols) * 4);
-            const bool plain = la[0].x == 0x7fffffff;
-            if (!warp_wait_phase(full, (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
+            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (r * T::BR + cg * cols) * 4);
+            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (r * T::BR + cg * cols) * 4);
+            if (!warp_wait_phase(bar(T::B_SFULL + r * T::KH + half), (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
             ptx::tc_fence_after();
+            const bool plain = la[0].x == INT_MAX;
             // (all columns see all of the block, or comparisons: two loops, so that the
             // first has none -- 6.9 instructions a weight in one loop with both)
             if (plain) take<false>(s_addr, cols, ls, la, pos, c2, sum0, sum1);
             else take<true>(s_addr, cols, ls, la, pos, c2, sum0, sum1);
             ptx::tc_fence_before();
             ptx::mbar_arrive_warp(bar(T::B_SEMPTY + r * T::KH + half));
-            ptx::mbar_arrive_warp(bar(T::B_LEMPTY + lr));
         }
         float s0, s1, s2, s3;
         ptx::unpack_f32x2(sum0, s0, s1);
@@ -575,10 +574,9 @@ __global__ void __launch_bounds__(ScoreTile<D>::THREADS, 1)
     }
     if (p.Z > 32) __syncthreads();
 
-    if (warp == 0) scoret::walk_and_load_k<D>(&tmK, p, walk, ring, sbase, bar0, ctl);
-    else if (warp == 1) { if (lane == 0) scoret::multiply<D, BF16>(p, ring, sbase, bar0, tmem, ctl); }
+    if (warp == 0) scoret::walk_and_load<D>(&tmQ, &tmK, p, walk, ring, sbase, bar0, ctl);
     else if (warp == 2) scoret::stage_lse<D>(p, ring, smem, bar0, ctl);
-    else if (warp == 3) { if (lane == 0) scoret::load_q<D>(&tmQ, p, ring, sbase, bar0, ctl); }
+    else if (warp < 4) { if (lane == 0 && warp / 2 < T::KH) scoret::multiply<D, BF16>(p, ring, sbase, bar0, tmem, warp / 2, ctl); }
     else scoret::weigh<D>(p, ring, smem, bar0, tmem, ctl);
 
     ptx::tc_fence_before();
