@@ -243,7 +243,7 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
         while (G << (p.token_shift + 1) <= tile.rows) ++p.token_shift;
         p.tokens = 1 << p.token_shift;
         p.tile_rows = p.tokens * G;
-        p.tile_cols = (int)cdiv(p.tile_rows, tile.step) * tile.step;
+        p.tile_cols = (int)cdiv(p.tile_rows, 16) * 16;
         p.box_rows = fa::paged_box_rows(c.page_size, 128);
         const fa::PagedMapDim dq[3] = {{x.Hq, x.sq.h, G}, {x.T, x.sq.n, p.tokens}, {c.Z, x.sq.b, 1}};
         const fa::PagedMapDim dk[3] = {{c.page_size, c.sk.n, p.box_rows}, {c.Hkv, c.sk.h, 1}, {c.P, c.sk.b, 1}};

@@ -29,7 +29,7 @@ struct ScoreParams {
     int workers;               // rows kernel: warps of the launch
     // tile kernel
     int tokens, token_shift;   // new tokens of a tile (a power of two), its log2
-    int tile_rows, tile_cols;  // tokens * G, and as many as the products have
+    int tile_rows, tile_cols;  // tokens * G, and that rounded up to 16
     int box_rows;              // positions a TMA box holds
     float* parts;              // two slots of sums a CTA, or nullptr: no unit is cut
     void* cuts;
@@ -47,12 +47,11 @@ struct ScoreLaunch {
     cudaStream_t stream;
 };
 
-// Facts of the tile kernel: query rows of a tile, positions of a unit, columns that its
-// products come in steps of.
+// Facts of the tile kernel: query rows of a tile, positions of a unit.
 struct ScoreTileFacts {
-    int rows, block, step;
+    int rows, block;
 };
-constexpr ScoreTileFacts score_tile_facts(int D) { return D == 256 ? ScoreTileFacts{64, 128, 64} : ScoreTileFacts{128, 256, 64}; }
+constexpr ScoreTileFacts score_tile_facts(int D) { return D == 256 ? ScoreTileFacts{64, 128} : ScoreTileFacts{128, 256}; }
 // Workspace: two slots of a unit's sums, and where its range starts, a CTA.
 constexpr size_t score_slot_bytes(int sms) { return (size_t)sms * 2 * 256 * sizeof(float); }
 constexpr size_t score_workspace_bytes(int sms) { return score_slot_bytes(sms) + (size_t)sms * 48; }

@@ -25,8 +25,8 @@ static cudaError_t launch_rows(const ScoreLaunch& a) {
 template <bool BF16>
 static cudaError_t launch_tiles(const ScoreLaunch& a) {
     using T = ScoreTile<FA_HEAD_DIM>;
-    static_assert(T::BR == score_tile_facts(FA_HEAD_DIM).rows && T::KB == score_tile_facts(FA_HEAD_DIM).block &&
-                  T::NCG * T::CW <= score_tile_facts(FA_HEAD_DIM).step, "the host's facts");
+    static_assert(T::BR == score_tile_facts(FA_HEAD_DIM).rows && T::KB == score_tile_facts(FA_HEAD_DIM).block,
+                  "the host's facts");
     static_assert(sizeof(scoret::Cut) == 48 && T::KB <= 256, "workspace");
     auto kernel = fa_score_tile_kernel<FA_HEAD_DIM, BF16>;
     static std::atomic<uint64_t> configured{0};  // context the opt-in shared memory size was set in

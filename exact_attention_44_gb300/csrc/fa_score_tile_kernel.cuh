@@ -4,16 +4,21 @@
 // Sᵀ = K Qᵀ on tcgen05 with the positions as the rows of the product, so that a position
 // is a lane of tensor memory and one thread's: the weights that it receives are summed in
 // that thread's registers, tile after tile of query rows, and nothing is exchanged until
-// the position's tiles are done.  A query row's lse is a column's, read from shared memory
-// as a broadcast.  A unit of work is a block of KB positions of one (sequence, kv head):
+// the position's tiles are done.  A query row's lse belongs to a column, so every thread
+// would need every lse; read from shared memory as broadcasts they took as long as the
+// exponentials (both return 128 bytes a cycle to an SM's registers), so -lse / scale goes
+// into the product: as three 16-bit pieces, 24 bits and more, against three constants, in
+// one more step of 16 of the contraction, the last one (its rounding then is that of the
+// result).  A unit of work is a block of KB positions of one (sequence, kv head):
 // its K stays in shared memory while the tiles of up to BR query rows that see it stream
 // by.  Units are laid end to end, counted in tiles, and cut into one equal range a CTA
 // (fa_score_sched.cuh); a unit that a cut crosses leaves its sums in slots of the
 // workspace, and fa_score_merge_kernel joins them in order.
 //
 // Roles: warp 0 walks the range, hands the units on and loads K through the block table
-// (a lane a box of rows) and Q; warps 1 and 3 issue the products of a half of the positions
-// each (one thread's instructions took longer than the products); warp 2 stages the lse;
+// (a lane a box of rows) and Q; warps 1 and 3 issue the products of every second tile each
+// (a thread's waits in front of a tile take as long as the tile's products, and the tensor
+// cores' queue does not reach across them); warp 2 stages the lse;
 // sixteen warps take the exponentials: a quarter of the lanes each (a warp reaches only its
 // own quarter of tensor memory), of one half of the positions, of a group of columns.
 // Every wait is bounded as in fa_fwd_kernel.cuh.
@@ -43,28 +48,33 @@ struct ScoreTile {
     static constexpr int Q_STAGES = D >= 128 ? 2 : 4;
     static constexpr int SR = 512 / (KH * BR) < 4 ? 512 / (KH * BR) : 4;  // score slots in tensor memory
     static constexpr int WARPS = 16;                     // of the exponentials
+    static constexpr int LR = 4;                         // lse slots
     static constexpr int NCG = WARPS / 4 / KH;           // column groups
-    static constexpr int CW = 16;                        // columns a thread takes at a time
     static constexpr int THREADS = 32 * (4 + WARPS);
     static constexpr int SEGS = 4;
     static constexpr int OFF_K = 0;
     static constexpr int OFF_Q = OFF_K + K_STAGES * K_BYTES;
-    static constexpr int OFF_LSE = OFF_Q + Q_STAGES * Q_BYTES;      // [SR][BR] -lse log2 e
-    static constexpr int OFF_LAST = OFF_LSE + SR * BR * 4;          // [SR][BR] last position seen
-    static constexpr int OFF_SUM = OFF_LAST + SR * BR * 4;          // [2][NCG][KB]
+    static constexpr int QL_BYTES = BR * 32;
+    static constexpr int OFF_KL = OFF_Q + Q_STAGES * Q_BYTES;       // [128] the constants of the lse step
+    static constexpr int OFF_QL = OFF_KL + 128 * 32;                // [LR][BR] the pieces of -lse / scale
+    static constexpr int OFF_LSE = OFF_QL + LR * QL_BYTES;          // [LR][BR] -lse log2 e, where it has no pieces
+    static constexpr int OFF_LAST = OFF_LSE + LR * BR * 4;          // [LR][BR] last position seen
+    static constexpr int OFF_SUM = OFF_LAST + LR * BR * 4;          // [2][NCG][KB]
     static constexpr int OFF_SEG = OFF_SUM + 2 * NCG * KB * 4;
     static constexpr int OFF_BAR = OFF_SEG + SEGS * 48;
     static constexpr int B_KFULL = 0;
     static constexpr int B_KEMPTY = B_KFULL + K_STAGES;
     static constexpr int B_QFULL = B_KEMPTY + K_STAGES;
     static constexpr int B_QEMPTY = B_QFULL + Q_STAGES;
-    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // [SR][KH] product done (commit), lse staged
-    static constexpr int B_SEMPTY = B_SFULL + SR * KH;    // [SR][KH] scores and lse read (its warps)
-    static constexpr int B_SEGFULL = B_SEMPTY + SR * KH;
+    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // [SR][KH] product done (commit), lse staged (its issuer)
+    static constexpr int B_SEMPTY = B_SFULL + SR * KH;    // [SR][KH] scores read (its warps)
+    static constexpr int B_LFULL = B_SEMPTY + SR * KH;    // [LR] lse staged
+    static constexpr int B_LEMPTY = B_LFULL + LR;         // [LR] lse used (every warp)
+    static constexpr int B_SEGFULL = B_LEMPTY + LR;
     static constexpr int B_SEGFREE = B_SEGFULL + SEGS;
     static constexpr int B_SUM = B_SEGFREE + SEGS;        // [2] the groups' sums are there
-    static constexpr int B_DRAIN = B_SUM + 2;             // [KH]
-    static constexpr int NUM_BARS = B_DRAIN + KH;
+    static constexpr int B_DRAIN = B_SUM + 2;             // [2] issuers
+    static constexpr int NUM_BARS = B_DRAIN + 2;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_USED = OFF_MISC + 16;
     // >= 120 KB keeps one CTA per SM, so no CTA ever waits on another's TMEM
@@ -74,8 +84,9 @@ struct ScoreTile {
     static __device__ __forceinline__ uint32_t bar_count(int i) {
         if (i >= B_SEMPTY && i < B_SEMPTY + SR * KH) return WARPS / KH;
         if (i >= B_SFULL && i < B_SFULL + SR * KH) return 2;
-        if ((i >= B_KEMPTY && i < B_KEMPTY + K_STAGES) || (i >= B_QEMPTY && i < B_QEMPTY + Q_STAGES)) return KH;
-        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 1 + KH + WARPS;
+        if (i >= B_LEMPTY && i < B_LEMPTY + LR) return WARPS;
+        if ((i >= B_KEMPTY && i < B_KEMPTY + K_STAGES) || (i >= B_QEMPTY && i < B_QEMPTY + Q_STAGES)) return 2;  // issuers
+        if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 3 + WARPS;
         if (i >= B_SUM && i < B_SUM + 2) return WARPS;
         return 1;
     }
@@ -86,6 +97,7 @@ namespace scoret {
 // A unit's part in a range: tiles i0 .. i1 - 1 of those that see its block.
 struct Unit {
     int z, hk, j, i0, i1, slot, len, nl;  // i1 = 0: the end; slot -1: all of the unit's tiles
+    int keep;                             // the next unit starts with the Q tile that this one ends with
 };
 
 // Tiles of a sequence's rows, and which of them is the first that sees block j: the one
@@ -177,7 +189,7 @@ __device__ __forceinline__ void put(volatile int* ring, const Unit& u, uint32_t 
     using T = ScoreTile<D>;
     volatile int* s = ring + (n % T::SEGS) * 12;
     if (threadIdx.x % 32 == 0) {
-        s[0] = u.z, s[1] = u.hk, s[2] = u.j, s[3] = u.i0, s[4] = u.i1, s[5] = u.slot, s[6] = u.len, s[7] = u.nl;
+        s[0] = u.z, s[1] = u.hk, s[2] = u.j, s[3] = u.i0, s[4] = u.i1, s[5] = u.slot, s[6] = u.len, s[7] = u.nl, s[8] = u.keep;
         ptx::mbar_arrive(bar(T::B_SEGFULL + n % T::SEGS));
     }
     __syncwarp();
@@ -191,7 +203,7 @@ __device__ __forceinline__ bool get(volatile const int* ring, Unit& u, uint32_t 
     ok = WARP ? warp_wait_phase(full, parity, ctl, SITE_SEG_FULL) : wait_phase(full, parity, ctl, SITE_SEG_FULL);
     if (!ok) return false;
     volatile const int* s = ring + (n % T::SEGS) * 12;
-    u.z = s[0], u.hk = s[1], u.j = s[2], u.i0 = s[3], u.i1 = s[4], u.slot = s[5], u.len = s[6], u.nl = s[7];
+    u.z = s[0], u.hk = s[1], u.j = s[2], u.i0 = s[3], u.i1 = s[4], u.slot = s[5], u.len = s[6], u.nl = s[7], u.keep = s[8];
     if (WARP) __syncwarp();
     if (!WARP || threadIdx.x % 32 == 0) ptx::mbar_arrive(bar(T::B_SEGFREE + n % T::SEGS));
     return u.i1 > 0;
@@ -207,11 +219,12 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
     // K passes once where all rows are one tile; else the units of a head are not far apart
     const uint64_t policy = ptx::policy_evict_first(), policy_q = ptx::policy_evict_last();
     uint32_t n = 0, ki = 0, qi = 0;
-    bool ok = true, withheld = false, have = true;
-    int z = -1, hk = -1, tile = -1;  // of the last Q
-    while (ok && have) {
-        Unit u{};
-        have = walk.next(p, u);
+    bool ok = true, withheld = false, loaded = false;  // loaded: the unit's first Q tile is there
+    Unit u{}, after{};
+    bool have = walk.next(p, u);
+    while (ok) {
+        const bool more = have && walk.next(p, after);
+        u.keep = more && after.z == u.z && after.hk == u.hk && after.i0 == u.i1 - 1;
         if (n >= (uint32_t)T::SEGS &&
             !warp_wait_phase(bar(T::B_SEGFREE + n % T::SEGS), (n / T::SEGS - 1) & 1u, ctl, SITE_SEG_FREE)) {
             ok = false;
@@ -249,9 +262,7 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
             }
         }
         ++ki;
-        for (int i = u.i0; i < u.i1; ++i) {
-            if (z == u.z && hk == u.hk && tile == i) continue;
-            z = u.z, hk = u.hk, tile = i;
+        for (int i = u.i0 + (loaded ? 1 : 0); i < u.i1; ++i) {
             const uint32_t qs = qi % T::Q_STAGES;
             if (!warp_wait_phase(bar(T::B_QEMPTY + qs), ((qi / T::Q_STAGES) & 1u) ^ 1u, ctl, SITE_Q_EMPTY)) { ok = false; break; }
             if (lane == 0) {
@@ -264,6 +275,9 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
             __syncwarp();
             ++qi;
         }
+        loaded = u.keep;
+        u = after;
+        have = more;
     }
     if (!ok) {
         for (uint32_t i = qi > (uint32_t)T::Q_STAGES ? qi - T::Q_STAGES : 0; i < qi; ++i)
@@ -273,62 +287,99 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
     }
 }
 
-// The products of one half of a unit's positions.
+// The products of every second tile (issuer 0 or 1).  K and Q are released by both: a
+// commit waits for the products of its own thread only.
 template <int D, bool BF16>
 __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
-                         int half, const Ctl& ctl) {
+                         uint32_t issuer, const Ctl& ctl) {
     using T = ScoreTile<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const uint32_t IDESC = ptx::idesc_f16(128, p.tile_cols, BF16, false, false);
-    constexpr uint32_t HI = ptx::smem_desc_hi(8 * T::SW, T::SWIZZLE_CODE);
+    constexpr uint32_t HI = ptx::smem_desc_hi(8 * T::SW, T::SWIZZLE_CODE), HI_L = ptx::smem_desc_hi(8 * 32, 6);
     const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16), q_lo0 = ptx::smem_desc_lo(sbase + T::OFF_Q, 16);
+    const uint64_t kl = ptx::desc64(ptx::smem_desc_lo(sbase + T::OFF_KL, 16), HI_L);
+    const uint32_t ql_lo = ptx::smem_desc_lo(sbase + T::OFF_QL, 16);
     uint32_t g = 0, qi = 0;  // tiles, Q tiles
-    bool ok = true, held = false;  // held: a Q tile that the next unit may use again
-    int z = -1, hk = -1, tile = -1;
+    bool ok = true;
     Unit u;
     for (uint32_t n = 0; get<D, false>(ring, u, n, bar, ctl, ok); ++n) {
         const uint32_t ks = n % T::K_STAGES;
+        bool waited = false;  // for K
         for (int i = u.i0; i < u.i1; ++i, ++g) {
-            if (z != u.z || hk != u.hk || tile != i) {
-                if (held) ptx::tc_commit(bar(T::B_QEMPTY + (qi - 1) % T::Q_STAGES));
-                if (!wait_phase(bar(T::B_QFULL + qi % T::Q_STAGES), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
-                ++qi;
-                z = u.z, hk = u.hk, tile = i;
-                held = true;
-            }
-            if (i == u.i0 && !wait_phase(bar(T::B_KFULL + ks), (n / T::K_STAGES) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
-            const uint32_t r = g % T::SR;
-            const uint32_t q_lo = q_lo0 + ((qi - 1) % T::Q_STAGES) * (T::Q_BYTES >> 4);
-            if (!wait_phase(bar(T::B_SEMPTY + r * T::KH + half), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
-            ptx::tc_fence_after();
-            const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + half * T::HALF_BYTES) >> 4);
-            const uint32_t d = tmem + (r * T::KH + half) * T::BR;
+            const uint32_t qs = qi % T::Q_STAGES;
+            if ((g & 1u) == issuer) {
+                const uint32_t r = g % T::SR, lr = g % T::LR;
+                if (!waited && !wait_phase(bar(T::B_KFULL + ks), (n / T::K_STAGES) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
+                waited = true;
+                if (!wait_phase(bar(T::B_QFULL + qs), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
+                if (!wait_phase(bar(T::B_LFULL + lr), (g / T::LR) & 1u, ctl, SITE_EPI_FULL)) { ok = false; break; }
+                const uint32_t q_lo = q_lo0 + qs * (T::Q_BYTES >> 4);
+                const uint64_t ql = ptx::desc64(ql_lo + lr * (T::QL_BYTES >> 4), HI_L);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
-                ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
-                            ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
+                for (int h = 0; h < T::KH; ++h) {
+                    const uint32_t full = bar(T::B_SFULL + r * T::KH + h);
+                    if (!wait_phase(bar(T::B_SEMPTY + r * T::KH + h), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
+                    ptx::tc_fence_after();
+                    const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + h * T::HALF_BYTES) >> 4);
+                    const uint32_t d = tmem + (r * T::KH + h) * T::BR;
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
+                        ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
+                                    ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
+                    }
+                    ptx::mma_ss(d, kl, ql, IDESC, 1u);
+                    ptx::mbar_arrive(full);  // (hands on what stage_lse wrote)
+                    ptx::tc_commit(full);
+                }
+                if (!ok) break;
             }
-            ptx::tc_commit(bar(T::B_SFULL + r * T::KH + half));
-            if (i + 1 < u.i1) {  // another tile follows for certain
-                ptx::tc_commit(bar(T::B_QEMPTY + (qi - 1) % T::Q_STAGES));
-                held = false;
+            if (i + 1 < u.i1 || u.keep == 0) {
+                ptx::tc_commit(bar(T::B_QEMPTY + qs));
+                ++qi;
             }
         }
         if (!ok) break;
         ptx::tc_commit(bar(T::B_KEMPTY + ks));
     }
     if (!ok) {
-        ptx::tc_commit(bar(T::B_DRAIN + half));
-        drain_phase(bar(T::B_DRAIN + half), 0u, ctl.limit_ns);
+        ptx::tc_commit(bar(T::B_DRAIN + issuer));
+        drain_phase(bar(T::B_DRAIN + issuer), 0u, ctl.limit_ns);
     }
+}
+
+// The lse step of the contraction: 32 bytes a row, in the 32-byte swizzle's order; this is
+// where the first 16 of row r are (the others are zeros).
+__device__ __forceinline__ uint32_t l_piece(int r) { return (uint32_t)(r * 32 + (((r >> 2) & 1) << 4)); }
+// x as a + f b + f f c with 16-bit a, b, c: bf16 has fp32's range (f = 1); fp16 pieces keep
+// their magnitude (f = 2^-11).  {a | b << 16, c}
+template <bool BF16>
+__device__ __forceinline__ void split3(float x, uint32_t& w0, uint32_t& w1) {
+    if constexpr (BF16) {
+        const __nv_bfloat16 a = __float2bfloat16_rn(x);
+        const float r = x - __bfloat162float(a);
+        const __nv_bfloat16 b = __float2bfloat16_rn(r), c = __float2bfloat16_rn(r - __bfloat162float(b));
+        w0 = __bfloat16_as_ushort(a) | (uint32_t)__bfloat16_as_ushort(b) << 16;
+        w1 = __bfloat16_as_ushort(c);
+    } else {
+        const __half a = __float2half_rn(x);
+        const float r = (x - __half2float(a)) * 2048.f;
+        const __half b = __float2half_rn(r), c = __float2half_rn((r - __half2float(b)) * 2048.f);
+        w0 = __half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
+        w1 = __half_as_ushort(c);
+    }
+}
+template <bool BF16>
+__device__ __forceinline__ void constants3(uint32_t& w0, uint32_t& w1) {  // 1, f, f f
+    w0 = BF16 ? 0x3f803f80u : 0x10003c00u;
+    w1 = BF16 ? 0x3f80u : 0x0004u;
 }
 
 // Each tile's lse and the last position that each of its rows sees, a warp, the loads two
 // tiles ahead.  A row that does not count (no token, nothing seen) sees nothing; columns
 // behind the tile's rows are products with zeros.  A tile all of whose rows see all of the
-// block needs no comparisons.
-template <int D>
+// block, their lse in pieces, needs no comparisons.
+template <int D, bool BF16>
 __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, const Ctl& ctl) {
     using T = ScoreTile<D>;
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
@@ -369,30 +420,37 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
     };
     auto finish = [&](const Tile& t) -> bool {
         float v[N];
+        uint32_t w0[N], w1[N];
         int last[N];
-        bool plain = true;
+        bool plain = p.tile_rows == p.tile_cols;
         const int last0 = t.len + (t.i << p.token_shift), need = (t.j + 1) * T::KB - 1;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
             const bool counts = t.l[x] != -INFINITY;
-            v[x] = counts ? -t.l[x] * 1.4426950408889634f : -INFINITY;
             last[x] = counts ? last0 + tok[x] : -1;
-            plain &= tok[x] == INT_MAX || last[x] >= need;
+            // -lse / scale in three pieces, or (out of the type's range, infinite or NaN) not
+            const float q = -t.l[x] / p.scale;
+            const bool pieces = fabsf(q) <= (BF16 ? 1e38f : 60000.f);
+            w0[x] = w1[x] = 0u;
+            if (pieces) split3<BF16>(q, w0[x], w1[x]);
+            v[x] = pieces ? 0.f : -t.l[x] * 1.4426950408889634f;
+            plain &= tok[x] == INT_MAX || (pieces && last[x] >= need);
         }
         plain = __all_sync(0xffffffffu, plain);
-        const uint32_t r = g % T::SR;
-#pragma unroll
-        for (int h = 0; h < T::KH; ++h)
-            if (!warp_wait_phase(bar(T::B_SEMPTY + r * T::KH + h), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
+        const uint32_t r = g % T::LR;
+        if (!warp_wait_phase(bar(T::B_LEMPTY + r), ((g / T::LR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
         float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
         int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
+        const uint32_t ql = ptx::smem_addr(smem + T::OFF_QL) + r * T::QL_BYTES;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-            ls[x * 32 + lane] = v[x];
-            la[x * 32 + lane] = plain ? INT_MAX : last[x];
+            const int c = x * 32 + lane;
+            ptx::st_shared_v4(ql + l_piece(c), w0[x], w1[x], 0u, 0u);
+            ls[c] = v[x];
+            la[c] = plain ? INT_MAX : last[x];
         }
-        __syncwarp();
-        if (lane < T::KH) ptx::mbar_arrive(bar(T::B_SFULL + r * T::KH + lane));
+        ptx::fence_proxy_async_smem();
+        ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
         ++g;
         return true;
     };
@@ -409,51 +467,32 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
 }
 
 // The weights of 16 columns of a position's scores, added to two pairs of sums.
-template <bool MASKED>
 __device__ __forceinline__ void add16(const uint32_t (&s)[16], const float4* ls, const int4* la, int pos, uint64_t c2,
                                       uint64_t& sum0, uint64_t& sum1) {
 #pragma unroll
     for (int x = 0; x < 16; x += 4) {
         const float4 l = ls[x / 4];
+        const int4 t = la[x / 4];
         float a[4];
         ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2,
                                      ptx::pack_f32x2(l.x, l.y)), a[0], a[1]);
         ptx::unpack_f32x2(ptx::ffma2(ptx::pack_f32x2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), c2,
                                      ptx::pack_f32x2(l.z, l.w)), a[2], a[3]);
-        if constexpr (MASKED) {
-            const int4 t = la[x / 4];
-            a[0] = pos <= t.x ? a[0] : -INFINITY;
-            a[1] = pos <= t.y ? a[1] : -INFINITY;
-            a[2] = pos <= t.z ? a[2] : -INFINITY;
-            a[3] = pos <= t.w ? a[3] : -INFINITY;
-        }
+        a[0] = pos <= t.x ? a[0] : -INFINITY;
+        a[1] = pos <= t.y ? a[1] : -INFINITY;
+        a[2] = pos <= t.z ? a[2] : -INFINITY;
+        a[3] = pos <= t.w ? a[3] : -INFINITY;
         sum0 = ptx::fadd2(sum0, ptx::pack_f32x2(ptx::ex2(a[0]), ptx::ex2(a[1])));
         sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
     }
 }
-// Those of `cols` columns from s_addr: 16 are on their way while the 16 before are used.
-template <bool MASKED>
-__device__ __forceinline__ void take(uint32_t s_addr, int cols, const float4* ls, const int4* la, int pos, uint64_t c2,
-                                     uint64_t& sum0, uint64_t& sum1) {
-    uint32_t s[16], next[16];
-    ptx::tmem_ld16_issue(s_addr, s);
-    for (int c0 = 0; c0 < cols; c0 += 32) {
-        ptx::tmem_wait_ld();
-        ptx::reg_fence16(s);
-        if (c0 + 16 < cols) ptx::tmem_ld16_issue(s_addr + c0 + 16, next);
-        add16<MASKED>(s, ls + c0 / 4, la + c0 / 4, pos, c2, sum0, sum1);
-        if (c0 + 16 >= cols) break;
-        ptx::tmem_wait_ld();
-        ptx::reg_fence16(next);
-        if (c0 + 32 < cols) ptx::tmem_ld16_issue(s_addr + c0 + 32, s);
-        add16<MASKED>(next, ls + c0 / 4 + 4, la + c0 / 4 + 4, pos, c2, sum0, sum1);
-    }
-}
+__device__ __forceinline__ void load_scores(uint32_t s_addr, uint32_t (&s)[64]) { ptx::tmem_ld64(s_addr, s); }
+__device__ __forceinline__ void load_scores(uint32_t s_addr, uint32_t (&s)[16]) { ptx::tmem_ld16(s_addr, s); }
 
 template <int D>
 __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, uint32_t tmem, const Ctl& ctl) {
     using T = ScoreTile<D>;
-    static_assert(T::CW == 16, "a tensor memory load");
+    constexpr int COLS = T::BR / T::NCG;  // columns of a group, at most
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const int w = threadIdx.x / 32 - 4, lane = threadIdx.x % 32;
     const int quad = w % 4, half = w / 4 % T::KH, cg = w / 4 / T::KH;
@@ -461,10 +500,12 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
     const uint32_t lane_addr = (uint32_t)(quad * 32) << 16;
     const float c = p.scale * 1.4426950408889634f;
     const uint64_t c2 = ptx::pack_f32x2(c, c);
-    const int cols = p.tile_cols / T::NCG;  // of a group: a multiple of CW
+    // columns of a group, a multiple of 16, and this one's (the last may have fewer)
+    const int group = (p.tile_cols + 16 * T::NCG - 1) / (16 * T::NCG) * 16;
+    const int col0 = min(cg * group, p.tile_cols), cols = min(group, p.tile_cols - col0);
     float* sums = reinterpret_cast<float*>(smem + T::OFF_SUM);
     uint32_t g = 0;
-    bool ok = true;
+    bool ok = true, ready = false;  // ready: the next scores were there when last asked
     Unit u;
     for (uint32_t n = 0; get<D, true>(ring, u, n, bar, ctl, ok); ++n) {
         const int pos = u.j * T::KB + key;
@@ -473,19 +514,46 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
         if (cg == 0 && u.slot < 0 && p.decay != 0.f && pos < u.len) old = __ldcg(score) * p.decay;
         uint64_t sum0 = ptx::pack_f32x2(0.f, 0.f), sum1 = sum0;
         for (int i = u.i0; i < u.i1; ++i, ++g) {
-            const uint32_t r = g % T::SR;
-            const uint32_t s_addr = tmem + lane_addr + (r * T::KH + half) * T::BR + cg * cols;
-            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (r * T::BR + cg * cols) * 4);
-            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (r * T::BR + cg * cols) * 4);
-            if (!warp_wait_phase(bar(T::B_SFULL + r * T::KH + half), (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
+            const uint32_t r = g % T::SR, lr = g % T::LR;
+            const uint32_t s_addr = tmem + lane_addr + (r * T::KH + half) * T::BR + col0;
+            const float4* ls = reinterpret_cast<const float4*>(smem + T::OFF_LSE + (lr * T::BR + col0) * 4);
+            const int4* la = reinterpret_cast<const int4*>(smem + T::OFF_LAST + (lr * T::BR + col0) * 4);
+            if (!__all_sync(0xffffffffu, ready) &&
+                !warp_wait_phase(bar(T::B_SFULL + r * T::KH + half), (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
             ptx::tc_fence_after();
-            const bool plain = la[0].x == INT_MAX;
-            // (all columns see all of the block, or comparisons: two loops, so that the
-            // first has none -- 6.9 instructions a weight in one loop with both)
-            if (plain) take<false>(s_addr, cols, ls, la, pos, c2, sum0, sum1);
-            else take<true>(s_addr, cols, ls, la, pos, c2, sum0, sum1);
-            ptx::tc_fence_before();
-            ptx::mbar_arrive_warp(bar(T::B_SEMPTY + r * T::KH + half));
+            const bool plain = cols > 0 && la[0].x == INT_MAX;
+            const uint32_t next = bar(T::B_SFULL + (g + 1) % T::SR * T::KH + half), next_ph = ((g + 1) / T::SR) & 1u;
+            if (plain && cols == COLS) {
+                // All of this warp's scores at once, so that their slot is free before they
+                // are used, and no comparisons (in one loop with the others they took 6.9
+                // instructions a weight).
+                uint32_t s[COLS];
+                load_scores(s_addr, s);
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane < 2) ptx::mbar_arrive(lane == 0 ? bar(T::B_SEMPTY + r * T::KH + half) : bar(T::B_LEMPTY + lr));
+                // (asked now, looked at after the exponentials)
+                ready = ptx::mbar_test_wait(next, next_ph);
+#pragma unroll
+                for (int x = 0; x < COLS; x += 4) {
+                    float a[4];
+                    ptx::unpack_f32x2(ptx::fmul2(ptx::pack_f32x2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), c2), a[0], a[1]);
+                    ptx::unpack_f32x2(ptx::fmul2(ptx::pack_f32x2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), c2), a[2], a[3]);
+                    sum0 = ptx::fadd2(sum0, ptx::pack_f32x2(ptx::ex2(a[0]), ptx::ex2(a[1])));
+                    sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
+                }
+            } else {
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += 16) {
+                    uint32_t s[16];
+                    ptx::tmem_ld16(s_addr + c0, s);
+                    add16(s, ls + c0 / 4, la + c0 / 4, pos, c2, sum0, sum1);
+                }
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane < 2) ptx::mbar_arrive(lane == 0 ? bar(T::B_SEMPTY + r * T::KH + half) : bar(T::B_LEMPTY + lr));
+                ready = ptx::mbar_test_wait(next, next_ph);
+            }
         }
         float s0, s1, s2, s3;
         ptx::unpack_f32x2(sum0, s0, s1);
@@ -534,14 +602,23 @@ __global__ void __launch_bounds__(ScoreTile<D>::THREADS, 1)
         ptx::tmem_alloc(ptx::smem_addr(const_cast<uint32_t*>(tmem_slot)), 512);
         ptx::tmem_relinquish();
     }
+    // the lse step's constants and zeros
+    for (int i = threadIdx.x; i < 128 * 2 + T::LR * T::BR * 2; i += T::THREADS)
+        ptx::st_shared_v4(sbase + T::OFF_KL + i * 16, 0u, 0u, 0u, 0u);
     // rows of Q's slots behind the tile's: zeros (no copy writes them)
     if (p.tile_rows < p.tile_cols) {
         constexpr int PR = T::SW / 16;
         const int n = (p.tile_cols - p.tile_rows) * PR;
         for (int i = threadIdx.x; i < n * T::Q_STAGES * T::NCHUNK; i += T::THREADS)
             ptx::st_shared_v4(sbase + T::OFF_Q + (i / n) * (T::BR * T::SW) + p.tile_rows * T::SW + (i % n) * 16, 0u, 0u, 0u, 0u);
-        ptx::fence_proxy_async_smem();
     }
+    __syncthreads();
+    if (threadIdx.x < 128) {
+        uint32_t w0, w1;
+        scoret::constants3<BF16>(w0, w1);
+        ptx::st_shared_v4(sbase + T::OFF_KL + scoret::l_piece(threadIdx.x), w0, w1, 0u, 0u);
+    }
+    ptx::fence_proxy_async_smem();
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -575,8 +652,8 @@ __global__ void __launch_bounds__(ScoreTile<D>::THREADS, 1)
     if (p.Z > 32) __syncthreads();
 
     if (warp == 0) scoret::walk_and_load<D>(&tmQ, &tmK, p, walk, ring, sbase, bar0, ctl);
-    else if (warp == 2) scoret::stage_lse<D>(p, ring, smem, bar0, ctl);
-    else if (warp < 4) { if (lane == 0 && warp / 2 < T::KH) scoret::multiply<D, BF16>(p, ring, sbase, bar0, tmem, warp / 2, ctl); }
+    else if (warp == 2) scoret::stage_lse<D, BF16>(p, ring, smem, bar0, ctl);
+    else if (warp < 4) { if (lane == 0) scoret::multiply<D, BF16>(p, ring, sbase, bar0, tmem, warp / 2, ctl); }
     else scoret::weigh<D>(p, ring, smem, bar0, tmem, ctl);
 
     ptx::tc_fence_before();
