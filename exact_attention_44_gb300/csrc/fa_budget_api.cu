@@ -252,6 +252,7 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
             return FA_ERR_CUDA;
         a.tmQ = &mq;
         a.tmK = &mk;
+        p.long_q = x.T >= 8 * p.tokens;
         // with one tile a unit there is nothing to cut
         if (x.T > p.tokens) {
             p.parts = static_cast<float*>(x.workspace);

@@ -31,6 +31,7 @@ struct ScoreParams {
     int tokens, token_shift;   // new tokens of a tile (a power of two), its log2
     int tile_rows, tile_cols;  // tokens * G, and that rounded up to 16
     int box_rows;              // positions a TMA box holds
+    int long_q;                // many tiles a unit: one slot for K, more for Q
     float* parts;              // two slots of sums a CTA, or nullptr: no unit is cut
     void* cuts;
     uint64_t wait_limit_ns;

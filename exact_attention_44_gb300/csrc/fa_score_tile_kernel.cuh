@@ -46,6 +46,8 @@ struct ScoreTile {
     static constexpr int Q_BYTES = BR * D * 2;
     static constexpr int K_STAGES = 2;
     static constexpr int Q_STAGES = D >= 128 ? 2 : 4;
+    // with one slot for K its second one's room holds more of Q (p.long_q)
+    static constexpr int Q_MORE = Q_STAGES + K_BYTES / Q_BYTES;
     static constexpr int SR = 512 / (KH * BR) < 4 ? 512 / (KH * BR) : 4;  // score slots in tensor memory
     static constexpr int WARPS = 16;                     // of the exponentials
     static constexpr int LR = 4;                         // lse slots
@@ -65,8 +67,8 @@ struct ScoreTile {
     static constexpr int B_KFULL = 0;
     static constexpr int B_KEMPTY = B_KFULL + K_STAGES;
     static constexpr int B_QFULL = B_KEMPTY + K_STAGES;
-    static constexpr int B_QEMPTY = B_QFULL + Q_STAGES;
-    static constexpr int B_SFULL = B_QEMPTY + Q_STAGES;   // [SR][KH] product done (commit), lse staged (its issuer)
+    static constexpr int B_QEMPTY = B_QFULL + Q_MORE;
+    static constexpr int B_SFULL = B_QEMPTY + Q_MORE;   // [SR][KH] product done (commit), lse staged (its issuer)
     static constexpr int B_SEMPTY = B_SFULL + SR * KH;    // [SR][KH] scores read (its warps)
     static constexpr int B_LFULL = B_SEMPTY + SR * KH;    // [LR] lse staged
     static constexpr int B_LEMPTY = B_LFULL + LR;         // [LR] lse used (every warp)
@@ -85,7 +87,7 @@ struct ScoreTile {
         if (i >= B_SEMPTY && i < B_SEMPTY + SR * KH) return WARPS / KH;
         if (i >= B_SFULL && i < B_SFULL + SR * KH) return 2;
         if (i >= B_LEMPTY && i < B_LEMPTY + LR) return WARPS;
-        if ((i >= B_KEMPTY && i < B_KEMPTY + K_STAGES) || (i >= B_QEMPTY && i < B_QEMPTY + Q_STAGES)) return 2;  // issuers
+        if ((i >= B_KEMPTY && i < B_KEMPTY + K_STAGES) || (i >= B_QEMPTY && i < B_QEMPTY + Q_MORE)) return 2;  // issuers
         if (i >= B_SEGFREE && i < B_SEGFREE + SEGS) return 3 + WARPS;
         if (i >= B_SUM && i < B_SUM + 2) return WARPS;
         return 1;
@@ -93,6 +95,26 @@ struct ScoreTile {
 };
 
 namespace scoret {
+
+// The slots of K and Q: two and Q_STAGES, or (p.long_q) one and Q_MORE; Q's come behind K's.
+template <int D>
+struct Slots {
+    using T = ScoreTile<D>;
+    uint32_t k, q;
+    int off_q;
+    __device__ __forceinline__ explicit Slots(const ScoreParams& p)
+        : k(p.long_q ? 1 : T::K_STAGES), q(p.long_q ? T::Q_MORE : T::Q_STAGES), off_q(T::OFF_K + (int)k * T::K_BYTES) {}
+};
+// A place in a ring of n slots: its slot, and how often it has come around.
+struct Place {
+    uint32_t slot = 0, round = 0;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++slot == n) {
+            slot = 0;
+            ++round;
+        }
+    }
+};
 
 // A unit's part in a range: tiles i0 .. i1 - 1 of those that see its block.
 struct Unit {
@@ -218,7 +240,9 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
     const int lane = threadIdx.x % 32;
     // K passes once where all rows are one tile; else the units of a head are not far apart
     const uint64_t policy = ptx::policy_evict_first(), policy_q = ptx::policy_evict_last();
-    uint32_t n = 0, ki = 0, qi = 0;
+    const Slots<D> slots(p);
+    uint32_t n = 0;
+    Place k, q;
     bool ok = true, withheld = false, loaded = false;  // loaded: the unit's first Q tile is there
     Unit u{}, after{};
     bool have = walk.next(p, u);
@@ -246,44 +270,45 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
                 page = p.P;  // outside the map: zeros
             }
         }
-        const uint32_t s = ki % T::K_STAGES, ph = (ki / T::K_STAGES) & 1u;
-        if (!warp_wait_phase(bar(T::B_KEMPTY + s), ph ^ 1u, ctl, SITE_K_EMPTY)) { ok = false; break; }
+        if (!warp_wait_phase(bar(T::B_KEMPTY + k.slot), (k.round & 1u) ^ 1u, ctl, SITE_K_EMPTY)) { ok = false; break; }
         if (p.inject_stall && blockIdx.x == 0 && !withheld) {
             withheld = true;  // never issued: the wait for this block must time out
         } else {
             const uint32_t boxes = __popc(__ballot_sync(0xffffffffu, there));
-            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(T::B_KFULL + s), boxes * p.box_rows * T::SW * T::NCHUNK);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(bar(T::B_KFULL + k.slot), boxes * p.box_rows * T::SW * T::NCHUNK);
             __syncwarp();
             if (there) {
                 const int r = lane * p.box_rows;
-                const uint32_t dst = sbase + T::OFF_K + s * T::K_BYTES + (r / 128) * T::HALF_BYTES + (r % 128) * T::SW;
+                const uint32_t dst = sbase + T::OFF_K + k.slot * T::K_BYTES + (r / 128) * T::HALF_BYTES + (r % 128) * T::SW;
                 for (int c = 0; c < T::NCHUNK; ++c)
-                    ptx::tma_load_4d(dst + c * (128 * T::SW), tmK, bar(T::B_KFULL + s), c * T::SWE, slot, u.hk, page, policy);
+                    ptx::tma_load_4d(dst + c * (128 * T::SW), tmK, bar(T::B_KFULL + k.slot), c * T::SWE, slot, u.hk, page, policy);
             }
         }
-        ++ki;
+        k.next(slots.k);
         for (int i = u.i0 + (loaded ? 1 : 0); i < u.i1; ++i) {
-            const uint32_t qs = qi % T::Q_STAGES;
-            if (!warp_wait_phase(bar(T::B_QEMPTY + qs), ((qi / T::Q_STAGES) & 1u) ^ 1u, ctl, SITE_Q_EMPTY)) { ok = false; break; }
+            if (!warp_wait_phase(bar(T::B_QEMPTY + q.slot), (q.round & 1u) ^ 1u, ctl, SITE_Q_EMPTY)) { ok = false; break; }
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(bar(T::B_QFULL + qs), (uint32_t)p.tile_rows * T::SW * T::NCHUNK);
-                const uint32_t dst = sbase + T::OFF_Q + qs * T::Q_BYTES;
+                ptx::mbar_arrive_expect_tx(bar(T::B_QFULL + q.slot), (uint32_t)p.tile_rows * T::SW * T::NCHUNK);
+                const uint32_t dst = sbase + slots.off_q + q.slot * T::Q_BYTES;
                 for (int c = 0; c < T::NCHUNK; ++c)
-                    ptx::tma_load_4d(dst + c * (T::BR * T::SW), tmQ, bar(T::B_QFULL + qs), c * T::SWE, u.hk * p.G,
+                    ptx::tma_load_4d(dst + c * (T::BR * T::SW), tmQ, bar(T::B_QFULL + q.slot), c * T::SWE, u.hk * p.G,
                                      i << p.token_shift, u.z, policy_q);
             }
             __syncwarp();
-            ++qi;
+            q.next(slots.q);
         }
         loaded = u.keep;
         u = after;
         have = more;
     }
     if (!ok) {
-        for (uint32_t i = qi > (uint32_t)T::Q_STAGES ? qi - T::Q_STAGES : 0; i < qi; ++i)
-            drain_phase(bar(T::B_QFULL + i % T::Q_STAGES), (i / T::Q_STAGES) & 1u, ctl.limit_ns);
-        for (uint32_t i = ki > (uint32_t)T::K_STAGES ? ki - T::K_STAGES : 0; i < ki; ++i)
-            drain_phase(bar(T::B_KFULL + i % T::K_STAGES), (i / T::K_STAGES) & 1u, withheld ? ctl.limit_ns / 64 : ctl.limit_ns);
+        // every slot's last copy
+        for (uint32_t i = 0; i < slots.q; ++i)
+            if (i < q.slot || q.round > 0)
+                drain_phase(bar(T::B_QFULL + i), (i < q.slot ? q.round : q.round - 1) & 1u, ctl.limit_ns);
+        for (uint32_t i = 0; i < slots.k; ++i)
+            if (i < k.slot || k.round > 0)
+                drain_phase(bar(T::B_KFULL + i), (i < k.slot ? k.round : k.round - 1) & 1u, withheld ? ctl.limit_ns / 64 : ctl.limit_ns);
     }
 }
 
@@ -296,31 +321,31 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
     const uint32_t IDESC = ptx::idesc_f16(128, p.tile_cols, BF16, false, false);
     constexpr uint32_t HI = ptx::smem_desc_hi(8 * T::SW, T::SWIZZLE_CODE), HI_L = ptx::smem_desc_hi(8 * 32, 6);
-    const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16), q_lo0 = ptx::smem_desc_lo(sbase + T::OFF_Q, 16);
+    const Slots<D> slots(p);
+    const uint32_t k_lo0 = ptx::smem_desc_lo(sbase + T::OFF_K, 16), q_lo0 = ptx::smem_desc_lo(sbase + slots.off_q, 16);
     const uint64_t kl = ptx::desc64(ptx::smem_desc_lo(sbase + T::OFF_KL, 16), HI_L);
     const uint32_t ql_lo = ptx::smem_desc_lo(sbase + T::OFF_QL, 16);
-    uint32_t g = 0, qi = 0;  // tiles, Q tiles
+    uint32_t g = 0;  // tiles
+    Place k, q;
     bool ok = true;
     Unit u;
     for (uint32_t n = 0; get<D, false>(ring, u, n, bar, ctl, ok); ++n) {
-        const uint32_t ks = n % T::K_STAGES;
         bool waited = false;  // for K
         for (int i = u.i0; i < u.i1; ++i, ++g) {
-            const uint32_t qs = qi % T::Q_STAGES;
             if ((g & 1u) == issuer) {
                 const uint32_t r = g % T::SR, lr = g % T::LR;
-                if (!waited && !wait_phase(bar(T::B_KFULL + ks), (n / T::K_STAGES) & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
+                if (!waited && !wait_phase(bar(T::B_KFULL + k.slot), k.round & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
                 waited = true;
-                if (!wait_phase(bar(T::B_QFULL + qs), (qi / T::Q_STAGES) & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
+                if (!wait_phase(bar(T::B_QFULL + q.slot), q.round & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
                 if (!wait_phase(bar(T::B_LFULL + lr), (g / T::LR) & 1u, ctl, SITE_EPI_FULL)) { ok = false; break; }
-                const uint32_t q_lo = q_lo0 + qs * (T::Q_BYTES >> 4);
+                const uint32_t q_lo = q_lo0 + q.slot * (T::Q_BYTES >> 4);
                 const uint64_t ql = ptx::desc64(ql_lo + lr * (T::QL_BYTES >> 4), HI_L);
 #pragma unroll
                 for (int h = 0; h < T::KH; ++h) {
                     const uint32_t full = bar(T::B_SFULL + r * T::KH + h);
                     if (!wait_phase(bar(T::B_SEMPTY + r * T::KH + h), ((g / T::SR) & 1u) ^ 1u, ctl, SITE_S_FREE)) { ok = false; break; }
                     ptx::tc_fence_after();
-                    const uint32_t k_lo = k_lo0 + ((ks * T::K_BYTES + h * T::HALF_BYTES) >> 4);
+                    const uint32_t k_lo = k_lo0 + ((k.slot * T::K_BYTES + h * T::HALF_BYTES) >> 4);
                     const uint32_t d = tmem + (r * T::KH + h) * T::BR;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
@@ -335,12 +360,13 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
                 if (!ok) break;
             }
             if (i + 1 < u.i1 || u.keep == 0) {
-                ptx::tc_commit(bar(T::B_QEMPTY + qs));
-                ++qi;
+                ptx::tc_commit(bar(T::B_QEMPTY + q.slot));
+                q.next(slots.q);
             }
         }
         if (!ok) break;
-        ptx::tc_commit(bar(T::B_KEMPTY + ks));
+        ptx::tc_commit(bar(T::B_KEMPTY + k.slot));
+        k.next(slots.k);
     }
     if (!ok) {
         ptx::tc_commit(bar(T::B_DRAIN + issuer));
@@ -608,9 +634,10 @@ __global__ void __launch_bounds__(ScoreTile<D>::THREADS, 1)
     // rows of Q's slots behind the tile's: zeros (no copy writes them)
     if (p.tile_rows < p.tile_cols) {
         constexpr int PR = T::SW / 16;
+        const scoret::Slots<D> slots(p);
         const int n = (p.tile_cols - p.tile_rows) * PR;
-        for (int i = threadIdx.x; i < n * T::Q_STAGES * T::NCHUNK; i += T::THREADS)
-            ptx::st_shared_v4(sbase + T::OFF_Q + (i / n) * (T::BR * T::SW) + p.tile_rows * T::SW + (i % n) * 16, 0u, 0u, 0u, 0u);
+        for (int i = threadIdx.x; i < n * (int)slots.q * T::NCHUNK; i += T::THREADS)
+            ptx::st_shared_v4(sbase + slots.off_q + (i / n) * (T::BR * T::SW) + p.tile_rows * T::SW + (i % n) * 16, 0u, 0u, 0u, 0u);
     }
     __syncthreads();
     if (threadIdx.x < 128) {
