@@ -17,7 +17,7 @@ static cudaError_t launch_rows(const ScoreLaunch& a) {
     ScoreParams p = a.params;
     // no more warps than there can be steps
     const int64_t steps = (int64_t)p.Z * p.Hkv * ((p.cap + T::KT - 1) / T::KT);
-    p.workers = (int)std::max<int64_t>(1, std::min<int64_t>(steps, (int64_t)a.sms * T::CTAS * SCORE_WARPS));
+    p.workers = (int)std::max<int64_t>(1, std::min<int64_t>(steps, (int64_t)a.sms * T::ctas(NT) * SCORE_WARPS));
     return launch_dependent(fa_score_rows_kernel<FA_HEAD_DIM, BF16, NT>, dim3((unsigned)((p.workers + SCORE_WARPS - 1) / SCORE_WARPS)),
                             32 * SCORE_WARPS, 0, a.stream, p);
 }

@@ -25,8 +25,7 @@ struct ScoreRows {
     static constexpr int KT = 16 * U;
     static constexpr int PW = D >= 32 ? 4 : 2;         // words a thread loads of a row at a time
     static constexpr int NP = D / (8 * PW);            // such pieces of a row
-    static constexpr int BUFS = D <= 128 ? 2 : 1;      // steps of K in registers
-    static constexpr int CTAS = 4;                     // an SM
+    static constexpr int ctas(int nt) { return D == 256 ? 3 : nt == 1 ? 5 : 4; }  // an SM
 };
 
 namespace score {
@@ -76,7 +75,7 @@ struct Keys {
 }  // namespace score
 
 template <int D, bool BF16, int NT>
-__global__ void __launch_bounds__(32 * SCORE_WARPS, ScoreRows<D>::CTAS) fa_score_rows_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(32 * SCORE_WARPS, ScoreRows<D>::ctas(NT)) fa_score_rows_kernel(const ScoreParams p) {
     using T = ScoreRows<D>;
     using namespace score;
     __shared__ ScoreFind<SCORE_WARPS> find;
@@ -89,10 +88,9 @@ __global__ void __launch_bounds__(32 * SCORE_WARPS, ScoreRows<D>::CTAS) fa_score
     int64_t left = place.left;
     if (left == 0) return;
 
-    Step ahead{place.z, 0, 0, place.s};   // the step after those whose table entries are asked for
-    ahead.hk = (int)(place.at / steps(place.s));
-    ahead.j = (int)(place.at - (int64_t)ahead.hk * steps(place.s));
-    int64_t to_ask = left;
+    Step cur{place.z, 0, 0, place.s};
+    cur.hk = (int)(place.at / steps(place.s));
+    cur.j = (int)(place.at - (int64_t)cur.hk * steps(place.s));
     auto advance = [&](Step& x) {
         if (++x.j < steps(x.s)) return;
         x.j = 0;
@@ -206,46 +204,18 @@ __global__ void __launch_bounds__(32 * SCORE_WARPS, ScoreRows<D>::CTAS) fa_score
         }
     };
 
-    // Table entries two steps ahead of the products, K one step (D <= 128).
-    Step cur = ahead, next = ahead;
-    int entries = ask(ahead);
-    if constexpr (T::BUFS == 2) {
-        Keys<D> a, b;
-        load(cur, entries, a);
-        if (--to_ask > 0) {
+    // table entries a step ahead
+    int entries = ask(cur);
+    Keys<D> k;
+    for (; left > 0; --left) {
+        load(cur, entries, k);
+        Step next = cur;
+        if (left > 1) {
             advance(next);
             entries = ask(next);
         }
-        auto round = [&](Keys<D>& now, Keys<D>& then) {
-            const Step after = next;
-            if (left > 1) {
-                load(next, entries, then);
-                if (--to_ask > 0) {
-                    advance(next);
-                    entries = ask(next);
-                }
-            }
-            use(cur, now);
-            cur = after;
-            --left;
-        };
-        while (true) {
-            round(a, b);
-            if (left == 0) break;
-            round(b, a);
-            if (left == 0) break;
-        }
-    } else {
-        Keys<D> a;
-        for (; left > 0; --left) {
-            load(cur, entries, a);
-            if (left > 1) {
-                advance(next);
-                entries = ask(next);
-            }
-            use(cur, a);
-            cur = next;
-        }
+        use(cur, k);
+        cur = next;
     }
 }
 
