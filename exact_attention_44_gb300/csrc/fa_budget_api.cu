@@ -279,7 +279,7 @@ fa_status fa_cache_evict(const fa_cache_evict_args* args, cudaStream_t stream) {
     fa_status st = check_cache(c, true);
     if (st != FA_OK) return st;
     if (c.P > (1 << 30) || (int64_t)c.Z * c.max_pages > INT32_MAX || c.L > 65535 ||
-        (int64_t)c.L * c.Hkv > INT32_MAX || (int64_t)c.L * c.Hkv * c.Z > INT32_MAX / 4)
+        (int64_t)c.L * c.Hkv > INT32_MAX || (int64_t)c.L * c.Hkv * c.Z > (1 << 26))
         return FA_ERR_UNSUPPORTED;
     if ((st = check_ints(x.missing, true)) != FA_OK) return st;
     const int64_t cap = (int64_t)c.max_pages * c.page_size;
@@ -313,6 +313,7 @@ fa_status fa_cache_evict(const fa_cache_evict_args* args, cudaStream_t stream) {
     p.missing = x.missing;
     p.Z = c.Z, p.L = c.L, p.H = c.Hkv, p.D = c.D, p.page = c.page_size, p.M = c.max_pages, p.P = c.P;
     p.budget = budget, p.first = x.first, p.recent = x.recent;
+    p.by_page = fa::FastDiv(p.page);
     p.ws = static_cast<int32_t*>(x.workspace);
     p.status = f.status;
     err = fa::launch_cache_evict(p, f.sms, stream);

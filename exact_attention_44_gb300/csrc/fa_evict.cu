@@ -1,9 +1,10 @@
 // Cutting the sequences of a paged cache back to a budget: of each (layer, sequence, kv
 // head) the positions with the highest scores stay, in their order, and move together.
 //
-// Three kernels.  The first, a CTA a (layer, sequence, head), selects: a radix selection
-// of the n-th highest score (three passes over 11, 11 and 10 bits of the keys), then the
-// list of the positions that stay.  The second, one CTA, does the books: pages that are
+// Three kernels.  The first, a CTA a (layer, sequence, head), selects: a histogram of the
+// keys' upper 11 bits finds where the n-th highest score lies, the few keys there are
+// ranked against one another (or, if they are many, 11 and 10 bits more are counted), and
+// then the positions that stay are listed.  The second, one CTA, does the books: pages that are
 // rewritten but shared with other sequences are replaced by free ones, lowest first in
 // the order of sequences and columns (so the result does not depend on timing).  The
 // third moves the rows, in place, and writes tables, counts and lengths.
@@ -56,6 +57,7 @@ __device__ __forceinline__ int held_len(const EvictParams& p, int z) { return mi
 constexpr int SELECT_THREADS = 256;
 constexpr int SELECT_WARPS = SELECT_THREADS / 32;
 constexpr int BINS = 2048;
+constexpr int LISTED = 512;  // keys that are ranked against one another
 
 // Unsigned keys in the order of the scores; -0 is 0, a NaN is above everything.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -64,10 +66,11 @@ __device__ __forceinline__ uint32_t score_key(float x) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(SELECT_THREADS) fa_evict_select_kernel(const EvictParams p, int held) {
+__global__ void __launch_bounds__(SELECT_THREADS, 6) fa_evict_select_kernel(const EvictParams p, int held) {
     extern __shared__ uint32_t keys_held[];  // the candidates' keys, if they fit
-    __shared__ int hist[BINS];
-    __shared__ int red[SELECT_WARPS], red2[SELECT_WARPS], found[2], first_moved;
+    __shared__ __align__(16) int hist[BINS];  // the highest digit first
+    __shared__ uint32_t list[LISTED];
+    __shared__ int red[SELECT_WARPS], red2[SELECT_WARPS], found[3], listed, first_moved;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const EvictWs w = evict_ws(p);
@@ -85,8 +88,17 @@ __global__ void __launch_bounds__(SELECT_THREADS) fa_evict_select_kernel(const E
     const int n = len - back - front, m = target - back - front;  // candidates, and how many of them stay: m < n
     const float* from = p.scores + l * p.ss_l + z * p.ss_z + h * p.ss_h + front;
     const bool fits = n <= held;
-    if (fits)
-        for (int i = tid; i < n; i += SELECT_THREADS) keys_held[i] = score_key(__ldcg(from + i));
+    if (fits) {
+        constexpr int U = 8;
+        for (int i0 = tid; i0 < n; i0 += U * SELECT_THREADS) {
+            float v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) v[u] = i0 + u * SELECT_THREADS < n ? __ldcg(from + i0 + u * SELECT_THREADS) : 0.f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (i0 + u * SELECT_THREADS < n) keys_held[i0 + u * SELECT_THREADS] = score_key(v[u]);
+        }
+    }
     auto key = [&](int i) { return fits ? keys_held[i] : score_key(__ldcg(from + i)); };
 
     // the m-th highest key: its bits from the top, 11, 11 and 10 at a time; `want` is how
@@ -97,18 +109,19 @@ __global__ void __launch_bounds__(SELECT_THREADS) fa_evict_select_kernel(const E
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
             const uint32_t above = pass == 0 ? 0u : ~0u << (shift + bits);
-            for (int i = tid; i < BINS; i += SELECT_THREADS) hist[i] = 0;
+            for (int i = tid; i < BINS / 4; i += SELECT_THREADS) reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+            if (tid == 0) listed = 0;
             __syncthreads();
             for (int i = tid; i < n; i += SELECT_THREADS) {
                 const uint32_t k = key(i);
-                if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
+                if ((k & above) == prefix) atomicAdd(&hist[BINS - 1 - ((k >> shift) & ((1u << bits) - 1))], 1);
             }
             __syncthreads();
-            // a thread sums BINS / SELECT_THREADS bins, the highest first
-            constexpr int B = BINS / SELECT_THREADS;
-            const int top = BINS - 1 - tid * B;
-            int mine = 0;
-            for (int b = 0; b < B; ++b) mine += hist[top - b];
+            // a thread sums eight bins
+            static_assert(BINS == 8 * SELECT_THREADS, "bins of a thread");
+            const int4 lo = reinterpret_cast<const int4*>(hist)[2 * tid], hi = reinterpret_cast<const int4*>(hist)[2 * tid + 1];
+            const int bin[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const int mine = ((bin[0] + bin[1]) + (bin[2] + bin[3])) + ((bin[4] + bin[5]) + (bin[6] + bin[7]));
             int x = mine;
             for (int d = 1; d < 32; d *= 2) {
                 const int y = __shfl_up_sync(0xffffffffu, x, d);
@@ -118,14 +131,48 @@ __global__ void __launch_bounds__(SELECT_THREADS) fa_evict_select_kernel(const E
             __syncthreads();
             for (int i = 0; i < warp; ++i) x += red[i];
             if (x >= want && x - mine < want) {  // one thread
-                int before = x - mine, b = 0;
-                while (before + hist[top - b] < want) before += hist[top - b++];
-                found[0] = top - b;
-                found[1] = want - before;
+                int before = x - mine;
+                bool done = false;
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (!done) {
+                        if (before + bin[b] >= want) {
+                            found[0] = BINS - 1 - (8 * tid + b);
+                            found[1] = want - before;
+                            found[2] = bin[b];
+                            done = true;
+                        }
+                        before += bin[b];
+                    }
             }
             __syncthreads();
             prefix |= (uint32_t)found[0] << shift;
             want = found[1];
+            const int same = found[2];
+            if (pass == 0 && same <= LISTED) {
+                for (int i = tid; i < n; i += SELECT_THREADS) {
+                    const uint32_t k = key(i);
+                    if (k >> 21 == prefix >> 21) list[atomicAdd(&listed, 1)] = k;
+                }
+                __syncthreads();
+                for (int i = tid; i < same; i += SELECT_THREADS) {
+                    const uint32_t k = list[i];
+                    int higher = 0, equal = 0;
+#pragma unroll 4
+                    for (int j = 0; j < same; ++j) {
+                        higher += list[j] > k;
+                        equal += list[j] == k;
+                    }
+                    if (higher < want && want <= higher + equal) {  // (equal ones write the same)
+                        found[0] = (int)k;
+                        found[1] = want - higher;
+                    }
+                }
+                __syncthreads();
+                prefix = (uint32_t)found[0];
+                want = found[1];
+                break;
+            }
         }
     __syncthreads();
     // Keys above the prefix stay, and of those equal to it the first `want`.  A warp takes
@@ -212,6 +259,7 @@ __global__ void __launch_bounds__(EVICT_PLAN_THREADS) fa_evict_plan_kernel(const
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     constexpr int WARPS = EVICT_PLAN_THREADS / 32;
     // a warp a sequence: its first page that is rewritten, and how many from there on are shared
+    bool any = false;
     for (int z = warp; z < p.Z; z += WARPS) {
         const int target = ldi(w.target + z);
         int count = 0, own = 0;
@@ -234,8 +282,15 @@ __global__ void __launch_bounds__(EVICT_PLAN_THREADS) fa_evict_plan_kernel(const
             w.own[z] = own;
             w.off[z] = count;
         }
+        any |= count > 0;
     }
-    __syncthreads();
+    if (!__syncthreads_or(any)) {  // each page is its sequence's own: the rows of the table only get shorter
+        if (tid == 0) {
+            *w.lack = -1;
+            *p.missing = 0;
+        }
+        return;
+    }
     int wanted = 0;
     for (int z0 = 0; z0 < p.Z; z0 += EVICT_PLAN_THREADS) {
         const int z = z0 + tid;
@@ -288,24 +343,29 @@ __global__ void __launch_bounds__(EVICT_PLAN_THREADS) fa_evict_plan_kernel(const
 // ------------------------------------------------------------ move ----------
 // Row idx[i] to row i of each (layer, sequence, head), K and V, and its score.  idx[i] >=
 // i increases with i, so what a row overwrites is read by no later row: within a CTA the
-// rows go in chunks whose reads come before their writes, and the reads of the next chunk
-// go ahead of the writes of this one.
+// rows go in chunks, the reads of a chunk before its writes, and those of the next chunk
+// go ahead of the writes of this one.  Where the rows are is looked up for 256 of them at
+// a time, a batch ahead.
 constexpr int MOVE_THREADS = 256;
 
 struct EvictMove {
     EvictParams p;
     int table_ctas;
+    int parts;       // CTAs that share the columns of a (layer, sequence, head, K or V)
+    int64_t movers;  // CTAs that move K and V
 };
 
-__global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const EvictMove a) {
+__global__ void __launch_bounds__(MOVE_THREADS, 4) fa_evict_move_kernel(const __grid_constant__ EvictMove a) {
     const EvictParams& p = a.p;
-    constexpr int U = 8;
-    __shared__ int64_t where[2][2][MOVE_THREADS];  // [chunk parity][from, to][row]; from -1: it stays
+    constexpr int U = 4;
+    __shared__ int64_t where[2][2][MOVE_THREADS];  // [batch parity][from, to][row]; from -1: it stays
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const EvictWs w = evict_ws(p);
     const int tid = threadIdx.x;
-    if (ldi(w.lack) > 0) return;
+    const int lack = ldi(w.lack);
+    if (lack > 0) return;
+    const int32_t* rows_after = lack < 0 ? w.before : w.after;
     if ((int)blockIdx.x < a.table_ctas) {  // the books
         for (int z = blockIdx.x; z < p.Z; z += a.table_ctas) {
             const int target = ldi(w.target + z);
@@ -313,26 +373,27 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const Evict
             const int need = (target + p.page - 1) / p.page;
             for (int c = tid; c < p.M; c += MOVE_THREADS) {
                 const int was = ldi(w.before + (int64_t)z * p.M + c);
-                const int now = c < need ? ldi(w.after + (int64_t)z * p.M + c) : -1;
+                const int now = c < need ? ldi(rows_after + (int64_t)z * p.M + c) : -1;
                 if (now == was) continue;
                 if ((unsigned)was < (unsigned)p.P) atomicAdd(p.refs + was, -1);
-                if (now >= 0) atomicAdd(p.refs + now, 1);
+                if ((unsigned)now < (unsigned)p.P) atomicAdd(p.refs + now, 1);
                 p.table[z * p.st_z + c] = now;
             }
             if (tid == 0) p.lens[z] = target;
         }
         return;
     }
-    // a CTA a unit: (layer, sequence, head, K or V or the scores)
-    const int64_t unit3 = (int64_t)blockIdx.x - a.table_ctas, unit = unit3 / 3;
-    const int kind = (int)(unit3 - unit * 3);
+    const int64_t block = (int64_t)blockIdx.x - a.table_ctas;
+    const bool moves = block < a.movers;  // else the scores of a (layer, sequence, head)
+    const int64_t both = moves ? block / a.parts : 2 * (block - a.movers), unit = both / 2;
     const int h = (int)(unit % p.H), z = (int)(unit / p.H % p.Z), l = (int)(unit / p.H / p.Z);
     const int target = ldi(w.target + z);
     if (target < 0) return;
-    const int32_t *idx = w.idx + unit * p.budget, *before = w.before + (int64_t)z * p.M, *after = w.after + (int64_t)z * p.M;
-    if (kind == 2) {
+    const int32_t *idx = w.idx + unit * p.budget, *before = w.before + (int64_t)z * p.M, *after = rows_after + (int64_t)z * p.M;
+    const int unmoved = ldi(w.first + unit);
+    if (!moves) {
         float* s = p.scores + l * p.ss_l + z * p.ss_z + h * p.ss_h;
-        for (int i0 = ldi(w.first + unit); i0 < target; i0 += U * MOVE_THREADS) {
+        for (int i0 = unmoved; i0 < target; i0 += U * MOVE_THREADS) {
             float v[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -348,20 +409,18 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const Evict
         }
         return;
     }
-    const CacheView& cache = kind == 0 ? p.k : p.v;
-    uint16_t* base = cache.base + l * cache.l + h * cache.h;
-    const int per = p.D / 8, side = MOVE_THREADS / per, rows = U * side;  // lanes a row, rows at a time, rows a chunk
-    const int row = tid / per, piece = (tid - row * per) * 8;
+    const CacheView& cache = both % 2 == 0 ? p.k : p.v;
+    // this CTA's columns of a row, in 16-byte pieces a lane; all powers of two
+    const int per = p.D / 8 / a.parts, shift = 31 - __clz(per), side = MOVE_THREADS >> shift;
+    uint16_t* base = cache.base + l * cache.l + h * cache.h + ((int)(block % a.parts) * per + (tid & (per - 1))) * 8;
+    const int row = tid >> shift;
     const int start = min(ldi(w.own + z) * p.page, target);
-    const int unmoved = ldi(w.first + unit);
     bool bad = false;
-    // rows of a chunk: at most U * 32 (D = 64: 256); for D < 64 in turns of MOVE_THREADS
-    auto find = [&](int i0, int half) {
-        const int i = i0 + tid;
+    auto find = [&](int i, int half) {  // row i, by thread i - the batch's first row
         int64_t from = -1, to = -1;
-        if (tid < rows && i < target) {
+        if (i < target) {
             const int j = i < unmoved ? i : ldi(idx + i);
-            const int cf = j / p.page, ct = i / p.page;
+            const int cf = p.by_page(j), ct = p.by_page(i);
             const int ef = ldi(before + cf), et = ldi(after + ct);
             if (j != i || ef != et) {
                 if ((unsigned)ef < (unsigned)p.P && (unsigned)et < (unsigned)p.P) {
@@ -375,38 +434,41 @@ __global__ void __launch_bounds__(MOVE_THREADS) fa_evict_move_kernel(const Evict
         where[half][0][tid] = from;
         where[half][1][tid] = to;
     };
-    const int chunk = min(rows, MOVE_THREADS);
+    const int chunk = min(U * side, MOVE_THREADS), chunks = (target - start + chunk - 1) / chunk;
+    const int a_batch = MOVE_THREADS / chunk;  // chunks: a power of two
     uint4 now[U], then[U];
-    auto load = [&](int half, uint4 (&v)[U]) {
+    auto load = [&](int k, uint4 (&v)[U]) {
+        const int r0 = (k & (a_batch - 1)) * chunk, half = (k / a_batch) & 1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = u * side + row;
-            if (r < chunk && where[half][0][r] >= 0) v[u] = __ldcg(reinterpret_cast<const uint4*>(base + where[half][0][r] + piece));
+            const int r = r0 + u * side + row;
+            if (u * side < chunk && where[half][0][r] >= 0) v[u] = __ldcg(reinterpret_cast<const uint4*>(base + where[half][0][r]));
         }
     };
-    auto store = [&](int half, const uint4 (&v)[U]) {
+    auto store = [&](int k, const uint4 (&v)[U]) {
+        const int r0 = (k & (a_batch - 1)) * chunk, half = (k / a_batch) & 1;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int r = u * side + row;
-            if (r < chunk && where[half][0][r] >= 0) *reinterpret_cast<uint4*>(base + where[half][1][r] + piece) = v[u];
+            const int r = r0 + u * side + row;
+            if (u * side < chunk && where[half][0][r] >= 0) *reinterpret_cast<uint4*>(base + where[half][1][r]) = v[u];
         }
     };
-    if (start < target) {
-        find(start, 0);
+    if (chunks > 0) {
+        find(start + tid, 0);
         __syncthreads();
         load(0, now);
     }
-    int half = 0;
-    for (int i0 = start; i0 < target; i0 += chunk) {
-        const bool more = i0 + chunk < target;
-        if (more) find(i0 + chunk, half ^ 1);
-        __syncthreads();  // this chunk has been read, and the places of the next are there
-        if (more) load(half ^ 1, then);
-        store(half, now);
+    for (int k = 0; k < chunks; ++k) {
+        __syncthreads();  // this chunk has been read, and the batch before is done
+        const int next = k / a_batch + 1;
+        if (k % a_batch == 0 && next * a_batch < chunks) {
+            find(start + next * MOVE_THREADS + tid, next & 1);
+            if (a_batch == 1) __syncthreads();
+        }
+        if (k + 1 < chunks) load(k + 1, then);
+        store(k, now);
 #pragma unroll
         for (int u = 0; u < U; ++u) now[u] = then[u];
-        half ^= 1;
-        __syncthreads();  // the places of this chunk may be overwritten
     }
     if (bad) bad_page(p.status, SITE_PAGE_EVICT);
 }
@@ -431,9 +493,13 @@ cudaError_t launch_cache_evict(const EvictParams& p, int sms, cudaStream_t strea
     if (err != cudaSuccess) return err;
     err = launch_dependent(fa_evict_plan_kernel, dim3(1), EVICT_PLAN_THREADS, 0, stream, p);
     if (err != cudaSuccess) return err;
-    const EvictMove a{p, p.Z < sms ? p.Z : sms};
-    const int64_t units = (int64_t)p.L * p.Z * p.H * 3;
-    return launch_dependent(fa_evict_move_kernel, dim3((unsigned)(a.table_ctas + units)), MOVE_THREADS, 0, stream, a);
+    EvictMove a{p, p.Z < sms ? p.Z : sms, 1, 0};
+    const int64_t units = (int64_t)p.L * p.Z * p.H;
+    // few units: their columns in up to four parts of 64 bytes at least, until every SM has
+    // its four CTAs
+    while (a.parts < 4 && p.D / 8 / a.parts > 4 && units * 2 * a.parts * 2 <= 4 * (int64_t)sms) a.parts *= 2;
+    a.movers = units * 2 * a.parts;
+    return launch_dependent(fa_evict_move_kernel, dim3((unsigned)(a.table_ctas + a.movers + units)), MOVE_THREADS, 0, stream, a);
 }
 
 }  // namespace fa

@@ -722,7 +722,7 @@ fa_status fa_cache_score_workspace_size(size_t* bytes);
  * any layer or head, stays shared.  *missing is the number of pages that lacked; if it is
  * not 0 nothing else is changed.  Rows whose page is not in the cache are recorded as
  * FA_ERR_PAGE and skipped.  Valid state before is valid state after (see fa_cache_fork).
- * L <= 65535, P <= 2^30, Z * max_pages < 2^31, L * Z * Hkv < 2^29.
+ * L <= 65535, P <= 2^30, Z * max_pages < 2^31, L * Z * Hkv <= 2^26.
  */
 typedef struct {
     fa_paged_cache cache;
