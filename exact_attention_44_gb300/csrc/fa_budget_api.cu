@@ -253,8 +253,9 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
         a.tmQ = &mq;
         a.tmK = &mk;
         p.long_q = x.T >= 8 * p.tokens;
-        // with one tile a unit there is nothing to cut
-        if (x.T > p.tokens) {
+        // Units of up to four tiles are not cut: the merge takes about 3 us, as long as
+        // the tiles that it could spare the busiest CTA.
+        if (x.T > 4 * p.tokens) {
             p.parts = static_cast<float*>(x.workspace);
             p.cuts = static_cast<char*>(x.workspace) + fa::score_slot_bytes(f.sms);
         }

@@ -13,7 +13,8 @@
 // its K stays in shared memory while the tiles of up to BR query rows that see it stream
 // by.  Units are laid end to end, counted in tiles, and cut into one equal range a CTA
 // (fa_score_sched.cuh); a unit that a cut crosses leaves its sums in slots of the
-// workspace, and fa_score_merge_kernel joins them in order.
+// workspace, and fa_score_merge_kernel joins them in order.  Units of up to four tiles are
+// counted whole and not cut (p.parts is nullptr): the merge costs more than it evens out.
 //
 // Roles: warp 0 walks the range, hands the units on and loads K through the block table
 // (a lane a box of rows) and Q; warps 1 and 3 issue the products of every second tile each
@@ -142,7 +143,9 @@ struct Shape {
     __device__ __forceinline__ int first(const ScoreParams& p, int j) const {
         return (int)max((int64_t)0, (int64_t)j * (T::KB >> p.token_shift) - lag);
     }
-    __device__ __forceinline__ int64_t before(const ScoreParams& p, int j) const {  // tiles of blocks 0 .. j - 1
+    // tiles of blocks 0 .. j - 1, or (units are not cut) the blocks
+    __device__ __forceinline__ int64_t before(const ScoreParams& p, int j) const {
+        if (p.parts == nullptr) return j;
         const int64_t r = T::KB >> p.token_shift, j0 = lag / r + 1;  // the first block with first() > 0
         int64_t n = (int64_t)j * nt;
         if (j > j0) n -= r * ((int64_t)(j - 1) * j - j0 * (j0 - 1)) / 2 - (int64_t)lag * (j - j0);
@@ -187,10 +190,10 @@ struct ScoreWalk {
         const int first = s.first(p, j), tiles = s.nt - first;
         u.z = w.z, u.hk = hk, u.j = j, u.len = w.s.len, u.nl = w.s.nl;
         u.i0 = first + i;
-        const int n = (int)min((int64_t)(tiles - i), w.left);
+        const int n = p.parts == nullptr ? tiles : (int)min((int64_t)(tiles - i), w.left);
         u.i1 = u.i0 + n;
         u.slot = i == 0 && n == tiles ? -1 : 2 * (int)blockIdx.x + (i > 0 ? 0 : 1);
-        w.left -= n;
+        w.left -= p.parts == nullptr ? 1 : n;
         i = 0;
         if (w.left > 0 && ++j == s.nb) {
             j = 0;
