@@ -63,7 +63,8 @@ struct ScoreTile {
     static constexpr int OFF_LSE = OFF_QL + LR * QL_BYTES;          // [LR][BR] -lse log2 e, where it has no pieces
     static constexpr int OFF_LAST = OFF_LSE + LR * BR * 4;          // [LR][BR] last position seen
     static constexpr int OFF_SUM = OFF_LAST + LR * BR * 4;          // [2][NCG][KB]
-    static constexpr int OFF_SEG = OFF_SUM + 2 * NCG * KB * 4;
+    static constexpr int OFF_FLAG = OFF_SUM + 2 * NCG * KB * 4;     // [LR] a tile that needs no comparisons
+    static constexpr int OFF_SEG = OFF_FLAG + LR * 4;
     static constexpr int OFF_BAR = OFF_SEG + SEGS * 48;
     static constexpr int B_KFULL = 0;
     static constexpr int B_KEMPTY = B_KFULL + K_STAGES;
@@ -417,7 +418,7 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
     struct Tile {
         float l[N];
         int j, i, len;
-        bool there;
+        bool there, whole;  // whole: each of its rows has a token
     };
     // this lane's columns: row c of a tile is head c % G of token c / G
     int tok[N];
@@ -441,43 +442,48 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
         t.there = true;
         t.j = u.j, t.i = u.i0++, t.len = u.len;
         const int t0 = t.i << p.token_shift, left = u.nl - t0;
+        t.whole = left >= p.tokens;
 #pragma unroll
         for (int x = 0; x < N; ++x) {
             t.l[x] = -INFINITY;
             if (tok[x] < left) t.l[x] = __ldcg(from + off[x] + t0);
         }
     };
+    // -lse / scale in three pieces, unless it is out of the type's range, infinite or NaN
+    const float per_scale = -1.f / p.scale;
+    constexpr float LIMIT = BF16 ? 1e38f : 60000.f;
+    int* flags = reinterpret_cast<int*>(smem + T::OFF_FLAG);
     auto finish = [&](const Tile& t) -> bool {
-        float v[N];
-        uint32_t w0[N], w1[N];
-        int last[N];
-        bool plain = p.tile_rows == p.tile_cols;
         const int last0 = t.len + (t.i << p.token_shift), need = (t.j + 1) * T::KB - 1;
+        // every row of the tile a token that sees all of the block: all of them plain?
+        bool plain = p.tile_rows == p.tile_cols && t.whole && last0 >= need;
+        uint32_t w0[N], w1[N];
 #pragma unroll
         for (int x = 0; x < N; ++x) {
-            const bool counts = t.l[x] != -INFINITY;
-            last[x] = counts ? last0 + tok[x] : -1;
-            // -lse / scale in three pieces, or (out of the type's range, infinite or NaN) not
-            const float q = -t.l[x] / p.scale;
-            const bool pieces = fabsf(q) <= (BF16 ? 1e38f : 60000.f);
+            const float q = t.l[x] * per_scale;
+            const bool pieces = fabsf(q) <= LIMIT;
             w0[x] = w1[x] = 0u;
             if (pieces) split3<BF16>(q, w0[x], w1[x]);
-            v[x] = pieces ? 0.f : -t.l[x] * 1.4426950408889634f;
-            plain &= tok[x] == INT_MAX || (pieces && last[x] >= need);
+            plain &= pieces || tok[x] == INT_MAX;
         }
         plain = __all_sync(0xffffffffu, plain);
         const uint32_t r = g % T::LR;
         if (!warp_wait_phase(bar(T::B_LEMPTY + r), ((g / T::LR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
-        float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
-        int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
         const uint32_t ql = ptx::smem_addr(smem + T::OFF_QL) + r * T::QL_BYTES;
 #pragma unroll
-        for (int x = 0; x < N; ++x) {
-            const int c = x * 32 + lane;
-            ptx::st_shared_v4(ql + l_piece(c), w0[x], w1[x], 0u, 0u);
-            ls[c] = v[x];
-            la[c] = plain ? INT_MAX : last[x];
+        for (int x = 0; x < N; ++x) ptx::st_shared_v4(ql + l_piece(x * 32 + lane), w0[x], w1[x], 0u, 0u);
+        if (!plain || p.tile_cols < T::BR) {  // (a group with fewer columns takes the comparisons' way)
+            float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
+            int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
+#pragma unroll
+            for (int x = 0; x < N; ++x) {
+                const int c = x * 32 + lane;
+                const bool pieces = fabsf(t.l[x] * per_scale) <= LIMIT;
+                ls[c] = pieces ? 0.f : -t.l[x] * 1.4426950408889634f;
+                la[c] = t.l[x] != -INFINITY ? last0 + tok[x] : -1;
+            }
         }
+        if (lane == 0) flags[r] = plain;
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
         ++g;
@@ -533,6 +539,7 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
     const int group = (p.tile_cols + 16 * T::NCG - 1) / (16 * T::NCG) * 16;
     const int col0 = min(cg * group, p.tile_cols), cols = min(group, p.tile_cols - col0);
     float* sums = reinterpret_cast<float*>(smem + T::OFF_SUM);
+    const int* flags = reinterpret_cast<const int*>(smem + T::OFF_FLAG);
     uint32_t g = 0;
     bool ok = true, ready = false;  // ready: the next scores were there when last asked
     Unit u;
@@ -550,7 +557,7 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
             if (!__all_sync(0xffffffffu, ready) &&
                 !warp_wait_phase(bar(T::B_SFULL + r * T::KH + half), (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
             ptx::tc_fence_after();
-            const bool plain = cols > 0 && la[0].x == INT_MAX;
+            const bool plain = flags[lr] != 0;
             const uint32_t next = bar(T::B_SFULL + (g + 1) % T::SR * T::KH + half), next_ph = ((g + 1) / T::SR) & 1u;
             if (plain && cols == COLS) {
                 // All of this warp's scores at once, so that their slot is free before they
