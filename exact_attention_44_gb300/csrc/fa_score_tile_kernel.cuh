@@ -317,7 +317,9 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
 }
 
 // The products of every second tile (issuer 0 or 1).  K and Q are released by both: a
-// commit waits for the products of its own thread only.
+// commit waits for the products of its own thread only.  Both also wait for every copy of
+// K and Q, whoever's tile it is for: an issuer that did not could release a slot's next
+// round before the other one has released this one.
 template <int D, bool BF16>
 __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbase, uint32_t bar0, uint32_t tmem,
                          uint32_t issuer, const Ctl& ctl) {
@@ -334,13 +336,11 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
     bool ok = true;
     Unit u;
     for (uint32_t n = 0; get<D, false>(ring, u, n, bar, ctl, ok); ++n) {
-        bool waited = false;  // for K
+        if (!wait_phase(bar(T::B_KFULL + k.slot), k.round & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
         for (int i = u.i0; i < u.i1; ++i, ++g) {
+            if (!wait_phase(bar(T::B_QFULL + q.slot), q.round & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
             if ((g & 1u) == issuer) {
                 const uint32_t r = g % T::SR, lr = g % T::LR;
-                if (!waited && !wait_phase(bar(T::B_KFULL + k.slot), k.round & 1u, ctl, SITE_K_FULL)) { ok = false; break; }
-                waited = true;
-                if (!wait_phase(bar(T::B_QFULL + q.slot), q.round & 1u, ctl, SITE_Q_FULL)) { ok = false; break; }
                 if (!wait_phase(bar(T::B_LFULL + lr), (g / T::LR) & 1u, ctl, SITE_EPI_FULL)) { ok = false; break; }
                 const uint32_t q_lo = q_lo0 + q.slot * (T::Q_BYTES >> 4);
                 const uint64_t ql = ptx::desc64(ql_lo + lr * (T::QL_BYTES >> 4), HI_L);
@@ -372,10 +372,9 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
         ptx::tc_commit(bar(T::B_KEMPTY + k.slot));
         k.next(slots.k);
     }
-    if (!ok) {
-        ptx::tc_commit(bar(T::B_DRAIN + issuer));
-        drain_phase(bar(T::B_DRAIN + issuer), 0u, ctl.limit_ns);
-    }
+    // everything issued here has arrived before the CTA ends
+    ptx::tc_commit(bar(T::B_DRAIN + issuer));
+    drain_phase(bar(T::B_DRAIN + issuer), 0u, ctl.limit_ns);
 }
 
 // The lse step of the contraction: 32 bytes a row, in the 32-byte swizzle's order; this is
