@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import _binding as _b
-from .budget import fa_rope
+from .budget import _calls
 
 
 def _plain(window, alibi_slopes) -> bool:
@@ -69,49 +69,23 @@ class _AttentionVarlen(torch.autograd.Function):
         return dq, dk, dv, None, None, None, None, None, None, None, None
 
 
-def _rows_ok(t):
-    """t, or a copy of it that fa_rope takes (a gradient may come with any strides)."""
-    fine = t.stride(3) == 1 and t.data_ptr() % 16 == 0 and all(s % 8 == 0 for n, s in zip(t.shape[:3], t.stride()) if n > 1)
-    return t if fine or t.numel() == 0 else t.contiguous()
-
-
-class _Rotary(torch.autograd.Function):
-    @staticmethod
-    def forward(ctx, q, k, turns, positions, interleaved, factor):
-        # (q and k are not kept: the gradient does not need them)
-        ctx.save_for_backward(turns, positions)
-        ctx.interleaved, ctx.factor = interleaved, factor
-        ctx.set_materialize_grads(False)
-        return fa_rope(q, k, turns, positions, interleaved=interleaved, factor=factor)
-
-    @staticmethod
-    def backward(ctx, dq, dk):
-        turns, positions = ctx.saved_tensors
-        kw = dict(interleaved=ctx.interleaved, inverse=True, factor=ctx.factor)
-        if dq is not None and dk is not None:
-            dq, dk = fa_rope(_rows_ok(dq), _rows_ok(dk), turns, positions, **kw)
-        elif dq is not None:
-            dq = fa_rope(_rows_ok(dq), None, turns, positions, **kw)[0]
-        elif dk is not None:
-            dk = fa_rope(_rows_ok(dk), None, turns, positions, **kw)[0]
-        return dq, dk, None, None, None, None
-
-
 def rotary(q, k, turns, positions=None, *, interleaved: bool = False, factor: float = 1.0):
     """fa_rope with autograd: rotary positions of q (Z, Hq, N, D) and k (Z, Hk, N, D), before ``attention``.
 
     turns: from fa_rope_turns.  positions: int32 (N) or (Z, N), default 0 .. N - 1.  Packed
     sequences, (total, H, D) as ``attention_varlen`` takes them, need positions (total).  The
-    gradient turns back (fa_rope with inverse).  k may be None.  Returns (q, k) turned.
+    gradient turns back (fa_rope with inverse) and has a gradient itself.  k may be None.
+    Returns (q, k) turned.
     """
-    if q.dim() == 3:
-        if positions is None:
-            raise ValueError("packed sequences need positions (total)")
-        view = lambda t: None if t is None else t.unsqueeze(0).transpose(1, 2)  # noqa: E731
-        yq, yk = _Rotary.apply(view(q), view(k), turns, positions, bool(interleaved), float(factor))
-        back = lambda t: None if t is None else t.transpose(1, 2).squeeze(0)  # noqa: E731
-        return back(yq), back(yk)
-    return _Rotary.apply(q, k, turns, positions, bool(interleaved), float(factor))
+    call = _calls().rotary
+    if q.dim() != 3:
+        return call(q, k, turns, positions, interleaved, factor)
+    if positions is None:
+        raise ValueError("packed sequences need positions (total)")
+    rows = lambda t: None if t is None else t.unsqueeze(0).transpose(1, 2)  # noqa: E731
+    back = lambda t: None if t is None else t.transpose(1, 2).squeeze(0)  # noqa: E731
+    yq, yk = call(rows(q), rows(k), turns, positions, interleaved, factor)
+    return back(yq), back(yk)
 
 
 def attention(q, k, v, *, scale: float | None = None, causal: bool = False, window=(-1, -1), alibi_slopes=None,

@@ -13,11 +13,14 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
 #include <cmath>
 #include <initializer_list>
+#include <optional>
+#include <stdexcept>
 #include <string>
 
 #include "fa.h"
@@ -41,12 +44,12 @@ struct Library {
 } lib;
 
 // A refused argument: the Python exception to raise.
-struct Refused {
+struct Refused : std::runtime_error {
     PyObject* type;
-    std::string text;
+    Refused(PyObject* t, const std::string& text) : std::runtime_error(text), type(t) {}
 };
-[[noreturn]] void value_error(std::string text) { throw Refused{PyExc_ValueError, std::move(text)}; }
-[[noreturn]] void type_error(std::string text) { throw Refused{PyExc_TypeError, std::move(text)}; }
+[[noreturn]] void value_error(std::string text) { throw Refused(PyExc_ValueError, text); }
+[[noreturn]] void type_error(std::string text) { throw Refused(PyExc_TypeError, text); }
 
 std::string shape_of(at::IntArrayRef s) {
     std::string t = "(";
@@ -194,10 +197,10 @@ template <typename F>
 PyObject* guarded(F&& fn) {
     HANDLE_TH_ERRORS
     try {
-        if (lib.fwd == nullptr) throw Refused{PyExc_ImportError, "libfa is not loaded"};
+        if (lib.fwd == nullptr) throw Refused(PyExc_ImportError, "libfa is not loaded");
         return fn();
     } catch (const Refused& r) {
-        PyErr_SetString(r.type, r.text.c_str());
+        PyErr_SetString(r.type, r.what());
         return nullptr;
     }
     END_HANDLE_TH_ERRORS
@@ -424,6 +427,59 @@ at::Tensor out_like(const at::Tensor& like) {
     return keep ? at::empty_strided(like.sizes(), like.strides(), like.options()) : at::empty(like.sizes(), like.options());
 }
 
+// A call that failed where there may be no interpreter (the gradient's thread).
+struct Failed : std::runtime_error {
+    fa_status status;
+    Failed(fa_status st, const char* call)
+        : std::runtime_error(std::string(call) + ": status " + std::to_string((int)st)), status(st) {}
+};
+
+// Arguments of fa_rope but for the outputs; k may be null.
+fa_rope_args rope_args(const at::Tensor& q, const at::Tensor* k, const at::Tensor& turns, const at::Tensor* pos, bool interleaved,
+                       bool inverse, double factor) {
+    if (q.dim() != 4) value_error("q must be 4-D (Z, H, N, D)");
+    fa_rope_args x{};
+    x.dtype = dtype_of(q, "fa_rope");
+    if (k != nullptr) {
+        if (k->dim() != 4 || k->size(0) != q.size(0) || k->size(2) != q.size(2) || k->size(3) != q.size(3))
+            value_error("k must be (Z, Hk, N, D) like q, got " + shape_of(k->sizes()) + " for " + shape_of(q.sizes()));
+        if (k->scalar_type() != q.scalar_type()) type_error("q and k must share one dtype");
+        x.k = k->data_ptr();
+        x.sk = strides4(*k);
+        x.Hk = to_int(k->size(1), "the heads");
+    }
+    x.rotary_dim = pairs_of(turns);
+    if (pos != nullptr) x.positions_stride = positions_stride(*pos, q.size(0), q.size(2));
+    x.interleaved = interleaved;
+    x.inverse = inverse;
+    x.factor = (float)factor;
+    x.q = q.data_ptr();
+    x.sq = strides4(q);
+    x.positions = ints(pos);
+    x.turns = static_cast<const int64_t*>(turns.data_ptr());
+    x.Z = to_int(q.size(0), "the batch");
+    x.Hq = to_int(q.size(1), "the heads");
+    x.N = to_int(q.size(2), "the rows");
+    x.D = to_int(q.size(3), "the head dim");
+    return x;
+}
+void rope_outputs(fa_rope_args& x, const at::Tensor& qo, const at::Tensor& ko) {
+    x.q_out = qo.data_ptr();
+    x.sq_out = strides4(qo);
+    if (ko.defined()) {
+        x.k_out = ko.data_ptr();
+        x.sk_out = strides4(ko);
+    }
+}
+PyObject* pair(const at::Tensor& a, const at::Tensor& b) {
+    PyObject* result = PyTuple_New(2);
+    if (result == nullptr) throw python_error();
+    PyTuple_SET_ITEM(result, 0, THPVariable_Wrap(a));
+    if (b.defined()) PyTuple_SET_ITEM(result, 1, THPVariable_Wrap(b));
+    else PyTuple_SET_ITEM(result, 1, (Py_INCREF(Py_None), Py_None));
+    return result;
+}
+
 // (q, k, turns, positions, interleaved, inverse, factor, q_out, k_out, stream)
 PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (!expect(n, 10)) return nullptr;
@@ -431,52 +487,89 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &q = tensor(a[0], "q"), &turns = tensor(a[2], "turns");
         const at::Tensor *k = maybe_tensor(a[1], "k"), *pos = maybe_tensor(a[3], "positions");
         const at::Tensor *qo_arg = maybe_tensor(a[7], "q_out"), *ko_arg = maybe_tensor(a[8], "k_out");
-        if (q.dim() != 4) value_error("q must be 4-D (Z, H, N, D)");
-        fa_rope_args x{};
-        x.dtype = dtype_of(q, "fa_rope");
-        if (k != nullptr) {
-            if (k->dim() != 4 || k->size(0) != q.size(0) || k->size(2) != q.size(2) || k->size(3) != q.size(3))
-                value_error("k must be (Z, Hk, N, D) like q, got " + shape_of(k->sizes()) + " for " + shape_of(q.sizes()));
-            if (k->scalar_type() != q.scalar_type()) type_error("q and k must share one dtype");
-        } else if (ko_arg != nullptr) {
-            value_error("k_out without k");
-        }
+        if (k == nullptr && ko_arg != nullptr) value_error("k_out without k");
+        fa_rope_args x = rope_args(q, k, turns, pos, flag_arg(a[4]), flag_arg(a[5]), float_arg(a[6]));
         check_out(qo_arg, q, "q_out");
         if (k != nullptr) check_out(ko_arg, *k, "k_out");
-        x.rotary_dim = pairs_of(turns);
-        if (pos != nullptr) x.positions_stride = positions_stride(*pos, q.size(0), q.size(2));
-        x.interleaved = flag_arg(a[4]);
-        x.inverse = flag_arg(a[5]);
-        x.factor = float_arg(a[6]);
         const int dev = cuda_device("fa_rope", q, {k, pos, qo_arg, ko_arg});
         const Place place(a[9], dev, {&q, k, pos, qo_arg, ko_arg});
         const at::Tensor qo = qo_arg != nullptr ? *qo_arg : out_like(q);
         at::Tensor ko;
         if (k != nullptr) ko = ko_arg != nullptr ? *ko_arg : out_like(*k);
-        x.q = q.data_ptr();
-        x.q_out = qo.data_ptr();
-        x.sq = strides4(q);
-        x.sq_out = strides4(qo);
-        if (k != nullptr) {
-            x.k = k->data_ptr();
-            x.k_out = ko.data_ptr();
-            x.sk = strides4(*k);
-            x.sk_out = strides4(ko);
-            x.Hk = to_int(k->size(1), "the heads");
-        }
-        x.positions = ints(pos);
-        x.turns = static_cast<const int64_t*>(turns.data_ptr());
-        x.Z = to_int(q.size(0), "the batch");
-        x.Hq = to_int(q.size(1), "the heads");
-        x.N = to_int(q.size(2), "the rows");
-        x.D = to_int(q.size(3), "the head dim");
+        rope_outputs(x, qo, ko);
         check(unlocked([&] { return lib.rope(&x, place.stream()); }), "fa_rope");
-        PyObject* result = PyTuple_New(2);
-        if (result == nullptr) throw python_error();
-        PyTuple_SET_ITEM(result, 0, THPVariable_Wrap(qo));
-        if (ko.defined()) PyTuple_SET_ITEM(result, 1, THPVariable_Wrap(ko));
-        else PyTuple_SET_ITEM(result, 1, (Py_INCREF(Py_None), Py_None));
-        return result;
+        return pair(qo, ko);
+    });
+}
+
+// A gradient comes with any strides: itself where fa_rope takes them, else a copy.
+at::Tensor rows_of(const at::Tensor& t) {
+    if (t.numel() == 0) return t;
+    bool fine = t.stride(3) == 1 && reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0;
+    for (int i = 0; i < 3; ++i) fine = fine && (t.size(i) <= 1 || t.stride(i) % 8 == 0);
+    return fine ? t : t.contiguous();
+}
+
+// fa_rope with autograd.  The gradient is the turn back, by this same function, so that it
+// has gradients of its own.  In C++ because a step's Python side took 160 us of 21 us of
+// kernels (4 x 32 heads x 1024 rows of D = 128, both directions).
+class Rotary : public torch::autograd::Function<Rotary> {
+  public:
+    static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx, const at::Tensor& q,
+                                                  const std::optional<at::Tensor>& k, const at::Tensor& turns,
+                                                  const std::optional<at::Tensor>& pos, bool interleaved, bool inverse,
+                                                  double factor) {
+        ctx->set_materialize_grads(false);
+        ctx->save_for_backward({turns, pos.value_or(at::Tensor())});
+        ctx->saved_data["interleaved"] = interleaved;
+        ctx->saved_data["inverse"] = inverse;
+        ctx->saved_data["factor"] = factor;
+        const at::Tensor *kp = k.has_value() ? &*k : nullptr, *pp = pos.has_value() ? &*pos : nullptr;
+        fa_rope_args x = rope_args(q, kp, turns, pp, interleaved, inverse, factor);
+        const int dev = cuda_device("rotary", q, {kp, pp});
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+        const cudaStream_t stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+        const at::Tensor qo = out_like(q);
+        at::Tensor ko;
+        if (kp != nullptr) ko = out_like(*kp);
+        rope_outputs(x, qo, ko);
+        const fa_status st = PyGILState_Check() ? unlocked([&] { return lib.rope(&x, stream); }) : lib.rope(&x, stream);
+        if (st != FA_OK) throw Failed(st, "fa_rope");
+        if (ko.defined()) return {qo, ko};
+        return {qo};
+    }
+    static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
+        const at::Tensor dq = grads[0], dk = grads.size() > 1 ? grads[1] : at::Tensor();
+        torch::autograd::variable_list out(7);
+        if (!dq.defined() && !dk.defined()) return out;
+        const auto saved = ctx->get_saved_variables();
+        const bool interleaved = ctx->saved_data["interleaved"].toBool(), inverse = ctx->saved_data["inverse"].toBool();
+        const double factor = ctx->saved_data["factor"].toDouble();
+        const at::Tensor first = rows_of(dq.defined() ? dq : dk);
+        std::optional<at::Tensor> second, positions;
+        if (dq.defined() && dk.defined()) second = rows_of(dk);
+        if (saved[1].defined()) positions = saved[1];
+        auto back = apply(first, second, saved[0], positions, interleaved, !inverse, factor);
+        if (dq.defined()) out[0] = back[0];
+        if (dk.defined()) out[1] = back[dq.defined() ? 1 : 0];
+        return out;
+    }
+};
+
+// (q, k, turns, positions, interleaved, factor)
+PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    if (!expect(n, 6)) return nullptr;
+    return guarded([&]() -> PyObject* {
+        const at::Tensor &q = tensor(a[0], "q"), &turns = tensor(a[2], "turns");
+        const at::Tensor *k = maybe_tensor(a[1], "k"), *pos = maybe_tensor(a[3], "positions");
+        try {
+            const auto some = [](const at::Tensor* t) { return t != nullptr ? std::optional<at::Tensor>(*t) : std::nullopt; };
+            const auto out = Rotary::apply(q, some(k), turns, some(pos), flag_arg(a[4]) != 0, false, (double)float_arg(a[5]));
+            return pair(out[0], out.size() > 1 ? out[1] : at::Tensor());
+        } catch (const Failed& f) {
+            check(f.status, "fa_rope");
+            throw;
+        }
     });
 }
 
@@ -674,6 +767,7 @@ PyMethodDef methods[] = {
     {"cache_commit", reinterpret_cast<PyCFunction>(cache_commit), METH_FASTCALL, nullptr},
     {"cache_fork", reinterpret_cast<PyCFunction>(cache_fork), METH_FASTCALL, nullptr},
     {"rope", reinterpret_cast<PyCFunction>(rope), METH_FASTCALL, nullptr},
+    {"rotary", reinterpret_cast<PyCFunction>(rotary), METH_FASTCALL, nullptr},
     {"cache_append_rope", reinterpret_cast<PyCFunction>(cache_append_rope), METH_FASTCALL, nullptr},
     {"cache_score", reinterpret_cast<PyCFunction>(cache_score), METH_FASTCALL, nullptr},
     {"cache_evict", reinterpret_cast<PyCFunction>(cache_evict), METH_FASTCALL, nullptr},

@@ -276,3 +276,68 @@ def test_append_bad_pages():
     out = fa.fa_cache_append_rope(q, k, v, *got, table.cuda(), lens, turns)
     assert fa.fa_device_status()[0] == fa.FA_ERR_PAGE
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(out, tq)
+
+
+def test_gradient_of_the_gradient():
+    """The gradient is a turn too: differentiated by what came in, it is the turn itself."""
+    import exact_attention_44_gb300 as fa
+    x = torch.randn(1, 2, 9, 64, device="cuda").half().requires_grad_()
+    up = torch.randn(1, 2, 9, 64, device="cuda").half().requires_grad_()
+    w = torch.randn(1, 2, 9, 64, device="cuda").half()
+    turns = turns_of(32)
+    y, none = fa.rotary(x, None, turns, factor=0.5)
+    assert none is None
+    grad, = torch.autograd.grad(y, x, up, create_graph=True)
+    second, = torch.autograd.grad(grad, up, w)
+    assert torch.equal(second, fa.fa_rope(w, None, turns, factor=0.5)[0])
+
+
+def test_positions_changed_between_the_directions_are_noticed():
+    import exact_attention_44_gb300 as fa
+    x = torch.randn(1, 2, 9, 64, device="cuda").half().requires_grad_()
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    y, _ = fa.rotary(x, None, turns_of(64), pos)
+    pos += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
+def test_backward_in_a_graph_and_on_another_stream():
+    """Forward and backward of a layer (rotary, then attention) captured in a CUDA graph replay to the eager bits; and
+    a side stream's gradients are that stream's."""
+    import exact_attention_44_gb300 as fa
+    turns = turns_of(64)
+    q, k, v = (torch.randn(1, h, 130, 64, device="cuda").half() for h in (4, 2, 2))
+    do = torch.randn(1, 4, 130, 64, device="cuda").half()
+
+    def layer(a, b, c):
+        x, y = fa.rotary(a, b, turns)
+        return fa.attention(x, y, c, causal=True)
+
+    def grads():
+        leaves = [t.detach().requires_grad_() for t in (q, k, v)]
+        return torch.autograd.grad(layer(*leaves), leaves, do)
+
+    want = grads()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = grads()
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(other, want))
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        grads()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = grads()
+    keep = [t.clone() for t in (q, k, v)]
+    for t in (q, k, v):
+        t.zero_()
+    graph.replay()
+    for t, c in zip((q, k, v), keep):
+        t.copy_(c)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
