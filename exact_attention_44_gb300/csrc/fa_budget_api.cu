@@ -101,6 +101,8 @@ fa_status fa_rope(const fa_rope_args* args, cudaStream_t stream) {
     if ((st = check_strided(x.k, &x.sk, x.Z, x.Hk, x.N, false)) != FA_OK) return st;
     if ((st = check_strided(x.k_out, &x.sk_out, x.Z, x.Hk, x.N, true)) != FA_OK) return st;
     if ((st = check_turns(x.turns, x.positions, x.positions_stride)) != FA_OK) return st;
+    // one tensor's output in place of the other tensor
+    if (x.Hq > 0 && x.Hk > 0 && (x.q_out == x.k_out || x.q_out == x.k || x.k_out == x.q)) return FA_ERR_INVALID_ARG;
     fa::DeviceFacts f;
     const cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
@@ -143,6 +145,7 @@ fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream
     if ((st = check_cache_data(c, true)) != FA_OK) return st;
     if ((st = check_ints(x.new_lens, false)) != FA_OK) return st;
     if ((st = check_turns(x.turns, x.positions, x.positions_stride)) != FA_OK) return st;
+    if (x.Hq > 0 && c.Hkv > 0 && (x.q_out == x.k || x.q_out == x.v)) return FA_ERR_INVALID_ARG;
     fa::DeviceFacts f;
     const cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);

@@ -77,12 +77,11 @@ __global__ void __launch_bounds__(SELECT_THREADS, 6) fa_evict_select_kernel(cons
     const int h = blockIdx.x, z = blockIdx.y, l = blockIdx.z;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int len = held_len(p, z), target = cut_to(p, z, len);
-    if (h == 0 && l == 0) {
-        if (tid == 0) w.target[z] = target;
-        if (target >= 0)
-            for (int c = tid; c < p.M; c += SELECT_THREADS) w.before[(int64_t)z * p.M + c] = ldi(p.table + z * p.st_z + c);
-    }
+    if (h == 0 && l == 0 && tid == 0) w.target[z] = target;
     if (target < 0) return;
+    // the sequence's table row, a share of it each (p.M may be large where sequences are short)
+    for (int64_t c = ((int64_t)l * p.H + h) * SELECT_THREADS + tid; c < p.M; c += (int64_t)p.L * p.H * SELECT_THREADS)
+        w.before[(int64_t)z * p.M + c] = ldi(p.table + z * p.st_z + c);
     const int64_t unit = ((int64_t)l * p.Z + z) * p.H + h;
     const int front = min(p.first, target), back = min(p.recent, target - front);
     const int n = len - back - front, m = target - back - front;  // candidates, and how many of them stay: m < n
@@ -367,19 +366,22 @@ __global__ void __launch_bounds__(MOVE_THREADS, 4) fa_evict_move_kernel(const __
     if (lack > 0) return;
     const int32_t* rows_after = lack < 0 ? w.before : w.after;
     if ((int)blockIdx.x < a.table_ctas) {  // the books
-        for (int z = blockIdx.x; z < p.Z; z += a.table_ctas) {
+        const int chunks = (p.M + MOVE_THREADS - 1) / MOVE_THREADS;
+        for (int64_t i = blockIdx.x; i < (int64_t)p.Z * chunks; i += a.table_ctas) {
+            const int z = (int)(i / chunks), k = (int)(i - (int64_t)z * chunks), c = k * MOVE_THREADS + tid;
             const int target = ldi(w.target + z);
             if (target < 0) continue;
             const int need = (target + p.page - 1) / p.page;
-            for (int c = tid; c < p.M; c += MOVE_THREADS) {
+            if (c < p.M) {
                 const int was = ldi(w.before + (int64_t)z * p.M + c);
                 const int now = c < need ? ldi(rows_after + (int64_t)z * p.M + c) : -1;
-                if (now == was) continue;
-                if ((unsigned)was < (unsigned)p.P) atomicAdd(p.refs + was, -1);
-                if ((unsigned)now < (unsigned)p.P) atomicAdd(p.refs + now, 1);
-                p.table[z * p.st_z + c] = now;
+                if (now != was) {
+                    if ((unsigned)was < (unsigned)p.P) atomicAdd(p.refs + was, -1);
+                    if ((unsigned)now < (unsigned)p.P) atomicAdd(p.refs + now, 1);
+                    p.table[z * p.st_z + c] = now;
+                }
             }
-            if (tid == 0) p.lens[z] = target;
+            if (k == 0 && tid == 0) p.lens[z] = target;
         }
         return;
     }
@@ -493,7 +495,8 @@ cudaError_t launch_cache_evict(const EvictParams& p, int sms, cudaStream_t strea
     if (err != cudaSuccess) return err;
     err = launch_dependent(fa_evict_plan_kernel, dim3(1), EVICT_PLAN_THREADS, 0, stream, p);
     if (err != cudaSuccess) return err;
-    EvictMove a{p, p.Z < sms ? p.Z : sms, 1, 0};
+    const int64_t chunks = (int64_t)p.Z * ((p.M + MOVE_THREADS - 1) / MOVE_THREADS);
+    EvictMove a{p, (int)(chunks < sms ? chunks : sms), 1, 0};
     const int64_t units = (int64_t)p.L * p.Z * p.H;
     // few units: their columns in up to four parts of 64 bytes at least, until every SM has
     // its four CTAs

@@ -138,13 +138,15 @@ I, U, A, W, OK = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_ERR_ALIGNME
     (dict(turns=None), I), (dict(ps=-1), I), (dict(so=_st(0, 192, 64)), I), (dict(D=96), U), (dict(dtype=2), U),
     (dict(Z=65536), U), (dict(Hq=65535), U), (dict(N=(1 << 30) + 1), U), (dict(q=PTR + 8), A), 
     (dict(pos=PTR + 2), A), (dict(so=_st(768, 190, 64)), A), (dict(so=_st(768, 192, 64, 2)), A),
+    (dict(ko=PTR), I), (dict(qo=PTR + 4096), I), (dict(ko=PTR, k=PTR + 64), I),
     (dict(Z=0), OK), (dict(N=0), OK), (dict(Hq=0, Hk=0), OK),
 ])
 def test_rope_arguments(lib, kw, code):
-    k = dict(q=PTR, ko=PTR, turns=PTR, pos=None, ps=0, so=None, Z=2, Hq=4, Hk=2, N=3, D=64, R=32, inter=0, inverse=0,
+    # q in place at PTR, k in place at PTR + 4096
+    k = dict(q=PTR, qo=PTR, k=PTR + 4096, ko=PTR + 4096, turns=PTR, pos=None, ps=0, so=None, Z=2, Hq=4, Hk=2, N=3, D=64, R=32, inter=0, inverse=0,
              factor=1.0, dtype=0) | kw
     st = _st(k["Hq"] * k["N"] * k["D"], k["N"] * k["D"], k["D"])
-    a = Rope(k["q"], PTR, PTR, k["ko"], st, st, k["so"] or st, st, k["pos"], k["ps"], k["turns"], k["Z"], k["Hq"], k["Hk"],
+    a = Rope(k["q"], k["k"], k["qo"], k["ko"], st, st, k["so"] or st, st, k["pos"], k["ps"], k["turns"], k["Z"], k["Hq"], k["Hk"],
              k["N"], k["D"], k["R"], k["inter"], k["inverse"], k["factor"], k["dtype"])
     assert lib.fa_rope(ctypes.addressof(a), None) == code
 
@@ -153,14 +155,14 @@ def test_rope_arguments(lib, kw, code):
     (dict(T=-1), I), (dict(Hq=-1), I), (dict(L=2), I), (dict(R=80), I), (dict(inter=3), I), (dict(factor=-math.inf), I),
     (dict(q=None), I), (dict(v=None), I), (dict(kc=None), I), (dict(turns=None), I), (dict(lens=None), I),
     (dict(sc=_st(0, 1024, 64)), I), (dict(dtype=-1), U), (dict(D=40), U), (dict(page=24), U), (dict(T=(1 << 30) + 1), U),
-    (dict(k=PTR + 2), A), (dict(new=PTR + 1), A), (dict(pos=PTR + 1), A),
+    (dict(k=PTR + 2), A), (dict(new=PTR + 1), A), (dict(pos=PTR + 1), A), (dict(qo=PTR + 4096), I),
     (dict(Z=0), OK), (dict(T=0), OK),
 ])
 def test_append_rope_arguments(lib, kw, code):
-    k = dict(q=PTR, k=PTR, v=PTR, turns=PTR, pos=None, new=None, T=3, Hq=4, R=32, inter=0, factor=1.0, dtype=1) | kw
+    k = dict(q=PTR, qo=PTR, k=PTR + 4096, v=PTR + 4096, turns=PTR, pos=None, new=None, T=3, Hq=4, R=32, inter=0, factor=1.0, dtype=1) | kw
     c = _cache(**{n: k.pop(n) for n in list(k) if n in ("kc", "lens", "L", "sc", "D", "page", "Z")})
     st = _st(4 * k["T"] * c.D, k["T"] * c.D, c.D)
-    a = AppendRope(c, k["q"], PTR, k["k"], k["v"], st, st, st, st, k["new"], k["pos"], 0, k["turns"], k["Hq"], k["T"], k["R"],
+    a = AppendRope(c, k["q"], k["qo"], k["k"], k["v"], st, st, st, st, k["new"], k["pos"], 0, k["turns"], k["Hq"], k["T"], k["R"],
                    k["inter"], k["factor"], k["dtype"])
     assert lib.fa_cache_append_rope(ctypes.addressof(a), None) == code
 

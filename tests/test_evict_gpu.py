@@ -171,6 +171,13 @@ def test_room_is_released_and_bad_pages_are_reported():
     assert torch.equal(bits(kg[0]), bits(want))
 
 
+def test_wide_tables():
+    """Far more columns than the sequences need, room in some of them."""
+    lens = [100, 7, 260]
+    kc, vc, table, refs = state(14, [160, 16, 300], 16, 2, 64, 2, cols=3001)
+    check(kc, vc, table, lens, refs, torch.rand(2, 3, 2, table.shape[1] * 16), 16, 50, first=1, recent=9)
+
+
 def test_nothing_to_do():
     import exact_attention_44_gb300 as fa
     kc, vc, table, refs = state(11, [30, 5], 16, 1, 64, 1)

@@ -152,6 +152,21 @@ def test_bad_pages_read_as_zeros(T):
 
 
 @pytest.mark.parametrize("T", [1, 48])
+def test_broadcast_queries(T):
+    """Heads that share one row of q: stride 0."""
+    import exact_attention_44_gb300 as fa
+    kc, _, table, _, _ = pu.make_cache(12, [100 + T] * 2, 2, 64, 16, "fp16", garbage=0.0)
+    q = torch.randn(2, 1, T, 64).half().cuda()
+    lse = torch.full((2, 4, T), 4.0, device="cuda")
+    out = []
+    for x in (q.expand(2, 4, T, 64), q.repeat(1, 4, 1, 1)):
+        s = torch.zeros(2, 2, table.shape[1] * 16, device="cuda")
+        fa.fa_cache_score(x, lse, kc.cuda(), table.cuda(), i32([100, 60]), s)
+        out.append(s)
+    assert torch.equal(*out) and fa.fa_device_status()[0] == 0
+
+
+@pytest.mark.parametrize("T", [1, 48])
 def test_lengths_past_the_table_are_clamped(T):
     import exact_attention_44_gb300 as fa
     kc, _, table, _, _ = pu.make_cache(4, [64, 64], 1, 64, 16, "fp16")
