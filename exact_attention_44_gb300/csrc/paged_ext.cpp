@@ -13,15 +13,19 @@
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
-#include <torch/csrc/autograd/custom_function.h>
+#include <torch/csrc/autograd/function.h>
+#include <torch/csrc/autograd/functions/utils.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/autograd/saved_variable.h>
 
 #include <climits>
 #include <cmath>
 #include <initializer_list>
-#include <optional>
+#include <memory>
+#include <mutex>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "fa.h"
 
@@ -511,50 +515,68 @@ at::Tensor rows_of(const at::Tensor& t) {
 }
 
 // fa_rope with autograd.  The gradient is the turn back, by this same function, so that it
-// has gradients of its own.  In C++ because a step's Python side took 160 us of 21 us of
-// kernels (4 x 32 heads x 1024 rows of D = 128, both directions).
-class Rotary : public torch::autograd::Function<Rotary> {
-  public:
-    static torch::autograd::variable_list forward(torch::autograd::AutogradContext* ctx, const at::Tensor& q,
-                                                  const std::optional<at::Tensor>& k, const at::Tensor& turns,
-                                                  const std::optional<at::Tensor>& pos, bool interleaved, bool inverse,
-                                                  double factor) {
-        ctx->set_materialize_grads(false);
-        ctx->save_for_backward({turns, pos.value_or(at::Tensor())});
-        ctx->saved_data["interleaved"] = interleaved;
-        ctx->saved_data["inverse"] = inverse;
-        ctx->saved_data["factor"] = factor;
-        const at::Tensor *kp = k.has_value() ? &*k : nullptr, *pp = pos.has_value() ? &*pos : nullptr;
-        fa_rope_args x = rope_args(q, kp, turns, pp, interleaved, inverse, factor);
-        const int dev = cuda_device("rotary", q, {kp, pp});
-        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
-        const cudaStream_t stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
-        const at::Tensor qo = out_like(q);
-        at::Tensor ko;
-        if (kp != nullptr) ko = out_like(*kp);
-        rope_outputs(x, qo, ko);
-        const fa_status st = PyGILState_Check() ? unlocked([&] { return lib.rope(&x, stream); }) : lib.rope(&x, stream);
-        if (st != FA_OK) throw Failed(st, "fa_rope");
-        if (ko.defined()) return {qo, ko};
-        return {qo};
-    }
-    static torch::autograd::variable_list backward(torch::autograd::AutogradContext* ctx, torch::autograd::variable_list grads) {
+// has gradients of its own.  A graph node in C++: a step's Python side took 160 us of 21 us
+// of kernels (4 x 32 heads x 1024 rows of D = 128, both directions).
+using torch::autograd::variable_list;
+struct Turn {  // how rows turn, but for the rows
+    at::Tensor turns;
+    bool interleaved, inverse;
+    double factor;
+};
+std::pair<at::Tensor, at::Tensor> turn_rows(const at::Tensor& q, const at::Tensor& k, const at::Tensor& pos, const Turn& how);
+
+struct TurnBackward : public torch::autograd::Node {
+    Turn how;
+    torch::autograd::SavedVariable positions;
+    bool has_positions = false;
+    std::string name() const override { return "RotaryBackward"; }
+    variable_list apply(variable_list&& grads) override {
         const at::Tensor dq = grads[0], dk = grads.size() > 1 ? grads[1] : at::Tensor();
-        torch::autograd::variable_list out(7);
+        variable_list out(grads.size());
         if (!dq.defined() && !dk.defined()) return out;
-        const auto saved = ctx->get_saved_variables();
-        const bool interleaved = ctx->saved_data["interleaved"].toBool(), inverse = ctx->saved_data["inverse"].toBool();
-        const double factor = ctx->saved_data["factor"].toDouble();
-        const at::Tensor first = rows_of(dq.defined() ? dq : dk);
-        std::optional<at::Tensor> second, positions;
-        if (dq.defined() && dk.defined()) second = rows_of(dk);
-        if (saved[1].defined()) positions = saved[1];
-        auto back = apply(first, second, saved[0], positions, interleaved, !inverse, factor);
-        if (dq.defined()) out[0] = back[0];
-        if (dk.defined()) out[1] = back[dq.defined() ? 1 : 0];
+        at::Tensor pos;
+        {
+            std::lock_guard<std::mutex> lock(mutex_);
+            if (has_positions) pos = positions.unpack();
+        }
+        const Turn back{how.turns, how.interleaved, !how.inverse, how.factor};
+        const auto r = turn_rows(rows_of(dq.defined() ? dq : dk), dq.defined() && dk.defined() ? rows_of(dk) : at::Tensor(), pos, back);
+        if (dq.defined()) out[0] = r.first;
+        if (dk.defined()) out[1] = dq.defined() ? r.second : r.first;
         return out;
     }
+    void release_variables() override {
+        std::lock_guard<std::mutex> lock(mutex_);
+        positions.reset_data();
+    }
 };
+
+// k and pos may be undefined; so is the second result then.
+std::pair<at::Tensor, at::Tensor> turn_rows(const at::Tensor& q, const at::Tensor& k, const at::Tensor& pos, const Turn& how) {
+    const at::Tensor *kp = k.defined() ? &k : nullptr, *pp = pos.defined() ? &pos : nullptr;
+    fa_rope_args x = rope_args(q, kp, how.turns, pp, how.interleaved, how.inverse, how.factor);
+    const int dev = cuda_device("rotary", q, {kp, pp});
+    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)dev);
+    const cudaStream_t stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream();
+    const at::Tensor qo = out_like(q), ko = kp != nullptr ? out_like(k) : at::Tensor();
+    rope_outputs(x, qo, ko);
+    const fa_status st = PyGILState_Check() ? unlocked([&] { return lib.rope(&x, stream); }) : lib.rope(&x, stream);
+    if (st != FA_OK) throw Failed(st, "fa_rope");
+    if (at::GradMode::is_enabled() && (q.requires_grad() || (kp != nullptr && k.requires_grad()))) {
+        std::shared_ptr<TurnBackward> node(new TurnBackward(), torch::autograd::deleteNode);
+        node->how = how;
+        if (pp != nullptr) {
+            node->positions = torch::autograd::SavedVariable(pos, false);
+            node->has_positions = true;
+        }
+        // (an input that needs no gradient has no edge)
+        if (kp != nullptr) node->set_next_edges(torch::autograd::collect_next_edges(q, k));
+        else node->set_next_edges(torch::autograd::collect_next_edges(q));
+        torch::autograd::set_history(qo, node);
+        if (kp != nullptr) torch::autograd::set_history(ko, node);
+    }
+    return {qo, ko};
+}
 
 // (q, k, turns, positions, interleaved, factor)
 PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -563,9 +585,9 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &q = tensor(a[0], "q"), &turns = tensor(a[2], "turns");
         const at::Tensor *k = maybe_tensor(a[1], "k"), *pos = maybe_tensor(a[3], "positions");
         try {
-            const auto some = [](const at::Tensor* t) { return t != nullptr ? std::optional<at::Tensor>(*t) : std::nullopt; };
-            const auto out = Rotary::apply(q, some(k), turns, some(pos), flag_arg(a[4]) != 0, false, (double)float_arg(a[5]));
-            return pair(out[0], out.size() > 1 ? out[1] : at::Tensor());
+            const Turn how{turns, flag_arg(a[4]) != 0, false, (double)float_arg(a[5])};
+            const auto out = turn_rows(q, k != nullptr ? *k : at::Tensor(), pos != nullptr ? *pos : at::Tensor(), how);
+            return pair(out.first, out.second);
         } catch (const Failed& f) {
             check(f.status, "fa_rope");
             throw;
