@@ -238,9 +238,13 @@ fa_status fa_cache_score(const fa_cache_score_args* args, cudaStream_t stream) {
     a.stream = stream;
     const bool bf16 = x.dtype == FA_DTYPE_BF16;
     const fa::ScoreTileFacts tile = fa::score_tile_facts(c.D);
-    // More than 16 rows of a (sequence, kv head) run on the tile kernel, which needs a
-    // whole group in a tile.
-    a.tiles = G <= tile.rows && (int64_t)x.T * G > 16;
+    // Up to 32 rows of a (sequence, kv head), 16 at D = 256, run on the rows kernel, the
+    // others on the tile kernel, which needs a whole group in a tile.  Both sides, rows
+    // against tile kernel, repeated in a graph, 16 sequences of 1000-4000, Hkv 8: 32 rows
+    // 18.7 / 25.5 us at D 128, 14.7 / 23.8 at D 64, 12.9 / 23.7 at D 16; 32 rows of one
+    // sequence of 1024 3.7 / 7.4, of 64 of 256-4096 67.8 / 75.2; 16 rows, D 256 and Hkv 4,
+    // 13.6 / 20.4, 32 rows 25.2 / 20.
+    a.tiles = G <= tile.rows && (int64_t)x.T * G > (c.D == 256 ? 16 : 32);
     CUtensorMap mq{}, mk{};
     if (a.tiles) {
         while (G << (p.token_shift + 1) <= tile.rows) ++p.token_shift;

@@ -13,10 +13,13 @@
 //
 // What bounds it is reading and writing each row once.  A thread takes 8 pairs (two
 // 16-byte pieces) of a token through some of its heads, so that a sine and cosine serve
-// several heads; the loads go out before the sines are worked out.  671 MB (32 + 8 heads of
-// D = 128, 32768 tokens): 98 us, 6.8 TB/s, a plain copy's rate.  The turns come with the
+// several heads; the loads go out before the sines are worked out, and where the rows go is
+// only looked at when they are there.  671 MB (32 + 8 heads of D = 128, 32768 tokens): 98
+// us, 6.8 TB/s, a plain copy's rate; five prompts of 1006 to 2011 tokens into the cache (123
+// MB) 24 us, 5.2 TB/s.  The turns come with the
 // launch's arguments: read from one place in global memory by every warp, through L2,
-// they took 367 us (one L2 slice serves them all).  One token: 1.9 us.
+// they took 367 us (one L2 slice serves them all).  One token: 1.9 us, 64 tokens into the
+// cache 2.8.
 #include "fa_rope.h"
 
 #include <cuda_bf16.h>
@@ -120,20 +123,14 @@ __global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const __grid_cons
     const int z = blockIdx.z * ((ROPE_THREADS >> shift) >> p.token_shift) + (token >> p.token_shift);
     const int n = (int)(blockIdx.x << p.token_shift) + (token & ((1 << p.token_shift) - 1));
     if (n >= p.N || z >= p.Z) return;
-    int64_t slot = 0;
+    uint32_t position = (uint32_t)n, col = 0;
     int page = -1;
-    uint32_t position = (uint32_t)n;
     if constexpr (CACHE) {
-        const int nl = p.news != nullptr ? ldi(p.news + z) : p.N;
+        const int nl = p.news != nullptr ? ldi(p.news + z) : p.N, len = ldi(p.lens + z);
         if (n >= nl) return;
-        position += (uint32_t)max(ldi(p.lens + z), 0);  // below 2^32: the slot
-        const uint32_t col = position / (uint32_t)p.page;
+        position += (uint32_t)max(len, 0);  // below 2^32: the slot
+        col = position / (uint32_t)p.page;
         page = col < (uint32_t)p.M ? ldi(p.table + z * p.st_z + col) : -1;
-        slot = position - col * (uint32_t)p.page;
-        if ((unsigned)page >= (unsigned)p.P) {
-            bad_page(p.status, SITE_PAGE_APPEND);
-            page = -1;
-        }
     }
     int64_t at = position;
     if (p.positions != nullptr) at = ldi(p.positions + z * p.pos_z + n);
@@ -146,37 +143,20 @@ __global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const __grid_cons
     const int apart = INTER || !turns ? V : p.R / 2;
     const int h0 = blockIdx.y * p.heads, h1 = min(h0 + p.heads, p.Hq + p.Hk + (CACHE ? p.Hk : 0));
     Pairs<V> x[U];
-    uint16_t* to[U];
-    bool rope[U];
+    // head i: of q, then of k, then (into a cache) of v
     auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = h + u;
-            to[u] = nullptr;
             if (i >= h1) continue;
             const uint16_t* from;
-            if (i < p.Hq) {
-                from = p.q + z * p.q_z + i * p.q_h + n * p.q_n;
-                if (turns || !p.q_in_place) to[u] = p.qo + z * p.qo_z + i * p.qo_h + n * p.qo_n;
-                rope[u] = turns;
-            } else if (i < p.Hq + p.Hk) {
-                from = p.k + z * p.k_z + (i - p.Hq) * p.k_h + n * p.k_n;
-                if constexpr (CACHE) {
-                    if (page >= 0) to[u] = p.kc.base + page * p.kc.p + (i - p.Hq) * p.kc.h + slot * p.kc.n;
-                } else if (turns || !p.k_in_place) {
-                    to[u] = p.ko + z * p.ko_z + (i - p.Hq) * p.ko_h + n * p.ko_n;
-                }
-                rope[u] = turns;
-            } else {
-                from = p.v + z * p.v_z + (i - p.Hq - p.Hk) * p.v_h + n * p.v_n;
-                if (page >= 0) to[u] = p.vc.base + page * p.vc.p + (i - p.Hq - p.Hk) * p.vc.h + slot * p.vc.n;
-                rope[u] = false;
-            }
+            if (i < p.Hq) from = p.q + z * p.q_z + i * p.q_h + n * p.q_n;
+            else if (!CACHE || i < p.Hq + p.Hk) from = p.k + z * p.k_z + (i - p.Hq) * p.k_h + n * p.k_n;
+            else from = p.v + z * p.v_z + (i - p.Hq - p.Hk) * p.v_h + n * p.v_n;
             x[u] = load_pairs<V>(from + first, apart);
         }
     };
-    load(h0);
-    // the angles while the first rows are on their way
+    load(h0);  // (the table entry and the position are on their way too)
     float c[V], s[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -186,14 +166,37 @@ __global__ void __launch_bounds__(ROPE_THREADS) fa_rope_kernel(const __grid_cons
         c[i] *= p.cos_factor;
         s[i] *= p.sin_factor;
     }
+    int64_t slot = 0;
+    if constexpr (CACHE) {
+        slot = position - col * (uint32_t)p.page;
+        if ((unsigned)page >= (unsigned)p.P) {
+            bad_page(p.status, SITE_PAGE_APPEND);
+            page = -1;
+        }
+    }
     for (int h = h0; h < h1; h += U) {
         if (h > h0) load(h);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (to[u] != nullptr) {
-                if (rope[u]) turn<BF16, INTER, V>(x[u], c, s);
-                store_pairs<V>(to[u] + first, apart, x[u]);
+        for (int u = 0; u < U; ++u) {
+            const int i = h + u;
+            if (i >= h1) continue;
+            uint16_t* to = nullptr;
+            bool rope = turns;
+            if (i < p.Hq) {
+                if (turns || !p.q_in_place) to = p.qo + z * p.qo_z + i * p.qo_h + n * p.qo_n;
+            } else if (!CACHE) {
+                if (turns || !p.k_in_place) to = p.ko + z * p.ko_z + (i - p.Hq) * p.ko_h + n * p.ko_n;
+            } else if (i < p.Hq + p.Hk) {
+                if (page >= 0) to = p.kc.base + page * p.kc.p + (i - p.Hq) * p.kc.h + slot * p.kc.n;
+            } else {
+                if (page >= 0) to = p.vc.base + page * p.vc.p + (i - p.Hq - p.Hk) * p.vc.h + slot * p.vc.n;
+                rope = false;
             }
+            if (to != nullptr) {
+                if (rope) turn<BF16, INTER, V>(x[u], c, s);
+                store_pairs<V>(to + first, apart, x[u]);
+            }
+        }
     }
 }
 
@@ -213,8 +216,8 @@ cudaError_t launch_v(RopeParams p, bool cache, int sms, cudaStream_t stream) {
     };
     // Eight heads a thread, all in flight, where that leaves 16 CTAs an SM (98 against 108
     // us for 40 heads x 32768 tokens of D = 128, 40 against 47 for the cache's 48 x 10055),
-    // else four (13.3 / 10.6 us for 32 x 4096), and with few tokens fewer, so that there
-    // are CTAs for every SM.
+    // else four (10.6 against 13.3 us for 32 x 4096), and with few tokens fewer, so that there
+    // are CTAs for every SM.  (Figures of before the addresses moved behind the loads.)
     if constexpr (V == 8)
         if (blocks(8) >= 16 * (int64_t)sms)
             return launch(fa_rope_kernel<BF16, INTER, V, true, 8>, fa_rope_kernel<BF16, INTER, V, false, 8>, 8);

@@ -51,9 +51,11 @@ static cudaError_t launch_tiles(const ScoreLaunch& a) {
 #define FA_CAT(a, b) FA_CAT2(a, b)
 cudaError_t FA_CAT(launch_score_d, FA_HEAD_DIM)(const ScoreLaunch& a, bool bf16) {
     if (a.tiles) return bf16 ? launch_tiles<true>(a) : launch_tiles<false>(a);
-    const bool one = (int64_t)a.params.T * a.params.G <= 8;
-    if (bf16) return one ? launch_rows<true, 1>(a) : launch_rows<true, 2>(a);
-    return one ? launch_rows<false, 1>(a) : launch_rows<false, 2>(a);
+    const int64_t rows = (int64_t)a.params.T * a.params.G;
+    if (rows <= 8) return bf16 ? launch_rows<true, 1>(a) : launch_rows<false, 1>(a);
+    if constexpr (FA_HEAD_DIM <= 128)
+        if (rows > 16) return bf16 ? launch_rows<true, 4>(a) : launch_rows<false, 4>(a);
+    return bf16 ? launch_rows<true, 2>(a) : launch_rows<false, 2>(a);
 }
 
 }  // namespace fa

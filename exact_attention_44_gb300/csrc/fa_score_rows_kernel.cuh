@@ -8,7 +8,14 @@
 // in which order its D terms are taken, a thread's share of A's columns can be any as
 // long as B's is the same: 16 contiguous bytes of its two rows, which it loads straight
 // from the cache.  Nothing goes through shared memory.  A position's weights lie in
-// four neighbouring lanes and are summed there, in fp32.
+// four neighbouring lanes and are summed there, in fp32.  Rows that do not fit in registers
+// (more than 32, groups wider than a tile) are loaded again for every step.
+//
+// What hides the way to memory is the number of warps: one step of K in 32 registers, 20
+// warps an SM for up to 8 rows.  Measured: 64 sequences of 256-4096 positions, one token,
+// 32 query heads on 8 of D = 128 (294 MB with the scores): 51 us, 5.8 TB/s (8000-12000: 214
+// us, 6.3 TB/s); with two steps in registers and 16 warps 54.  One sequence of 1024: 3.1 us.
+// 12 warps an SM 61 us, 28 (72 registers, spilled) 65.
 #pragma once
 
 #include "fa_ptx.cuh"
@@ -25,7 +32,7 @@ struct ScoreRows {
     static constexpr int KT = 16 * U;
     static constexpr int PW = D >= 32 ? 4 : 2;         // words a thread loads of a row at a time
     static constexpr int NP = D / (8 * PW);            // such pieces of a row
-    static constexpr int ctas(int nt) { return D == 256 ? 3 : nt == 1 ? 5 : 4; }  // an SM
+    static constexpr int ctas(int nt) { return D == 256 || (D == 128 && nt == 4) ? 3 : nt == 1 ? 5 : 4; }  // an SM
 };
 
 namespace score {

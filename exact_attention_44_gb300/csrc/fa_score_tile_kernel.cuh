@@ -23,6 +23,18 @@
 // sixteen warps take the exponentials: a quarter of the lanes each (a warp reaches only its
 // own quarter of tensor memory), of one half of the positions, of a group of columns.
 // Every wait is bounded as in fa_fwd_kernel.cuh.
+//
+// What bounds it.  With one tile a unit, DRAM: 32 sequences of 4096-8192 x 128 rows (417 MB)
+// take 72 to 75 us, 5.6 to 5.8 TB/s, about 6 of them from launch to the first weights.  With
+// many, the sixteen warps: 1600 cycles a tile of 256 positions x 128 rows, of which the two
+// warps of a pair spend 1050 on 64 exponentials a thread each and the rest on the wait, the
+// load of the scores and the loop; the products take 1000 of them (four prompts of 2000 tokens
+// after 0-3000, 164 GFLOP: 126 to 130 us on normal data, 1.3 PFLOP/s, 0.67 of the measured
+// bf16 peak; tensor pipe 55 % busy).  On the way there, in us (constant lse, 32 heads):
+// 228 with lse from shared memory and one issuer; 214 with the comparisons in a loop of their
+// own; 200 with the halves' slots apart; 186 with two issuers and one barrier for scores and
+// lse; 177 with lse in the product and the scores read at once; 168 with four slots for Q;
+// 156 with a quarter of the instructions where lse is staged.
 #pragma once
 
 #include <climits>
