@@ -12,14 +12,17 @@ seen, which runs ahead of seq_lens once positions have been evicted):
 
     fa_cache_fork(k, v, table, lens, refs, source, room=1, missing=missing, all_or_nothing=True)
     for i in range(layers):
-        q = fa_cache_append_rope(q[i], k_new[i], v_new[i], k[i], v[i], table, lens, turns, positions=positions)
-        o, lse = fa_fwd_paged(q, k[i], v[i], table, lens)
-        fa_cache_score(q, lse, k[i], table, lens, scores[i])
+        qi = fa_cache_append_rope(q[i], k_new[i], v_new[i], k[i], v[i], table, lens, turns,
+                                  positions=positions[:, None])
+        o, lse = fa_fwd_paged(qi, k[i], v[i], table, lens)
+        fa_cache_score(qi, lse, k[i], table, lens, scores[i])
     lens += 1
     positions += 1
     fa_cache_evict(k, v, table, lens, refs, scores, budget, missing, keep=keep)   # now and then
 
-Everything is argument marshalling, and no call synchronises.
+A sequence's scores follow it only where the caller moves them: after a fork that gives
+sequence z the cache of another, scores[:, z] = scores[:, source[z]].  Everything is
+argument marshalling, and no call synchronises.
 """
 from __future__ import annotations
 

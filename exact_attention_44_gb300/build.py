@@ -7,11 +7,11 @@ ignored).  A content hash of the sources, headers and flags is stored next to
 the library; an unchanged tree is not rebuilt.  --debug-checks builds a
 second library, _build/checks/libfa.so, whose forward kernels check every
 unit they decode against the launch's sizes (FA_DEBUG_CHECKS=1).  Where torch
-with CUDA is installed, the binding of the paged-cache calls (_paged_ext.so, a CPython
-extension over torch's headers) is built beside libfa.so with g++, under a hash of
-its own.  The library does not need it: if it cannot be compiled, the compiler's
-output is printed, the library is built all the same, and the paged-cache calls of
-the package raise ImportError.
+with CUDA is installed, the binding of the paged-cache and rotary calls (_paged_ext.so,
+a CPython extension over torch's headers) is built beside libfa.so with g++, under a
+hash of its own.  The library does not need it: if it cannot be compiled, the
+compiler's output is printed, the library is built all the same, and those calls of the
+package raise ImportError.
 """
 from __future__ import annotations
 

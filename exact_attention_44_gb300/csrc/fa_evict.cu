@@ -13,7 +13,7 @@
 // selection a position.  32 sequences of 1500-2900 positions cut to 1024, 8 layers x 8 heads
 // of D = 128 (2.2 GB): the rows 318 us, 6.7 TB/s, a plain copy's rate; in all 361 us.  One
 // sequence of 1200, 16 layers (134 MB): 8.5 us to select, 7.6 for the books, 23.5 to move, 32
-// in all.
+// in all, of which the books are one CTA's chain of dependent loads.
 #include "fa_evict.h"
 
 #include <climits>

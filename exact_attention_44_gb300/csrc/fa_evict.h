@@ -25,11 +25,10 @@ struct EvictParams {
     int32_t* ws;                     // evict_workspace_ints(L, Z, H, M, budget)
     uint32_t* status;
 };
-// per sequence: length it is cut to (-1: it stays as it is), first page it needs of its
-// own, place in the page list; the number of pages lacking (-1: none is
-// replaced); each sequence's table row as
-// it was and as it will be; the page list; per (layer, sequence, head) the first row that
-// moves and the positions that stay
+// per sequence: length it is cut to (-1: it stays as it is), first page it needs of its own,
+// place in the page list; the number of pages lacking (-1: none is replaced); each sequence's
+// table row as it was and as it will be; the page list; per (layer, sequence, head) the first
+// row that moves and the positions that stay
 inline int64_t evict_workspace_ints(int64_t L, int64_t Z, int64_t H, int64_t M, int64_t budget) {
     return 3 * Z + 1 + 3 * Z * M + L * Z * H * (1 + budget);
 }

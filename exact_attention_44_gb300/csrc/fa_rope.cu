@@ -16,10 +16,9 @@
 // several heads; the loads go out before the sines are worked out, and where the rows go is
 // only looked at when they are there.  671 MB (32 + 8 heads of D = 128, 32768 tokens): 98
 // us, 6.8 TB/s, a plain copy's rate; five prompts of 1006 to 2011 tokens into the cache (123
-// MB) 24 us, 5.2 TB/s.  The turns come with the
-// launch's arguments: read from one place in global memory by every warp, through L2,
-// they took 367 us (one L2 slice serves them all).  One token: 1.9 us, 64 tokens into the
-// cache 2.8.
+// MB) 24 us, 5.2 TB/s.  The turns come with the launch's arguments: read from one place in
+// global memory by every warp, through L2, they took 367 us (one L2 slice serves them all).
+// One token: 1.9 us, 64 tokens into the cache 2.8.
 #include "fa_rope.h"
 
 #include <cuda_bf16.h>

@@ -28,10 +28,12 @@
 // take 72 to 75 us, 5.6 to 5.8 TB/s, about 6 of them from launch to the first weights.  With
 // many, the sixteen warps: 1600 cycles a tile of 256 positions x 128 rows, of which the two
 // warps of a pair spend 1050 on 64 exponentials a thread each and the rest on the wait, the
-// load of the scores and the loop; the products take 1000 of them (four prompts of 2000 tokens
-// after 0-3000, 164 GFLOP: 126 to 130 us on normal data, 1.3 PFLOP/s, 0.67 of the measured
-// bf16 peak; tensor pipe 55 % busy).  On the way there, in us (constant lse, 32 heads):
-// 228 with lse from shared memory and one issuer; 214 with the comparisons in a loop of their
+// load of the scores and the loop; the products take 1000 of them, and the special function
+// units, which give a warp's exponential in 4 cycles, 1024.  Four prompts of 1000 to 2000
+// tokens after 0 to 3000 positions, 111 GFLOP: 113 us repeated in a graph, 126 to 130 on new
+// inputs, 0.98 to 0.85 PFLOP/s, half of the measured bf16 peak (tensor pipe 55 % busy).  On
+// the way there, in us, four prompts of 2000 tokens each (164 GFLOP, 84 us at that peak,
+// constant lse, 32 heads): 228 with lse from shared memory and one issuer; 214 with the comparisons in a loop of their
 // own; 200 with the halves' slots apart; 186 with two issuers and one barrier for scores and
 // lse; 177 with lse in the product and the scores read at once; 168 with four slots for Q;
 // 156 with a quarter of the instructions where lse is staged.

@@ -41,7 +41,8 @@ def score(q, lse, k, lens, new, scores, decay, scale):
     list of (Hkv, lens[z] + new[z], D).
 
     A score is a sum of D products, exact in fp32, added by the tensor core (which may truncate): off by at most
-    (D + 2) 2^-23 sum |q k| |scale|; its difference to lse, in one rounding, and that times log2 e by 2^-23 of the
+    (D + 2) 2^-23 sum |q k| |scale|; its difference to lse, in one rounding (or as the last products of the same
+    sum, three 16-bit pieces of lse / scale that hold 24 bits of it), and that times log2 e by 2^-23 of the
     difference; the exponential by 2^-22.  A sum of n weights in fp32 is off by n 2^-24 of itself, joining decay
     times the old score adds two roundings."""
     Z, Hq, T, D = q.shape
