@@ -31,8 +31,9 @@ fa_status check_turns(const void* turns, const void* positions, int64_t position
     if (turns == nullptr || positions_stride < 0) return FA_ERR_INVALID_ARG;
     return check_ints(positions, false);
 }
-bool same_place(const void* a, const fa_strides& sa, const void* b, const fa_strides& sb) {
-    return a == b && sa.b == sb.b && sa.h == sb.h && sa.n == sb.n;
+// The same rows: one address and the same strides where there is more than one row to step to.
+bool same_place(const void* a, const fa_strides& sa, const void* b, const fa_strides& sb, int64_t Z, int64_t H, int64_t N) {
+    return a == b && (Z <= 1 || sa.b == sb.b) && (H <= 1 || sa.h == sb.h) && (N <= 1 || sa.n == sb.n);
 }
 
 fa_status launch_score(int D, const fa::ScoreLaunch& a, bool bf16) {
@@ -101,8 +102,11 @@ fa_status fa_rope(const fa_rope_args* args, cudaStream_t stream) {
     if ((st = check_strided(x.k, &x.sk, x.Z, x.Hk, x.N, false)) != FA_OK) return st;
     if ((st = check_strided(x.k_out, &x.sk_out, x.Z, x.Hk, x.N, true)) != FA_OK) return st;
     if ((st = check_turns(x.turns, x.positions, x.positions_stride)) != FA_OK) return st;
-    // one tensor's output in place of the other tensor
+    // one tensor's output in place of the other tensor, or of its own in another layout
     if (x.Hq > 0 && x.Hk > 0 && (x.q_out == x.k_out || x.q_out == x.k || x.k_out == x.q)) return FA_ERR_INVALID_ARG;
+    const bool q_same = x.Hq > 0 && same_place(x.q, x.sq, x.q_out, x.sq_out, x.Z, x.Hq, x.N);
+    const bool k_same = x.Hk > 0 && same_place(x.k, x.sk, x.k_out, x.sk_out, x.Z, x.Hk, x.N);
+    if ((x.Hq > 0 && x.q == x.q_out && !q_same) || (x.Hk > 0 && x.k == x.k_out && !k_same)) return FA_ERR_INVALID_ARG;
     fa::DeviceFacts f;
     const cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
@@ -115,8 +119,8 @@ fa_status fa_rope(const fa_rope_args* args, cudaStream_t stream) {
     p.k_z = x.sk.b, p.k_h = x.sk.h, p.k_n = x.sk.n;
     p.qo_z = x.sq_out.b, p.qo_h = x.sq_out.h, p.qo_n = x.sq_out.n;
     p.ko_z = x.sk_out.b, p.ko_h = x.sk_out.h, p.ko_n = x.sk_out.n;
-    p.q_in_place = same_place(x.q, x.sq, x.q_out, x.sq_out);
-    p.k_in_place = same_place(x.k, x.sk, x.k_out, x.sk_out);
+    p.q_in_place = q_same;
+    p.k_in_place = k_same;
     p.positions = x.positions;
     p.pos_z = x.positions_stride;
     std::memcpy(p.turns, x.turns, (size_t)x.rotary_dim / 2 * sizeof(int64_t));  // (at most 128: D is 256 at most)
@@ -146,6 +150,8 @@ fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream
     if ((st = check_ints(x.new_lens, false)) != FA_OK) return st;
     if ((st = check_turns(x.turns, x.positions, x.positions_stride)) != FA_OK) return st;
     if (x.Hq > 0 && c.Hkv > 0 && (x.q_out == x.k || x.q_out == x.v)) return FA_ERR_INVALID_ARG;
+    const bool q_same = x.Hq > 0 && same_place(x.q, x.sq, x.q_out, x.sq_out, c.Z, x.Hq, x.T);
+    if (x.Hq > 0 && x.q == x.q_out && !q_same) return FA_ERR_INVALID_ARG;
     fa::DeviceFacts f;
     const cudaError_t err = fa::device_facts(&f);
     if (err != cudaSuccess) return fa::report_cuda("device query", err);
@@ -158,7 +164,7 @@ fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream
     p.k_z = x.sk.b, p.k_h = x.sk.h, p.k_n = x.sk.n;
     p.v_z = x.sv.b, p.v_h = x.sv.h, p.v_n = x.sv.n;
     p.qo_z = x.sq_out.b, p.qo_h = x.sq_out.h, p.qo_n = x.sq_out.n;
-    p.q_in_place = same_place(x.q, x.sq, x.q_out, x.sq_out);
+    p.q_in_place = q_same;
     p.positions = x.positions;
     p.pos_z = x.positions_stride;
     std::memcpy(p.turns, x.turns, (size_t)x.rotary_dim / 2 * sizeof(int64_t));  // (at most 128: D is 256 at most)

@@ -520,9 +520,11 @@ at::Tensor rows_of(const at::Tensor& t) {
 using torch::autograd::variable_list;
 struct Turn {  // how rows turn, but for the rows
     at::Tensor turns;
+    int64_t version;  // of turns when the graph was made
     bool interleaved, inverse;
     double factor;
 };
+int64_t version_of(const at::Tensor& t) { return t.is_inference() ? 0 : (int64_t)t._version(); }
 std::pair<at::Tensor, at::Tensor> turn_rows(const at::Tensor& q, const at::Tensor& k, const at::Tensor& pos, const Turn& how);
 
 struct TurnBackward : public torch::autograd::Node {
@@ -539,7 +541,9 @@ struct TurnBackward : public torch::autograd::Node {
             std::lock_guard<std::mutex> lock(mutex_);
             if (has_positions) pos = positions.unpack();
         }
-        const Turn back{how.turns, how.interleaved, !how.inverse, how.factor};
+        if (version_of(how.turns) != how.version)
+            throw std::runtime_error("rotary: turns, needed for the gradient, has been modified by an inplace operation");
+        const Turn back{how.turns, how.version, how.interleaved, !how.inverse, how.factor};
         const auto r = turn_rows(rows_of(dq.defined() ? dq : dk), dq.defined() && dk.defined() ? rows_of(dk) : at::Tensor(), pos, back);
         if (dq.defined()) out[0] = r.first;
         if (dk.defined()) out[1] = dq.defined() ? r.second : r.first;
@@ -585,7 +589,7 @@ PyObject* rotary(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &q = tensor(a[0], "q"), &turns = tensor(a[2], "turns");
         const at::Tensor *k = maybe_tensor(a[1], "k"), *pos = maybe_tensor(a[3], "positions");
         try {
-            const Turn how{turns, flag_arg(a[4]) != 0, false, (double)float_arg(a[5])};
+            const Turn how{turns, version_of(turns), flag_arg(a[4]) != 0, false, (double)float_arg(a[5])};
             const auto out = turn_rows(q, k != nullptr ? *k : at::Tensor(), pos != nullptr ? *pos : at::Tensor(), how);
             return pair(out.first, out.second);
         } catch (const Failed& f) {

@@ -629,7 +629,7 @@ fa_status fa_rope_turns(int pairs, const double* inv_freq, int64_t* turns);
  * fa_rope -- turn the rows of q and k (either may have no heads).  inverse 1 turns back
  * (still times factor): the gradient of the same call.  Outputs may be the inputs (same
  * pointer and strides); they must not overlap them, or each other, otherwise (an output at
- * the other tensor's address is refused).  Any even
+ * the other tensor's address, or at its own in another layout, is refused).  Any even
  * rotary_dim up to D; D in {16, 32, 64, 128, 256}; fp16 / bf16; strides as for fa_fwd,
  * inputs of stride 0 included.  Z and Hq + Hk <= 65535, N <= 2^30.
  */

@@ -139,6 +139,7 @@ I, U, A, W, OK = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED, fa.FA_ERR_ALIGNME
     (dict(Z=65536), U), (dict(Hq=65535), U), (dict(N=(1 << 30) + 1), U), (dict(q=PTR + 8), A), 
     (dict(pos=PTR + 2), A), (dict(so=_st(768, 190, 64)), A), (dict(so=_st(768, 192, 64, 2)), A),
     (dict(ko=PTR), I), (dict(qo=PTR + 4096), I), (dict(ko=PTR, k=PTR + 64), I),
+    (dict(so=_st(1536, 384, 128)), I), (dict(so=_st(8, 192, 64), Z=1, N=0), OK),
     (dict(Z=0), OK), (dict(N=0), OK), (dict(Hq=0, Hk=0), OK),
 ])
 def test_rope_arguments(lib, kw, code):
@@ -156,13 +157,13 @@ def test_rope_arguments(lib, kw, code):
     (dict(q=None), I), (dict(v=None), I), (dict(kc=None), I), (dict(turns=None), I), (dict(lens=None), I),
     (dict(sc=_st(0, 1024, 64)), I), (dict(dtype=-1), U), (dict(D=40), U), (dict(page=24), U), (dict(T=(1 << 30) + 1), U),
     (dict(k=PTR + 2), A), (dict(new=PTR + 1), A), (dict(pos=PTR + 1), A), (dict(qo=PTR + 4096), I),
-    (dict(Z=0), OK), (dict(T=0), OK),
+    (dict(so=_st(1536, 384, 128)), I), (dict(Z=0), OK), (dict(T=0), OK),
 ])
 def test_append_rope_arguments(lib, kw, code):
-    k = dict(q=PTR, qo=PTR, k=PTR + 4096, v=PTR + 4096, turns=PTR, pos=None, new=None, T=3, Hq=4, R=32, inter=0, factor=1.0, dtype=1) | kw
+    k = dict(q=PTR, qo=PTR, k=PTR + 4096, v=PTR + 4096, turns=PTR, pos=None, new=None, T=3, Hq=4, R=32, inter=0, factor=1.0, dtype=1, so=None) | kw
     c = _cache(**{n: k.pop(n) for n in list(k) if n in ("kc", "lens", "L", "sc", "D", "page", "Z")})
     st = _st(4 * k["T"] * c.D, k["T"] * c.D, c.D)
-    a = AppendRope(c, k["q"], k["qo"], k["k"], k["v"], st, st, st, st, k["new"], k["pos"], 0, k["turns"], k["Hq"], k["T"], k["R"],
+    a = AppendRope(c, k["q"], k["qo"], k["k"], k["v"], st, k["so"] or st, st, st, k["new"], k["pos"], 0, k["turns"], k["Hq"], k["T"], k["R"],
                    k["inter"], k["factor"], k["dtype"])
     assert lib.fa_cache_append_rope(ctypes.addressof(a), None) == code
 

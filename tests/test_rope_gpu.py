@@ -302,6 +302,16 @@ def test_positions_changed_between_the_directions_are_noticed():
         y.sum().backward()
 
 
+def test_turns_changed_between_the_directions_are_noticed():
+    import exact_attention_44_gb300 as fa
+    x = torch.randn(1, 2, 9, 64, device="cuda").half().requires_grad_()
+    turns = turns_of(64)
+    y, _ = fa.rotary(x, None, turns)
+    turns += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.sum().backward()
+
+
 def test_backward_in_a_graph_and_on_another_stream():
     """Forward and backward of a layer (rotary, then attention) captured in a CUDA graph replay to the eager bits; and
     a side stream's gradients are that stream's."""
