@@ -77,7 +77,7 @@ struct ScoreTile {
     static constexpr int OFF_LSE = OFF_QL + LR * QL_BYTES;          // [LR][BR] -lse log2 e, where it has no pieces
     static constexpr int OFF_LAST = OFF_LSE + LR * BR * 4;          // [LR][BR] last position seen
     static constexpr int OFF_SUM = OFF_LAST + LR * BR * 4;          // [2][NCG][KB]
-    static constexpr int OFF_FLAG = OFF_SUM + 2 * NCG * KB * 4;     // [LR] a tile that needs no comparisons
+    static constexpr int OFF_FLAG = OFF_SUM + 2 * NCG * KB * 4;     // [LR] last position that a tile's first token sees
     static constexpr int OFF_SEG = OFF_FLAG + LR * 4;
     static constexpr int OFF_BAR = OFF_SEG + SEGS * 48;
     static constexpr int B_KFULL = 0;
@@ -420,8 +420,11 @@ __device__ __forceinline__ void constants3(uint32_t& w0, uint32_t& w1) {  // 1, 
 
 // Each tile's lse and the last position that each of its rows sees, a warp, the loads two
 // tiles ahead.  A row that does not count (no token, nothing seen) sees nothing; columns
-// behind the tile's rows are products with zeros.  A tile all of whose rows see all of the
-// block, their lse in pieces, needs no comparisons.
+// behind the tile's rows are products with zeros.  A tile all of whose rows are tokens, their
+// lse in pieces, hands on the last position that its first token sees: a warp whose positions
+// are all seen by its columns' first token needs no comparisons, and one whose positions are
+// seen by none has nothing to add (on a prompt's diagonal most warps are either: with one
+// answer for the whole block the ranges there took 159000 cycles, the others 110000).
 template <int D, bool BF16>
 __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* smem, uint32_t bar0, const Ctl& ctl) {
     using T = ScoreTile<D>;
@@ -468,8 +471,7 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
     int* flags = reinterpret_cast<int*>(smem + T::OFF_FLAG);
     auto finish = [&](const Tile& t) -> bool {
         const int last0 = t.len + (t.i << p.token_shift), need = (t.j + 1) * T::KB - 1;
-        // every row of the tile a token that sees all of the block: all of them plain?
-        bool plain = p.tile_rows == p.tile_cols && t.whole && last0 >= need;
+        bool pure = p.tile_rows == p.tile_cols && t.whole;  // every row a token, its lse in pieces
         uint32_t w0[N], w1[N];
 #pragma unroll
         for (int x = 0; x < N; ++x) {
@@ -477,15 +479,16 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
             const bool pieces = fabsf(q) <= LIMIT;
             w0[x] = w1[x] = 0u;
             if (pieces) split3<BF16>(q, w0[x], w1[x]);
-            plain &= pieces || tok[x] == INT_MAX;
+            pure &= pieces || tok[x] == INT_MAX;
         }
-        plain = __all_sync(0xffffffffu, plain);
+        pure = __all_sync(0xffffffffu, pure);
         const uint32_t r = g % T::LR;
         if (!warp_wait_phase(bar(T::B_LEMPTY + r), ((g / T::LR) & 1u) ^ 1u, ctl, SITE_S_FREE)) return false;
         const uint32_t ql = ptx::smem_addr(smem + T::OFF_QL) + r * T::QL_BYTES;
 #pragma unroll
         for (int x = 0; x < N; ++x) ptx::st_shared_v4(ql + l_piece(x * 32 + lane), w0[x], w1[x], 0u, 0u);
-        if (!plain || p.tile_cols < T::BR) {  // (a group with fewer columns takes the comparisons' way)
+        // (a group with fewer columns takes the comparisons' way)
+        if (!pure || last0 < need || p.tile_cols < T::BR) {
             float* ls = reinterpret_cast<float*>(smem + T::OFF_LSE) + r * T::BR;
             int* la = reinterpret_cast<int*>(smem + T::OFF_LAST) + r * T::BR;
 #pragma unroll
@@ -496,7 +499,7 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
                 la[c] = t.l[x] != -INFINITY ? last0 + tok[x] : -1;
             }
         }
-        if (lane == 0) flags[r] = plain;
+        if (lane == 0) flags[r] = pure ? last0 : INT_MIN;
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
         ++g;
@@ -551,6 +554,7 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
     // columns of a group, a multiple of 16, and this one's (the last may have fewer)
     const int group = (p.tile_cols + 16 * T::NCG - 1) / (16 * T::NCG) * 16;
     const int col0 = min(cg * group, p.tile_cols), cols = min(group, p.tile_cols - col0);
+    const int tok0 = p.by_g(col0), tok1 = p.by_g(col0 + max(cols, 1) - 1);  // its first and last token
     float* sums = reinterpret_cast<float*>(smem + T::OFF_SUM);
     const int* flags = reinterpret_cast<const int*>(smem + T::OFF_FLAG);
     uint32_t g = 0;
@@ -570,9 +574,16 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
             if (!__all_sync(0xffffffffu, ready) &&
                 !warp_wait_phase(bar(T::B_SFULL + r * T::KH + half), (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
             ptx::tc_fence_after();
-            const bool plain = flags[lr] != 0;
+            // do the columns' first and last token see the warp's last and first position?
+            const int last = flags[lr], warp_pos = pos - lane;
+            const bool plain = last != INT_MIN && warp_pos + 31 <= last + tok0;
+            const bool none = last != INT_MIN && warp_pos > last + tok1;
             const uint32_t next = bar(T::B_SFULL + (g + 1) % T::SR * T::KH + half), next_ph = ((g + 1) / T::SR) & 1u;
-            if (plain && cols == COLS) {
+            if (none) {
+                __syncwarp();
+                if (lane < 2) ptx::mbar_arrive(lane == 0 ? bar(T::B_SEMPTY + r * T::KH + half) : bar(T::B_LEMPTY + lr));
+                ready = ptx::mbar_test_wait(next, next_ph);
+            } else if (plain && cols == COLS) {
                 // All of this warp's scores at once, so that their slot is free before they
                 // are used, and no comparisons (in one loop with the others they took 6.9
                 // instructions a weight).
