@@ -365,13 +365,16 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
                     ptx::tc_fence_after();
                     const uint32_t k_lo = k_lo0 + ((k.slot * T::K_BYTES + h * T::HALF_BYTES) >> 4);
                     const uint32_t d = tmem + (r * T::KH + h) * T::BR;
+                    // a half that the tile's last token does not see: whatever is there, nothing is added
+                    if (u.j * T::KB + h * 128 < u.len + ((i + 1) << p.token_shift)) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
-                        ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
-                                    ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
+                            ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
+                                        ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
+                        }
+                        ptx::mma_ss(d, kl, ql, IDESC, 1u);
                     }
-                    ptx::mma_ss(d, kl, ql, IDESC, 1u);
                     ptx::mbar_arrive(full);  // (hands on what stage_lse wrote)
                     ptx::tc_commit(full);
                 }
