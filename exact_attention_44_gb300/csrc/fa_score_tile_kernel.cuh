@@ -11,10 +11,12 @@
 // one more step of 16 of the contraction, the last one (its rounding then is that of the
 // result).  A unit of work is a block of KB positions of one (sequence, kv head):
 // its K stays in shared memory while the tiles of up to BR query rows that see it stream
-// by.  Units are laid end to end, counted in tiles, and cut into one equal range a CTA
-// (fa_score_sched.cuh); a unit that a cut crosses leaves its sums in slots of the
-// workspace, and fa_score_merge_kernel joins them in order.  Units of up to four tiles are
-// counted whole and not cut (p.parts is nullptr): the merge costs more than it evens out.
+// by.  Units are laid end to end, counted in tiles and UNIT_COST for each (a prompt's last
+// blocks are seen by few tiles: without it 96 us for the prompts below, with one tile 95), and
+// cut into one equal range a CTA (fa_score_sched.cuh); a unit that a cut crosses leaves its
+// sums in slots of the workspace, and fa_score_merge_kernel joins them in order.  Units of up
+// to four tiles are counted whole and not cut (p.parts is nullptr): the merge costs more than
+// it evens out.
 //
 // Roles: warp 0 walks the range, hands the units on and loads K through the block table
 // (a lane a box of rows) and Q; warps 1 and 3 issue the products of every second tile each
@@ -25,18 +27,20 @@
 // Every wait is bounded as in fa_fwd_kernel.cuh.
 //
 // What bounds it.  With one tile a unit, DRAM: 32 sequences of 4096-8192 x 128 rows (417 MB)
-// take 72 to 75 us, 5.6 to 5.8 TB/s, about 6 of them from launch to the first weights.  With
+// take 74 to 77 us, 5.5 to 5.7 TB/s, about 6 of them from launch to the first weights.  With
 // many, the sixteen warps: 1600 cycles a tile of 256 positions x 128 rows, of which the two
 // warps of a pair spend 1050 on 64 exponentials a thread each and the rest on the wait, the
-// load of the scores and the loop; the products take 1000 of them, and the special function
+// load of the scores and the loop; the products take 1150 of them, and the special function
 // units, which give a warp's exponential in 4 cycles, 1024.  Four prompts of 1000 to 2000
-// tokens after 0 to 3000 positions, 111 GFLOP: 113 us repeated in a graph, 126 to 130 on new
-// inputs, 0.98 to 0.85 PFLOP/s, half of the measured bf16 peak (tensor pipe 55 % busy).  On
+// tokens after 0 to 3000 positions, 111 GFLOP: 93 us repeated in a graph, 105 on new inputs,
+// 1.19 to 1.05 PFLOP/s, 0.61 to 0.54 of the measured bf16 peak (tensor pipe 56 % busy).  On
 // the way there, in us, four prompts of 2000 tokens each (164 GFLOP, 84 us at that peak,
-// constant lse, 32 heads): 228 with lse from shared memory and one issuer; 214 with the comparisons in a loop of their
-// own; 200 with the halves' slots apart; 186 with two issuers and one barrier for scores and
-// lse; 177 with lse in the product and the scores read at once; 168 with four slots for Q;
-// 156 with a quarter of the instructions where lse is staged.
+// constant lse, 32 heads): 228 with lse from shared memory and one issuer; 214 with the
+// comparisons in a loop of their own; 200 with the halves' slots apart; 186 with two issuers
+// and one barrier for scores and lse; 177 with lse in the product and the scores read at once;
+// 168 with four slots for Q; 156 with a quarter of the instructions where lse is staged; 136
+// with comparisons decided by each warp; 130 with UNIT_COST.  Not multiplying halves that a
+// tile does not see: no gain.
 #pragma once
 
 #include <climits>
@@ -138,6 +142,8 @@ struct Unit {
     int keep;                             // the next unit starts with the Q tile that this one ends with
 };
 
+// What a unit costs besides its tiles, in tiles: the way of its K to the first product.
+constexpr int UNIT_COST = 2;
 // Tiles of a sequence's rows, and which of them is the first that sees block j: the one
 // with token j KB - len.
 template <int D>
@@ -158,11 +164,11 @@ struct Shape {
     __device__ __forceinline__ int first(const ScoreParams& p, int j) const {
         return (int)max((int64_t)0, (int64_t)j * (T::KB >> p.token_shift) - lag);
     }
-    // tiles of blocks 0 .. j - 1, or (units are not cut) the blocks
+    // cost of blocks 0 .. j - 1, in tiles and UNIT_COST for each, or (units are not cut) the blocks
     __device__ __forceinline__ int64_t before(const ScoreParams& p, int j) const {
         if (p.parts == nullptr) return j;
         const int64_t r = T::KB >> p.token_shift, j0 = lag / r + 1;  // the first block with first() > 0
-        int64_t n = (int64_t)j * nt;
+        int64_t n = (int64_t)j * (nt + UNIT_COST);
         if (j > j0) n -= r * ((int64_t)(j - 1) * j - j0 * (j0 - 1)) / 2 - (int64_t)lag * (j - j0);
         return n;
     }
@@ -172,7 +178,7 @@ struct Shape {
 struct alignas(16) Cut {
     int z, hk, j, skip;   // tiles of the unit in front of the range
     int tiles, len, end, pad;
-    int64_t start, total; // in tiles
+    int64_t start, total; // the unit's next tile and the end of all, in cost
 };
 
 }  // namespace scoret
@@ -181,7 +187,7 @@ template <int D>
 struct ScoreWalk {
     using T = ScoreTile<D>;
     ScorePlace w;
-    int hk, j, i;  // the next tile: of the unit's, counted from first()
+    int hk, j, i;  // the next one of the unit's cost: UNIT_COST, then its tiles from first()
     __device__ __forceinline__ void start(const ScoreParams& p, const ScorePlace& place) {
         w = place;
         if (w.left == 0) return;
@@ -200,25 +206,28 @@ struct ScoreWalk {
     }
     // the next unit of the range; false at its end
     __device__ __forceinline__ bool next(const ScoreParams& p, scoret::Unit& u) {
-        if (w.left == 0) return false;
-        const scoret::Shape<D> s(p, w.s);
-        const int first = s.first(p, j), tiles = s.nt - first;
-        u.z = w.z, u.hk = hk, u.j = j, u.len = w.s.len, u.nl = w.s.nl;
-        u.i0 = first + i;
-        const int n = p.parts == nullptr ? tiles : (int)min((int64_t)(tiles - i), w.left);
-        u.i1 = u.i0 + n;
-        u.slot = i == 0 && n == tiles ? -1 : 2 * (int)blockIdx.x + (i > 0 ? 0 : 1);
-        w.left -= p.parts == nullptr ? 1 : n;
-        i = 0;
-        if (w.left > 0 && ++j == s.nb) {
-            j = 0;
-            if (++hk == p.Hkv) {
-                hk = 0;
-                do w.s = score_len(p, ++w.z);
-                while (scoret::Shape<D>(p, w.s).nb == 0);
+        while (w.left > 0) {
+            const scoret::Shape<D> s(p, w.s);
+            const int first = s.first(p, j), tiles = s.nt - first, ahead = p.parts == nullptr ? 0 : scoret::UNIT_COST;
+            const int take = p.parts == nullptr ? tiles : (int)min((int64_t)(ahead + tiles - i), w.left);
+            const int lo = max(i - ahead, 0), hi = max(i + take - ahead, 0);
+            u.z = w.z, u.hk = hk, u.j = j, u.len = w.s.len, u.nl = w.s.nl;
+            u.i0 = first + lo;
+            u.i1 = first + hi;
+            u.slot = lo == 0 && hi == tiles ? -1 : 2 * (int)blockIdx.x + (lo > 0 ? 0 : 1);
+            w.left -= p.parts == nullptr ? 1 : take;
+            i = 0;
+            if (w.left > 0 && ++j == s.nb) {
+                j = 0;
+                if (++hk == p.Hkv) {
+                    hk = 0;
+                    do w.s = score_len(p, ++w.z);
+                    while (scoret::Shape<D>(p, w.s).nb == 0);
+                }
             }
+            if (hi > lo) return true;  // (a range may end in front of a unit's first tile)
         }
-        return true;
+        return false;
     }
 };
 
@@ -365,16 +374,13 @@ __device__ void multiply(const ScoreParams& p, volatile int* ring, uint32_t sbas
                     ptx::tc_fence_after();
                     const uint32_t k_lo = k_lo0 + ((k.slot * T::K_BYTES + h * T::HALF_BYTES) >> 4);
                     const uint32_t d = tmem + (r * T::KH + h) * T::BR;
-                    // a half that the tile's last token does not see: whatever is there, nothing is added
-                    if (u.j * T::KB + h * 128 < u.len + ((i + 1) << p.token_shift)) {
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
-                            ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
-                                        ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
-                        }
-                        ptx::mma_ss(d, kl, ql, IDESC, 1u);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t in = ((kk * 16) % T::SWE) * 2, chunk = (kk * 16) / T::SWE;
+                        ptx::mma_ss(d, ptx::desc64(k_lo + ((chunk * (128 * T::SW) + in) >> 4), HI),
+                                    ptx::desc64(q_lo + ((chunk * (T::BR * T::SW) + in) >> 4), HI), IDESC, kk > 0 ? 1u : 0u);
                     }
+                    ptx::mma_ss(d, kl, ql, IDESC, 1u);
                     ptx::mbar_arrive(full);  // (hands on what stage_lse wrote)
                     ptx::tc_commit(full);
                 }
@@ -502,7 +508,7 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
                 la[c] = t.l[x] != -INFINITY ? last0 + tok[x] : -1;
             }
         }
-        if (lane == 0) flags[r] = pure ? last0 : INT_MIN;
+        if (lane == 0) flags[r] = pure ? last0 : INT_MIN / 2;
         ptx::fence_proxy_async_smem();
         ptx::mbar_arrive_warp(bar(T::B_LFULL + r));
         ++g;
@@ -557,7 +563,10 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
     // columns of a group, a multiple of 16, and this one's (the last may have fewer)
     const int group = (p.tile_cols + 16 * T::NCG - 1) / (16 * T::NCG) * 16;
     const int col0 = min(cg * group, p.tile_cols), cols = min(group, p.tile_cols - col0);
-    const int tok0 = p.by_g(col0), tok1 = p.by_g(col0 + max(cols, 1) - 1);  // its first and last token
+    // A block at `at` of a tile whose first token sees `last`: at <= last + plain_by, the group's
+    // first token sees the warp's last position; at > last + none_by, its last token not the first.
+    const int plain_by = cols == COLS ? p.by_g(col0) - half * 128 - quad * 32 - 31 : INT_MIN / 2;
+    const int none_by = p.by_g(col0 + max(cols, 1) - 1) - half * 128 - quad * 32;
     float* sums = reinterpret_cast<float*>(smem + T::OFF_SUM);
     const int* flags = reinterpret_cast<const int*>(smem + T::OFF_FLAG);
     uint32_t g = 0;
@@ -577,16 +586,10 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
             if (!__all_sync(0xffffffffu, ready) &&
                 !warp_wait_phase(bar(T::B_SFULL + r * T::KH + half), (g / T::SR) & 1u, ctl, SITE_S_FULL)) return;
             ptx::tc_fence_after();
-            // do the columns' first and last token see the warp's last and first position?
-            const int last = flags[lr], warp_pos = pos - lane;
-            const bool plain = last != INT_MIN && warp_pos + 31 <= last + tok0;
-            const bool none = last != INT_MIN && warp_pos > last + tok1;
+            const int last = flags[lr], at = u.j * T::KB;
+            const bool plain = at <= last + plain_by;
             const uint32_t next = bar(T::B_SFULL + (g + 1) % T::SR * T::KH + half), next_ph = ((g + 1) / T::SR) & 1u;
-            if (none) {
-                __syncwarp();
-                if (lane < 2) ptx::mbar_arrive(lane == 0 ? bar(T::B_SEMPTY + r * T::KH + half) : bar(T::B_LEMPTY + lr));
-                ready = ptx::mbar_test_wait(next, next_ph);
-            } else if (plain && cols == COLS) {
+            if (plain) {
                 // All of this warp's scores at once, so that their slot is free before they
                 // are used, and no comparisons (in one loop with the others they took 6.9
                 // instructions a weight).
@@ -605,6 +608,10 @@ __device__ void weigh(const ScoreParams& p, volatile int* ring, uint8_t* smem, u
                     sum0 = ptx::fadd2(sum0, ptx::pack_f32x2(ptx::ex2(a[0]), ptx::ex2(a[1])));
                     sum1 = ptx::fadd2(sum1, ptx::pack_f32x2(ptx::ex2(a[2]), ptx::ex2(a[3])));
                 }
+            } else if (last >= 0 && at > last + none_by) {
+                __syncwarp();
+                if (lane < 2) ptx::mbar_arrive(lane == 0 ? bar(T::B_SEMPTY + r * T::KH + half) : bar(T::B_LEMPTY + lr));
+                ready = ptx::mbar_test_wait(next, next_ph);
             } else {
 #pragma unroll 1
                 for (int c0 = 0; c0 < cols; c0 += 16) {
@@ -707,7 +714,8 @@ __global__ void __launch_bounds__(ScoreTile<D>::THREADS, 1)
             cut.z = -1;
             if (place.left > 0) {
                 const scoret::Shape<D> s(p, place.s);
-                cut = scoret::Cut{place.z, walk.hk, walk.j, walk.i, s.nt - s.first(p, walk.j), place.s.len,
+                const int past = walk.i - scoret::UNIT_COST;  // tiles in front, or (negative) cost before the first
+                cut = scoret::Cut{place.z, walk.hk, walk.j, max(past, 0), s.nt - s.first(p, walk.j), place.s.len,
                                   place.s.len + place.s.nl, 0, start, total};
             }
             static_cast<scoret::Cut*>(p.cuts)[blockIdx.x] = cut;
