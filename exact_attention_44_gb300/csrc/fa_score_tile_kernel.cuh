@@ -32,8 +32,8 @@
 // warps of a pair spend 1050 on 64 exponentials a thread each and the rest on the wait, the
 // load of the scores and the loop; the products take 1150 of them, and the special function
 // units, which give a warp's exponential in 4 cycles, 1024.  Four prompts of 1000 to 2000
-// tokens after 0 to 3000 positions, 111 GFLOP: 93 us repeated in a graph, 105 on new inputs,
-// 1.19 to 1.05 PFLOP/s, 0.61 to 0.54 of the measured bf16 peak (tensor pipe 56 % busy).  On
+// tokens after 0 to 3000 positions, 111 GFLOP: 93 us repeated in a graph, 105 to 112 on new
+// inputs, 1.19 to 0.99 PFLOP/s, 0.61 to 0.51 of the measured bf16 peak (tensor pipe 56 % busy).  On
 // the way there, in us, four prompts of 2000 tokens each (164 GFLOP, 84 us at that peak,
 // constant lse, 32 heads): 228 with lse from shared memory and one issuer; 214 with the
 // comparisons in a loop of their own; 200 with the halves' slots apart; 186 with two issuers
