@@ -118,6 +118,16 @@ def test_many_sequences(Z, T):
     check(Z, r.randint(0, 60, Z).tolist(), r.randint(0, T + 1, Z).tolist(), T, 4, 2, 16, 16, "fp16")
 
 
+@pytest.mark.parametrize("Z,D,G", [(3, 64, 4), (40, 32, 4), (9, 256, 2), (35, 128, 32)])
+def test_many_units_of_few_and_many_tiles(Z, D, G):
+    """Chunks of every length up to several tiles, none among them: ranges end in front of, in and behind a unit's tiles."""
+    r = np.random.RandomState(Z)
+    new = r.randint(0, 301, Z)
+    new[::4] = 0
+    new[1] = 300
+    check(Z, r.randint(0, 600, Z).tolist(), new.tolist(), 300, G, 1, D, 16, "bf16", decay=0.5)
+
+
 def test_columns_beyond_the_lengths_and_no_work():
     import exact_attention_44_gb300 as fa
     kc = torch.randn(4, 2, 16, 64).half().cuda()
