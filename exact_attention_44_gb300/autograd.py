@@ -74,7 +74,8 @@ def rotary(q, k, turns, positions=None, *, interleaved: bool = False, factor: fl
 
     turns: from fa_rope_turns.  positions: int32 (N) or (Z, N), default 0 .. N - 1.  Packed
     sequences, (total, H, D) as ``attention_varlen`` takes them, need positions (total).  The
-    gradient turns back (fa_rope with inverse) and has a gradient itself.  k may be None.
+    gradient turns back (fa_rope with inverse) and has a gradient itself; forward mode is
+    refused (NotImplementedError), as ``attention`` refuses it.  k may be None.
     Returns (q, k) turned.
     """
     call = _calls().rotary

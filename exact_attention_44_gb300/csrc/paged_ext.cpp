@@ -557,6 +557,10 @@ struct TurnBackward : public torch::autograd::Node {
 
 // k and pos may be undefined; so is the second result then.
 std::pair<at::Tensor, at::Tensor> turn_rows(const at::Tensor& q, const at::Tensor& k, const at::Tensor& pos, const Turn& how) {
+    // (the outputs would have none, which reads as a derivative of zero)
+    for (const at::Tensor* t : {&q, &k})
+        TORCH_CHECK_NOT_IMPLEMENTED(!t->defined() || !t->_fw_grad(0).defined(),
+                                    "rotary has no forward-mode gradient: an input carries a tangent");
     const at::Tensor *kp = k.defined() ? &k : nullptr, *pp = pos.defined() ? &pos : nullptr;
     fa_rope_args x = rope_args(q, kp, how.turns, pp, how.interleaved, how.inverse, how.factor);
     const int dev = cuda_device("rotary", q, {kp, pp});

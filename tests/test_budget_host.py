@@ -257,6 +257,21 @@ def test_python_cache_checks(lib):
             fa.fa_cache_evict(**{**good, **change})
 
 
+def test_rotary_refuses_forward_mode(lib):
+    """A tangent is refused before anything else is looked at: it would be lost, and read as a derivative of zero."""
+    import torch.autograd.forward_ad as fwd
+
+    turns = torch.zeros(32, dtype=torch.int64)
+    q = torch.zeros(2, 4, 3, 64, dtype=torch.half)
+    with fwd.dual_level():
+        dual = fwd.make_dual(q, torch.ones_like(q))
+        for args in ((dual, None), (dual, q), (q, dual)):
+            with pytest.raises(NotImplementedError, match="tangent"):
+                fa.rotary(*args, turns)
+        with pytest.raises(ValueError, match="CUDA"):
+            fa.rotary(q, q, turns)
+
+
 # ------------------------------------------------------------- the plain statements
 
 def test_turn_statement():
