@@ -527,15 +527,17 @@ struct Turn {  // how rows turn, but for the rows
 int64_t version_of(const at::Tensor& t) { return t.is_inference() ? 0 : (int64_t)t._version(); }
 std::pair<at::Tensor, at::Tensor> turn_rows(const at::Tensor& q, const at::Tensor& k, const at::Tensor& pos, const Turn& how);
 
-struct TurnBackward : public torch::autograd::Node {
+struct TurnBackward : public torch::autograd::Node {  // of q and k, or of the one that needs a gradient
     Turn how;
     torch::autograd::SavedVariable positions;
     bool has_positions = false;
     std::string name() const override { return "RotaryBackward"; }
     variable_list apply(variable_list&& grads) override {
-        const at::Tensor dq = grads[0], dk = grads.size() > 1 ? grads[1] : at::Tensor();
+        // an input with an edge, a gradient, and somebody who asked for it
+        auto wanted = [&](size_t i) { return i < grads.size() && grads[i].defined() && task_should_compute_output(i); };
+        const bool first = wanted(0), second = wanted(1);
         variable_list out(grads.size());
-        if (!dq.defined() && !dk.defined()) return out;
+        if (!first && !second) return out;
         at::Tensor pos;
         {
             std::lock_guard<std::mutex> lock(mutex_);
@@ -544,9 +546,9 @@ struct TurnBackward : public torch::autograd::Node {
         if (version_of(how.turns) != how.version)
             throw std::runtime_error("rotary: turns, needed for the gradient, has been modified by an inplace operation");
         const Turn back{how.turns, how.version, how.interleaved, !how.inverse, how.factor};
-        const auto r = turn_rows(rows_of(dq.defined() ? dq : dk), dq.defined() && dk.defined() ? rows_of(dk) : at::Tensor(), pos, back);
-        if (dq.defined()) out[0] = r.first;
-        if (dk.defined()) out[1] = dq.defined() ? r.second : r.first;
+        const auto r = turn_rows(rows_of(grads[first ? 0 : 1]), first && second ? rows_of(grads[1]) : at::Tensor(), pos, back);
+        if (first) out[0] = r.first;
+        if (second) out[1] = first ? r.second : r.first;
         return out;
     }
     void release_variables() override {
@@ -570,18 +572,20 @@ std::pair<at::Tensor, at::Tensor> turn_rows(const at::Tensor& q, const at::Tenso
     rope_outputs(x, qo, ko);
     const fa_status st = PyGILState_Check() ? unlocked([&] { return lib.rope(&x, stream); }) : lib.rope(&x, stream);
     if (st != FA_OK) throw Failed(st, "fa_rope");
-    if (at::GradMode::is_enabled() && (q.requires_grad() || (kp != nullptr && k.requires_grad()))) {
+    // an input that needs no gradient is not in the graph, nor is its output
+    const bool q_needs = at::GradMode::is_enabled() && q.requires_grad();
+    const bool k_needs = at::GradMode::is_enabled() && kp != nullptr && k.requires_grad();
+    if (q_needs || k_needs) {
         std::shared_ptr<TurnBackward> node(new TurnBackward(), torch::autograd::deleteNode);
         node->how = how;
         if (pp != nullptr) {
             node->positions = torch::autograd::SavedVariable(pos, false);
             node->has_positions = true;
         }
-        // (an input that needs no gradient has no edge)
-        if (kp != nullptr) node->set_next_edges(torch::autograd::collect_next_edges(q, k));
-        else node->set_next_edges(torch::autograd::collect_next_edges(q));
-        torch::autograd::set_history(qo, node);
-        if (kp != nullptr) torch::autograd::set_history(ko, node);
+        if (q_needs && k_needs) node->set_next_edges(torch::autograd::collect_next_edges(q, k));
+        else node->set_next_edges(torch::autograd::collect_next_edges(q_needs ? q : k));
+        if (q_needs) torch::autograd::set_history(qo, node);
+        if (k_needs) torch::autograd::set_history(ko, node);
     }
     return {qo, ko};
 }

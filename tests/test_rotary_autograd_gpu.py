@@ -41,3 +41,37 @@ def test_forward_mode_is_refused():
             torch.autograd.grad(y, x, dual[0])
         fa.rotary(q, k, turns)  # (no tangent, no refusal)
     fa.rotary(fwd.unpack_dual(dual[0]).primal, k, turns)
+
+
+@pytest.mark.parametrize("needed", [(True, False), (False, True), (True, True), (False, False)])
+def test_only_what_needs_a_gradient_is_in_the_graph(needed):
+    import exact_attention_44_gb300 as fa
+    turns, grads = turns_of(32), rows(2)
+    both = [t.clone().requires_grad_() for t in rows()]
+    want = torch.autograd.grad(fa.rotary(*both, turns), both, grads)
+    some = [t.clone().requires_grad_(n) for t, n in zip(rows(), needed)]
+    y = fa.rotary(*some, turns)
+    assert tuple(t.requires_grad for t in y) == needed
+    for t, u, g, n, w in zip(y, some, grads, needed, want):
+        if n:
+            assert torch.equal(torch.autograd.grad(t, u, g, retain_graph=True)[0], w)
+    for t, u in zip(y, fa.fa_rope(*rows(), turns)):
+        assert torch.equal(t, u)
+
+
+@pytest.mark.parametrize("side", [0, 1])
+def test_only_what_is_asked_for_is_turned_back(side):
+    """Both sides need gradients and both come back, but only one leaf's is asked for: one tensor is made, as where there
+    is only that side."""
+    import exact_attention_44_gb300 as fa
+    turns, grads = turns_of(64), rows(3)
+    leaves = [t.requires_grad_() for t in rows()]
+
+    def made(outs, leaf, up):
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        g, = torch.autograd.grad(outs, leaf, up, retain_graph=True)
+        return torch.cuda.memory_stats()["allocation.all.allocated"] - before, g
+
+    alone, want = made(fa.rotary(leaves[side], None, turns)[0], leaves[side], grads[side])
+    n, g = made(fa.rotary(*leaves, turns), leaves[side], grads)
+    assert torch.equal(g, want) and n == alone == 1
