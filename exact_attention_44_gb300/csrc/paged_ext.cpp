@@ -188,6 +188,12 @@ fa_status unlocked(F&& fn) {
     return st;
 }
 
+// A call has written these: autograd may have saved them, and compares versions.
+void written(std::initializer_list<const at::Tensor*> tensors) {
+    for (const at::Tensor* t : tensors)
+        if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // A workspace argument: its bytes are counted, so they must lie together.
 void check_workspace(const at::Tensor* t) {
     if (t != nullptr && !t->is_contiguous()) value_error("workspace must be contiguous");
@@ -502,6 +508,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         if (k != nullptr) ko = ko_arg != nullptr ? *ko_arg : out_like(*k);
         rope_outputs(x, qo, ko);
         check(unlocked([&] { return lib.rope(&x, place.stream()); }), "fa_rope");
+        written({qo_arg, ko_arg});
         return pair(qo, ko);
     });
 }
@@ -653,6 +660,7 @@ PyObject* cache_append_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x.Hq = to_int(q.size(1), "the heads");
         x.T = to_int(T, "T");
         check(unlocked([&] { return lib.append_rope(&x, place.stream()); }), "fa_cache_append_rope");
+        written({qo_arg, &kc, &vc});
         return THPVariable_Wrap(qo);
     });
 }
@@ -712,6 +720,7 @@ PyObject* cache_score(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x.Hq = to_int(q.size(1), "the heads");
         x.T = to_int(q.size(2), "T");
         check(unlocked([&] { return lib.score(&x, place.stream()); }), "fa_cache_score");
+        written({&scores});
         Py_RETURN_NONE;
     });
 }
@@ -760,6 +769,7 @@ PyObject* cache_evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
         x.workspace = ws.data_ptr();
         x.workspace_bytes = ws.nbytes();
         check(unlocked([&] { return lib.evict(&x, place.stream()); }), "fa_cache_evict");
+        written({&kc, &vc, &table, &lens, &refs, &scores, &missing});
         Py_RETURN_NONE;
     });
 }
