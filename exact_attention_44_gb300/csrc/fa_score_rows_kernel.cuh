@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(32 * SCORE_WARPS, ScoreRows<D>::ctas(NT)) fa_s
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, c = lane % 4;
-    auto steps = [&](const ScoreLen& s) { return (s.len + s.nl + T::KT - 1) / T::KT; };
+    // (without a new token K has no say, and with decay 1 the scores stay as they are)
+    auto steps = [&](const ScoreLen& s) { return s.nl == 0 && p.decay == 1.f ? 0 : (s.len + s.nl + T::KT - 1) / T::KT; };
     const ScorePlace place = score_place<SCORE_WARPS>(p, &find, blockIdx.x * SCORE_WARPS, warp, p.workers,
                                                       [&](const ScoreLen& s) { return (int64_t)steps(s) * p.Hkv; });
     int64_t left = place.left;
@@ -111,15 +112,15 @@ __global__ void __launch_bounds__(32 * SCORE_WARPS, ScoreRows<D>::ctas(NT)) fa_s
     // lane u's table entry of group u of a step
     auto ask = [&](const Step& x) -> int {
         const int pos = x.j * T::KT + lane * 16;
-        return lane < T::U && pos < x.s.len + x.s.nl ? ldi(p.table + x.z * p.st_z + p.by_page(pos)) : 0;
+        return lane < T::U && x.s.nl > 0 && pos < x.s.len + x.s.nl ? ldi(p.table + x.z * p.st_z + p.by_page(pos)) : 0;
     };
     auto load = [&](const Step& x, int entries, Keys<D>& k) {
         const int end = x.s.len + x.s.nl;
 #pragma unroll
         for (int u = 0; u < T::U; ++u) {
             const int e = __shfl_sync(0xffffffffu, entries, u), pos = x.j * T::KT + u * 16;
-            const bool there = (unsigned)e < (unsigned)p.P;
-            if (!there && pos < end && lane == 0) bad_page(p.status, SITE_PAGE_SCORE);
+            const bool asked = x.s.nl > 0 && pos < end, there = asked && (unsigned)e < (unsigned)p.P;
+            if (asked && !there && lane == 0) bad_page(p.status, SITE_PAGE_SCORE);
             const int slot = pos - p.by_page(pos) * p.page;
 #pragma unroll
             for (int y = 0; y < 2; ++y) {

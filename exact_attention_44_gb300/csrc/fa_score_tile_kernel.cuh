@@ -284,8 +284,9 @@ __device__ void walk_and_load(const CUtensorMap* tmQ, const CUtensorMap* tmK, co
         if (!have) u.i1 = 0;
         put<D>(ring, u, n++, bar);
         if (!have) break;
-        // lane b: the box of positions j KB + b box_rows ..
-        const int end = u.len + u.nl, k0 = u.j * T::KB + lane * p.box_rows;
+        // lane b: the box of positions j KB + b box_rows .. (without a new token K has no say: its
+        // products, with whatever is in its slot, are of rows that see nothing)
+        const int end = u.nl > 0 ? u.len + u.nl : 0, k0 = u.j * T::KB + lane * p.box_rows;
         const bool there = lane * p.box_rows < T::KB && k0 < end;
         int page = p.P, slot = 0;
         if (there) {

@@ -688,8 +688,8 @@ fa_status fa_cache_append_rope(const fa_cache_append_rope_args* args, cudaStream
  * the rows of the accepted tokens.  To let only the last W tokens of a prompt speak, pass
  * their q and lse and seq_lens less W.  Only the cache's k is read (v may be NULL).  A
  * row whose lse is -inf adds nothing; what q, lse and a page hold behind the last token
- * has no effect.  Sums are fp32, in an order that depends on the sizes only (bitwise
- * reproducible).
+ * has no effect.  Where new_lens[z] is 0 scores only decay and no page is looked at.  Sums
+ * are fp32, in an order that depends on the sizes only (bitwise reproducible).
  */
 typedef struct {
     fa_paged_cache cache;
