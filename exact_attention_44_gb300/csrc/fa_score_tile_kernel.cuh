@@ -475,9 +475,12 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
             if (tok[x] < left) t.l[x] = __ldcg(from + off[x] + t0);
         }
     };
-    // -lse / scale in three pieces, unless it is out of the type's range, infinite or NaN
+    // -lse / scale in three pieces, unless it is out of the type's range, infinite or NaN, or the
+    // scale so large that what the last piece leaves out matters: in fp16 up to 2^-25 f f = 2^-47,
+    // at LARGEST 2^-31 of an exponent; bf16 has bits down to 2^-133.
     const float per_scale = -1.f / p.scale;
-    constexpr float LIMIT = BF16 ? 1e38f : 60000.f;
+    constexpr float LARGEST = BF16 ? 0x1p96f : 0x1p16f;
+    const float limit = fabsf(p.scale) <= LARGEST ? (BF16 ? 1e38f : 60000.f) : -1.f;
     int* flags = reinterpret_cast<int*>(smem + T::OFF_FLAG);
     auto finish = [&](const Tile& t) -> bool {
         const int last0 = t.len + (t.i << p.token_shift), need = (t.j + 1) * T::KB - 1;
@@ -486,7 +489,7 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
 #pragma unroll
         for (int x = 0; x < N; ++x) {
             const float q = t.l[x] * per_scale;
-            const bool pieces = fabsf(q) <= LIMIT;
+            const bool pieces = fabsf(q) <= limit;
             w0[x] = w1[x] = 0u;
             if (pieces) split3<BF16>(q, w0[x], w1[x]);
             pure &= pieces || tok[x] == INT_MAX;
@@ -504,7 +507,7 @@ __device__ void stage_lse(const ScoreParams& p, volatile int* ring, uint8_t* sme
 #pragma unroll
             for (int x = 0; x < N; ++x) {
                 const int c = x * 32 + lane;
-                const bool pieces = fabsf(t.l[x] * per_scale) <= LIMIT;
+                const bool pieces = fabsf(t.l[x] * per_scale) <= limit;
                 ls[c] = pieces ? 0.f : -t.l[x] * 1.4426950408889634f;
                 la[c] = t.l[x] != -INFINITY ? last0 + tok[x] : -1;
             }

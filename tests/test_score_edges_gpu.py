@@ -1,7 +1,11 @@
 """The received attention weight where its kernels change their way."""
+import math
+
+import numpy as np
 import pytest
 import torch
 
+import budget_util as bu
 import paged_util as pu
 
 pytestmark = pytest.mark.gpu
@@ -47,3 +51,44 @@ def test_sequences_without_a_new_token_read_no_page(T, decay, Z):
     for z in range(Z):
         assert torch.equal(nobody[z, :, :lens[z]], was[z, :, :lens[z]] * decay)
         assert torch.equal(nobody[z, :, lens[z]:], was[z, :, lens[z]:])
+
+
+def against_the_statement(q, lse, kc, k, table, lens, T, scale):
+    """One call on empty scores, element by element."""
+    import exact_attention_44_gb300 as fa
+    Z, Hkv = len(lens), k[0].shape[0]
+    s = torch.zeros(Z, Hkv, table.shape[1] * kc.shape[2], device="cuda")
+    fa.fa_cache_score(q.cuda(), lse.cuda(), kc.cuda(), table.cuda(), i32(lens), s, scale=scale)
+    assert fa.fa_device_status()[0] == 0
+    want, bound = bu.score(q.double().numpy(), lse.double().numpy(), k, lens, [T] * Z, np.zeros(s.shape), 1.0, scale)
+    got = s.cpu().double().numpy()
+    for z in range(Z):
+        n = lens[z] + T
+        off = np.abs(got[z, :, :n] - want[z, :, :n])
+        assert (off <= bound[z, :, :n]).all(), (z, np.nanmax(off / bound[z, :, :n]))
+
+
+def sums(q, k, lens, scale):
+    """lse of each row over the positions that it sees."""
+    Z, Hq, T, _ = q.shape
+    lse = np.empty((Z, Hq, T))
+    for z in range(Z):
+        for h in range(Hq):
+            x = scale * (q[z, h].double().numpy() @ k[z][h * k[z].shape[0] // Hq].T)
+            x[np.arange(lens[z] + T)[None] > lens[z] + np.arange(T)[:, None]] = -math.inf
+            top = x.max(1)
+            lse[z, h] = top + np.log(np.exp(x - top[:, None]).sum(1))
+    return torch.from_numpy(lse).float()
+
+
+@pytest.mark.parametrize("dtype,scale", [("fp16", 2.0 ** 28), ("fp16", -2.0 ** 38), ("bf16", 2.0 ** 100)])
+@pytest.mark.parametrize("T", [2, 40, 200])
+def test_large_scales(T, dtype, scale):
+    """Queries and keys nearly as small as the type has them under a scale that makes up for it: lse / scale may be too
+    small for pieces of 16 bits."""
+    lens, D, small = [3, 700], 64, 2.0 * abs(scale) ** -0.5
+    kc, _, table, k, _ = pu.make_cache(21, [n + T for n in lens], 1, D, 16, dtype, garbage=0.0)
+    kc = (kc.float() * small).to(pu.DT[dtype])
+    k = [(torch.from_numpy(x) * small).to(pu.DT[dtype]).double().numpy() for x in k]
+    q = (small * torch.randn(2, 2, T, D, generator=torch.Generator().manual_seed(22))).to(pu.DT[dtype])
+    against_the_statement(q, sums(q, k, lens, scale), kc, k, table, lens, T, scale)
