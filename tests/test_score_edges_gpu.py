@@ -1,4 +1,5 @@
-"""The received attention weight where its kernels change their way."""
+"""The received attention weight where its kernels change their way: sequences without a new token, and unusual
+magnitudes, among them in tiles that are full and seen whole (test_score_gpu.py has them in tiles that are not)."""
 import math
 
 import numpy as np
@@ -7,6 +8,7 @@ import torch
 
 import budget_util as bu
 import paged_util as pu
+from test_score_gpu import check
 
 pytestmark = pytest.mark.gpu
 
@@ -92,3 +94,37 @@ def test_large_scales(T, dtype, scale):
     k = [(torch.from_numpy(x) * small).to(pu.DT[dtype]).double().numpy() for x in k]
     q = (small * torch.randn(2, 2, T, D, generator=torch.Generator().manual_seed(22))).to(pu.DT[dtype])
     against_the_statement(q, sums(q, k, lens, scale), kc, k, table, lens, T, scale)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1.0, 1e-30])
+def test_scales_of_full_tiles(scale, dtype):
+    check(24, [3, 200, 700], [200] * 3, 200, 2, 1, 64, 16, dtype, scale=scale, spread=0.5)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_sharp_attention_of_full_tiles(dtype):
+    check(25, [700, 663], [200, 200], 200, 2, 1, 128, 16, dtype, spread=40.0)
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_single_rows_of_full_tiles(dtype):
+    """A full tile seen whole, one of whose rows has no sum, one an lse / scale just within fp16's pieces and one just
+    outside: the tile's other rows are as they are without them."""
+    T, D, lens = 256, 64, [700]
+    scale = 0.125
+    kc, _, table, k, _ = pu.make_cache(26, [lens[0] + T], 1, D, 16, dtype, garbage=0.0)
+    q = torch.randn(1, 2, T, D, generator=torch.Generator().manual_seed(27))
+    for t, target in ((5, 59000.0), (70, 61000.0), (130, -59000.0)):  # lse is proportional to so sharp a row
+        q[0, 1, t] *= 1000
+        for _ in range(3):
+            rows = q.to(pu.DT[dtype])
+            q[0, 1, t] *= abs(target) / (sums(rows, k, lens, scale)[0, 1, t].item() / scale)
+        if target < 0:
+            q[0, 1, t] *= -1
+    q = q.to(pu.DT[dtype])
+    lse = sums(q, k, lens, scale)
+    ratio = lse / scale
+    assert 55000 < ratio[0, 1, 5] < 60000 < ratio[0, 1, 70] < 65000
+    lse[0, 0, 3] = lse[0, 1, 200] = -math.inf
+    against_the_statement(q, lse, kc, k, table, lens, T, scale)
