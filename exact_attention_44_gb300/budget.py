@@ -163,9 +163,11 @@ def fa_cache_evict(k_cache, v_cache, block_table, seq_lens, ref_counts, scores, 
     for a cache of one layer; ties: the lowest position).  They keep their order, their
     scores move along, seq_lens[z] becomes n, and pages behind are released.  Shared pages
     that would be written are replaced by free ones; missing, (1) int32, receives how many
-    lacked: if it is not 0 nothing else has changed.  workspace: a CUDA uint8 tensor of
-    fa_cache_evict_workspace_size(layers, Z, Hkv, max_pages, budget) bytes; one is
-    allocated when omitted.
+    lacked: if it is not 0 nothing else has changed; then cut in several calls, through
+    keep: the sequences that share nothing first, the others one by one.  Every row behind
+    the first one that goes moves, so cut by many positions now and then, not by one every
+    step.  workspace: a CUDA uint8 tensor of fa_cache_evict_workspace_size(layers, Z, Hkv,
+    max_pages, budget) bytes; one is allocated when omitted.
     """
     _calls().cache_evict(k_cache, v_cache, block_table, seq_lens, ref_counts, scores, budget, missing, keep, first, recent,
                          workspace, None if stream is None else stream.cuda_stream)

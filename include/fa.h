@@ -723,6 +723,14 @@ fa_status fa_cache_score_workspace_size(size_t* bytes);
  * any layer or head, stays shared.  *missing is the number of pages that lacked; if it is
  * not 0 nothing else is changed.  Rows whose page is not in the cache are recorded as
  * FA_ERR_PAGE and skipped.  Valid state before is valid state after (see fa_cache_fork).
+ *
+ * Where pages lack, cut in several calls, through keep: first the sequences that share
+ * nothing, whose pages are free for the next call, then the others one by one (each
+ * needs pages for what it still shares; what the last one shared is its own by then).  If
+ * no sequence can be cut, one has to go (fa_cache_fork with source -1).
+ * Every row behind the first one that goes moves, so a cut by one position costs half as
+ * much as a deep one, or more: cut by a slack of many positions now and then, not by one
+ * every step.
  * L <= 65535, P <= 2^30, Z * max_pages < 2^31, L * Z * Hkv <= 2^26.
  */
 typedef struct {
