@@ -69,8 +69,9 @@ def fa_rope_frequencies(rotary_dim: int, *, base: float = 10000.0, scaling: str 
 def fa_rope_turns(inv_freq):
     """The frequencies (radians a position, a 1-D tensor) as fa_rope takes them: an int64 tensor on the host.
 
-    Turns a position in units of 2^-64, which wrap after a whole turn, so that angles are
-    exact at any position.  Made once for a model; calls pass them on as launch arguments.
+    Turns a position in units of 2^-64, which wrap after a whole turn, so that angles keep
+    their precision at any position.  Made once for a model; calls pass them on as launch
+    arguments.
     """
     import torch
 

@@ -11,9 +11,12 @@
 //
 // What bounds it is the rows that move: 8 D bytes each, against 4 to 12 bytes of
 // selection a position.  32 sequences of 1500-2900 positions cut to 1024, 8 layers x 8 heads
-// of D = 128 (2.2 GB): the rows 318 us, 6.7 TB/s, a plain copy's rate; in all 361 us.  One
-// sequence of 1200, 16 layers (134 MB): 8.5 us to select, 7.6 for the books, 23.5 to move, 32
-// in all, of which the books are one CTA's chain of dependent loads.
+// of D = 128 (2.2 GB): 36 us to select, 19 for the books, 326 to move (6.6 TB/s, nearly a
+// plain copy's rate), in all, since the launches overlap, 366.  One sequence of 1200, 16 layers
+// (134 MB): 6.4, 6.7 and 25 us, in all 32.5, of which the books are one CTA's chain of dependent
+// loads.  (In all: repeated in a graph, without the copies that put the sequences back.)  Every
+// row behind the first one that goes moves: from 1025 positions to 1024 the one sequence takes
+// 27 us and the 32 take 214, where 1200 and 1500-2900 take 31 and 410 on the same pages of 16.
 #include "fa_evict.h"
 
 #include <climits>

@@ -8,17 +8,18 @@
 //
 // The angle.  p f in fp32 would be off by p 2^-24 radians (0.06 at a million), so f is
 // given in turns as a 64-bit fixed-point fraction and the product with the integer p
-// is taken modulo a whole turn by letting it wrap: what is left is exact but for f's
-// own rounding, p 2^-65 turns.  Its upper 32 bits go to sincospi.
+// is taken modulo a whole turn by letting it wrap: what is left is off by f's own roundings,
+// p (2^-65 + f 2^-54) turns for f radians a position (a quotient of 53 bits, then 64 fixed ones).
+// Its upper 32 bits, as an fp32 number (2^-26 turns), go to sincospi.
 //
 // What bounds it is reading and writing each row once.  A thread takes 8 pairs (two
 // 16-byte pieces) of a token through some of its heads, so that a sine and cosine serve
 // several heads; the loads go out before the sines are worked out, and where the rows go is
 // only looked at when they are there.  671 MB (32 + 8 heads of D = 128, 32768 tokens): 98
-// us, 6.8 TB/s, a plain copy's rate; five prompts of 1006 to 2011 tokens into the cache (123
-// MB) 24 us, 5.2 TB/s.  The turns come with the launch's arguments: read from one place in
-// global memory by every warp, through L2, they took 367 us (one L2 slice serves them all).
-// One token: 1.9 us, 64 tokens into the cache 2.8.
+// us, 6.8 TB/s, a plain copy's rate; five prompts of 1006 to 2011 tokens into the cache (124
+// MB) 24 us called on new inputs, 5.2 TB/s.  The turns come with the launch's arguments: read
+// from one place in global memory by every warp, through L2, they took 367 us (one L2 slice
+// serves them all).  One token: 1.9 us, 64 tokens into the cache 2.8 (in L2).
 #include "fa_rope.h"
 
 #include <cuda_bf16.h>
@@ -213,10 +214,14 @@ cudaError_t launch_v(RopeParams p, bool cache, int sms, cudaStream_t stream) {
         const dim3 grid((unsigned)x, (unsigned)((heads + n - 1) / n), (unsigned)z);
         return launch_dependent(cache ? with_cache : without, grid, ROPE_THREADS, 0, stream, p);
     };
-    // Eight heads a thread, all in flight, where that leaves 16 CTAs an SM (98 against 108
-    // us for 40 heads x 32768 tokens of D = 128, 40 against 47 for the cache's 48 x 10055),
-    // else four (10.6 against 13.3 us for 32 x 4096), and with few tokens fewer, so that there
-    // are CTAs for every SM.  (Figures of before the addresses moved behind the loads.)
+    // Eight heads a thread, all in flight, where that leaves 16 CTAs an SM, else four, and with
+    // few tokens fewer, so that there are CTAs for every SM.  Eight against four, inputs from
+    // DRAM, D = 128, by CTAs of eight heads: 40 heads x 32768 tokens (10240) 99.5 / 99.8 us, 40 x
+    // 8192 (2560) 27.5 / 26.9, 40 x 4096 (1280) 14.9 / 14.5, 32 x 4096 (1024) 12.4 / 12.0; into the
+    // cache, q, k and v, 5 x 2011 tokens of 48 heads (3780) 37.2 / 39.9, of 32 (2520) 25.3 / 27.1, 8 x
+    // 1000 of 32 (2016) 21.0 / 22.0, 64 x 17 of 48 (768) 9.3 / 8.4.  (With tensors in L2 eight is
+    // ahead from 1000 CTAs on: 32 x 4096 8.3 / 9.4.)  One head against four: 40 x 1 1.8 / 2.2, 40 x
+    // 256 3.8 / 3.0.
     if constexpr (V == 8)
         if (blocks(8) >= 16 * (int64_t)sms)
             return launch(fa_rope_kernel<BF16, INTER, V, true, 8>, fa_rope_kernel<BF16, INTER, V, false, 8>, 8);

@@ -9,13 +9,18 @@
 // long as B's is the same: 16 contiguous bytes of its two rows, which it loads straight
 // from the cache.  Nothing goes through shared memory.  A position's weights lie in
 // four neighbouring lanes and are summed there, in fp32.  Rows that do not fit in registers
-// (more than 32, groups wider than a tile) are loaded again for every step.
+// (more than 32, groups wider than a tile) are loaded again for every step: right for any
+// number, but slow for many (512 tokens of 136 heads after 1000 positions, one kv head, D =
+// 128: 1.7 ms, against 33 us for 128 heads on the tile kernel).
 //
 // What hides the way to memory is the number of warps: one step of K in 32 registers, 20
 // warps an SM for up to 8 rows.  Measured: 64 sequences of 256-4096 positions, one token,
-// 32 query heads on 8 of D = 128 (294 MB with the scores): 51 us, 5.8 TB/s (8000-12000: 214
-// us, 6.3 TB/s); with two steps in registers and 16 warps 54.  One sequence of 1024: 3.1 us.
-// 12 warps an SM 61 us, 28 (72 registers, spilled) 65.
+// 32 query heads on 8 of D = 128 (294 MB with the scores): 51 to 52 us repeated in a graph,
+// 52 to 53 called on new inputs, 5.6 to 5.8 TB/s (8000-12000: 214 us, 6.3 TB/s); with two steps
+// in registers and 16 warps 54 in a graph, with 12 warps an SM 61, 28 (72 registers, spilled)
+// 65.  One sequence of 1024: 2.9 to 3.1 us in a graph.  A sequence without a new token is no
+// work with decay 1, else a read and a write of its scores: 64 of 2000, half of them idle, 25 and
+// 35 us, none 48.
 #pragma once
 
 #include "fa_ptx.cuh"

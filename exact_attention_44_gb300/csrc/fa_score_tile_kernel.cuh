@@ -32,7 +32,7 @@
 // warps of a pair spend 1050 on 64 exponentials a thread each and the rest on the wait, the
 // load of the scores and the loop; the products take 1150 of them, and the special function
 // units, which give a warp's exponential in 4 cycles, 1024.  Four prompts of 1000 to 2000
-// tokens after 0 to 3000 positions, 111 GFLOP: 93 us repeated in a graph, 105 to 112 on new
+// tokens after 0 to 3000 positions, 111 GFLOP: 93 us repeated in a graph, 100 to 112 on new
 // inputs, 1.19 to 0.99 PFLOP/s, 0.61 to 0.51 of the measured bf16 peak (tensor pipe 56 % busy).  On
 // the way there, in us, four prompts of 2000 tokens each (164 GFLOP, 84 us at that peak,
 // constant lse, 32 heads): 228 with lse from shared memory and one issuer; 214 with the
@@ -41,6 +41,12 @@
 // 168 with four slots for Q; 156 with a quarter of the instructions where lse is staged; 136
 // with comparisons decided by each warp; 130 with UNIT_COST.  Not multiplying halves that a
 // tile does not see: no gain.
+//
+// These are groups of 4, whose tiles of 32 tokens fill the 128 columns.  A group that does not
+// (a tile's tokens are a power of two) pays for the columns left empty, and the warps whose
+// column group is not full compare for every tile, since the way without comparisons is laid
+// out for 64 columns: four prompts of 2000 tokens, 8 kv heads of D = 128, in us, groups of 4 and 8
+// 63 and 115, of 3, 5, 6, 7 and 12 85, 143, 157, 138 and 308.
 #pragma once
 
 #include <climits>

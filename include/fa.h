@@ -595,12 +595,13 @@ fa_status fa_cache_fork_workspace_size(int Z, int max_pages, size_t* bytes);
  *     (a, b) -> factor (a cos - b sin, a sin + b cos),
  * in fp32, rounded once; the rest of the row stays as it is.
  *
- * The angles are exact at any position: frequencies are given as turns a position in
- * units of 2^-64 (an integer that wraps after a whole turn), which fa_rope_turns makes of
- * radians a position.  They travel with the launch as its arguments, from a host array
- * that need not outlive the call (a captured graph keeps those that it was captured
- * with).  The angle of position p is then off by at most p inv_freq 2^-52
- * radians.
+ * The angles keep their precision at any position: frequencies are given as turns a
+ * position in units of 2^-64 (an integer that wraps after a whole turn), which
+ * fa_rope_turns makes of radians a position.  They travel with the launch as its
+ * arguments, from a host array that need not outlive the call (a captured graph keeps
+ * those that it was captured with).  Position p's angle is off by at most p (2^-65 +
+ * inv_freq 2^-54) turns, the frequency's own roundings, and by 2^-26 + 2^-32 turns where
+ * its fraction of a turn becomes an fp32 number.
  *
  * fa_rope_frequencies -- the usual frequencies, base^(-2 i / rotary_dim), host only, for
  * a context that is `stretch` times as long as the one they were made for:
